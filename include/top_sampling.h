@@ -337,6 +337,152 @@ int sampler_assemble_and_sample(const float* const* slices, const int64_t* slice
                                 size_t workspace_bytes, void* stream);
 
 /*
+ * Scoring, losses and adapters: what a serving or training step does next to
+ * the sampling path.  The pages only name the sampled tokens'
+ * log-probabilities; the calls below take GIVEN tokens, and the definitions
+ * are written out here.
+ *
+ * Shared by token_logprobs, token_logprobs_backward, policy_loss and
+ * preference_loss:
+ *   logits       [rows, vocab], leading dimension ld_logits, of logits_type
+ *                TS_F32 or TS_BF16; any alignment of the rows.  -inf marks a
+ *                token that is not allowed (probability 0).
+ *   token_ids    int32 [rows]: the token of each row.  A negative id leaves
+ *                the row out: its logits are not read, its log-probability
+ *                is 0 and its gradient row is 0, whatever the row holds.
+ *   temperature  finite, >= TS_GREEDY_EPS (else TS_EINVAL).  Log-probabilities
+ *                are those of logits / temperature; 1 gives the sampler's raw
+ *                log_softmax.
+ *   row_status   int32 [rows] or NULL: TS_ROW_BAD_PARAMS for a token id >=
+ *                vocab, TS_ROW_BAD_LOGITS for a row with a NaN or +inf logit
+ *                or no finite one.  Such a row's outputs and gradient row are
+ *                NaN, and so is a loss it takes part in.
+ *   grad_logits  [rows, vocab] in the logits' type, leading dimension
+ *                ld_grad >= vocab.  It may be the logits themselves (same
+ *                pointer and leading dimension: the gradient replaces them);
+ *                any other overlap is TS_EINVAL.  Columns past vocab are not
+ *                written.
+ *   workspace    as for sampler_sample: 256-byte aligned scratch, no
+ *                initialisation, ordered on one stream by whoever shares it.
+ * Sums over the vocabulary are fp32 per thread and double from there on;
+ * per-row arithmetic is double, outputs are rounded once.  Results do not
+ * depend on the order in which workgroups run.  rows == 0 writes nothing but
+ * a loss of 0.  rows, vocab < 2^31.
+ */
+enum { TS_F32 = 0, TS_BF16 = 1 };
+
+/*
+ * token_logprobs: lp[r] = z_t - ln sum_j exp(z_j), z = logits[r] / temperature,
+ * t = token_ids[r], and optionally the entropy H[r] = -sum_j p_j ln p_j of
+ * p = softmax(z).
+ *   logprobs   fp32 [rows]
+ *   entropies  fp32 [rows] or NULL
+ *   row_stats  fp32 [rows, 2] or NULL: max_j logits[r, j] and
+ *              sum_j exp((logits[r, j] - max) / temperature), for
+ *              token_logprobs_backward
+ *
+ * token_logprobs_backward: the gradient of the logits of any function of the
+ * two, from grad_logprobs = dL/dlp (fp32 [rows]) and, with the forward pass's
+ * entropies, grad_entropies = dL/dH (fp32 [rows] or NULL):
+ *   dL/dlogits[r, j] = (dL/dlp (1[j = t] - p_j)
+ *                       - dL/dH p_j (ln p_j + H)) / temperature.
+ * token_ids, temperature and the logits are the forward call's.  A row whose
+ * gradients are both 0 gives a row of zeros without reading its logits.  No
+ * workspace.
+ */
+size_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab);
+int token_logprobs(const void* logits, int32_t logits_type, int64_t rows, int64_t vocab,
+                   int64_t ld_logits, const int32_t* token_ids, float temperature,
+                   float* logprobs, float* entropies, float* row_stats, int32_t* row_status,
+                   void* workspace, size_t workspace_bytes, void* stream);
+int token_logprobs_backward(const void* logits, int32_t logits_type, int64_t rows, int64_t vocab,
+                            int64_t ld_logits, const int32_t* token_ids, float temperature,
+                            const float* row_stats, const float* grad_logprobs,
+                            const float* entropies, const float* grad_entropies,
+                            void* grad_logits, int64_t ld_grad, void* stream);
+
+/*
+ * policy_loss: the clipped policy loss with a KL term,
+ *   r   = exp(lp - old_logprobs)
+ *   s   = min(r A, clip(r, 1 - clip_low, 1 + clip_high) A),  A = advantages
+ *   kl  = exp(ref_logprobs - lp) - (ref_logprobs - lp) - 1
+ *   loss = sum over rows of weights (-s + kl_coef kl),
+ * and, with grad_logits, grad_loss times its gradient:
+ *   dloss/dlp = weights (-A r [s = r A] + kl_coef (1 - exp(ref - lp))).
+ * The weights hold the average the caller wants (1 / tokens, 1 / (sequences x
+ * length), ...).  A row of weight 0, like one of a negative token id, is left
+ * out.  A = 0 gives s = 0 at any ratio.
+ *   params         HOST struct; clip_low and clip_high >= 0, inf for no clip
+ *   old_logprobs   fp32 [rows]: log-probabilities when the tokens were drawn
+ *   ref_logprobs   fp32 [rows], or NULL if kl_coef == 0
+ *   advantages     fp32 [rows]
+ *   weights        fp32 [rows], or NULL for 1
+ *   grad_loss      fp32 [1] (device), or NULL for 1
+ *   loss           fp32 [1]
+ *   logprobs, ratios, kl   fp32 [rows] or NULL: lp, r and kl (0, 1 and 0 for
+ *                  a row that is left out; kl is 0 without ref_logprobs)
+ *   grad_logits    or NULL for the loss alone
+ * Workspace: token_logprobs_workspace_bytes.
+ */
+typedef struct ts_policy_params {
+  float temperature;
+  float clip_low;
+  float clip_high;
+  float kl_coef;
+} ts_policy_params;
+int policy_loss(const void* logits, int32_t logits_type, int64_t rows, int64_t vocab,
+                int64_t ld_logits, const int32_t* token_ids, const ts_policy_params* params,
+                const float* old_logprobs, const float* ref_logprobs, const float* advantages,
+                const float* weights, const float* grad_loss, float* loss, float* logprobs,
+                float* ratios, float* kl, int32_t* row_status, void* grad_logits, int64_t ld_grad,
+                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * preference_loss: the loss of paired log ratios.  Sequence i is rows
+ * [seq_offsets[i], seq_offsets[i + 1]); sequences 0 .. n_pairs - 1 are the
+ * chosen answers and n_pairs + i is the rejected one of pair i.
+ *   rho_i  = sum over the sequence's rows that are not left out of
+ *            (lp - ref_logprobs), divided by their number (if any) with
+ *            TS_PREFERENCE_MEAN
+ *   z      = beta (rho_chosen - rho_rejected) - margin
+ *   l      = -(1 - label_smoothing) ln sigmoid(z)
+ *            - label_smoothing ln sigmoid(-z)
+ *   loss   = sum over pairs of pair_weights l,
+ * and, with grad_logits, grad_loss times its gradient.  An empty sequence
+ * has rho = 0.  Rows before the first and after the last sequence take no
+ * part (log-probability and gradient row 0).  A pair of weight 0 adds
+ * nothing to the loss and the gradient.
+ *   seq_offsets    int32 [2 n_pairs + 1], non-decreasing; used clamped to
+ *                  [0, rows]
+ *   params         HOST struct; beta > 0, label_smoothing in [0, 1]
+ *   ref_logprobs   fp32 [rows], or NULL for 0 (no reference)
+ *   pair_weights   fp32 [n_pairs], or NULL for 1 / n_pairs
+ *   grad_loss      fp32 [1] (device), or NULL for 1
+ *   loss           fp32 [1]
+ *   pair_losses    fp32 [n_pairs] or NULL: l
+ *   rewards        fp32 [2 n_pairs] or NULL: beta rho
+ *   logprobs       fp32 [rows] or NULL
+ *   grad_logits    or NULL for the loss alone
+ * Workspace: preference_loss_workspace_bytes.  n_pairs < 2^30.
+ */
+#define TS_PREFERENCE_MEAN 1
+typedef struct ts_preference_params {
+  float temperature;
+  float beta;
+  float label_smoothing;
+  float margin;
+  int32_t flags;
+} ts_preference_params;
+size_t preference_loss_workspace_bytes(int64_t rows, int64_t vocab, int64_t n_pairs);
+int preference_loss(const void* logits, int32_t logits_type, int64_t rows, int64_t vocab,
+                    int64_t ld_logits, const int32_t* token_ids, const int32_t* seq_offsets,
+                    int64_t n_pairs, const ts_preference_params* params,
+                    const float* ref_logprobs, const float* pair_weights, const float* grad_loss,
+                    float* loss, float* pair_losses, float* rewards, float* logprobs,
+                    int32_t* row_status, void* grad_logits, int64_t ld_grad, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/*
  * ts_status_string: name of a TS_* return code (a static string; unknown
  * codes give "TS_UNKNOWN").  ts_last_error: a description of the calling
  * thread's last nonzero return (a per-thread static buffer, overwritten by

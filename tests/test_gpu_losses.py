@@ -1,0 +1,551 @@
+"""Token scoring, the policy and preference losses and their gradients on the
+GPU against the float64 oracle (oracle/losses.py).
+
+Tolerances.  u = 2^-24 is fp32's rounding.  A row's sum is added up per thread
+in fp32, at most 128 terms one after the other (relative error at most 128 u),
+each term exp2 of an argument with two roundings (relative error at most
+2 u |z - max z| plus 2 u of exp2 itself), and in double from there on.  So ln S
+is off by at most
+    LSE = 130 u + 2 u * (the p-weighted mean of |z - max z|, below 30 here)
+        < 1.2e-5,
+a log-probability by LSE plus its own rounding, and the other outputs follow
+by their derivatives.  A gradient entry e_j a has the relative errors of e_j
+(2 u |z_j - max z| + 4 u), of S (LSE) and of a (LSE where it holds a ratio),
+and is rounded once to its type.
+"""
+import numpy as np
+import pytest
+
+from oracle import losses as ref
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+LSE = 1.2e-5
+HALF = {"fp32": U, "bf16": 2.0 ** -8}
+
+
+def _dev():
+    import torch
+
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    return torch.device("cuda:0")
+
+
+def say(*a):
+    print(*a, flush=True)
+
+
+def make_logits(rows, vocab, dtype, pad, seed, masks=True):
+    """(device logits [rows, vocab] in a buffer pad columns wider, the same
+    values in float64).  With masks: rows with -inf entries, with a single
+    finite entry, with entries of the type's lowest value, and with one token
+    far above the rest."""
+    import torch
+
+    g = np.random.default_rng(seed)
+    x = g.normal(0, 1.5, (rows, vocab)).astype(np.float32)
+    if masks:
+        for r in range(rows):
+            kind = r % 6
+            if kind == 1 and vocab > 1:
+                x[r, g.random(vocab) < 0.6] = -np.inf
+                x[r, g.integers(vocab)] = 0.5
+            elif kind == 2:
+                x[r] = -np.inf
+                x[r, g.integers(vocab)] = -3.0
+            elif kind == 3:
+                x[r, g.random(vocab) < 0.5] = -3.3e38
+                x[r, g.integers(vocab)] = 2.0
+            elif kind == 4:
+                x[r, g.integers(vocab)] += 25.0
+            elif kind == 5:
+                x[r] += 300.0
+    wide = torch.full((rows, vocab + pad), 7.0, device=_dev(),
+                      dtype=torch.float32 if dtype == "fp32" else torch.bfloat16)
+    t = wide[:, :vocab]
+    t.copy_(torch.from_numpy(x))
+    return t, t.cpu().double().numpy()
+
+
+def allowed_tokens(x, seed, skip=0.15):
+    """A finite token of each row; some rows left out."""
+    g = np.random.default_rng(seed)
+    tok = np.array([g.choice(np.flatnonzero(np.isfinite(r) & (r > -1e38))) for r in x])
+    out = g.random(len(x)) < skip
+    out[0] = False
+    tok[out] = -1 - g.integers(0, 100, out.sum())
+    return tok.astype(np.int32)
+
+
+def to_dev(a, dtype=None):
+    import torch
+
+    return torch.from_numpy(np.ascontiguousarray(a)).to(_dev(), dtype or torch.float32)
+
+
+def close(got, want, tol, what):
+    got = got.detach().double().cpu().numpy()
+    want = np.asarray(want, dtype=np.float64)
+    tol = np.broadcast_to(tol, want.shape)
+    assert got.shape == want.shape, what
+    same = (got == want) | (np.isnan(got) & np.isnan(want))
+    with np.errstate(invalid="ignore"):
+        off = np.where(same, 0.0, np.abs(got - want) - tol)
+    off = np.where(np.isnan(off), np.inf, off)
+    i = np.unravel_index(off.argmax(), off.shape) if off.size else None
+    assert not off.size or off[i] <= 0, (what, i, got[i], want[i], tol[i])
+
+
+def grad_tol(want, x, temperature, dtype, slack):
+    """Entry by entry: rounding to the type, the entry's own exp2, the row's
+    sum and coefficient.  An e_j below 2^-126 may be taken as 0; |a| < 64."""
+    with np.errstate(invalid="ignore", over="ignore"):
+        top = x.max(-1, keepdims=True)
+        far = np.minimum(np.where(np.isfinite(x), (top - x) / temperature, 0.0), 140.0)
+    rel = HALF[dtype] + 2 * U * far + 6 * U + slack
+    return np.abs(np.where(np.isfinite(want), want, 0.0)) * rel + 2.0 ** -120
+
+
+SHAPES = [
+    # rows, vocab, pad: one and two tokens, odd sizes, below and above a
+    # vector, a slab (1,024 vectors) and a chunk, unaligned row starts
+    (1, 1, 0), (1, 2, 0), (5, 3, 1), (7, 9, 0), (6, 255, 0), (13, 1000, 24), (12, 4096, 0),
+    (6, 4097, 0), (37, 8192, 3), (8, 30011, 0), (3, 151936, 0), (70, 16390, 5), (1100, 257, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows,vocab,pad", SHAPES)
+def test_token_logprobs(rows, vocab, pad, dtype):
+    import torch
+
+    import top_sampling_amd as ts
+
+    for temperature in (1.0, 0.37):
+        say("token_logprobs", rows, vocab, pad, dtype, temperature)
+        logits, x = make_logits(rows, vocab, dtype, pad, rows + vocab)
+        tok = allowed_tokens(x, 5)
+        lp, ent = ref.score(x, tok, temperature)
+        tk = to_dev(tok, torch.int32)
+        out = ts.token_logprobs(logits, tk, temperature, entropies=True)
+        plain = ts.token_logprobs(logits, tk, temperature)
+        torch.cuda.synchronize()
+        close(out.logprobs, lp, LSE + U * np.abs(lp), "logprobs")
+        # H = ln S - E[z - max]: the mean's error is LSE of its size
+        close(out.entropies, ent, LSE * (2 + 30), "entropies")
+        assert plain.entropies is None
+        close(plain.logprobs, lp, LSE + U * np.abs(lp), "logprobs without entropies")
+        assert not out.row_status.any() and not plain.row_status.any()
+        # gradients of both
+        g = np.random.default_rng(3)
+        a, b = g.normal(size=rows).astype(np.float32), g.normal(size=rows).astype(np.float32)
+        b[rows // 2:] = 0.0
+        if rows > 3:
+            a[rows - 2:] = 0.0
+        for gh, fwd in ((b, out), (None, plain)):
+            want = ref.score_gradient(x, tok, temperature, a.astype(np.float64),
+                                      None if gh is None else gh.astype(np.float64))
+            wide = torch.full((rows, vocab + 2), 7.0, dtype=logits.dtype, device=logits.device)
+            got = ts.token_logprobs_backward(logits, tk, fwd, to_dev(a),
+                                             None if gh is None else to_dev(gh), temperature,
+                                             grad_logits=wide[:, :vocab])
+            torch.cuda.synchronize()
+            assert (wide[:, vocab:] == 7.0).all()
+            tol = grad_tol(want, x, temperature, dtype, 2 * LSE)
+            # a term and an entropy term of opposite sign cancel: LSE of the
+            # larger, h p (|ln p| + H) with p (|ln p| + H) <= p (140 + 12)
+            p = np.exp(ref.log_softmax(x, temperature))
+            size = np.abs(a)[:, None] * p
+            if gh is not None:
+                with np.errstate(invalid="ignore"):
+                    far = np.where(p > 0, np.abs(ref.log_softmax(x, temperature)), 0.0)
+                size = size + np.abs(gh)[:, None] * p * (far + np.abs(ent)[:, None] + 32)
+            size[np.arange(rows), np.maximum(tok, 0)] += np.abs(a) * LSE
+            close(got, want, tol + size * (2 * LSE) / temperature, ("gradient", gh is None))
+            out_rows = tok < 0
+            assert not got[to_dev(out_rows, torch.bool)].any()
+
+
+def test_backward_in_place_and_repeatable():
+    import torch
+
+    import top_sampling_amd as ts
+
+    for dtype in ("fp32", "bf16"):
+        logits, x = make_logits(9, 30011, dtype, 0, 1)
+        tk = to_dev(allowed_tokens(x, 2), torch.int32)
+        g = torch.randn(9, device=_dev())
+        fwd = ts.token_logprobs(logits, tk, 0.8, entropies=True)
+        one = ts.token_logprobs_backward(logits, tk, fwd, g, g, 0.8)
+        two = ts.token_logprobs_backward(logits, tk, fwd, g, g, 0.8)
+        same = logits.clone()
+        three = ts.token_logprobs_backward(same, tk, fwd, g, g, 0.8, grad_logits=same)
+        assert three.data_ptr() == same.data_ptr()
+        assert torch.equal(one, two) and torch.equal(one, three)
+        adv = torch.randn(9, device=_dev())
+        kw = dict(weights=torch.rand(9, device=_dev()), temperature=0.8)
+        a = ts.policy_loss(logits, tk, fwd.logprobs, adv, backward=True, **kw)
+        same = logits.clone()
+        b = ts.policy_loss(same, tk, fwd.logprobs, adv, grad_logits=same, **kw)
+        assert torch.equal(a.grad_logits, same) and torch.equal(a.loss, b.loss)
+
+
+def policy_inputs(rows, x, tok, temperature, seed):
+    g = np.random.default_rng(seed)
+    lp, _ = ref.score(x, tok, temperature)
+    lp = np.where(np.isfinite(lp), lp, -1.0)
+    # Ratios away from the clip borders by far more than their error, so both
+    # sides take the same branch: spread them over fixed points.
+    steps = np.array([-0.6, -0.1, 0.0, 0.15, 0.55])
+    old = (lp - steps[g.integers(0, 5, rows)]).astype(np.float32)
+    rf = (lp + g.normal(0, 0.4, rows)).astype(np.float32)
+    adv = g.normal(size=rows).astype(np.float32)
+    w = g.uniform(0.1, 1.0, rows).astype(np.float32) / rows
+    if rows > 4:
+        adv[3] = 0.0
+        w[4] = 0.0
+    return old, rf, adv, w
+
+
+def check_policy(got, want, x, temperature, dtype, rows, w, adv, kl_coef, scale=1.0):
+    r = want["ratios"]
+    close(got.logprobs, want["logprobs"], LSE + U * np.abs(want["logprobs"]), "logprobs")
+    close(got.ratios, r, r * (LSE + 2 * U), "ratios")
+    # dkl/dlp = 1 - exp(gap), at most e^2 here
+    k = want["kl"]
+    close(got.kl, k, 8 * LSE + U * np.abs(k), "kl")
+    each = w * (np.abs(adv) * r + kl_coef * 8)
+    close(got.loss, want["loss"], (each * LSE).sum() + 2 * U * abs(want["loss"]), "loss")
+    if got.grad_logits is not None:
+        # the coefficient's absolute error, beside the entry's relative one
+        coef = scale * w * (np.abs(adv) * r + kl_coef * 8) * 2 * LSE / temperature
+        p = np.exp(ref.log_softmax(x, temperature))
+        tol = grad_tol(want["grad"], x, temperature, dtype, 2 * LSE) + coef[:, None] * \
+            np.maximum(p, (want["grad"] != 0))
+        close(got.grad_logits, want["grad"], tol, "gradient")
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows,vocab,pad", SHAPES)
+def test_policy_loss(rows, vocab, pad, dtype):
+    import torch
+
+    import top_sampling_amd as ts
+
+    for temperature, kl_coef, scale in ((1.0, 0.0, 1.0), (0.7, 0.2, 3.0)):
+        say("policy_loss", rows, vocab, pad, dtype, temperature, kl_coef)
+        logits, x = make_logits(rows, vocab, dtype, pad, rows * 3 + vocab)
+        tok = allowed_tokens(x, 6)
+        old, rf, adv, w = policy_inputs(rows, x, tok, temperature, 8)
+        kw = dict(clip_low=0.2, clip_high=0.28, kl_coef=kl_coef, temperature=temperature)
+        f = lambda a: a.astype(np.float64)  # noqa: E731
+        with_ref = kl_coef > 0
+        want = ref.policy(x, tok, f(old), f(adv), f(rf) if with_ref else None, f(w),
+                          grad_loss=scale, **kw)
+        args = (to_dev(tok, torch.int32), to_dev(old), to_dev(adv))
+        kws = dict(ref_logprobs=to_dev(rf) if with_ref else None, weights=to_dev(w), **kw)
+        gl = torch.full((1,), scale, device=_dev()) if scale != 1.0 else None
+        got = ts.policy_loss(logits, *args, backward=True, grad_loss=gl, **kws)
+        fwd = ts.policy_loss(logits, *args, **kws)
+        torch.cuda.synchronize()
+        assert fwd.grad_logits is None and not got.row_status.any()
+        for o in (got, fwd):
+            check_policy(o, want, x, temperature, dtype, rows, f(w), f(adv), kl_coef, scale)
+        assert torch.equal(got.logprobs, fwd.logprobs) and torch.equal(got.ratios, fwd.ratios)
+
+
+def test_policy_clip_limits_and_no_weights():
+    import torch
+
+    import top_sampling_amd as ts
+
+    rows, vocab = 10, 500
+    logits, x = make_logits(rows, vocab, "fp32", 0, 4, masks=False)
+    tok = allowed_tokens(x, 1, skip=0.0)
+    old, rf, adv, _ = policy_inputs(rows, x, tok, 1.0, 2)
+    f = lambda a: a.astype(np.float64)  # noqa: E731
+    for low, high in ((0.0, 0.0), (np.inf, np.inf), (0.5, np.inf)):
+        want = ref.policy(x, tok, f(old), f(adv), clip_low=low, clip_high=high)
+        if low == 0.0:
+            # the fixed point 0 of the ratios' logarithms is the border itself
+            keep = np.abs(want["ratios"] - 1) > 1e-3
+        else:
+            keep = np.ones(rows, bool)
+        got = ts.policy_loss(logits, to_dev(tok, torch.int32), to_dev(old), to_dev(adv),
+                             clip_low=low, clip_high=high, backward=True)
+        torch.cuda.synchronize()
+        tol = grad_tol(want["grad"], x, 1.0, "fp32", 4 * LSE) + \
+            (np.abs(adv) * want["ratios"] * 2 * LSE)[:, None] * (want["grad"] != 0)
+        close(got.grad_logits[to_dev(keep, torch.bool)], want["grad"][keep], tol[keep],
+              (low, high))
+
+
+def pref_offsets(rows, pairs, seed):
+    g = np.random.default_rng(seed)
+    cuts = np.sort(g.integers(0, rows + 1, 2 * pairs - 1))
+    return np.concatenate([[0], cuts, [rows]]).astype(np.int32)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows,vocab,pad,pairs", [
+    (1, 1, 0, 1), (2, 2, 0, 1), (5, 3, 1, 2), (13, 1000, 24, 3), (37, 4097, 0, 9),
+    (8, 30011, 0, 1), (300, 600, 0, 2), (1100, 257, 0, 40),
+])
+def test_preference_loss(rows, vocab, pad, pairs, dtype):
+    import torch
+
+    import top_sampling_amd as ts
+
+    for mean, smoothing, temperature, margin in ((False, 0.0, 1.0, 0.0), (True, 0.1, 0.7, 0.3)):
+        say("preference_loss", rows, vocab, pad, pairs, dtype, mean)
+        logits, x = make_logits(rows, vocab, dtype, pad, rows * 5 + vocab)
+        tok = allowed_tokens(x, 7)
+        off = pref_offsets(rows, pairs, 11)
+        if rows > 30:  # rows outside the sequences on both sides
+            off = np.clip(off, 2, rows - 5)
+        g = np.random.default_rng(9)
+        lp, _ = ref.score(x, tok, temperature)
+        rf = (lp + g.normal(0, 0.5, rows)).astype(np.float32)
+        w = g.uniform(0.1, 1, pairs).astype(np.float32)
+        if pairs > 2:
+            w[1] = 0.0
+        beta = 0.3
+        kw = dict(beta=beta, label_smoothing=smoothing, margin=margin, mean=mean,
+                  temperature=temperature)
+        for weights, reference, scale in ((w, rf, 2.0), (None, None, 1.0)):
+            f = lambda a: None if a is None else a.astype(np.float64)  # noqa: E731
+            d = lambda a: None if a is None else to_dev(a)  # noqa: E731
+            want = ref.preference(x, tok, off, f(reference), f(weights), grad_loss=scale, **kw)
+            args = (to_dev(tok, torch.int32), to_dev(off, torch.int32), d(reference), d(weights))
+            gl = torch.full((), scale, device=_dev()) if scale != 1.0 else None
+            got = ts.preference_loss(logits, *args, backward=True, grad_loss=gl, **kw)
+            fwd = ts.preference_loss(logits, *args, **kw)
+            torch.cuda.synchronize()
+            # every row of a sequence may be off by LSE
+            live = np.maximum(np.diff(off), 1)
+            rho_tol = beta * LSE * (1.0 if mean else live)
+            z_tol = (np.broadcast_to(rho_tol, 2 * pairs)[:pairs]
+                     + np.broadcast_to(rho_tol, 2 * pairs)[pairs:])
+            pw = np.full(pairs, 1 / pairs) if weights is None else f(weights)
+            for o in (got, fwd):
+                close(o.logprobs, want["logprobs"], LSE + U * np.abs(want["logprobs"]), "lp")
+                close(o.rewards, want["rewards"], rho_tol + U * np.abs(want["rewards"]), "rewards")
+                close(o.pair_losses, want["pair_losses"],
+                      z_tol + 2 * U * np.abs(want["pair_losses"]), "pair losses")
+                close(o.loss, want["loss"], (pw * z_tol).sum() + 2 * U * abs(want["loss"]), "loss")
+                assert not o.row_status.any()
+            assert fwd.grad_logits is None
+            # dl/dz changes by at most z_tol / 4
+            p = np.exp(ref.log_softmax(x, temperature))
+            k = np.zeros(rows)
+            for i in range(2 * pairs):
+                n = 1 if not mean else max(1, int((tok[off[i]:off[i + 1]] >= 0).sum()))
+                k[off[i]:off[i + 1]] = scale * pw[i % pairs] * beta / n * \
+                    (z_tol[i % pairs] + 2 * LSE) / temperature
+            tol = grad_tol(want["grad"], x, temperature, dtype, 2 * LSE) + k[:, None] * \
+                np.maximum(p, want["grad"] != 0)
+            close(got.grad_logits, want["grad"], tol, "gradient")
+
+
+def test_rows_left_out_may_hold_anything():
+    """NaN and infinite logits in rows that take no part change nothing; in a
+    row that does they are reported and reach the loss."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    for dtype in ("fp32", "bf16"):
+        logits, x = make_logits(12, 777, dtype, 0, 3, masks=False)
+        tok = allowed_tokens(x, 4, skip=0.0)
+        tok[5] = -1
+        w = np.full(12, 0.25, np.float32)
+        w[8] = 0.0
+        old, rf, adv, _ = policy_inputs(12, x, tok, 1.0, 2)
+        args = (to_dev(tok, torch.int32), to_dev(old), to_dev(adv))
+        clean = ts.policy_loss(logits, *args, weights=to_dev(w), backward=True)
+        spoilt = logits.clone()
+        spoilt[5] = float("nan")
+        spoilt[8, 3] = float("inf")
+        got = ts.policy_loss(spoilt, *args, weights=to_dev(w), backward=True)
+        assert torch.equal(got.loss, clean.loss) and torch.isfinite(got.loss)
+        assert torch.equal(got.grad_logits, clean.grad_logits)
+        assert not got.grad_logits[5].any() and not got.grad_logits[8].any()
+        # preference: rows 10 and 11 lie behind the last sequence
+        off = torch.tensor([0, 4, 10], dtype=torch.int32, device=_dev())
+        a = ts.preference_loss(logits, args[0], off, backward=True)
+        spoilt = logits.clone()
+        spoilt[5] = float("nan")
+        spoilt[10:] = float("nan")
+        b = ts.preference_loss(spoilt, args[0], off, backward=True)
+        assert torch.equal(a.loss, b.loss) and torch.equal(a.grad_logits, b.grad_logits)
+        assert not b.grad_logits[10:].any() and not b.logprobs[10:].any()
+
+
+def test_bad_rows_are_reported():
+    import torch
+
+    import top_sampling_amd as ts
+
+    vocab = 5000
+    for dtype in ("fp32", "bf16"):
+        logits, x = make_logits(8, vocab, dtype, 0, 3, masks=False)
+        tok = allowed_tokens(x, 4, skip=0.0)
+        tok[1] = vocab
+        logits[2, 4999] = float("nan")
+        logits[3, 17] = float("inf")
+        logits[4] = -float("inf")
+        logits[6, int(tok[6])] = -float("inf")  # a token of probability 0: not a bad row
+        logits[7] = torch.finfo(logits.dtype).min
+        tk = to_dev(tok, torch.int32)
+        out = ts.token_logprobs(logits, tk, entropies=True)
+        assert out.row_status.tolist() == [0, 1, 2, 2, 2, 0, 0, 0]
+        for v in (out.logprobs, out.entropies):
+            assert torch.isnan(v).tolist() == [False, True, True, True, True, False, False, False]
+        assert out.logprobs[6] == -float("inf")
+        # a row of nothing but the lowest value is uniform
+        assert abs(out.logprobs[7].item() + np.log(vocab)) < LSE + 9 * U
+        assert abs(out.entropies[7].item() - np.log(vocab)) < LSE + 9 * U
+        ones = torch.ones(8, device=_dev())
+        d = ts.token_logprobs_backward(logits, tk, out, ones)
+        assert torch.isnan(d[1:5]).all() and torch.isfinite(d[[0, 5, 6, 7]]).all()
+        skip = ones.clone()
+        skip[1:5] = 0
+        d = ts.token_logprobs_backward(logits, tk, out, skip)
+        assert torch.isfinite(d).all() and not d[1:5].any()
+        got = ts.policy_loss(logits, tk, -ones, ones, backward=True)
+        assert torch.isnan(got.loss) and got.row_status.tolist() == [0, 1, 2, 2, 2, 0, 0, 0]
+        assert torch.isnan(got.grad_logits[1:5]).all()
+        zero = torch.zeros(8, device=_dev())
+        assert torch.isnan(ts.policy_loss(logits, tk, -ones, zero).loss)
+        keep = ones.clone()
+        keep[1:5] = 0
+        good = ts.policy_loss(logits, tk, -ones, ones, weights=keep, backward=True)
+        assert torch.isfinite(good.loss) and not good.row_status.any()
+        off = torch.tensor([0, 1, 5, 6, 8], dtype=torch.int32, device=_dev())
+        pref = ts.preference_loss(logits, tk, off, backward=True)
+        # pair 0 is rows 0 and 5; pair 1 rows 1-4 (bad) and 6-7
+        assert torch.isnan(pref.pair_losses).tolist() == [False, True]
+        assert torch.isfinite(pref.grad_logits[[0, 5]]).all()
+        one = torch.tensor([1.0, 0.0], device=_dev())
+        pref = ts.preference_loss(logits, tk, off, pair_weights=one, backward=True)
+        assert torch.isfinite(pref.loss) and not pref.grad_logits[1:5].any()
+
+
+def test_bad_offsets_stay_in_bounds():
+    """Offsets outside the rows are clamped, descending ones give empty
+    sequences."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    logits, x = make_logits(9, 300, "fp32", 0, 3, masks=False)
+    tk = to_dev(allowed_tokens(x, 4, skip=0.0), torch.int32)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=_dev())  # noqa: E731
+    a = ts.preference_loss(logits, tk, i32(-5, 4, 2 ** 30), backward=True)
+    b = ts.preference_loss(logits, tk, i32(0, 4, 9), backward=True)
+    assert torch.equal(a.loss, b.loss) and torch.equal(a.grad_logits, b.grad_logits)
+    c = ts.preference_loss(logits, tk, i32(9, 3, 0), backward=True)
+    assert abs(c.loss.item() - np.log(2)) < 2 * U and not c.rewards.any()
+
+
+def test_empty_calls():
+    import torch
+
+    import top_sampling_amd as ts
+
+    e = torch.empty(0, 100, device=_dev())
+    t = torch.empty(0, dtype=torch.int32, device=_dev())
+    f = torch.empty(0, device=_dev())
+    assert ts.token_logprobs(e, t).logprobs.numel() == 0
+    assert ts.policy_loss(e, t, f, f, backward=True).loss.item() == 0.0
+    z = torch.zeros(1, dtype=torch.int32, device=_dev())
+    assert ts.preference_loss(e, t, z, backward=True).loss.item() == 0.0
+    p = ts.preference_loss(e, t, torch.zeros(5, dtype=torch.int32, device=_dev()), backward=True)
+    assert abs(p.loss.item() - np.log(2)) < 2 * U
+    # rows but no pairs: a loss of 0 and zero gradients
+    x = torch.randn(3, 50, device=_dev())
+    p = ts.preference_loss(x, torch.zeros(3, dtype=torch.int32, device=_dev()), z, backward=True)
+    assert p.loss.item() == 0.0 and not p.grad_logits.any()
+
+
+def test_every_row_left_out():
+    import torch
+
+    import top_sampling_amd as ts
+
+    x = torch.full((4, 3000), float("nan"), device=_dev())
+    t = torch.full((4,), -1, dtype=torch.int32, device=_dev())
+    f = torch.zeros(4, device=_dev())
+    got = ts.policy_loss(x, t, f, f, backward=True)
+    assert got.loss.item() == 0.0 and not got.grad_logits.any() and (got.ratios == 1).all()
+    off = torch.tensor([0, 2, 4], dtype=torch.int32, device=_dev())
+    for mean in (False, True):
+        p = ts.preference_loss(x, t, off, mean=mean, backward=True)
+        assert abs(p.loss.item() - np.log(2)) < 2 * U and not p.grad_logits.any()
+
+
+def test_streams_and_graph():
+    """On a stream of its own, and captured once and replayed with new inputs
+    between other work."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    rows, vocab = 24, 9001
+    logits, x = make_logits(rows, vocab, "fp32", 0, 3)
+    tok = allowed_tokens(x, 4)
+    old, rf, adv, w = policy_inputs(rows, x, tok, 1.0, 2)
+    tk, old, rf, adv, w = to_dev(tok, torch.int32), *(to_dev(a) for a in (old, rf, adv, w))
+    off = to_dev(pref_offsets(rows, 3, 1), torch.int32)
+
+    def step(x, stream=None):
+        p = ts.policy_loss(x, tk, old, adv, rf, w, kl_coef=0.1, backward=True, stream=stream)
+        q = ts.preference_loss(x, tk, off, rf, backward=True, stream=stream)
+        s = ts.token_logprobs(x, tk, entropies=True, stream=stream)
+        d = ts.token_logprobs_backward(x, tk, s, adv, adv, stream=stream)
+        return [p.loss, p.kl, p.grad_logits, q.loss, q.grad_logits, s.logprobs, d]
+
+    plain = step(logits)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (side, side.cuda_stream):
+        got = step(logits, stream)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(plain, got))
+
+    static = logits.clone()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(static)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step(static)
+    for i in range(4):
+        static.copy_(logits * (1 + 0.1 * i))
+        graph.replay()
+        want = step(static)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, captured)), i
+
+
+def test_long_rows_pass_32_bits():
+    """Row offsets past 2^31 elements (fp32: a buffer of 9 GB)."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    rows, vocab, ld = 3, 2000, 1_150_000_000
+    wide = torch.empty((rows - 1) * ld + vocab, device=_dev())
+    big = wide.as_strided((rows, vocab), (ld, 1))
+    logits, x = make_logits(rows, vocab, "fp32", 0, 3, masks=False)
+    big.copy_(logits)
+    tk = to_dev(allowed_tokens(x, 4, skip=0.0), torch.int32)
+    a, b = ts.token_logprobs(big, tk), ts.token_logprobs(logits, tk)
+    assert torch.equal(a.logprobs, b.logprobs)
+    g = torch.ones(rows, device=_dev())
+    want = ts.token_logprobs_backward(logits, tk, b, g)
+    got = ts.token_logprobs_backward(big, tk, a, g, grad_logits=big)
+    assert torch.equal(got, want)

@@ -16,6 +16,10 @@ Calls mirror the C entry points:
                                  slices in place (no stitched buffer)
   sampler_sample_ex              slices plus flags (processed log-probabilities)
   sampler_workspace_bytes(_slices)  workspace size queries
+  token_logprobs(_backward)      log-probability and entropy of given tokens,
+                                 and the gradient of a function of them
+  policy_loss                    clipped policy loss with a KL term
+  preference_loss                loss of paired log ratios
 and ``compute_logits_local`` returns the rank's own ``[rows, V_local]`` slice,
 the local-logits hook of batch-sharded sampling (page "Qwen4Exp batch-sharded
 sampling: inside vLLM PR #61018", section "Why three lines were the whole
@@ -40,10 +44,13 @@ TS_LOGPROBS_PROCESSED = 1
 TS_PROBE_SMALL_OPERANDS, TS_PROBE_RANDOM_OPERANDS = 0, 1
 TS_NOALLOC_SCRATCH_BYTES = 96 << 20
 PARAMS_BYTES = 24
+TS_F32, TS_BF16 = 0, 1
+TS_PREFERENCE_MEAN = 1
 
 # (name, restype, argtypes) of every symbol the headers declare
 # (include/top_sampling.h and the measurement aids of top_sampling_measure.h).
 _VP, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+_F32 = ctypes.c_float
 SYMBOLS = {
     "lmhead_logits_local": (ctypes.c_int, [_VP, _I64, _I64, _I64, _VP, _I64, _I64, _VP, _I64, _VP]),
     "quantize_rows_e4m3": (ctypes.c_int, [_VP, _I64, _I64, _I64, _VP, _I64, _VP, _VP]),
@@ -65,6 +72,16 @@ SYMBOLS = {
                                                    _VP]),
     "ts_mfma_clock_probe": (ctypes.c_int, [_VP, _I32, _I64, _I32, _VP]),
     "ts_gumbel_keys": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP, _VP, _VP]),
+    "token_logprobs_workspace_bytes": (_SZ, [_I64, _I64]),
+    "token_logprobs": (ctypes.c_int, [_VP, _I32, _I64, _I64, _I64, _VP, _F32, _VP, _VP, _VP, _VP,
+                                      _VP, _SZ, _VP]),
+    "token_logprobs_backward": (ctypes.c_int, [_VP, _I32, _I64, _I64, _I64, _VP, _F32, _VP, _VP,
+                                               _VP, _VP, _VP, _I64, _VP]),
+    "policy_loss": (ctypes.c_int, [_VP, _I32, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
+                                   _VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP, _SZ, _VP]),
+    "preference_loss_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "preference_loss": (ctypes.c_int, [_VP, _I32, _I64, _I64, _I64, _VP, _VP, _I64, _VP, _VP, _VP,
+                                       _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP, _SZ, _VP]),
     "ts_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "ts_last_error": (ctypes.c_char_p, []),
 }
@@ -378,6 +395,262 @@ def sampler_assemble_and_sample(slices, params, row_offset: int = 0, max_logprob
         _ptr(out.topn_logprobs) if max_logprobs > 0 else None,
         _ptr(out.row_status), _ptr(workspace), workspace.numel(), _stream_ptr(stream)))
     return assembled, out
+
+
+# ------------------------------------------------------- scoring and losses
+class _PolicyParams(ctypes.Structure):
+    _fields_ = [("temperature", _F32), ("clip_low", _F32), ("clip_high", _F32),
+                ("kl_coef", _F32)]
+
+
+class _PreferenceParams(ctypes.Structure):
+    _fields_ = [("temperature", _F32), ("beta", _F32), ("label_smoothing", _F32),
+                ("margin", _F32), ("flags", _I32)]
+
+
+@dataclass
+class TokenLogprobs:
+    logprobs: object    # fp32 [rows]
+    entropies: object   # fp32 [rows], or None if not asked for
+    row_stats: object   # fp32 [rows, 2], for token_logprobs_backward
+    row_status: object  # int32 [rows]
+
+
+@dataclass
+class PolicyLoss:
+    loss: object         # fp32 scalar
+    logprobs: object     # fp32 [rows]
+    ratios: object       # fp32 [rows]
+    kl: object           # fp32 [rows]
+    row_status: object   # int32 [rows]
+    grad_logits: object  # the logits' type [rows, vocab], or None
+
+
+@dataclass
+class PreferenceLoss:
+    loss: object         # fp32 scalar
+    pair_losses: object  # fp32 [n_pairs]
+    rewards: object      # fp32 [2 n_pairs]: chosen, then rejected
+    logprobs: object     # fp32 [rows]
+    row_status: object   # int32 [rows]
+    grad_logits: object  # the logits' type [rows, vocab], or None
+
+
+class _OnDevice:
+    """Makes the device of a call's tensors and its stream current, so that
+    outputs and workspaces are allocated for that stream."""
+
+    def __init__(self, device, stream):
+        torch = _torch()
+        if device.type != "cuda":
+            raise ValueError("tensors must be on the GPU")
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        elif not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        elif stream.device != device:
+            raise ValueError("the stream belongs to another device than the tensors")
+        self.pointer = int(stream.cuda_stream)
+        self._guard = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self._guard.__enter__()
+        return self.pointer
+
+    def __exit__(self, *exc):
+        self._guard.__exit__(*exc)
+
+
+def _check_vector(t, name, n, device, dtype=None):
+    torch = _torch()
+    dtype = dtype or torch.float32
+    if t is None:
+        return
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the logits on {device}")
+
+
+def _token_rows(logits, token_ids):
+    """Checks logits and token ids; returns (type code, leading dimension)."""
+    torch = _torch()
+    types = {torch.float32: TS_F32, torch.bfloat16: TS_BF16}
+    if logits.dim() != 2 or logits.dtype not in types:
+        raise ValueError("logits must be fp32 or bf16 [rows, vocab]")
+    rows, vocab = logits.shape
+    if vocab > 1 and logits.stride(1) != 1:
+        raise ValueError("logits must have unit column stride")
+    if rows > 1 and logits.stride(0) < vocab:
+        raise ValueError("logits rows overlap")
+    _check_vector(token_ids, "token_ids", rows, logits.device, torch.int32)
+    return types[logits.dtype], max(int(logits.stride(0)), int(vocab))
+
+
+def _grad_rows(grad_logits, logits):
+    if grad_logits.shape != logits.shape or grad_logits.dtype != logits.dtype or \
+            grad_logits.device != logits.device:
+        raise ValueError("grad_logits must have the shape, type and device of logits")
+    if grad_logits.shape[1] > 1 and grad_logits.stride(1) != 1:
+        raise ValueError("grad_logits must have unit column stride")
+    if grad_logits.shape[0] > 1 and grad_logits.stride(0) < grad_logits.shape[1]:
+        raise ValueError("grad_logits rows overlap")
+    return max(int(grad_logits.stride(0)), int(grad_logits.shape[1]))
+
+
+def _check_workspace(workspace, device):
+    torch = _torch()
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
+            workspace.device != device:
+        raise ValueError("workspace must be a contiguous uint8 tensor on the logits' device")
+    return workspace
+
+
+def token_logprobs_workspace_bytes(rows: int, vocab: int) -> int:
+    return int(lib.token_logprobs_workspace_bytes(rows, vocab))
+
+
+def preference_loss_workspace_bytes(rows: int, vocab: int, n_pairs: int) -> int:
+    return int(lib.preference_loss_workspace_bytes(rows, vocab, n_pairs))
+
+
+def token_logprobs(logits, token_ids, temperature: float = 1.0, entropies: bool = False,
+                   workspace=None, stream=None) -> TokenLogprobs:
+    """Log-probability of ``token_ids[r]`` (int32; negative: row left out)
+    under ``softmax(logits[r] / temperature)``, fp32 or bf16 ``logits [rows,
+    vocab]``, and with ``entropies`` that distribution's entropy."""
+    torch = _torch()
+    kind, ld = _token_rows(logits, token_ids)
+    rows, vocab = logits.shape
+    dev = logits.device
+    with _OnDevice(dev, stream) as s:
+        if workspace is None:
+            workspace = torch.empty(max(256, token_logprobs_workspace_bytes(rows, vocab)),
+                                    dtype=torch.uint8, device=dev)
+        _check_workspace(workspace, dev)
+        out = TokenLogprobs(
+            torch.empty(rows, dtype=torch.float32, device=dev),
+            torch.empty(rows, dtype=torch.float32, device=dev) if entropies else None,
+            torch.empty(rows, 2, dtype=torch.float32, device=dev),
+            torch.empty(rows, dtype=torch.int32, device=dev))
+        _check(lib.token_logprobs(
+            _ptr(logits), kind, rows, vocab, ld, _ptr(token_ids), temperature, _ptr(out.logprobs),
+            _ptr(out.entropies), _ptr(out.row_stats), _ptr(out.row_status), _ptr(workspace),
+            workspace.numel(), s))
+    return out
+
+
+def token_logprobs_backward(logits, token_ids, forward: TokenLogprobs, grad_logprobs,
+                            grad_entropies=None, temperature: float = 1.0, grad_logits=None,
+                            stream=None):
+    """Gradient of the logits from ``grad_logprobs`` (fp32 ``[rows]``) and
+    ``grad_entropies`` (or None), with the ``TokenLogprobs`` that
+    ``token_logprobs`` gave for the same logits, tokens and temperature.
+    ``grad_logits`` may be ``logits`` itself."""
+    torch = _torch()
+    kind, ld = _token_rows(logits, token_ids)
+    rows, vocab = logits.shape
+    dev = logits.device
+    _check_vector(grad_logprobs, "grad_logprobs", rows, dev)
+    _check_vector(grad_entropies, "grad_entropies", rows, dev)
+    _check_vector(forward.row_stats, "forward.row_stats", 2 * rows, dev)
+    _check_vector(forward.entropies, "forward.entropies", rows, dev)
+    with _OnDevice(dev, stream) as s:
+        if grad_logits is None:
+            grad_logits = torch.empty(rows, vocab, dtype=logits.dtype, device=dev)
+        ldg = _grad_rows(grad_logits, logits)
+        _check(lib.token_logprobs_backward(
+            _ptr(logits), kind, rows, vocab, ld, _ptr(token_ids), temperature,
+            _ptr(forward.row_stats), _ptr(grad_logprobs), _ptr(forward.entropies),
+            _ptr(grad_entropies), _ptr(grad_logits), ldg, s))
+    return grad_logits
+
+
+def policy_loss(logits, token_ids, old_logprobs, advantages, ref_logprobs=None, weights=None, *,
+                clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
+                temperature: float = 1.0, backward: bool = False, grad_loss=None,
+                grad_logits=None, workspace=None, stream=None) -> PolicyLoss:
+    """Clipped policy loss with a KL term over rows of ``logits`` (see
+    ``policy_loss`` in top_sampling.h for the formula).  ``weights`` (fp32
+    ``[rows]``) holds the average wanted; None sums the rows.  With
+    ``backward``, or a ``grad_logits`` buffer (``logits`` itself is allowed),
+    the same call writes ``grad_loss`` (a device scalar, None for 1) times
+    the gradient of the logits."""
+    torch = _torch()
+    kind, ld = _token_rows(logits, token_ids)
+    rows, vocab = logits.shape
+    dev = logits.device
+    for t, name, n in ((old_logprobs, "old_logprobs", rows), (advantages, "advantages", rows),
+                       (ref_logprobs, "ref_logprobs", rows), (weights, "weights", rows),
+                       (grad_loss, "grad_loss", 1)):
+        _check_vector(t, name, n, dev)
+    with _OnDevice(dev, stream) as s:
+        if workspace is None:
+            workspace = torch.empty(max(256, token_logprobs_workspace_bytes(rows, vocab)),
+                                    dtype=torch.uint8, device=dev)
+        _check_workspace(workspace, dev)
+        if grad_logits is None and backward:
+            grad_logits = torch.empty(rows, vocab, dtype=logits.dtype, device=dev)
+        ldg = _grad_rows(grad_logits, logits) if grad_logits is not None else 0
+        out = PolicyLoss(
+            torch.empty((), dtype=torch.float32, device=dev),
+            torch.empty(rows, dtype=torch.float32, device=dev),
+            torch.empty(rows, dtype=torch.float32, device=dev),
+            torch.empty(rows, dtype=torch.float32, device=dev),
+            torch.empty(rows, dtype=torch.int32, device=dev), grad_logits)
+        params = _PolicyParams(temperature, clip_low, clip_high, kl_coef)
+        _check(lib.policy_loss(
+            _ptr(logits), kind, rows, vocab, ld, _ptr(token_ids), ctypes.addressof(params),
+            _ptr(old_logprobs), _ptr(ref_logprobs), _ptr(advantages), _ptr(weights),
+            _ptr(grad_loss), _ptr(out.loss), _ptr(out.logprobs), _ptr(out.ratios), _ptr(out.kl),
+            _ptr(out.row_status), _ptr(grad_logits), ldg, _ptr(workspace), workspace.numel(), s))
+    return out
+
+
+def preference_loss(logits, token_ids, seq_offsets, ref_logprobs=None, pair_weights=None, *,
+                    beta: float = 0.1, label_smoothing: float = 0.0, margin: float = 0.0,
+                    mean: bool = False, temperature: float = 1.0, backward: bool = False,
+                    grad_loss=None, grad_logits=None, workspace=None,
+                    stream=None) -> PreferenceLoss:
+    """Loss of paired log ratios (see ``preference_loss`` in top_sampling.h).
+    ``seq_offsets`` (int32 ``[2 n_pairs + 1]``) bounds the sequences, chosen
+    answers first, then the rejected ones in the same order.  ``mean`` divides
+    each sequence's sum by its tokens.  ``backward``, ``grad_loss`` and
+    ``grad_logits`` as in ``policy_loss``."""
+    torch = _torch()
+    kind, ld = _token_rows(logits, token_ids)
+    rows, vocab = logits.shape
+    dev = logits.device
+    if seq_offsets.numel() % 2 != 1:
+        raise ValueError("seq_offsets must hold 2 n_pairs + 1 values")
+    n_pairs = seq_offsets.numel() // 2
+    _check_vector(seq_offsets, "seq_offsets", 2 * n_pairs + 1, dev, torch.int32)
+    for t, name, n in ((ref_logprobs, "ref_logprobs", rows),
+                       (pair_weights, "pair_weights", n_pairs), (grad_loss, "grad_loss", 1)):
+        _check_vector(t, name, n, dev)
+    with _OnDevice(dev, stream) as s:
+        if workspace is None:
+            workspace = torch.empty(
+                max(256, preference_loss_workspace_bytes(rows, vocab, n_pairs)),
+                dtype=torch.uint8, device=dev)
+        _check_workspace(workspace, dev)
+        if grad_logits is None and backward:
+            grad_logits = torch.empty(rows, vocab, dtype=logits.dtype, device=dev)
+        ldg = _grad_rows(grad_logits, logits) if grad_logits is not None else 0
+        out = PreferenceLoss(
+            torch.empty((), dtype=torch.float32, device=dev),
+            torch.empty(n_pairs, dtype=torch.float32, device=dev),
+            torch.empty(2 * n_pairs, dtype=torch.float32, device=dev),
+            torch.empty(rows, dtype=torch.float32, device=dev),
+            torch.empty(rows, dtype=torch.int32, device=dev), grad_logits)
+        params = _PreferenceParams(temperature, beta, label_smoothing, margin,
+                                   TS_PREFERENCE_MEAN if mean else 0)
+        _check(lib.preference_loss(
+            _ptr(logits), kind, rows, vocab, ld, _ptr(token_ids), _ptr(seq_offsets), n_pairs,
+            ctypes.addressof(params), _ptr(ref_logprobs), _ptr(pair_weights), _ptr(grad_loss),
+            _ptr(out.loss), _ptr(out.pair_losses), _ptr(out.rewards), _ptr(out.logprobs),
+            _ptr(out.row_status), _ptr(grad_logits), ldg, _ptr(workspace), workspace.numel(), s))
+    return out
 
 
 def mfma_clock_probe(workgroups: int, iters: int, device, stream=None, random: bool = False):

@@ -1,0 +1,798 @@
+// Log-probabilities of given tokens, the two losses built on them, and the
+// gradients of the logits, on gfx950.
+//
+// For a row x of logits, a token t and a temperature T:
+//   m = max_j x_j,  e_j = exp((x_j - m) / T),  S = sum_j e_j,  p_j = e_j / S
+//   lp = (x_t - m) / T - ln S                              (log-probability)
+//   H  = ln S - (1 / (S T)) sum_j e_j (x_j - m)            (entropy)
+// A scalar that depends on the row through g = dL/dlp and h = dL/dH has
+//   dL/dx_j = [g (1[j = t] - p_j) - h p_j (lp_j + H)] / T
+//           = e_j (a + b (x_j - m)) + 1[j = t] g / T,
+//   a = -(g + h (H - ln S)) / (S T),   b = -h / (S T^2),
+// and the entry of the token itself is written as a value of its own, from
+// 1 - p_t = -expm1(lp), which keeps its digits when p_t is near 1.
+//
+// All of it is bound by the logits' bytes: about eight instructions an
+// element against four (two) bytes read.  Three kernels:
+//   stats  one pass over the logits with a running maximum and sum per
+//          thread; a row is cut into chunks so that a few rows fill the card
+//          too; one record per (row, chunk)
+//   rows   joins a row's records and does the per-row arithmetic in double
+//          (a ratio next to a clip border decides a whole gradient row)
+//   grad   reads the logits again and writes the gradient
+// exp(x / T) is taken as exp2((x - m) c) with c = log2(e) / T held as two
+// floats, so a temperature's rounding does not tilt the whole sum.
+#include <math.h>
+
+#include <algorithm>
+
+#include "losses.hpp"
+
+namespace ts {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBatch = 4;                       // 16-byte vectors a thread has in flight
+constexpr int kSlab = kThreads * kBatch;        // vectors a workgroup takes at a time
+constexpr int kMaxChunkSlabs = 4;               // longest chunk, in slabs
+constexpr int kTargetGroups = 1024;             // workgroups wanted for few rows
+constexpr int kMaxGrid = 1 << 23;               // workgroups of one launch (grid-stride beyond)
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+// Rows start wherever the caller's leading dimension puts them; the 16-byte
+// accesses only assume the element's own alignment.
+typedef f32x4 f32x4u __attribute__((aligned(4)));
+typedef bf16x8 bf16x8u __attribute__((aligned(2)));
+
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int n = 4;
+  using Type = f32x4u;
+};
+template <>
+struct Vec<__bf16> {
+  static constexpr int n = 8;
+  using Type = bf16x8u;
+};
+
+// The temperature, as the kernels use it.
+struct Scale {
+  float c_hi, c_lo;  // log2(e) / T in two floats
+  float floor;       // x - m below this gives exp2 = 0 (also x = -inf)
+  double c, inv_t;
+};
+
+Scale make_scale(float temperature) {
+  Scale s;
+  s.c = M_LOG2E / static_cast<double>(temperature);
+  s.c_hi = static_cast<float>(s.c);
+  s.c_lo = static_cast<float>(s.c - static_cast<double>(s.c_hi));
+  s.inv_t = 1.0 / static_cast<double>(temperature);
+  s.floor = static_cast<float>(-200.0 / s.c);
+  return s;
+}
+
+// exp((x - m) / T) of t = max(x - m, floor).
+__device__ __forceinline__ float exp_t(float t, const Scale& s) {
+  return __builtin_amdgcn_exp2f(fmaf(t, s.c_hi, t * s.c_lo));
+}
+
+// The running maximum keeps a NaN (and +inf), so a bad logit shows in it.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  return __builtin_elementwise_maximum(a, b);
+}
+
+// One chunk's share of a row.
+struct Part {
+  double s, u;  // sum of e, sum of e (x - m)
+  float m, pad;
+};
+
+// What the gradient pass needs of a row: entry j is e_j (a + b (x_j - m)),
+// the token's entry is `own`.  All zero: the row's gradient is zero.
+struct RowGrad {
+  float m, a, b, own;
+};
+
+struct Cut {
+  int len;     // vectors per chunk
+  int chunks;  // chunks per row
+};
+
+// A chunk is at most kMaxChunkSlabs slabs.  With few rows the chunks get
+// shorter until there are about kTargetGroups of them, down to one vector a
+// thread.
+Cut cut_rows(int64_t rows, int64_t vocab, int vec) {
+  const int64_t nvec = vocab > 0 ? (vocab + vec - 1) / vec : 1;
+  int64_t want = (nvec + kSlab * kMaxChunkSlabs - 1) / (kSlab * kMaxChunkSlabs);
+  const int64_t fill = rows > 0 ? (kTargetGroups + rows - 1) / rows : 1;
+  const int64_t most = (nvec + kThreads - 1) / kThreads;
+  if (fill > want) want = fill < most ? fill : most;
+  if (want < 1) want = 1;
+  int64_t len = (nvec + want - 1) / want;
+  const int64_t unit = len > kSlab ? kSlab : kThreads;
+  len = (len + unit - 1) / unit * unit;
+  Cut c;
+  c.len = static_cast<int>(len);
+  c.chunks = static_cast<int>((nvec + len - 1) / len);
+  return c;
+}
+
+template <typename T>
+__device__ __forceinline__ void load_vec(const T* p, float (&v)[Vec<T>::n]) {
+  const typename Vec<T>::Type w = *reinterpret_cast<const typename Vec<T>::Type*>(p);
+#pragma unroll
+  for (int e = 0; e < Vec<T>::n; ++e) v[e] = static_cast<float>(w[e]);
+}
+
+// Vector i of a row of `vocab` logits; entries past the row read -inf.
+template <typename T>
+__device__ __forceinline__ void load_edge(const T* row, int64_t i, int vocab,
+                                          float (&v)[Vec<T>::n]) {
+  constexpr int VN = Vec<T>::n;
+  const int64_t at = i * VN;
+  if (at + VN <= vocab) {
+    load_vec(row + at, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VN; ++e) v[e] = at + e < vocab ? static_cast<float>(row[at + e]) : -INFINITY;
+  }
+}
+
+__device__ __forceinline__ bool left_out(const int32_t* tokens, const float* weights, int row) {
+  return tokens[row] < 0 || (weights != nullptr && weights[row] == 0.0f);
+}
+
+// Joins (m, s, u) of a group of `width` lanes (a power of two); every lane
+// gets the result.  An empty part has m = -inf and s = u = 0.
+template <bool ENT>
+__device__ __forceinline__ void join_lanes(float& m, double& s, double& u, int width, double c) {
+  float top = m;
+  for (int d = width >> 1; d > 0; d >>= 1) top = max_nan(top, __shfl_xor(top, d, width));
+  const float ref = top == -INFINITY ? 0.0f : top;
+  const double shift = m == -INFINITY ? 0.0 : static_cast<double>(m) - ref;
+  const double f = m == -INFINITY ? 0.0 : exp2(shift * c);
+  if (ENT) u = f * (u + shift * s);
+  s *= f;
+  for (int d = width >> 1; d > 0; d >>= 1) {
+    s += __shfl_xor(s, d, width);
+    if (ENT) u += __shfl_xor(u, d, width);
+  }
+  m = top;
+}
+
+// ------------------------------------------------------------------- stats
+// What the pass sets for every row before the later kernels fill in the rows
+// that take part (any pointer may be null), and the rows that do: with
+// `offsets`, only those of [offsets[0], offsets[n_seqs]).
+struct RowInit {
+  RowGrad* grads;
+  float* logprobs;
+  int32_t* row_status;
+  const int32_t* offsets;
+  int n_seqs;
+};
+
+template <typename T, bool ENT>
+__global__ __launch_bounds__(kThreads) void stats_kernel(
+    const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,
+    const float* __restrict__ weights, Scale sc, Cut cut, Part* __restrict__ parts, RowInit init) {
+  constexpr int VN = Vec<T>::n;
+  __shared__ Part wave_part[kThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t total = static_cast<int64_t>(rows) * cut.chunks;
+  for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
+    const int row = static_cast<int>(b / cut.chunks), chunk = static_cast<int>(b % cut.chunks);
+    if (chunk == 0 && tid == 0) {
+      if (init.grads) init.grads[row] = RowGrad{0.0f, 0.0f, 0.0f, 0.0f};
+      if (init.logprobs) init.logprobs[row] = 0.0f;
+      if (init.row_status) init.row_status[row] = TS_ROW_OK;
+    }
+    if (left_out(tokens, weights, row)) continue;
+    if (init.offsets && (row < init.offsets[0] || row >= init.offsets[init.n_seqs])) continue;
+    const T* rx = x + static_cast<int64_t>(row) * ld;
+    const int64_t v0 = static_cast<int64_t>(chunk) * cut.len, v1 = v0 + cut.len;
+    const int64_t whole = vocab / VN;  // vectors that lie wholly inside the row
+    float m = -INFINITY, s = 0.0f, u = 0.0f;
+    for (int64_t v = v0; v < v1; v += kSlab) {
+      float w[kBatch][VN];
+      if (v + kSlab <= v1 && v + kSlab <= whole) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) load_vec(rx + (v + j * kThreads + tid) * VN, w[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int64_t i = v + j * kThreads + tid;
+          load_edge(rx, i < v1 ? i : INT32_MAX, vocab, w[j]);
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+        for (int e = 0; e < VN; e += 2) top = max_nan(max_nan(top, w[j][e]), w[j][e + 1]);
+      const float ref = top == -INFINITY ? 0.0f : top;
+      const float shift = fmaxf(m - ref, sc.floor);
+      const float f = exp_t(shift, sc);
+      if (ENT) u = f * fmaf(shift, s, u);
+      s *= f;
+      m = top;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+        for (int e = 0; e < VN; ++e) {
+          const float t = fmaxf(w[j][e] - ref, sc.floor);
+          const float ex = exp_t(t, sc);
+          s += ex;
+          if (ENT) u = fmaf(ex, t, u);
+        }
+    }
+    double ds = s, du = u;
+    join_lanes<ENT>(m, ds, du, 64, sc.c);
+    if (lane == 0) wave_part[wave] = Part{ds, du, m, 0.0f};
+    __syncthreads();
+    if (tid < kThreads / 64) {
+      Part p = wave_part[tid];
+      join_lanes<ENT>(p.m, p.s, p.u, kThreads / 64, sc.c);
+      if (tid == 0) parts[b] = p;
+    }
+    __syncthreads();
+  }
+}
+
+// -------------------------------------------------------------------- rows
+constexpr int kRowLanes = 8;                          // lanes that join one row's records
+constexpr int kRowsPerGroup = kThreads / kRowLanes;
+
+struct RowStats {
+  float m;
+  double s, u;
+  double lp;   // log-probability of the token (NaN for a bad row)
+  int status;
+};
+
+// A row's records joined by kRowLanes lanes; the row is not left out.
+template <bool ENT, typename T>
+__device__ __forceinline__ RowStats join_row(const T* x, int64_t ld, int vocab, int token, int row,
+                                             const Part* parts, int chunks, const Scale& sc) {
+  const int lane = threadIdx.x % kRowLanes;
+  RowStats r;
+  r.m = -INFINITY;
+  r.s = r.u = 0.0;
+  for (int i = lane; i < chunks; i += kRowLanes) {
+    const Part p = parts[static_cast<int64_t>(row) * chunks + i];
+    const float top = max_nan(r.m, p.m);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    const double d0 = r.m == -INFINITY ? 0.0 : static_cast<double>(r.m) - ref;
+    const double d1 = p.m == -INFINITY ? 0.0 : static_cast<double>(p.m) - ref;
+    const double f0 = r.m == -INFINITY ? 0.0 : exp2(d0 * sc.c);
+    const double f1 = p.m == -INFINITY ? 0.0 : exp2(d1 * sc.c);
+    if (ENT) r.u = f0 * (r.u + d0 * r.s) + f1 * (p.u + d1 * p.s);
+    r.s = f0 * r.s + f1 * p.s;
+    r.m = top;
+  }
+  join_lanes<ENT>(r.m, r.s, r.u, kRowLanes, sc.c);
+  if (token >= vocab) {
+    r.status = TS_ROW_BAD_PARAMS;
+    r.lp = NAN;
+  } else if (!(fabsf(r.m) < INFINITY)) {
+    r.status = TS_ROW_BAD_LOGITS;
+    r.lp = NAN;
+  } else {
+    r.status = TS_ROW_OK;
+    const float xt = static_cast<float>(x[static_cast<int64_t>(row) * ld + token]);
+    r.lp = (static_cast<double>(xt) - r.m) * sc.inv_t - log(r.s);
+  }
+  return r;
+}
+
+// The gradient record of dL/dlp = g (no entropy term).
+__device__ __forceinline__ RowGrad row_grad(const RowStats& r, double g, const Scale& sc) {
+  if (r.status != TS_ROW_OK) return RowGrad{0.0f, NAN, 0.0f, NAN};
+  if (g == 0.0) return RowGrad{0.0f, 0.0f, 0.0f, 0.0f};
+  return RowGrad{r.m, static_cast<float>(-g * sc.inv_t / r.s), 0.0f,
+                 static_cast<float>(g * sc.inv_t * -expm1(r.lp))};
+}
+
+template <bool ENT, typename T>
+__global__ __launch_bounds__(kThreads) void score_rows_kernel(
+    const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,
+    Scale sc, const Part* __restrict__ parts, int chunks, ScoreOut o) {
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsPerGroup + threadIdx.x / kRowLanes;
+       row < rows; row += static_cast<int64_t>(gridDim.x) * kRowsPerGroup) {
+    const int r = static_cast<int>(row);
+    const bool writes = threadIdx.x % kRowLanes == 0;
+    if (tokens[r] < 0) {
+      if (writes) {
+        o.logprobs[r] = 0.0f;
+        if (ENT) o.entropies[r] = 0.0f;
+        if (o.row_stats) o.row_stats[2 * row] = o.row_stats[2 * row + 1] = 0.0f;
+        if (o.row_status) o.row_status[r] = TS_ROW_OK;
+      }
+      continue;
+    }
+    const RowStats st = join_row<ENT>(x, ld, vocab, tokens[r], r, parts, chunks, sc);
+    if (!writes) continue;
+    const bool ok = st.status == TS_ROW_OK;
+    o.logprobs[r] = static_cast<float>(st.lp);
+    if (ENT) o.entropies[r] = ok ? static_cast<float>(log(st.s) - st.u * sc.inv_t / st.s) : NAN;
+    if (o.row_stats) {
+      o.row_stats[2 * row] = ok ? st.m : NAN;
+      o.row_stats[2 * row + 1] = ok ? static_cast<float>(st.s) : NAN;
+    }
+    if (o.row_status) o.row_status[r] = st.status;
+  }
+}
+
+// Sum of n doubles by one workgroup, in a fixed order; thread 0 gets it.
+__device__ __forceinline__ double group_sum(const double* v, int64_t n) {
+  __shared__ double wave_sum[kThreads / 64];
+  double s = 0.0;
+  for (int64_t i = threadIdx.x; i < n; i += kThreads) s += v[i];
+  for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d, 64);
+  if ((threadIdx.x & 63) == 0) wave_sum[threadIdx.x >> 6] = s;
+  __syncthreads();
+  s = 0.0;
+  for (int w = 0; w < kThreads / 64; ++w) s += wave_sum[w];
+  return s;
+}
+
+__global__ __launch_bounds__(kThreads) void sum_kernel(const double* __restrict__ v, int64_t n,
+                                                       float* __restrict__ out) {
+  const double s = group_sum(v, n);
+  if (threadIdx.x == 0) *out = static_cast<float>(s);
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void policy_rows_kernel(
+    const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,
+    const float* __restrict__ weights, Scale sc, const Part* __restrict__ parts, int chunks,
+    PolicyArgs p, RowGrad* __restrict__ grads, double* __restrict__ losses) {
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsPerGroup + threadIdx.x / kRowLanes;
+       row < rows; row += static_cast<int64_t>(gridDim.x) * kRowsPerGroup) {
+    const int r = static_cast<int>(row);
+    const bool writes = threadIdx.x % kRowLanes == 0;
+    if (left_out(tokens, weights, r)) {
+      if (writes) {
+        losses[r] = 0.0;
+        if (grads) grads[r] = RowGrad{0.0f, 0.0f, 0.0f, 0.0f};
+        if (p.logprobs) p.logprobs[r] = 0.0f;
+        if (p.ratios) p.ratios[r] = 1.0f;
+        if (p.kl) p.kl[r] = 0.0f;
+        if (p.row_status) p.row_status[r] = TS_ROW_OK;
+      }
+      continue;
+    }
+    const RowStats st = join_row<false>(x, ld, vocab, tokens[r], r, parts, chunks, sc);
+    if (!writes) continue;
+    const double w = weights ? static_cast<double>(weights[r]) : 1.0;
+    const double adv = p.advantages[r];
+    const double ratio = exp(st.lp - static_cast<double>(p.old_logprobs[r]));
+    const double low = 1.0 - static_cast<double>(p.clip_low);
+    const double high = 1.0 + static_cast<double>(p.clip_high);
+    // min(r A, clip(r) A): the bound that holds against the advantage's sign
+    // is the only one that can bind.  A = 0 gives 0 at any ratio.
+    const bool inside = adv >= 0.0 ? !(ratio > high) : !(ratio < low);
+    double gain = 0.0, g = 0.0;
+    if (adv != 0.0) {
+      gain = (inside ? ratio : (adv >= 0.0 ? high : low)) * adv;
+      g = inside ? -adv * ratio : 0.0;
+    }
+    double kl = 0.0;
+    if (p.ref_logprobs != nullptr) {
+      const double gap = static_cast<double>(p.ref_logprobs[r]) - st.lp;
+      const double em = expm1(gap);
+      kl = em - gap;
+      if (p.kl_coef != 0.0f) g -= static_cast<double>(p.kl_coef) * em;
+    }
+    double loss = -gain;
+    if (p.kl_coef != 0.0f) loss += static_cast<double>(p.kl_coef) * kl;
+    losses[r] = st.status == TS_ROW_OK ? w * loss : NAN;
+    if (p.logprobs) p.logprobs[r] = static_cast<float>(st.lp);
+    if (p.ratios) p.ratios[r] = static_cast<float>(ratio);
+    if (p.kl) p.kl[r] = static_cast<float>(kl);
+    if (p.row_status) p.row_status[r] = st.status;
+    if (grads != nullptr) {
+      const double up = p.grad_loss ? static_cast<double>(*p.grad_loss) : 1.0;
+      grads[r] = row_grad(st, up * w * g, sc);
+    }
+  }
+}
+
+// One workgroup per pair: the log-ratio sums of its two sequences, the pair's
+// loss, and the gradient records of its rows.
+__device__ __forceinline__ void seq_bounds(const int32_t* offsets, int seq, int rows, int& from,
+                                           int& to) {
+  from = min(max(offsets[seq], 0), rows);
+  to = min(max(offsets[seq + 1], from), rows);
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void preference_pairs_kernel(
+    const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,
+    Scale sc, const Part* __restrict__ parts, int chunks, PreferenceArgs p,
+    RowGrad* __restrict__ grads, double* __restrict__ losses) {
+  __shared__ double wave_sum[2][kThreads / 64];
+  __shared__ int wave_n[2][kThreads / 64];
+  __shared__ double coef[2];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int group = tid / kRowLanes;
+  const bool writes = tid % kRowLanes == 0;
+  for (int pair = blockIdx.x; pair < p.n_pairs; pair += gridDim.x) {
+    for (int side = 0; side < 2; ++side) {
+      int from, to;
+      seq_bounds(p.seq_offsets, pair + side * p.n_pairs, rows, from, to);
+      double sum = 0.0;
+      int n = 0;
+      for (int row = from + group; row < to; row += kRowsPerGroup) {
+        if (tokens[row] < 0) continue;
+        const RowStats st = join_row<false>(x, ld, vocab, tokens[row], row, parts, chunks, sc);
+        if (!writes) continue;
+        sum += st.lp - (p.ref_logprobs ? static_cast<double>(p.ref_logprobs[row]) : 0.0);
+        ++n;
+        if (p.logprobs) p.logprobs[row] = static_cast<float>(st.lp);
+        if (p.row_status) p.row_status[row] = st.status;
+        if (grads != nullptr) grads[row] = row_grad(st, 1.0, sc);
+      }
+      for (int d = 32; d > 0; d >>= 1) {
+        sum += __shfl_xor(sum, d, 64);
+        n += __shfl_xor(n, d, 64);
+      }
+      if (lane == 0) {
+        wave_sum[side][wave] = sum;
+        wave_n[side][wave] = n;
+      }
+    }
+    __syncthreads();
+    if (tid == 0) {
+      double rho[2], per[2];
+      for (int side = 0; side < 2; ++side) {
+        double s = 0.0;
+        int n = 0;
+        for (int w = 0; w < kThreads / 64; ++w) {
+          s += wave_sum[side][w];
+          n += wave_n[side][w];
+        }
+        per[side] = p.mean && n > 0 ? 1.0 / n : 1.0;
+        rho[side] = s * per[side];
+      }
+      const double beta = p.beta, eps = p.label_smoothing;
+      const double z = beta * (rho[0] - rho[1]) - static_cast<double>(p.margin);
+      const double soft = log1p(exp(-fabs(z)));  // -ln sigmoid(|z|)
+      const double loss = (1.0 - eps) * (soft + fmax(-z, 0.0)) + eps * (soft + fmax(z, 0.0));
+      const double weight = p.pair_weights ? static_cast<double>(p.pair_weights[pair])
+                                           : 1.0 / p.n_pairs;
+      // dl/dz = -(1 - eps) sigmoid(-z) + eps sigmoid(z)
+      const double small = exp(-fabs(z)) / (1.0 + exp(-fabs(z))), large = 1.0 - small;
+      const double up = z >= 0.0 ? large : small, down = z >= 0.0 ? small : large;
+      const double dz = z != z ? z : eps * up - (1.0 - eps) * down;
+      const double gl = p.grad_loss ? static_cast<double>(*p.grad_loss) : 1.0;
+      // A pair of weight 0 is out of the sum, whatever its rows hold.
+      losses[pair] = weight == 0.0 ? 0.0 : weight * (z != z ? z : loss);
+      coef[0] = weight == 0.0 ? 0.0 : gl * weight * dz * beta * per[0];
+      coef[1] = weight == 0.0 ? 0.0 : -gl * weight * dz * beta * per[1];
+      if (p.pair_losses) p.pair_losses[pair] = static_cast<float>(z != z ? z : loss);
+      if (p.rewards) {
+        p.rewards[pair] = static_cast<float>(beta * rho[0]);
+        p.rewards[pair + p.n_pairs] = static_cast<float>(beta * rho[1]);
+      }
+    }
+    __syncthreads();
+    if (grads != nullptr && writes) {
+      // The same lanes as above, so each scales the records that it wrote.
+      for (int side = 0; side < 2; ++side) {
+        int from, to;
+        seq_bounds(p.seq_offsets, pair + side * p.n_pairs, rows, from, to);
+        const double k = coef[side];
+        for (int row = from + group; row < to; row += kRowsPerGroup) {
+          if (tokens[row] < 0) continue;
+          RowGrad r = grads[row];
+          if (k == 0.0) {
+            r = RowGrad{0.0f, 0.0f, 0.0f, 0.0f};
+          } else {
+            r.a = static_cast<float>(r.a * k);
+            r.own = static_cast<float>(r.own * k);
+          }
+          grads[row] = r;
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// -------------------------------------------------------------------- grad
+// A row's record from the forward pass's statistics and the caller's
+// gradients of the log-probability and the entropy.
+__device__ __forceinline__ RowGrad score_row_grad(const ScoreGrad& g, int row, bool skip, float xt,
+                                                  const Scale& sc) {
+  const double dg = g.grad_logprobs[row];
+  const double dh = g.grad_entropies ? static_cast<double>(g.grad_entropies[row]) : 0.0;
+  if (skip || (dg == 0.0 && dh == 0.0)) return RowGrad{0.0f, 0.0f, 0.0f, 0.0f};
+  const float m = g.row_stats[2 * static_cast<int64_t>(row)];
+  const double s = g.row_stats[2 * static_cast<int64_t>(row) + 1];
+  const double ln_s = log(s);
+  const double lp = (static_cast<double>(xt) - m) * sc.inv_t - ln_s;
+  const double h = g.entropies && dh != 0.0 ? static_cast<double>(g.entropies[row]) : 0.0;
+  double own = dg * -expm1(lp);
+  if (dh != 0.0 && lp > -1e30) own -= dh * exp(lp) * (lp + h);
+  return RowGrad{m, static_cast<float>(-(dg + (dh != 0.0 ? dh * (h - ln_s) : 0.0)) * sc.inv_t / s),
+                 static_cast<float>(-dh * sc.inv_t * sc.inv_t / s),
+                 static_cast<float>(own * sc.inv_t)};
+}
+
+template <typename T>
+__device__ __forceinline__ void store_vec(T* p, const float (&v)[Vec<T>::n]) {
+  typename Vec<T>::Type w;
+#pragma unroll
+  for (int e = 0; e < Vec<T>::n; ++e) w[e] = static_cast<T>(v[e]);
+  *reinterpret_cast<typename Vec<T>::Type*>(p) = w;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_edge(T* row, int64_t i, int vocab,
+                                           const float (&v)[Vec<T>::n]) {
+  constexpr int VN = Vec<T>::n;
+  const int64_t at = i * VN;
+  if (at + VN <= vocab) {
+    store_vec(row + at, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VN; ++e)
+      if (at + e < vocab) row[at + e] = static_cast<T>(v[e]);
+  }
+}
+
+// ENT: the records have an entropy term (b).  With SCORE the records are made
+// here from the caller's gradients; otherwise they come from the row kernels,
+// and workgroup 0 also sums the loss terms that those left.
+template <typename T, bool SCORE, bool ENT>
+__global__ __launch_bounds__(kThreads) void grad_kernel(
+    const T* x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens, Scale sc,
+    Cut cut, const RowGrad* __restrict__ grads, ScoreGrad sg, T* d, int64_t ldd,
+    const double* __restrict__ losses, int64_t n_losses, float* __restrict__ loss) {
+  constexpr int VN = Vec<T>::n;
+  const int tid = threadIdx.x;
+  const int64_t total = static_cast<int64_t>(rows) * cut.chunks;
+  if (!SCORE && blockIdx.x == 0) {
+    const double s = group_sum(losses, n_losses);
+    if (tid == 0) *loss = static_cast<float>(s);
+  }
+  for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
+    const int row = static_cast<int>(b / cut.chunks), chunk = static_cast<int>(b % cut.chunks);
+    const T* rx = x + static_cast<int64_t>(row) * ld;
+    T* rd = d + static_cast<int64_t>(row) * ldd;
+    const int token = tokens[row];
+    RowGrad g;
+    if (SCORE) {
+      const bool skip = token < 0;
+      // The gradient may replace the logits, so the token's own logit is only
+      // read by the workgroup that also writes it.
+      const bool mine = token >= 0 && token < vocab &&
+                        token / VN / cut.len == chunk;
+      const float xt = mine ? static_cast<float>(rx[token]) : 0.0f;
+      g = score_row_grad(sg, row, skip, xt, sc);
+      __syncthreads();
+    } else {
+      g = grads[row];
+    }
+    const int64_t v0 = static_cast<int64_t>(chunk) * cut.len, v1 = v0 + cut.len;
+    const int64_t whole = vocab / VN;
+    const bool zero = g.a == 0.0f && g.b == 0.0f && g.own == 0.0f;
+    for (int64_t v = v0; v < v1; v += kSlab) {
+      float w[kBatch][VN];
+      const bool inner = v + kSlab <= v1 && v + kSlab <= whole;
+      if (zero) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+          for (int e = 0; e < VN; ++e) w[j][e] = 0.0f;
+      } else {
+        if (inner) {
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) load_vec(rx + (v + j * kThreads + tid) * VN, w[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            const int64_t i = v + j * kThreads + tid;
+            load_edge(rx, i < v1 ? i : INT32_MAX, vocab, w[j]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int64_t at = (v + j * kThreads + tid) * VN;
+#pragma unroll
+          for (int e = 0; e < VN; ++e) {
+            const float t = fmaxf(w[j][e] - g.m, sc.floor);
+            const float ex = exp_t(t, sc);
+            const float out = ENT ? ex * fmaf(g.b, t, g.a) : ex * g.a;
+            w[j][e] = at + e == token ? g.own : out;
+          }
+        }
+      }
+      if (inner) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) store_vec(rd + (v + j * kThreads + tid) * VN, w[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int64_t i = v + j * kThreads + tid;
+          if (i < v1) store_edge(rd, i, vocab, w[j]);
+        }
+      }
+    }
+  }
+}
+
+// -------------------------------------------------------------- workspace
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+struct Workspace {
+  Part* parts;
+  RowGrad* grads;
+  double* losses;
+  size_t bytes;
+};
+
+Workspace lay_out(void* base, int64_t rows, int64_t vocab, int64_t terms) {
+  const int chunks = std::max(cut_rows(rows, vocab, Vec<float>::n).chunks,
+                              cut_rows(rows, vocab, Vec<__bf16>::n).chunks);
+  char* p = static_cast<char*>(base);
+  size_t at = 0;
+  Workspace w;
+  w.parts = reinterpret_cast<Part*>(p + at);
+  at += round256(sizeof(Part) * static_cast<size_t>(rows) * chunks);
+  w.grads = reinterpret_cast<RowGrad*>(p + at);
+  at += round256(sizeof(RowGrad) * static_cast<size_t>(rows));
+  w.losses = reinterpret_cast<double*>(p + at);
+  at += round256(sizeof(double) * static_cast<size_t>(terms > rows ? terms : rows));
+  w.bytes = at;
+  return w;
+}
+
+int grid_of(int64_t groups) {
+  return static_cast<int>(groups < kMaxGrid ? (groups > 0 ? groups : 1) : kMaxGrid);
+}
+
+template <typename T, bool ENT>
+hipError_t launch_stats(const TokenRows& t, const Scale& sc, const Cut& cut, const Workspace& w,
+                        const RowInit& init, hipStream_t stream) {
+  hipLaunchKernelGGL((stats_kernel<T, ENT>), dim3(grid_of(int64_t{t.rows} * cut.chunks)),
+                     dim3(kThreads), 0, stream, static_cast<const T*>(t.x), t.ld, t.rows, t.vocab,
+                     t.tokens, t.weights, sc, cut, w.parts, init);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_grad(const TokenRows& t, const Scale& sc, const Cut& cut, const Workspace& w,
+                       const GradRows& d, int64_t terms, float* loss, hipStream_t stream) {
+  hipLaunchKernelGGL((grad_kernel<T, false, false>), dim3(grid_of(int64_t{t.rows} * cut.chunks)),
+                     dim3(kThreads), 0, stream, static_cast<const T*>(t.x), t.ld, t.rows, t.vocab,
+                     t.tokens, sc, cut, w.grads, ScoreGrad{}, static_cast<T*>(d.x), d.ld, w.losses,
+                     terms, loss);
+  return hipGetLastError();
+}
+
+hipError_t launch_sum(const double* v, int64_t n, float* out, hipStream_t stream) {
+  hipLaunchKernelGGL(sum_kernel, dim3(1), dim3(kThreads), 0, stream, v, n, out);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t token_logprobs_t(const TokenRows& t, const ScoreOut& o, void* ws, hipStream_t stream) {
+  const Scale sc = make_scale(t.temperature);
+  const Cut cut = cut_rows(t.rows, t.vocab, Vec<T>::n);
+  const Workspace w = lay_out(ws, t.rows, t.vocab, 0);
+  const dim3 grid(grid_of((t.rows + kRowsPerGroup - 1) / kRowsPerGroup));
+  if (o.entropies != nullptr) {
+    const hipError_t e = launch_stats<T, true>(t, sc, cut, w, RowInit{}, stream);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((score_rows_kernel<true, T>), grid, dim3(kThreads), 0, stream,
+                       static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, t.tokens, sc, w.parts,
+                       cut.chunks, o);
+  } else {
+    const hipError_t e = launch_stats<T, false>(t, sc, cut, w, RowInit{}, stream);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((score_rows_kernel<false, T>), grid, dim3(kThreads), 0, stream,
+                       static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, t.tokens, sc, w.parts,
+                       cut.chunks, o);
+  }
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t token_logprobs_backward_t(const TokenRows& t, const ScoreGrad& g, const GradRows& d,
+                                     hipStream_t stream) {
+  const Scale sc = make_scale(t.temperature);
+  const Cut cut = cut_rows(t.rows, t.vocab, Vec<T>::n);
+  const dim3 grid(grid_of(int64_t{t.rows} * cut.chunks));
+  if (g.grad_entropies != nullptr)
+    hipLaunchKernelGGL((grad_kernel<T, true, true>), grid, dim3(kThreads), 0, stream,
+                       static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, t.tokens, sc, cut,
+                       nullptr, g, static_cast<T*>(d.x), d.ld, nullptr, 0, nullptr);
+  else
+    hipLaunchKernelGGL((grad_kernel<T, true, false>), grid, dim3(kThreads), 0, stream,
+                       static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, t.tokens, sc, cut,
+                       nullptr, g, static_cast<T*>(d.x), d.ld, nullptr, 0, nullptr);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t policy_loss_t(const TokenRows& t, const PolicyArgs& p, const GradRows& d, void* ws,
+                         hipStream_t stream) {
+  const Scale sc = make_scale(t.temperature);
+  const Cut cut = cut_rows(t.rows, t.vocab, Vec<T>::n);
+  const Workspace w = lay_out(ws, t.rows, t.vocab, 0);
+  const bool back = d.x != nullptr;
+  hipError_t e = launch_stats<T, false>(t, sc, cut, w, RowInit{}, stream);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((policy_rows_kernel<T>),
+                     dim3(grid_of((t.rows + kRowsPerGroup - 1) / kRowsPerGroup)), dim3(kThreads),
+                     0, stream, static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, t.tokens,
+                     t.weights, sc, w.parts, cut.chunks, p, back ? w.grads : nullptr, w.losses);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return back ? launch_grad<T>(t, sc, cut, w, d, t.rows, p.loss, stream)
+              : launch_sum(w.losses, t.rows, p.loss, stream);
+}
+
+template <typename T>
+hipError_t preference_loss_t(const TokenRows& t, const PreferenceArgs& p, const GradRows& d,
+                             void* ws, hipStream_t stream) {
+  const Scale sc = make_scale(t.temperature);
+  const Cut cut = cut_rows(t.rows, t.vocab, Vec<T>::n);
+  const Workspace w = lay_out(ws, t.rows, t.vocab, p.n_pairs);
+  const bool back = d.x != nullptr && t.rows > 0;
+  hipError_t e = hipSuccess;
+  if (t.rows > 0) {
+    const RowInit init{back ? w.grads : nullptr, p.logprobs, p.row_status, p.seq_offsets,
+                       2 * p.n_pairs};
+    e = launch_stats<T, false>(t, sc, cut, w, init, stream);
+    if (e != hipSuccess) return e;
+  }
+  if (p.n_pairs > 0) {
+    hipLaunchKernelGGL((preference_pairs_kernel<T>), dim3(grid_of(p.n_pairs)), dim3(kThreads), 0,
+                       stream, static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, t.tokens, sc,
+                       w.parts, cut.chunks, p, back ? w.grads : nullptr, w.losses);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return back ? launch_grad<T>(t, sc, cut, w, d, p.n_pairs, p.loss, stream)
+              : launch_sum(w.losses, p.n_pairs, p.loss, stream);
+}
+
+}  // namespace
+
+size_t token_rows_workspace_size(int64_t rows, int64_t vocab, int64_t n_pairs) {
+  return lay_out(nullptr, rows, vocab, n_pairs).bytes;
+}
+
+hipError_t launch_token_logprobs(const TokenRows& t, const ScoreOut& o, void* ws,
+                                 hipStream_t stream) {
+  return t.bf16 ? token_logprobs_t<__bf16>(t, o, ws, stream)
+                : token_logprobs_t<float>(t, o, ws, stream);
+}
+
+hipError_t launch_token_logprobs_backward(const TokenRows& t, const ScoreGrad& g,
+                                          const GradRows& d, hipStream_t stream) {
+  return t.bf16 ? token_logprobs_backward_t<__bf16>(t, g, d, stream)
+                : token_logprobs_backward_t<float>(t, g, d, stream);
+}
+
+hipError_t launch_policy_loss(const TokenRows& t, const PolicyArgs& p, const GradRows& d, void* ws,
+                              hipStream_t stream) {
+  if (t.rows == 0) return launch_sum(nullptr, 0, p.loss, stream);
+  return t.bf16 ? policy_loss_t<__bf16>(t, p, d, ws, stream)
+                : policy_loss_t<float>(t, p, d, ws, stream);
+}
+
+hipError_t launch_preference_loss(const TokenRows& t, const PreferenceArgs& p, const GradRows& d,
+                                  void* ws, hipStream_t stream) {
+  return t.bf16 ? preference_loss_t<__bf16>(t, p, d, ws, stream)
+                : preference_loss_t<float>(t, p, d, ws, stream);
+}
+
+}  // namespace ts

@@ -11,6 +11,9 @@
 
 namespace ts {
 
+// Records a failure for ts_last_error (api.hip) and returns its code.
+int fail_message(int code, const char* msg);
+
 // ---------------------------------------------------------------- projection
 hipError_t launch_lmhead_gemm(const uint16_t* hidden, int64_t ld_hidden, const uint16_t* lm_head,
                               int64_t ld_lm_head, float* logits, int64_t ld_logits, int rows,
