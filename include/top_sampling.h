@@ -392,11 +392,11 @@ enum { TS_F32 = 0, TS_BF16 = 1 };
  */
 size_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab);
 int token_logprobs(const void* logits, int32_t logits_type, int64_t rows, int64_t vocab,
-                   int64_t ld_logits, const int32_t* token_ids, float temperature,
+                   int64_t ld_logits, const int32_t* token_ids, double temperature,
                    float* logprobs, float* entropies, float* row_stats, int32_t* row_status,
                    void* workspace, size_t workspace_bytes, void* stream);
 int token_logprobs_backward(const void* logits, int32_t logits_type, int64_t rows, int64_t vocab,
-                            int64_t ld_logits, const int32_t* token_ids, float temperature,
+                            int64_t ld_logits, const int32_t* token_ids, double temperature,
                             const float* row_stats, const float* grad_logprobs,
                             const float* entropies, const float* grad_entropies,
                             void* grad_logits, int64_t ld_grad, void* stream);
@@ -425,10 +425,10 @@ int token_logprobs_backward(const void* logits, int32_t logits_type, int64_t row
  * Workspace: token_logprobs_workspace_bytes.
  */
 typedef struct ts_policy_params {
-  float temperature;
-  float clip_low;
-  float clip_high;
-  float kl_coef;
+  double temperature;
+  double clip_low;
+  double clip_high;
+  double kl_coef;
 } ts_policy_params;
 int policy_loss(const void* logits, int32_t logits_type, int64_t rows, int64_t vocab,
                 int64_t ld_logits, const int32_t* token_ids, const ts_policy_params* params,
@@ -467,10 +467,10 @@ int policy_loss(const void* logits, int32_t logits_type, int64_t rows, int64_t v
  */
 #define TS_PREFERENCE_MEAN 1
 typedef struct ts_preference_params {
-  float temperature;
-  float beta;
-  float label_smoothing;
-  float margin;
+  double temperature;
+  double beta;
+  double label_smoothing;
+  double margin;
   int32_t flags;
 } ts_preference_params;
 size_t preference_loss_workspace_bytes(int64_t rows, int64_t vocab, int64_t n_pairs);

@@ -2,8 +2,8 @@
 GPU against the float64 oracle (oracle/losses.py).
 
 Tolerances.  u = 2^-24 is fp32's rounding.  A row's sum is added up per thread
-in fp32, at most 128 terms one after the other (relative error at most 128 u),
-each term exp2 of an argument with two roundings (relative error at most
+in fp32, at most 128 terms one after the other (relative error at most 128 u;
+the kernel adds 32 as a tree), each term exp2 of an argument with two roundings (relative error at most
 2 u |z - max z| plus 2 u of exp2 itself), and in double from there on.  So ln S
 is off by at most
     LSE = 130 u + 2 u * (the p-weighted mean of |z - max z|, below 30 here)

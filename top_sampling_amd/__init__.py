@@ -50,7 +50,7 @@ TS_PREFERENCE_MEAN = 1
 # (name, restype, argtypes) of every symbol the headers declare
 # (include/top_sampling.h and the measurement aids of top_sampling_measure.h).
 _VP, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
-_F32 = ctypes.c_float
+_F64 = ctypes.c_double
 SYMBOLS = {
     "lmhead_logits_local": (ctypes.c_int, [_VP, _I64, _I64, _I64, _VP, _I64, _I64, _VP, _I64, _VP]),
     "quantize_rows_e4m3": (ctypes.c_int, [_VP, _I64, _I64, _I64, _VP, _I64, _VP, _VP]),
@@ -73,9 +73,9 @@ SYMBOLS = {
     "ts_mfma_clock_probe": (ctypes.c_int, [_VP, _I32, _I64, _I32, _VP]),
     "ts_gumbel_keys": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP, _VP, _VP]),
     "token_logprobs_workspace_bytes": (_SZ, [_I64, _I64]),
-    "token_logprobs": (ctypes.c_int, [_VP, _I32, _I64, _I64, _I64, _VP, _F32, _VP, _VP, _VP, _VP,
+    "token_logprobs": (ctypes.c_int, [_VP, _I32, _I64, _I64, _I64, _VP, _F64, _VP, _VP, _VP, _VP,
                                       _VP, _SZ, _VP]),
-    "token_logprobs_backward": (ctypes.c_int, [_VP, _I32, _I64, _I64, _I64, _VP, _F32, _VP, _VP,
+    "token_logprobs_backward": (ctypes.c_int, [_VP, _I32, _I64, _I64, _I64, _VP, _F64, _VP, _VP,
                                                _VP, _VP, _VP, _I64, _VP]),
     "policy_loss": (ctypes.c_int, [_VP, _I32, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
                                    _VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP, _SZ, _VP]),
@@ -399,13 +399,13 @@ def sampler_assemble_and_sample(slices, params, row_offset: int = 0, max_logprob
 
 # ------------------------------------------------------- scoring and losses
 class _PolicyParams(ctypes.Structure):
-    _fields_ = [("temperature", _F32), ("clip_low", _F32), ("clip_high", _F32),
-                ("kl_coef", _F32)]
+    _fields_ = [("temperature", _F64), ("clip_low", _F64), ("clip_high", _F64),
+                ("kl_coef", _F64)]
 
 
 class _PreferenceParams(ctypes.Structure):
-    _fields_ = [("temperature", _F32), ("beta", _F32), ("label_smoothing", _F32),
-                ("margin", _F32), ("flags", _I32)]
+    _fields_ = [("temperature", _F64), ("beta", _F64), ("label_smoothing", _F64),
+                ("margin", _F64), ("flags", _I32)]
 
 
 @dataclass

@@ -32,16 +32,16 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 // The logits, tokens and temperature of a call into t.  rows == 0 passes
 // without looking at the pointers.
 int token_rows(ts::TokenRows& t, const void* logits, int32_t logits_type, int64_t rows,
-               int64_t vocab, int64_t ld_logits, const int32_t* token_ids, float temperature) {
+               int64_t vocab, int64_t ld_logits, const int32_t* token_ids, double temperature) {
   if (rows < 0 || vocab < 0)
     return fail(TS_EINVAL, "negative size (rows=%lld vocab=%lld)", (long long)rows,
                 (long long)vocab);
   if (logits_type != TS_F32 && logits_type != TS_BF16)
     return fail(TS_EINVAL, "logits_type %d is neither TS_F32 nor TS_BF16", logits_type);
   if (rows > kMaxDim || vocab > kMaxDim) return fail(TS_EUNSUPPORTED, "size above 2^31-1");
-  if (!(temperature >= TS_GREEDY_EPS) || !(temperature < INFINITY))
+  if (!(temperature >= static_cast<double>(TS_GREEDY_EPS)) || !(temperature < INFINITY))
     return fail(TS_EINVAL, "temperature %g is not a finite number of at least TS_GREEDY_EPS",
-                (double)temperature);
+                temperature);
   t = ts::TokenRows{};
   t.rows = static_cast<int>(rows);
   t.vocab = static_cast<int>(vocab);
@@ -95,7 +95,7 @@ bool all_aligned4(std::initializer_list<const void*> ps) {
 }
 
 // Finite and at least 0.
-bool bound_ok(float v) { return v >= 0.0f && v < INFINITY; }
+bool bound_ok(double v) { return v >= 0.0 && v < INFINITY; }
 
 }  // namespace
 
@@ -114,7 +114,7 @@ size_t preference_loss_workspace_bytes(int64_t rows, int64_t vocab, int64_t n_pa
 }
 
 int token_logprobs(const void* logits, int32_t logits_type, int64_t rows, int64_t vocab,
-                   int64_t ld_logits, const int32_t* token_ids, float temperature,
+                   int64_t ld_logits, const int32_t* token_ids, double temperature,
                    float* logprobs, float* entropies, float* row_stats, int32_t* row_status,
                    void* workspace, size_t workspace_bytes, void* stream) {
   ts::TokenRows t;
@@ -131,7 +131,7 @@ int token_logprobs(const void* logits, int32_t logits_type, int64_t rows, int64_
 }
 
 int token_logprobs_backward(const void* logits, int32_t logits_type, int64_t rows, int64_t vocab,
-                            int64_t ld_logits, const int32_t* token_ids, float temperature,
+                            int64_t ld_logits, const int32_t* token_ids, double temperature,
                             const float* row_stats, const float* grad_logprobs,
                             const float* entropies, const float* grad_entropies,
                             void* grad_logits, int64_t ld_grad, void* stream) {
@@ -165,15 +165,15 @@ int policy_loss(const void* logits, int32_t logits_type, int64_t rows, int64_t v
   int st = token_rows(t, logits, logits_type, rows, vocab, ld_logits, token_ids,
                       params->temperature);
   if (st != TS_OK) return st;
-  if (!(params->clip_low >= 0.0f) || !(params->clip_high >= 0.0f))
+  if (!(params->clip_low >= 0.0) || !(params->clip_high >= 0.0))
     return fail(TS_EINVAL, "clip_low and clip_high must be at least 0 (inf: no clip)");
   if (!bound_ok(params->kl_coef))
-    return fail(TS_EINVAL, "kl_coef %g is negative or not finite", (double)params->kl_coef);
+    return fail(TS_EINVAL, "kl_coef %g is negative or not finite", params->kl_coef);
   if (!loss) return fail(TS_EINVAL, "NULL loss");
   if (!aligned(loss, 4)) return fail(TS_EUNSUPPORTED, "loss misaligned");
   if (rows > 0 && (!old_logprobs || !advantages))
     return fail(TS_EINVAL, "NULL old_logprobs/advantages");
-  if (rows > 0 && params->kl_coef != 0.0f && !ref_logprobs)
+  if (rows > 0 && params->kl_coef != 0.0 && !ref_logprobs)
     return fail(TS_EINVAL, "kl_coef without ref_logprobs");
   if (!all_aligned4({old_logprobs, ref_logprobs, advantages, weights, grad_loss, logprobs, ratios,
                      kl, row_status}))
@@ -207,12 +207,12 @@ int preference_loss(const void* logits, int32_t logits_type, int64_t rows, int64
   if (st != TS_OK) return st;
   if (n_pairs < 0) return fail(TS_EINVAL, "n_pairs < 0");
   if (n_pairs > kMaxDim / 2) return fail(TS_EUNSUPPORTED, "n_pairs above 2^30-1");
-  if (!(params->beta > 0.0f) || !(params->beta < INFINITY))
-    return fail(TS_EINVAL, "beta %g is not a finite number above 0", (double)params->beta);
-  if (!(params->label_smoothing >= 0.0f) || !(params->label_smoothing <= 1.0f))
+  if (!(params->beta > 0.0) || !(params->beta < INFINITY))
+    return fail(TS_EINVAL, "beta %g is not a finite number above 0", params->beta);
+  if (!(params->label_smoothing >= 0.0) || !(params->label_smoothing <= 1.0))
     return fail(TS_EINVAL, "label_smoothing %g is not in [0, 1]",
-                (double)params->label_smoothing);
-  if (!(fabsf(params->margin) < INFINITY)) return fail(TS_EINVAL, "margin is not finite");
+                params->label_smoothing);
+  if (!(fabs(params->margin) < INFINITY)) return fail(TS_EINVAL, "margin is not finite");
   if (params->flags & ~TS_PREFERENCE_MEAN)
     return fail(TS_EINVAL, "unknown flag bits 0x%x", params->flags);
   if (!loss) return fail(TS_EINVAL, "NULL loss");

@@ -65,12 +65,12 @@ struct Scale {
   double c, inv_t;
 };
 
-Scale make_scale(float temperature) {
+Scale make_scale(double temperature) {
   Scale s;
-  s.c = M_LOG2E / static_cast<double>(temperature);
+  s.c = M_LOG2E / temperature;
   s.c_hi = static_cast<float>(s.c);
   s.c_lo = static_cast<float>(s.c - static_cast<double>(s.c_hi));
-  s.inv_t = 1.0 / static_cast<double>(temperature);
+  s.inv_t = 1.0 / temperature;
   s.floor = static_cast<float>(-200.0 / s.c);
   return s;
 }
@@ -164,6 +164,17 @@ __device__ __forceinline__ void join_lanes(float& m, double& s, double& u, int w
   m = top;
 }
 
+// The sum of a thread's batch, added up pair by pair (in place).
+template <int VN>
+__device__ __forceinline__ float tree_sum(float (&w)[kBatch][VN]) {
+  float* v = &w[0][0];
+#pragma unroll
+  for (int n = kBatch * VN / 2; n > 0; n >>= 1)
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] += v[i + n];
+  return v[0];
+}
+
 // ------------------------------------------------------------------- stats
 // What the pass sets for every row before the later kernels fill in the rows
 // that take part (any pointer may be null), and the rows that do: with
@@ -196,9 +207,10 @@ __global__ __launch_bounds__(kThreads) void stats_kernel(
     const T* rx = x + static_cast<int64_t>(row) * ld;
     const int64_t v0 = static_cast<int64_t>(chunk) * cut.len, v1 = v0 + cut.len;
     const int64_t whole = vocab / VN;  // vectors that lie wholly inside the row
-    float m = -INFINITY, s = 0.0f, u = 0.0f;
+    float m = -INFINITY;
+    double s = 0.0, u = 0.0;
     for (int64_t v = v0; v < v1; v += kSlab) {
-      float w[kBatch][VN];
+      float w[kBatch][VN], ut[kBatch][VN];
       if (v + kSlab <= v1 && v + kSlab <= whole) {
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) load_vec(rx + (v + j * kThreads + tid) * VN, w[j]);
@@ -216,23 +228,27 @@ __global__ __launch_bounds__(kThreads) void stats_kernel(
         for (int e = 0; e < VN; e += 2) top = max_nan(max_nan(top, w[j][e]), w[j][e + 1]);
       const float ref = top == -INFINITY ? 0.0f : top;
       const float shift = fmaxf(m - ref, sc.floor);
-      const float f = exp_t(shift, sc);
-      if (ENT) u = f * fmaf(shift, s, u);
+      const double f = exp_t(shift, sc);
+      if (ENT) u = f * (u + shift * s);
       s *= f;
       m = top;
+      // A batch is added up as a tree, and the batches in double: behind a
+      // term near 1, terms below half an fp32 step would all be lost one by
+      // one, and every row with one likely token came out 1e-7 too likely.
 #pragma unroll
       for (int j = 0; j < kBatch; ++j)
 #pragma unroll
         for (int e = 0; e < VN; ++e) {
           const float t = fmaxf(w[j][e] - ref, sc.floor);
           const float ex = exp_t(t, sc);
-          s += ex;
-          if (ENT) u = fmaf(ex, t, u);
+          w[j][e] = ex;
+          if (ENT) ut[j][e] = ex * t;
         }
+      s += tree_sum(w);
+      if (ENT) u += tree_sum(ut);
     }
-    double ds = s, du = u;
-    join_lanes<ENT>(m, ds, du, 64, sc.c);
-    if (lane == 0) wave_part[wave] = Part{ds, du, m, 0.0f};
+    join_lanes<ENT>(m, s, u, 64, sc.c);
+    if (lane == 0) wave_part[wave] = Part{s, u, m, 0.0f};
     __syncthreads();
     if (tid < kThreads / 64) {
       Part p = wave_part[tid];
@@ -371,8 +387,8 @@ __global__ __launch_bounds__(kThreads) void policy_rows_kernel(
     const double w = weights ? static_cast<double>(weights[r]) : 1.0;
     const double adv = p.advantages[r];
     const double ratio = exp(st.lp - static_cast<double>(p.old_logprobs[r]));
-    const double low = 1.0 - static_cast<double>(p.clip_low);
-    const double high = 1.0 + static_cast<double>(p.clip_high);
+    const double low = 1.0 - p.clip_low;
+    const double high = 1.0 + p.clip_high;
     // min(r A, clip(r) A): the bound that holds against the advantage's sign
     // is the only one that can bind.  A = 0 gives 0 at any ratio.
     const bool inside = adv >= 0.0 ? !(ratio > high) : !(ratio < low);
@@ -386,10 +402,10 @@ __global__ __launch_bounds__(kThreads) void policy_rows_kernel(
       const double gap = static_cast<double>(p.ref_logprobs[r]) - st.lp;
       const double em = expm1(gap);
       kl = em - gap;
-      if (p.kl_coef != 0.0f) g -= static_cast<double>(p.kl_coef) * em;
+      if (p.kl_coef != 0.0) g -= p.kl_coef * em;
     }
     double loss = -gain;
-    if (p.kl_coef != 0.0f) loss += static_cast<double>(p.kl_coef) * kl;
+    if (p.kl_coef != 0.0) loss += p.kl_coef * kl;
     losses[r] = st.status == TS_ROW_OK ? w * loss : NAN;
     if (p.logprobs) p.logprobs[r] = static_cast<float>(st.lp);
     if (p.ratios) p.ratios[r] = static_cast<float>(ratio);
@@ -460,7 +476,7 @@ __global__ __launch_bounds__(kThreads) void preference_pairs_kernel(
         rho[side] = s * per[side];
       }
       const double beta = p.beta, eps = p.label_smoothing;
-      const double z = beta * (rho[0] - rho[1]) - static_cast<double>(p.margin);
+      const double z = beta * (rho[0] - rho[1]) - p.margin;
       const double soft = log1p(exp(-fabs(z)));  // -ln sigmoid(|z|)
       const double loss = (1.0 - eps) * (soft + fmax(-z, 0.0)) + eps * (soft + fmax(z, 0.0));
       const double weight = p.pair_weights ? static_cast<double>(p.pair_weights[pair])

@@ -15,7 +15,7 @@ struct TokenRows {
   int rows, vocab;
   const int32_t* tokens;  // [rows]; negative: the row is left out
   const float* weights;   // [rows] or null; 0: the row is left out
-  float temperature;
+  double temperature;
 };
 
 // Gradient rows in the logits' type; x null: no gradient is written.
@@ -39,7 +39,7 @@ struct ScoreGrad {
 };
 
 struct PolicyArgs {
-  float clip_low, clip_high, kl_coef;
+  double clip_low, clip_high, kl_coef;
   const float* old_logprobs;
   const float* ref_logprobs;  // null: no KL term, kl rows are 0
   const float* advantages;
@@ -52,7 +52,7 @@ struct PolicyArgs {
 };
 
 struct PreferenceArgs {
-  float beta, label_smoothing, margin;
+  double beta, label_smoothing, margin;
   int mean;
   int n_pairs;
   const int32_t* seq_offsets;  // [2 n_pairs + 1]
