@@ -22,6 +22,7 @@
 //   grad   reads the logits again and writes the gradient
 // exp(x / T) is taken as exp2((x - m) c) with c = log2(e) / T held as two
 // floats, so a temperature's rounding does not tilt the whole sum.
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -34,7 +35,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kBatch = 4;                       // 16-byte vectors a thread has in flight
 constexpr int kSlab = kThreads * kBatch;        // vectors a workgroup takes at a time
-constexpr int kMaxChunkSlabs = 4;               // longest chunk, in slabs
+constexpr int kMaxChunkSlabs = 2;               // longest chunk, in slabs
 constexpr int kTargetGroups = 1024;             // workgroups wanted for few rows
 constexpr int kMaxGrid = 1 << 23;               // workgroups of one launch (grid-stride beyond)
 
@@ -60,8 +61,8 @@ struct Vec<__bf16> {
 
 // The temperature, as the kernels use it.
 struct Scale {
-  float c_hi, c_lo;  // log2(e) / T in two floats
-  float floor;       // x - m below this gives exp2 = 0 (also x = -inf)
+  float c_hi, c_lo;  // log2(e) / T in two floats, both above 0
+  float floor;       // x - m below this gives exp2 = 0
   double c, inv_t;
 };
 
@@ -69,13 +70,17 @@ Scale make_scale(double temperature) {
   Scale s;
   s.c = M_LOG2E / temperature;
   s.c_hi = static_cast<float>(s.c);
-  s.c_lo = static_cast<float>(s.c - static_cast<double>(s.c_hi));
+  if (s.c_hi >= s.c) s.c_hi = nextafterf(s.c_hi, 0.0f);
+  // A temperature beyond 1e30 leaves normal numbers here, and e_j at 1.
+  s.c_hi = std::max(s.c_hi, FLT_MIN);
+  s.c_lo = std::max(static_cast<float>(s.c - static_cast<double>(s.c_hi)), FLT_MIN);
   s.inv_t = 1.0 / temperature;
-  s.floor = static_cast<float>(-200.0 / s.c);
+  s.floor = static_cast<float>(std::max(-200.0 / s.c, -static_cast<double>(FLT_MAX)));
   return s;
 }
 
-// exp((x - m) / T) of t = max(x - m, floor).
+// exp((x - m) / T) of t = x - m.  Both products of t = -inf are -inf, so a
+// token that is not allowed gives exp2(-inf) = 0 without a test.
 __device__ __forceinline__ float exp_t(float t, const Scale& s) {
   return __builtin_amdgcn_exp2f(fmaf(t, s.c_hi, t * s.c_lo));
 }
@@ -106,7 +111,7 @@ struct Cut {
 // shorter until there are about kTargetGroups of them, down to one vector a
 // thread.
 Cut cut_rows(int64_t rows, int64_t vocab, int vec) {
-  const int64_t nvec = vocab > 0 ? (vocab + vec - 1) / vec : 1;
+  const int64_t nvec = vocab >= vec ? vocab / vec : 1;  // whole vectors
   int64_t want = (nvec + kSlab * kMaxChunkSlabs - 1) / (kSlab * kMaxChunkSlabs);
   const int64_t fill = rows > 0 ? (kTargetGroups + rows - 1) / rows : 1;
   const int64_t most = (nvec + kThreads - 1) / kThreads;
@@ -121,27 +126,6 @@ Cut cut_rows(int64_t rows, int64_t vocab, int vec) {
   return c;
 }
 
-template <typename T>
-__device__ __forceinline__ void load_vec(const T* p, float (&v)[Vec<T>::n]) {
-  const typename Vec<T>::Type w = *reinterpret_cast<const typename Vec<T>::Type*>(p);
-#pragma unroll
-  for (int e = 0; e < Vec<T>::n; ++e) v[e] = static_cast<float>(w[e]);
-}
-
-// Vector i of a row of `vocab` logits; entries past the row read -inf.
-template <typename T>
-__device__ __forceinline__ void load_edge(const T* row, int64_t i, int vocab,
-                                          float (&v)[Vec<T>::n]) {
-  constexpr int VN = Vec<T>::n;
-  const int64_t at = i * VN;
-  if (at + VN <= vocab) {
-    load_vec(row + at, v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < VN; ++e) v[e] = at + e < vocab ? static_cast<float>(row[at + e]) : -INFINITY;
-  }
-}
-
 __device__ __forceinline__ bool left_out(const int32_t* tokens, const float* weights, int row) {
   return tokens[row] < 0 || (weights != nullptr && weights[row] == 0.0f);
 }
@@ -149,12 +133,12 @@ __device__ __forceinline__ bool left_out(const int32_t* tokens, const float* wei
 // Joins (m, s, u) of a group of `width` lanes (a power of two); every lane
 // gets the result.  An empty part has m = -inf and s = u = 0.
 template <bool ENT>
-__device__ __forceinline__ void join_lanes(float& m, double& s, double& u, int width, double c) {
+__device__ __forceinline__ void join_lanes(float& m, double& s, double& u, int width,
+                                           const Scale& sc) {
   float top = m;
   for (int d = width >> 1; d > 0; d >>= 1) top = max_nan(top, __shfl_xor(top, d, width));
-  const float ref = top == -INFINITY ? 0.0f : top;
-  const double shift = m == -INFINITY ? 0.0 : static_cast<double>(m) - ref;
-  const double f = m == -INFINITY ? 0.0 : exp2(shift * c);
+  const float shift = fmaxf(m - (top == -INFINITY ? 0.0f : top), sc.floor);
+  const double f = exp_t(shift, sc);
   if (ENT) u = f * (u + shift * s);
   s *= f;
   for (int d = width >> 1; d > 0; d >>= 1) {
@@ -187,13 +171,115 @@ struct RowInit {
   int n_seqs;
 };
 
+// A slab of a row's whole vectors, kThreads x kBatch of them from v on; past
+// `end` the loads repeat the last vector and are not used.
+template <typename T, int THREADS>
+struct Slab {
+  typename Vec<T>::Type raw[kBatch];
+
+  __device__ __forceinline__ void load(const T* row, int v, int end) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = min(v + j * THREADS + static_cast<int>(threadIdx.x), end - 1);
+      raw[j] = *reinterpret_cast<const typename Vec<T>::Type*>(row + static_cast<int64_t>(i) *
+                                                                         Vec<T>::n);
+    }
+  }
+  __device__ __forceinline__ void unpack(float (&w)[kBatch][Vec<T>::n]) const {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+      for (int e = 0; e < Vec<T>::n; ++e) w[j][e] = static_cast<float>(raw[j][e]);
+  }
+};
+
+// A thread's share of vectors [v0, v1) of a row joined into m, s, u; `tail`:
+// also the row's last entries, short of a vector.  The next slab's loads are
+// in flight while a slab is added up.
+template <typename T, bool ENT, int THREADS>
+__device__ __forceinline__ void row_stats(const T* row, int vocab, int v0, int v1, bool tail,
+                                          const Scale& sc, float& m, double& s, double& u) {
+  constexpr int VN = Vec<T>::n;
+  const int tid = threadIdx.x;
+  const int end = min(v1, vocab / VN);
+  Slab<T, THREADS> next;
+  if (v0 < end) next.load(row, v0, end);
+  for (int v = v0; v < end; v += THREADS * kBatch) {
+    float w[kBatch][VN], ut[kBatch][VN];
+    next.unpack(w);
+    if (v + THREADS * kBatch < end) {
+      next.load(row, v + THREADS * kBatch, end);
+    }
+    if (v + THREADS * kBatch > end) {
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+        for (int e = 0; e < VN; ++e)
+          w[j][e] = v + j * THREADS + tid < end ? w[j][e] : -INFINITY;
+    }
+    float top = m;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+      for (int e = 0; e < VN; e += 2) top = max_nan(max_nan(top, w[j][e]), w[j][e + 1]);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    const float shift = fmaxf(m - ref, sc.floor);
+    const double f = exp_t(shift, sc);
+    if (ENT) u = f * (u + shift * s);
+    s *= f;
+    m = top;
+    // A batch is added up as a tree, and the batches in double: behind a term
+    // near 1, terms below half an fp32 step would all be lost one by one, and
+    // every row with one likely token came out 1e-7 too likely.
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+      for (int e = 0; e < VN; ++e) {
+        const float t = w[j][e] - ref;
+        const float ex = exp_t(t, sc);
+        w[j][e] = ex;
+        if (ENT) ut[j][e] = ex * fmaxf(t, sc.floor);
+      }
+    s += tree_sum(w);
+    if (ENT) u += tree_sum(ut);
+  }
+  const int at = vocab / VN * VN + tid;
+  if (tail && at < vocab) {
+    const float x = static_cast<float>(row[at]);
+    const float top = max_nan(m, x), ref = top == -INFINITY ? 0.0f : top;
+    const float shift = fmaxf(m - ref, sc.floor), t = fmaxf(x - ref, sc.floor);
+    const double f = exp_t(shift, sc), ex = exp_t(t, sc);
+    if (ENT) u = f * (u + shift * s) + ex * t;
+    s = f * s + ex;
+    m = top;
+  }
+}
+
+// The workgroup's (m, s, u) joined; threads below THREADS / 64 of the first
+// wave have the result.
+template <bool ENT, int THREADS>
+__device__ __forceinline__ void join_group(float& m, double& s, double& u, const Scale& sc,
+                                           Part* wave_part) {
+  constexpr int WAVES = THREADS / 64;
+  const int tid = threadIdx.x;
+  join_lanes<ENT>(m, s, u, 64, sc);
+  if ((tid & 63) == 0) wave_part[tid >> 6] = Part{s, u, m, 0.0f};
+  __syncthreads();
+  if (tid < WAVES) {
+    const Part p = wave_part[tid];
+    m = p.m;
+    s = p.s;
+    u = p.u;
+    join_lanes<ENT>(m, s, u, WAVES, sc);
+  }
+}
+
 template <typename T, bool ENT>
 __global__ __launch_bounds__(kThreads) void stats_kernel(
     const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,
     const float* __restrict__ weights, Scale sc, Cut cut, Part* __restrict__ parts, RowInit init) {
-  constexpr int VN = Vec<T>::n;
   __shared__ Part wave_part[kThreads / 64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x;
   const int64_t total = static_cast<int64_t>(rows) * cut.chunks;
   for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
     const int row = static_cast<int>(b / cut.chunks), chunk = static_cast<int>(b % cut.chunks);
@@ -204,57 +290,12 @@ __global__ __launch_bounds__(kThreads) void stats_kernel(
     }
     if (left_out(tokens, weights, row)) continue;
     if (init.offsets && (row < init.offsets[0] || row >= init.offsets[init.n_seqs])) continue;
-    const T* rx = x + static_cast<int64_t>(row) * ld;
-    const int64_t v0 = static_cast<int64_t>(chunk) * cut.len, v1 = v0 + cut.len;
-    const int64_t whole = vocab / VN;  // vectors that lie wholly inside the row
     float m = -INFINITY;
     double s = 0.0, u = 0.0;
-    for (int64_t v = v0; v < v1; v += kSlab) {
-      float w[kBatch][VN], ut[kBatch][VN];
-      if (v + kSlab <= v1 && v + kSlab <= whole) {
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) load_vec(rx + (v + j * kThreads + tid) * VN, w[j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          const int64_t i = v + j * kThreads + tid;
-          load_edge(rx, i < v1 ? i : INT32_MAX, vocab, w[j]);
-        }
-      }
-      float top = m;
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-#pragma unroll
-        for (int e = 0; e < VN; e += 2) top = max_nan(max_nan(top, w[j][e]), w[j][e + 1]);
-      const float ref = top == -INFINITY ? 0.0f : top;
-      const float shift = fmaxf(m - ref, sc.floor);
-      const double f = exp_t(shift, sc);
-      if (ENT) u = f * (u + shift * s);
-      s *= f;
-      m = top;
-      // A batch is added up as a tree, and the batches in double: behind a
-      // term near 1, terms below half an fp32 step would all be lost one by
-      // one, and every row with one likely token came out 1e-7 too likely.
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-#pragma unroll
-        for (int e = 0; e < VN; ++e) {
-          const float t = fmaxf(w[j][e] - ref, sc.floor);
-          const float ex = exp_t(t, sc);
-          w[j][e] = ex;
-          if (ENT) ut[j][e] = ex * t;
-        }
-      s += tree_sum(w);
-      if (ENT) u += tree_sum(ut);
-    }
-    join_lanes<ENT>(m, s, u, 64, sc.c);
-    if (lane == 0) wave_part[wave] = Part{s, u, m, 0.0f};
-    __syncthreads();
-    if (tid < kThreads / 64) {
-      Part p = wave_part[tid];
-      join_lanes<ENT>(p.m, p.s, p.u, kThreads / 64, sc.c);
-      if (tid == 0) parts[b] = p;
-    }
+    row_stats<T, ENT, kThreads>(x + static_cast<int64_t>(row) * ld, vocab, chunk * cut.len,
+                                (chunk + 1) * cut.len, chunk == cut.chunks - 1, sc, m, s, u);
+    join_group<ENT, kThreads>(m, s, u, sc, wave_part);
+    if (tid == 0) parts[b] = Part{s, u, m, 0.0f};
     __syncthreads();
   }
 }
@@ -282,15 +323,13 @@ __device__ __forceinline__ RowStats join_row(const T* x, int64_t ld, int vocab, 
     const Part p = parts[static_cast<int64_t>(row) * chunks + i];
     const float top = max_nan(r.m, p.m);
     const float ref = top == -INFINITY ? 0.0f : top;
-    const double d0 = r.m == -INFINITY ? 0.0 : static_cast<double>(r.m) - ref;
-    const double d1 = p.m == -INFINITY ? 0.0 : static_cast<double>(p.m) - ref;
-    const double f0 = r.m == -INFINITY ? 0.0 : exp2(d0 * sc.c);
-    const double f1 = p.m == -INFINITY ? 0.0 : exp2(d1 * sc.c);
+    const float d0 = fmaxf(r.m - ref, sc.floor), d1 = fmaxf(p.m - ref, sc.floor);
+    const double f0 = exp_t(d0, sc), f1 = exp_t(d1, sc);
     if (ENT) r.u = f0 * (r.u + d0 * r.s) + f1 * (p.u + d1 * p.s);
     r.s = f0 * r.s + f1 * p.s;
     r.m = top;
   }
-  join_lanes<ENT>(r.m, r.s, r.u, kRowLanes, sc.c);
+  join_lanes<ENT>(r.m, r.s, r.u, kRowLanes, sc);
   if (token >= vocab) {
     r.status = TS_ROW_BAD_PARAMS;
     r.lp = NAN;
@@ -540,25 +579,62 @@ __device__ __forceinline__ RowGrad score_row_grad(const ScoreGrad& g, int row, b
                  static_cast<float>(own * sc.inv_t)};
 }
 
-template <typename T>
-__device__ __forceinline__ void store_vec(T* p, const float (&v)[Vec<T>::n]) {
-  typename Vec<T>::Type w;
-#pragma unroll
-  for (int e = 0; e < Vec<T>::n; ++e) w[e] = static_cast<T>(v[e]);
-  *reinterpret_cast<typename Vec<T>::Type*>(p) = w;
-}
-
-template <typename T>
-__device__ __forceinline__ void store_edge(T* row, int64_t i, int vocab,
-                                           const float (&v)[Vec<T>::n]) {
+// The gradient of vectors [v0, v1) of a row (and with `tail` of its last
+// entries), slab by slab from the last to the first: the end of what the
+// statistics pass read is still in the caches.  The stores go past them.
+template <typename T, bool ENT, int THREADS>
+__device__ __forceinline__ void row_grad_pass(const T* row, T* out, int vocab, int v0, int v1,
+                                              bool tail, int token, const RowGrad& g,
+                                              const Scale& sc) {
   constexpr int VN = Vec<T>::n;
-  const int64_t at = i * VN;
-  if (at + VN <= vocab) {
-    store_vec(row + at, v);
-  } else {
+  constexpr int SLAB = THREADS * kBatch;
+  using V = typename Vec<T>::Type;
+  const int tid = threadIdx.x;
+  const int end = min(v1, vocab / VN);
+  const bool zero = g.a == 0.0f && g.b == 0.0f && g.own == 0.0f;
+  auto entry = [&](float x, bool is_token) {
+    const float t = ENT ? fmaxf(x - g.m, sc.floor) : x - g.m;
+    const float ex = exp_t(t, sc);
+    return is_token ? g.own : (ENT ? ex * fmaf(g.b, t, g.a) : ex * g.a);
+  };
+  const int at = vocab / VN * VN + tid;
+  if (tail && at < vocab)
+    out[at] = static_cast<T>(zero ? 0.0f : entry(static_cast<float>(row[at]), at == token));
+  if (v0 >= end) return;
+  // The token's vector, and its place in there, if it is one of these.
+  const int token_vec = token >= 0 ? token / VN : -1, token_e = token >= 0 ? token % VN : 0;
+  int v = v0 + (end - 1 - v0) / SLAB * SLAB;
+  Slab<T, THREADS> next;
+  if (!zero) next.load(row, v, end);
+  for (; v >= v0; v -= SLAB) {
+    float w[kBatch][VN];
+    if (zero) {
 #pragma unroll
-    for (int e = 0; e < VN; ++e)
-      if (at + e < vocab) row[at + e] = static_cast<T>(v[e]);
+      for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+        for (int e = 0; e < VN; ++e) w[j][e] = 0.0f;
+    } else {
+      next.unpack(w);
+      if (v > v0) next.load(row, v - SLAB, end);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+#pragma unroll
+        for (int e = 0; e < VN; ++e) w[j][e] = entry(w[j][e], false);
+        if (v + j * THREADS + tid == token_vec) {
+#pragma unroll
+          for (int e = 0; e < VN; ++e) w[j][e] = e == token_e ? g.own : w[j][e];
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = v + j * THREADS + tid;
+      V o;
+#pragma unroll
+      for (int e = 0; e < VN; ++e) o[e] = static_cast<T>(w[j][e]);
+      if (i < end)
+        __builtin_nontemporal_store(o, reinterpret_cast<V*>(out + static_cast<int64_t>(i) * VN));
+    }
   }
 }
 
@@ -571,14 +647,15 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(
     Cut cut, const RowGrad* __restrict__ grads, ScoreGrad sg, T* d, int64_t ldd,
     const double* __restrict__ losses, int64_t n_losses, float* __restrict__ loss) {
   constexpr int VN = Vec<T>::n;
-  const int tid = threadIdx.x;
   const int64_t total = static_cast<int64_t>(rows) * cut.chunks;
   if (!SCORE && blockIdx.x == 0) {
     const double s = group_sum(losses, n_losses);
-    if (tid == 0) *loss = static_cast<float>(s);
+    if (threadIdx.x == 0) *loss = static_cast<float>(s);
   }
   for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
-    const int row = static_cast<int>(b / cut.chunks), chunk = static_cast<int>(b % cut.chunks);
+    // Last row first, as the end of the logits is what the caches still hold.
+    const int row = rows - 1 - static_cast<int>(b / cut.chunks);
+    const int chunk = cut.chunks - 1 - static_cast<int>(b % cut.chunks);
     const T* rx = x + static_cast<int64_t>(row) * ld;
     T* rd = d + static_cast<int64_t>(row) * ldd;
     const int token = tokens[row];
@@ -587,59 +664,16 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(
       const bool skip = token < 0;
       // The gradient may replace the logits, so the token's own logit is only
       // read by the workgroup that also writes it.
-      const bool mine = token >= 0 && token < vocab &&
-                        token / VN / cut.len == chunk;
+      const int owner = min(token / VN / cut.len, cut.chunks - 1);
+      const bool mine = token >= 0 && token < vocab && owner == chunk;
       const float xt = mine ? static_cast<float>(rx[token]) : 0.0f;
       g = score_row_grad(sg, row, skip, xt, sc);
       __syncthreads();
     } else {
       g = grads[row];
     }
-    const int64_t v0 = static_cast<int64_t>(chunk) * cut.len, v1 = v0 + cut.len;
-    const int64_t whole = vocab / VN;
-    const bool zero = g.a == 0.0f && g.b == 0.0f && g.own == 0.0f;
-    for (int64_t v = v0; v < v1; v += kSlab) {
-      float w[kBatch][VN];
-      const bool inner = v + kSlab <= v1 && v + kSlab <= whole;
-      if (zero) {
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-#pragma unroll
-          for (int e = 0; e < VN; ++e) w[j][e] = 0.0f;
-      } else {
-        if (inner) {
-#pragma unroll
-          for (int j = 0; j < kBatch; ++j) load_vec(rx + (v + j * kThreads + tid) * VN, w[j]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            const int64_t i = v + j * kThreads + tid;
-            load_edge(rx, i < v1 ? i : INT32_MAX, vocab, w[j]);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          const int64_t at = (v + j * kThreads + tid) * VN;
-#pragma unroll
-          for (int e = 0; e < VN; ++e) {
-            const float t = fmaxf(w[j][e] - g.m, sc.floor);
-            const float ex = exp_t(t, sc);
-            const float out = ENT ? ex * fmaf(g.b, t, g.a) : ex * g.a;
-            w[j][e] = at + e == token ? g.own : out;
-          }
-        }
-      }
-      if (inner) {
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) store_vec(rd + (v + j * kThreads + tid) * VN, w[j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          const int64_t i = v + j * kThreads + tid;
-          if (i < v1) store_edge(rd, i, vocab, w[j]);
-        }
-      }
-    }
+    row_grad_pass<T, ENT, kThreads>(rx, rd, vocab, chunk * cut.len, (chunk + 1) * cut.len,
+                                    chunk == cut.chunks - 1, token, g, sc);
   }
 }
 
