@@ -129,6 +129,44 @@ int lmhead_logits_local(const void* hidden, int64_t rows, int64_t hidden_dim,
                         void* stream);
 
 /*
+ * lmhead_logits_local_lora: lmhead_logits_local for rows that each have their
+ * own low-rank adapter:
+ *   logits[r, v] = sum_h hidden[r, h] lm_head[v, h]
+ *                + adapter_scales[a] sum_k lora_b[a][v, k]
+ *                                    (sum_h hidden[r, h] lora_a[a][k, h]),
+ *   a = adapter_ids[r].
+ * One call serves the requests of a batch whatever adapters they have; rows
+ * need no order.  A row of adapter -1 has none and gets exactly what
+ * lmhead_logits_local gives.  A row whose id is below -1 or >= n_adapters gets
+ * a row of NaN, which the sampler reports as TS_ROW_BAD_LOGITS.  A row only
+ * depends on its own adapter: infinities or NaN in another one's weights do
+ * not reach it.
+ *   lora_a   bf16 [n_adapters][rank, hidden_dim]: adapter a at lora_a +
+ *            a * stride_a, leading dimension ld_a
+ *   lora_b   bf16 [n_adapters][vocab_local, rank]: this rank's vocabulary
+ *            slice of every adapter, adapter a at lora_b + a * stride_b,
+ *            leading dimension ld_b
+ *   adapter_scales  fp32 [n_adapters], or NULL for 1
+ *   adapter_ids     int32 [rows]
+ *   workspace       as for sampler_sample; lmhead_lora_workspace_bytes
+ * Adapters of several ranks are padded with zeros to the largest.  Products
+ * and sums are fp32; the inner sums are not rounded to bf16.
+ * Requirements (else TS_EUNSUPPORTED): those of lmhead_logits_local, rank a
+ * multiple of 8 up to TS_MAX_LORA_RANK, ld_a, ld_b and the strides multiples
+ * of 8, lora_a and lora_b 16-byte aligned.  n_adapters == 0 or rank == 0 is
+ * TS_EINVAL.
+ */
+#define TS_MAX_LORA_RANK 256   /* largest accepted adapter rank              */
+size_t lmhead_lora_workspace_bytes(int64_t rows, int64_t rank);
+int lmhead_logits_local_lora(const void* hidden, int64_t rows, int64_t hidden_dim,
+                             int64_t ld_hidden, const void* lm_head, int64_t vocab_local,
+                             int64_t ld_lm_head, const void* lora_a, int64_t stride_a,
+                             int64_t ld_a, const void* lora_b, int64_t stride_b, int64_t ld_b,
+                             int64_t n_adapters, int64_t rank, const float* adapter_scales,
+                             const int32_t* adapter_ids, float* logits, int64_t ld_logits,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * FP8 projection.  The pages' measured deployment is an FP8 checkpoint and
  * their patch cluster unpacks e4m3 bytes (sections "The 1.5% estimate, and
  * the measurement next to it" and "The patch cluster"); they state no

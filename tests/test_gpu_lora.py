@@ -1,0 +1,240 @@
+"""The adapter projection on the GPU against the float64 oracle.
+
+Tolerance.  An fp32 sum of n products of random signs and size s is off by
+about 0.41 u n s (u = 2^-24: a rounding of u / sqrt(3) at each of the n partial
+sums, which grow as sqrt(i) s); six times that is allowed, for the base sum
+(n = H), for u (n = H, carried through B) and for the sum over the rank.  The
+three bf16 parts of u keep 24 bits, and the sum and the result are rounded
+once more.  A u that were rounded to bf16 would be off by 2^-9 of the
+adapter's share, hundreds of times as much.
+"""
+import numpy as np
+import pytest
+
+from oracle import losses as ref
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+def say(*a):
+    print(*a, flush=True)
+
+
+def _dev():
+    import torch
+
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    return torch.device("cuda:0")
+
+
+def make(rows, hidden, vocab, rank, n, seed, pad=0):
+    """Device tensors (rows `pad` * 8 elements apart from dense) and scales."""
+    import torch
+
+    g = torch.Generator(device="cpu")
+    g.manual_seed(seed)
+
+    def bf(*shape, std):
+        wide = torch.zeros(*shape[:-1], shape[-1] + 8 * pad, dtype=torch.bfloat16)
+        wide[..., :shape[-1]] = (torch.randn(*shape, generator=g) * std).to(torch.bfloat16)
+        return wide.to(_dev())[..., :shape[-1]]
+
+    return (bf(rows, hidden, std=1.0), bf(vocab, hidden, std=0.05),
+            bf(n, rank, hidden, std=hidden ** -0.5), bf(n, vocab, rank, std=0.2),
+            (torch.rand(n, generator=g) * 3 + 0.1).to(_dev()))
+
+
+def f64(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def check(got, x, w, a, b, ids, scales):
+    n, rank = a.shape[:2]
+    xs, ws, as_, bs = f64(x), f64(w), f64(a), f64(b)
+    sc = np.ones(n) if scales is None else f64(scales)
+    want = ref.lora_logits(xs, ws, as_, bs, ids, sc)
+    hidden = xs.shape[1]
+    rms = lambda m: np.sqrt((m * m).mean())  # noqa: E731
+    six = 6 * 0.41 * U
+    row = np.sqrt((xs * xs).mean(1))
+    tol = (six * hidden * row * rms(ws))[:, None] + 2 * U * np.abs(want)
+    live = (ids >= 0) & (ids < n)
+    u = np.zeros((len(ids), rank))
+    for r in np.flatnonzero(live):
+        u[r] = sc[ids[r]] * (as_[ids[r]] @ xs[r])
+    du = np.where(live, six * hidden * row * rms(as_) * sc[np.clip(ids, 0, n - 1)], 0)
+    # carried through B at random signs, and the sum over the rank
+    size = rms(bs)
+    tol += (6 * du * size * np.sqrt(rank) + six * (rank + 4) * np.abs(u).max(1) * size
+            + 8 * U * np.abs(u).max(1) * np.abs(bs).max() * np.sqrt(rank))[:, None]
+    got = got.double().cpu().numpy()
+    both = np.isnan(got) & np.isnan(want)
+    off = np.where(both, 0, np.abs(got - want) - tol)
+    off = np.where(np.isnan(off), np.inf, off)
+    i = np.unravel_index(off.argmax(), off.shape)
+    assert off[i] <= 0, (i, got[i], want[i], tol[i] if tol.shape == off.shape else tol[i[0]])
+
+
+def some_ids(kind, rows, n, seed):
+    g = np.random.default_rng(seed)
+    ids = {"random": lambda: g.integers(-1, n, rows), "none": lambda: np.full(rows, -1),
+           "one": lambda: np.full(rows, n - 1), "sorted": lambda: np.sort(g.integers(-1, n, rows)),
+           "bad": lambda: g.choice([-1, 0, n - 1, n, -2, 2 ** 31 - 1, -2 ** 31], rows),
+           "runs": lambda: np.repeat(g.integers(-1, n, rows // 5 + 1), 5)[:rows]}[kind]()
+    return ids.astype(np.int64)
+
+
+CASES = [
+    # rows, hidden, vocab, rank, adapters, pad, ids
+    (1, 64, 1, 8, 1, 0, "one"), (1, 256, 1000, 16, 4, 0, "random"), (3, 128, 7, 8, 2, 1, "random"),
+    (33, 256, 130, 24, 5, 0, "random"), (64, 4096, 515, 16, 32, 0, "random"),
+    (64, 64, 300, 256, 3, 0, "runs"), (65, 192, 129, 64, 70, 0, "random"),
+    (128, 512, 257, 40, 9, 1, "sorted"), (128, 64, 64, 8, 128, 0, "random"),
+    (200, 320, 511, 16, 3, 0, "none"), (300, 256, 260, 32, 300, 0, "random"),
+    (320, 128, 400, 16, 1, 0, "one"), (640, 256, 700, 32, 16, 0, "runs"),
+    (641, 128, 100, 48, 7, 0, "random"), (50, 128, 90, 16, 4, 0, "bad"),
+    (700, 64, 33, 8, 6, 0, "bad"),
+    # hidden sizes that are no multiple of 64
+    (5, 72, 33, 8, 2, 0, "random"), (70, 200, 300, 24, 9, 1, "runs"), (260, 136, 140, 64, 5, 0, "bad"),
+]
+
+
+@pytest.mark.parametrize("rows,hidden,vocab,rank,n,pad,kind", CASES)
+def test_lora_logits(rows, hidden, vocab, rank, n, pad, kind):
+    import torch
+
+    import top_sampling_amd as ts
+
+    say("lora", rows, hidden, vocab, rank, n, pad, kind)
+    x, w, a, b, scales = make(rows, hidden, vocab, rank, n, rows + hidden, pad)
+    ids = some_ids(kind, rows, n, 7)
+    dev_ids = torch.from_numpy(ids.astype(np.int32)).to(_dev())
+    wide = torch.full((rows, vocab + 3), 7.0, device=_dev())
+    got = ts.lmhead_logits_local_lora(x, w, a, b, dev_ids, scales, out=wide[:, :vocab])
+    torch.cuda.synchronize()
+    assert (wide[:, vocab:] == 7.0).all()
+    check(got, x, w, a, b, ids, scales)
+    dense = ts.lmhead_logits_local_lora(x, w, a, b, dev_ids, scales)
+    same = ts.lmhead_logits_local_lora(x, w, a, b, dev_ids, scales)
+    torch.cuda.synchronize()
+    nan = torch.isnan(dense)
+    assert torch.equal(torch.isnan(got), nan) and torch.equal(dense[~nan], same[~nan])
+    assert torch.equal(dense[~nan], got[~nan])
+    # rows without an adapter are exactly the shared projection
+    base = ts.lmhead_logits_local(x, w)
+    none = torch.from_numpy(ids == -1).to(_dev())
+    assert torch.equal(dense[none], base[none])
+    if n > 1:
+        check(ts.lmhead_logits_local_lora(x, w, a, b, dev_ids), x, w, a, b, ids, None)
+
+
+def test_vocabulary_slices_and_strides():
+    """A rank's vocabulary slice of the lm_head and of every adapter's B, in
+    place, written into its columns of a wider buffer."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    rows, hidden, vocab, rank, n = 70, 256, 900, 16, 6
+    x, w, a, b, scales = make(rows, hidden, vocab, rank, n, 1)
+    ids = torch.from_numpy(some_ids("random", rows, n, 2).astype(np.int32)).to(_dev())
+    whole = ts.lmhead_logits_local_lora(x, w, a, b, ids, scales)
+    parts = torch.empty_like(whole)
+    for lo, hi in ((0, 300), (300, 301), (301, 900)):
+        ts.lmhead_logits_local_lora(x, w[lo:hi], a, b[:, lo:hi], ids, scales,
+                                    out=parts[:, lo:hi])
+    torch.cuda.synchronize()
+    assert torch.equal(whole, parts)
+
+
+@pytest.mark.parametrize("hidden", [256, 264])
+def test_rows_do_not_reach_each_other(hidden):
+    """A row's logits are bit for bit those of its own call, whatever stands
+    beside it: other adapters, in any order, with infinities and NaN."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    rows, vocab, rank, n = 90, 333, 24, 5
+    x, w, a, b, scales = make(rows, hidden, vocab, rank, n, 3)
+    ids = torch.from_numpy(some_ids("random", rows, n, 4).astype(np.int32)).to(_dev())
+    clean = ts.lmhead_logits_local_lora(x, w, a, b, ids, scales)
+    order = torch.randperm(rows, device=_dev())
+    mixed = ts.lmhead_logits_local_lora(x[order].contiguous(), w, a, b, ids[order].contiguous(),
+                                        scales)
+    assert torch.equal(mixed, clean[order])
+    b[1] = float("nan")
+    a[2, 3] = float("inf")
+    x[11] = float("nan")
+    got = ts.lmhead_logits_local_lora(x, w, a, b, ids, scales)
+    torch.cuda.synchronize()
+    keep = (ids != 1) & (ids != 2)
+    keep[11] = False
+    assert torch.equal(got[keep], clean[keep])
+    assert torch.isnan(got[ids == 1]).all() and torch.isnan(got[11]).all()
+
+
+def test_streams_and_graph():
+    import torch
+
+    import top_sampling_amd as ts
+
+    rows, hidden, vocab, rank, n = 20, 256, 4099, 16, 4
+    x, w, a, b, scales = make(rows, hidden, vocab, rank, n, 5)
+    ids = torch.from_numpy(some_ids("random", rows, n, 6).astype(np.int32)).to(_dev())
+    plain = ts.lmhead_logits_local_lora(x, w, a, b, ids, scales)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = ts.lmhead_logits_local_lora(x, w, a, b, ids, scales, stream=side)
+    side.synchronize()
+    assert torch.equal(plain, got)
+    static_x, static_ids = x.clone(), ids.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = ts.lmhead_logits_local_lora(static_x, w, a, b, static_ids, scales)
+    for i in range(4):
+        static_x.copy_(x * (1 + i))
+        static_ids.copy_((ids + i) % n)
+        graph.replay()
+        want = ts.lmhead_logits_local_lora(static_x, w, a, b, static_ids, scales)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), i
+
+
+def test_adapter_offsets_pass_32_bits():
+    """Adapters 2^31 elements and more apart in one buffer (9 GB)."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    rows, hidden, vocab, rank, n = 9, 64, 200, 16, 3
+    x, w, a, b, scales = make(rows, hidden, vocab, rank, n, 8)
+    ids = torch.tensor([0, 1, 2, 2, -1, 1, 0, 2, 1], dtype=torch.int32, device=_dev())
+    want = ts.lmhead_logits_local_lora(x, w, a, b, ids, scales)
+    step = (1 << 31) + 64
+    buf = torch.empty(2 * step + vocab * rank, dtype=torch.bfloat16, device=_dev())
+    far = buf.as_strided((n, vocab, rank), (step, rank, 1))
+    far.copy_(b)
+    got = ts.lmhead_logits_local_lora(x, w, a, far, ids, scales)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_sampler_reports_a_bad_adapter():
+    import torch
+
+    import top_sampling_amd as ts
+    import workloads
+
+    rows, hidden, vocab = 6, 128, 4096
+    x, w, a, b, scales = make(rows, hidden, vocab, 16, 2, 9)
+    ids = torch.tensor([0, 5, -1, 1, -7, 0], dtype=torch.int32, device=_dev())
+    logits = ts.lmhead_logits_local_lora(x, w, a, b, ids, scales)
+    params = np.zeros(rows, dtype=workloads.PARAMS_DTYPE)
+    params["temperature"], params["top_p"] = 1.0, 1.0
+    out = ts.sampler_sample(logits, ts.params_to_device(params, _dev()))
+    torch.cuda.synchronize()
+    assert out.row_status.tolist() == [0, ts.TS_ROW_BAD_LOGITS, 0, 0, ts.TS_ROW_BAD_LOGITS, 0]

@@ -7,6 +7,8 @@ not built (``python top_sampling_amd/build.py``); there is no fallback.
 
 Calls mirror the C entry points:
   lmhead_logits_local            local vocabulary projection, bf16 -> fp32
+  lmhead_logits_local_lora       the same, each row with its own low-rank
+                                 adapter
   quantize_rows_e4m3             per-row FP8 (E4M3) quantization of bf16 rows
   lmhead_logits_local_e4m3       the same projection from FP8 codes and scales
   sampler_assemble_vocab_slices  stitch received vocabulary slices
@@ -46,6 +48,7 @@ TS_NOALLOC_SCRATCH_BYTES = 96 << 20
 PARAMS_BYTES = 24
 TS_F32, TS_BF16 = 0, 1
 TS_PREFERENCE_MEAN = 1
+TS_MAX_LORA_RANK = 256
 
 # (name, restype, argtypes) of every symbol the headers declare
 # (include/top_sampling.h and the measurement aids of top_sampling_measure.h).
@@ -53,6 +56,10 @@ _VP, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c
 _F64 = ctypes.c_double
 SYMBOLS = {
     "lmhead_logits_local": (ctypes.c_int, [_VP, _I64, _I64, _I64, _VP, _I64, _I64, _VP, _I64, _VP]),
+    "lmhead_lora_workspace_bytes": (_SZ, [_I64, _I64]),
+    "lmhead_logits_local_lora": (ctypes.c_int, [_VP, _I64, _I64, _I64, _VP, _I64, _I64, _VP, _I64,
+                                                _I64, _VP, _I64, _I64, _I64, _I64, _VP, _VP, _VP,
+                                                _I64, _VP, _SZ, _VP]),
     "quantize_rows_e4m3": (ctypes.c_int, [_VP, _I64, _I64, _I64, _VP, _I64, _VP, _VP]),
     "lmhead_logits_local_e4m3": (ctypes.c_int, [_VP, _VP, _I64, _I64, _I64, _VP, _VP, _I64, _I64,
                                                 _VP, _I64, _VP]),
@@ -650,6 +657,64 @@ def preference_loss(logits, token_ids, seq_offsets, ref_logprobs=None, pair_weig
             ctypes.addressof(params), _ptr(ref_logprobs), _ptr(pair_weights), _ptr(grad_loss),
             _ptr(out.loss), _ptr(out.pair_losses), _ptr(out.rewards), _ptr(out.logprobs),
             _ptr(out.row_status), _ptr(grad_logits), ldg, _ptr(workspace), workspace.numel(), s))
+    return out
+
+
+# ------------------------------------------------------ projection with adapters
+def lmhead_lora_workspace_bytes(rows: int, rank: int) -> int:
+    return int(lib.lmhead_lora_workspace_bytes(rows, rank))
+
+
+def lmhead_logits_local_lora(hidden, lm_head, lora_a, lora_b, adapter_ids, adapter_scales=None,
+                             out=None, workspace=None, stream=None):
+    """``lmhead_logits_local`` with a low-rank adapter per row: fp32 ``[rows,
+    V_local]`` = hidden @ lm_head^T + scale (hidden @ A^T) @ B^T with the
+    row's own ``A = lora_a[id]``, ``B = lora_b[id]`` (bf16 ``[n, rank, H]`` and
+    ``[n, V_local, rank]``, inner stride 1) and ``adapter_scales[id]`` (fp32,
+    None for 1); id -1 has no adapter."""
+    torch = _torch()
+    if hidden.dim() != 2 or lm_head.dim() != 2 or lora_a.dim() != 3 or lora_b.dim() != 3:
+        raise ValueError("hidden and lm_head must be 2-D, lora_a and lora_b 3-D")
+    rows, h = hidden.shape
+    vocab = lm_head.shape[0]
+    n, rank = lora_a.shape[:2]
+    if lm_head.shape[1] != h or lora_a.shape[2] != h or tuple(lora_b.shape) != (n, vocab, rank):
+        raise ValueError("sizes do not fit: hidden [rows, H], lm_head [V, H], lora_a [n, rank, H], "
+                         "lora_b [n, V, rank]")
+    dev = hidden.device
+    for t, name in ((hidden, "hidden"), (lm_head, "lm_head"), (lora_a, "lora_a"),
+                    (lora_b, "lora_b")):
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be bfloat16")
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name} must have unit inner stride")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, hidden on {dev}")
+    _check_vector(adapter_ids, "adapter_ids", rows, dev, torch.int32)
+    _check_vector(adapter_scales, "adapter_scales", n, dev)
+
+    def row_stride(t, width):
+        return int(t.stride(-2)) if t.shape[-2] > 1 else width
+
+    def adapter_stride(t):
+        return int(t.stride(0)) if n > 1 else 0
+
+    with _OnDevice(dev, stream) as s:
+        if out is None:
+            out = torch.empty(rows, vocab, dtype=torch.float32, device=dev)
+        if out.shape != (rows, vocab) or out.dtype != torch.float32 or out.device != dev or \
+                (vocab > 1 and out.stride(1) != 1):
+            raise ValueError("out must be fp32 [rows, V_local] with unit column stride")
+        if workspace is None:
+            workspace = torch.empty(max(256, lmhead_lora_workspace_bytes(rows, rank)),
+                                    dtype=torch.uint8, device=dev)
+        _check_workspace(workspace, dev)
+        _check(lib.lmhead_logits_local_lora(
+            _ptr(hidden), rows, h, row_stride(hidden, h), _ptr(lm_head), vocab,
+            row_stride(lm_head, h), _ptr(lora_a), adapter_stride(lora_a), row_stride(lora_a, h),
+            _ptr(lora_b), adapter_stride(lora_b), row_stride(lora_b, rank), n, rank,
+            _ptr(adapter_scales), _ptr(adapter_ids), _ptr(out), row_stride(out, vocab),
+            _ptr(workspace), workspace.numel(), s))
     return out
 
 
