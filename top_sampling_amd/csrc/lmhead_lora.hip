@@ -85,6 +85,340 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraArgs p, Dow
   }
 }
 
+// ---------------------------------------------------------------------------
+// The projection with the up step inside (hidden size a multiple of 64).
+//
+// The main loop is lmhead_logits_local's: v_mfma_f32_32x32x16_bf16, 64-wide K
+// steps through two LDS stages filled by direct loads, the XOR swizzle of the
+// 16-byte chunks, row tiles of an lm_head strip back to back on one XCD.  Rows
+// are taken in the order of their adapters, through a row list for the loads
+// and the stores, so a tile holds few adapters and each in one run of rows.
+//
+// After the last K step the same two stages carry on with "panels" of B: for
+// the tile's adapters one after the other, the strip's BN rows of B_a, 64
+// values wide (four adapters of rank 16, or a quarter of one of rank 256).
+// The A operand is u, straight from global memory (a few KB per tile), its
+// three bf16 parts against the same B fragment.  A 32-row block only takes the
+// adapters that its rows have.  The product of one 16-wide slice goes into an
+// accumulator of its own and is added to the rows of its adapter alone: a row
+// never sees another adapter's weights (0 x inf is not 0), and its sum does
+// not depend on the rows beside it.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef f32x4 f32x4u __attribute__((aligned(4)));
+
+constexpr int kBK = 64;  // K per LDS stage
+constexpr int kXcds = 8;
+constexpr int kStoreStride = 36;  // floats of a row of the store scratch
+constexpr int kStoreFloats = 32 * kStoreStride;
+
+template <int LOADS, int FIRST, int NW, int AUX>
+__device__ __forceinline__ void load_stage(const uint16_t* const* src, uint8_t* stage, int wave,
+                                           int k0) {
+#pragma unroll
+  for (int q = 0; q < FIRST; ++q)
+    __builtin_amdgcn_global_load_lds(src[q] + k0, stage + (wave + NW * q) * 1024, 16, 0, 0);
+#pragma unroll
+  for (int q = FIRST; q < LOADS; ++q)
+    __builtin_amdgcn_global_load_lds(src[q] + k0, stage + (wave + NW * q) * 1024, 16, 0, AUX);
+}
+
+template <int LOADS, int FIRST, int NW>
+__device__ __forceinline__ void load_panel(const uint16_t* const* src, uint8_t* stage, int wave) {
+#pragma unroll
+  for (int q = FIRST; q < LOADS; ++q)
+    __builtin_amdgcn_global_load_lds(src[q], stage + (wave + NW * q) * 1024, 16, 0, 0);
+}
+
+// The adapters of a tile's rows, in the rows' order.
+template <int BM>
+struct TileRuns {
+  int row[BM];      // the row at each place, ~row for a bad adapter
+  int run[BM];      // the run that the place belongs to, -1 for none
+  int adapter[BM];  // the runs' adapters
+  int runs;
+};
+
+template <int BM, int BN, int WAVES_M, int WAVES_N, int AUX>
+__global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void lora_gemm_kernel(
+    LoraArgs p, DownRows d, int tiles_m, int tiles_total, int tiles_per_xcd) {
+  constexpr int NW = WAVES_M * WAVES_N;
+  constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
+  constexpr int TM = WM / 32, TN = WN / 32;
+  constexpr int ROWS = BM + BN;
+  constexpr int STAGE = ROWS * 128;
+  constexpr int LOADS = ROWS / 8 / NW;
+  constexpr int A_LOADS = BM / 8 / NW;
+  static_assert(ROWS / 8 % NW == 0 && BM / 8 % NW == 0, "blocks split evenly over the waves");
+  static_assert(WM % 32 == 0 && WN % 32 == 0, "wave tile of whole 32x32 blocks");
+  static_assert(NW * kStoreFloats * 4 <= 2 * STAGE, "store scratch fits the stages");
+  static_assert(BM <= 64 * NW, "a thread for every row of the tile");
+
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE];
+  __shared__ TileRuns<BM> tr;
+  __shared__ int wave_runs[NW];
+
+  const int bid = blockIdx.x;
+  const int tile = (bid % kXcds) * tiles_per_xcd + bid / kXcds;
+  if (tile >= tiles_total) return;
+  const int m0 = tile % tiles_m * BM, n0 = tile / tiles_m * BN;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm0 = (wave / WAVES_N) * WM, wn0 = (wave % WAVES_N) * WN;
+  const int M = p.rows, N = p.vocab;
+
+  // Source of this lane's 16 bytes in each of the wave's blocks: chunk c of
+  // LDS row r sits at c ^ ((r >> 1) & 7).
+  const int chunk_row = lane >> 3;
+  const uint16_t* src[LOADS];
+#pragma unroll
+  for (int q = 0; q < LOADS; ++q) {
+    const int r = 8 * (wave + NW * q) + chunk_row;
+    const int c = (lane & 7) ^ ((r >> 1) & 7);
+    if (q < A_LOADS)
+      src[q] = p.hidden + static_cast<int64_t>(d.row[min(m0 + r, M - 1)]) * p.ld_hidden + c * 8;
+    else
+      src[q] = p.lm_head + static_cast<int64_t>(min(n0 + r - BM, N - 1)) * p.ld_lm_head + c * 8;
+  }
+  load_stage<LOADS, A_LOADS, NW, AUX>(src, lds, wave, 0);
+
+  // The tile's runs of adapters.
+  {
+    const bool in = tid < BM && m0 + tid < M;
+    const int id = in ? d.id[m0 + tid] : kNoAdapter;
+    const int last = in && tid > 0 ? d.id[m0 + tid - 1] : kNoAdapter;
+    const bool starts = id >= 0 && (tid == 0 || id != last);
+    const uint64_t mask = __ballot(starts);
+    if (lane == 0) wave_runs[wave] = __popcll(mask);
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < NW; ++w) {
+      before += w < wave ? wave_runs[w] : 0;
+      all += wave_runs[w];
+    }
+    const int run = before + __popcll(mask & ((2ull << lane) - 1)) - 1;
+    if (tid < BM) {
+      const int row = in ? d.row[m0 + tid] : 0;
+      tr.row[tid] = id == kBadAdapter ? ~row : row;
+      tr.run[tid] = id >= 0 ? run : -1;
+      if (starts) tr.adapter[run] = id;
+    }
+    if (tid == 0) tr.runs = all;
+  }
+
+  f32x16 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+  const int frow = lane & 31, fhalf = lane >> 5;
+  int aoff[TM], boff[TN], aswz[TM], bswz[TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int r = wm0 + i * 32 + frow;
+    aoff[i] = r * 128;
+    aswz[i] = (r >> 1) & 7;
+  }
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    const int r = BM + wn0 + j * 32 + frow;
+    boff[j] = r * 128;
+    bswz[j] = (r >> 1) & 7;
+  }
+  auto frags = [&](int buf, int kk, bf16x8 (&af)[TM], bf16x8 (&bfr)[TN]) {
+    const int chunk = kk * 2 + fhalf;
+    const uint8_t* base = lds + buf * STAGE;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+      af[i] = *reinterpret_cast<const bf16x8*>(base + aoff[i] + ((chunk ^ aswz[i]) << 4));
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+      bfr[j] = *reinterpret_cast<const bf16x8*>(base + boff[j] + ((chunk ^ bswz[j]) << 4));
+  };
+
+  constexpr int kPerRead = (TM * TN) / (TM + TN) > 0 ? (TM * TN) / (TM + TN) : 1;
+  const int ksteps = p.hidden_dim / kBK;
+  for (int ks = 0; ks < ksteps; ++ks) {
+    const int cur = ks & 1;
+    __builtin_amdgcn_s_waitcnt(0);  // this step's loads have landed in LDS
+    __syncthreads();                // ... for every wave; the other buffer is free
+    if (ks + 1 < ksteps)
+      load_stage<LOADS, A_LOADS, NW, AUX>(src, lds + (cur ^ 1) * STAGE, wave, (ks + 1) * kBK);
+    bf16x8 af[2][TM], bfr[2][TN];
+    frags(cur, 0, af[0], bfr[0]);
+#pragma unroll
+    for (int kk = 0; kk < kBK / 16; ++kk) {
+      if (kk + 1 < kBK / 16) frags(cur, kk + 1, af[(kk + 1) & 1], bfr[(kk + 1) & 1]);
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[kk & 1][i], bfr[kk & 1][j],
+                                                               acc[i][j], 0, 0, 0);
+    }
+    // This step's first fragments, then per 16-wide slice its MFMAs with the
+    // next slice's fragment reads spread between them.
+    __builtin_amdgcn_sched_group_barrier(0x100, TM + TN, 0);
+#pragma unroll
+    for (int kk = 0; kk < kBK / 16; ++kk) {
+      if (kk + 1 < kBK / 16) {
+#pragma unroll
+        for (int t = 0; t < TM + TN; ++t) {
+          __builtin_amdgcn_sched_group_barrier(0x008, kPerRead, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        if (TM * TN > kPerRead * (TM + TN))
+          __builtin_amdgcn_sched_group_barrier(0x008, TM * TN - kPerRead * (TM + TN), 0);
+      } else {
+        __builtin_amdgcn_sched_group_barrier(0x008, TM * TN, 0);
+      }
+    }
+  }
+
+  // ---- the adapters
+  const int rp = padded_rank(p.rank);
+  const int runs = tr.runs;
+  const int width = runs * rp;                  // of all the tile's adapters side by side
+  const int panels = (width + kBK - 1) / kBK;
+  // Sources of panel `pn`: the B_a values that each lane brings.  Past the
+  // rank (or the last adapter) any valid address: those are not used.
+  auto panel_sources = [&](int pn) {
+#pragma unroll
+    for (int q = A_LOADS; q < LOADS; ++q) {
+      const int r = 8 * (wave + NW * q) + chunk_row;
+      const int c = (lane & 7) ^ ((r >> 1) & 7);
+      const int k = pn * kBK + c * 8;
+      const int run = min(k / rp, runs - 1);
+      int kin = k - run * rp;
+      if (kin >= p.rank) kin = 0;
+      src[q] = p.b + static_cast<int64_t>(tr.adapter[run]) * p.stride_b +
+               static_cast<int64_t>(min(n0 + r - BM, N - 1)) * p.ld_b + kin;
+    }
+  };
+  // First and last run of each of the wave's row blocks (none: last < first).
+  int first[TM], last[TM];
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int run = tr.run[wm0 + i * 32 + frow];
+    const uint64_t has = __ballot(run >= 0 && lane < 32);
+    first[i] = has ? __shfl(run, __ffsll(static_cast<unsigned long long>(has)) - 1) : 0;
+    last[i] = has ? __shfl(run, 63 - __clzll(static_cast<long long>(has))) : -1;
+  }
+  const int buf0 = ksteps & 1;
+  if (panels > 0) {
+    panel_sources(0);
+    load_panel<LOADS, A_LOADS, NW>(src, lds + buf0 * STAGE, wave);
+  }
+  for (int pn = 0; pn < panels; ++pn) {
+    const int cur = (buf0 + pn) & 1;
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (pn + 1 < panels) {
+      panel_sources(pn + 1);
+      load_panel<LOADS, A_LOADS, NW>(src, lds + (cur ^ 1) * STAGE, wave);
+    }
+#pragma unroll
+    for (int kk = 0; kk < kBK / 16; ++kk) {
+      const int k = pn * kBK + kk * 16;
+      const int run = k / rp, kin = k - run * rp;
+      if (run >= runs) break;
+      bool any = false;
+#pragma unroll
+      for (int i = 0; i < TM; ++i) any = any || (run >= first[i] && run <= last[i]);
+      if (!any) continue;
+      bf16x8 bfr[TN];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        bfr[j] = *reinterpret_cast<const bf16x8*>(lds + cur * STAGE + boff[j] +
+                                                  (((kk * 2 + fhalf) ^ bswz[j]) << 4));
+        if (kin + fhalf * 8 >= p.rank)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) bfr[j][e] = static_cast<__bf16>(0.0f);
+      }
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        if (run < first[i] || run > last[i]) continue;
+        const int place = min(m0 + wm0 + i * 32 + frow, M - 1);
+        const __bf16* u = d.u + static_cast<int64_t>(place) * kParts * rp + kin + fhalf * 8;
+        bf16x8 uf[kParts];
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) uf[q] = *reinterpret_cast<const bf16x8*>(u + q * rp);
+        bool mine[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          mine[e] = tr.run[wm0 + i * 32 + 8 * (e >> 2) + 4 * fhalf + (e & 3)] == run;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          f32x16 part;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) part[e] = 0.0f;
+#pragma unroll
+          for (int q = kParts - 1; q >= 0; --q)
+            part = __builtin_amdgcn_mfma_f32_32x32x16_bf16(uf[q], bfr[j], part, 0, 0, 0);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[i][j][e] = mine[e] ? acc[i][j][e] + part[e] : acc[i][j][e];
+        }
+      }
+    }
+  }
+
+  // ---- the logits, a row segment at a time through a scratch of the wave's
+  __syncthreads();  // every wave is done reading the stages
+  float* scr = reinterpret_cast<float*>(lds) + wave * kStoreFloats;
+  const int c0 = (lane & 7) * 4;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        scr[(8 * (e >> 2) + 4 * fhalf + (e & 3)) * kStoreStride + frow] = acc[i][j][e];
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      const int col = n0 + wn0 + j * 32 + c0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int rr = (lane >> 3) + 8 * q;
+        const int at = wm0 + i * 32 + rr;
+        f32x4 v = *reinterpret_cast<const f32x4*>(scr + rr * kStoreStride + c0);
+        if (m0 + at >= M || col >= N) continue;
+        int row = tr.row[at];
+        if (row < 0) {
+          row = ~row;
+#pragma unroll
+          for (int t = 0; t < 4; ++t) v[t] = NAN;
+        }
+        float* dst = p.logits + static_cast<int64_t>(row) * p.ld_logits + col;
+        if (col + 3 < N) {
+          *reinterpret_cast<f32x4u*>(dst) = v;
+        } else {
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+            if (col + t < N) dst[t] = v[t];
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    }
+  }
+}
+
+template <int BM, int BN, int WAVES_M, int WAVES_N, int AUX>
+hipError_t launch_fused(const LoraArgs& p, const DownRows& d, hipStream_t stream) {
+  const int tiles_m = (p.rows + BM - 1) / BM;
+  const int tiles_n = (p.vocab + BN - 1) / BN;
+  const int total = tiles_m * tiles_n;
+  const int per_xcd = (total + kXcds - 1) / kXcds;
+  hipLaunchKernelGGL((lora_gemm_kernel<BM, BN, WAVES_M, WAVES_N, AUX>), dim3(per_xcd * kXcds),
+                     dim3(64 * WAVES_M * WAVES_N), 0, stream, p, d, tiles_m, total, per_xcd);
+  return hipGetLastError();
+}
+
+// ------------------------------------------- other hidden sizes: a second pass
 constexpr int kUpCols = 256;
 
 // logits += B_a u, one workgroup per row and kUpCols columns.
@@ -147,6 +481,16 @@ hipError_t launch_lmhead_lora(const LoraArgs& p, void* ws, hipStream_t stream) {
                      dim3(kDownThreads), 0, stream, p, d);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  if (p.hidden_dim % kBK == 0) {
+    // The tile that pads the rows least, as for the shared projection.  Up to
+    // 128 rows one row tile reads the lm_head once: past the caches.
+    const int64_t pad256 = (p.rows + int64_t{255}) / 256 * 256;
+    const int64_t pad320 = (p.rows + int64_t{319}) / 320 * 320;
+    if (p.rows <= 64) return launch_fused<64, 128, 1, 4, 2>(p, d, stream);
+    if (p.rows <= 128) return launch_fused<128, 128, 2, 4, 2>(p, d, stream);
+    if (pad320 < pad256) return launch_fused<320, 256, 2, 4, 0>(p, d, stream);
+    return launch_fused<256, 256, 2, 4, 0>(p, d, stream);
+  }
   e = launch_lmhead_gemm(p.hidden, p.ld_hidden, p.lm_head, p.ld_lm_head, p.logits, p.ld_logits,
                          p.rows, p.vocab, p.hidden_dim, stream);
   if (e != hipSuccess) return e;
