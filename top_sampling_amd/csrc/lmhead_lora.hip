@@ -34,51 +34,73 @@ __device__ __forceinline__ int adapter_of(int id, int n_adapters) {
   return id == kNoAdapter ? kNoAdapter : kBadAdapter;
 }
 
-// One workgroup per row.
+// One workgroup per row and kDownRanks ranks, four ranks a wave; kDownStep
+// 512-wide pieces of the row are in flight at a time.
+constexpr int kDownRanks = 16;
+constexpr int kDownStep = 2;
+
 __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraArgs p, DownRows out) {
+  constexpr int kPerWave = kDownRanks / (kDownThreads / 64);
   __shared__ int before_wave[kDownThreads / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int rp = padded_rank(p.rank);
+  const int k0 = blockIdx.y * kDownRanks + wave * kPerWave;
   for (int r = blockIdx.x; r < p.rows; r += gridDim.x) {
     const int id = adapter_of(p.ids[r], p.n_adapters);
+    float sum[kPerWave] = {};
+    if (id >= 0 && k0 < p.rank) {  // the rank is a multiple of 8, so of kPerWave
+      const uint16_t* x = p.hidden + static_cast<int64_t>(r) * p.ld_hidden;
+      const uint16_t* a = p.a + static_cast<int64_t>(id) * p.stride_a +
+                          static_cast<int64_t>(k0) * p.ld_a;
+      for (int h0 = lane * 8; h0 < p.hidden_dim; h0 += kDownStep * 512) {
+        bf16x8 xv[kDownStep], av[kDownStep][kPerWave];
+#pragma unroll
+        for (int q = 0; q < kDownStep; ++q) {
+          const int h = min(h0 + q * 512, p.hidden_dim - 8);
+          xv[q] = *reinterpret_cast<const bf16x8*>(x + h);
+#pragma unroll
+          for (int k = 0; k < kPerWave; ++k)
+            av[q][k] = *reinterpret_cast<const bf16x8*>(a + k * p.ld_a + h);
+        }
+#pragma unroll
+        for (int q = 0; q < kDownStep; ++q) {
+          if (h0 + q * 512 >= p.hidden_dim) continue;
+#pragma unroll
+          for (int k = 0; k < kPerWave; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              sum[k] = fmaf(static_cast<float>(xv[q][e]), static_cast<float>(av[q][k][e]), sum[k]);
+        }
+      }
+    }
     int before = 0;
     for (int i = tid; i < p.rows; i += kDownThreads) {
       const int other = adapter_of(p.ids[i], p.n_adapters);
       before += other < id || (other == id && i < r);
     }
-    for (int d = 32; d > 0; d >>= 1) before += __shfl_xor(before, d, 64);
+    for (int d = 32; d > 0; d >>= 1) {
+      before += __shfl_xor(before, d, 64);
+#pragma unroll
+      for (int k = 0; k < kPerWave; ++k) sum[k] += __shfl_xor(sum[k], d, 64);
+    }
     if (lane == 0) before_wave[wave] = before;
     __syncthreads();
     int place = 0;
     for (int w = 0; w < kDownThreads / 64; ++w) place += before_wave[w];
-    if (tid == 0) {
+    if (tid == 0 && blockIdx.y == 0) {
       out.row[place] = r;
       out.id[place] = id;
     }
-    const int rp = padded_rank(p.rank);
+    const float scale = id >= 0 && p.scales ? p.scales[id] : 1.0f;
     __bf16* u = out.u + static_cast<int64_t>(place) * kParts * rp;
-    const uint16_t* x = p.hidden + static_cast<int64_t>(r) * p.ld_hidden;
-    for (int k = wave; k < rp; k += kDownThreads / 64) {
-      float sum = 0.0f;
-      if (id >= 0 && k < p.rank) {
-        const uint16_t* a = p.a + static_cast<int64_t>(id) * p.stride_a + static_cast<int64_t>(k) * p.ld_a;
-        for (int h = lane * 8; h < p.hidden_dim; h += 64 * 8) {
-          const bf16x8 xv = *reinterpret_cast<const bf16x8*>(x + h);
-          const bf16x8 av = *reinterpret_cast<const bf16x8*>(a + h);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            sum = fmaf(static_cast<float>(xv[e]), static_cast<float>(av[e]), sum);
-        }
-        for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, 64);
-        if (p.scales) sum *= p.scales[id];
-      }
-      if (lane == 0) {
-        float rest = sum;
+    for (int k = 0; k < kPerWave; ++k) {
+      float rest = sum[k] * scale;
 #pragma unroll
-        for (int q = 0; q < kParts; ++q) {
-          const __bf16 part = static_cast<__bf16>(rest);
-          u[q * rp + k] = part;
-          rest -= static_cast<float>(part);
-        }
+      for (int q = 0; q < kParts; ++q) {
+        const __bf16 part = static_cast<__bf16>(rest);
+        if (lane == k) u[q * rp + k0 + k] = part;
+        rest -= static_cast<float>(part);
       }
     }
     __syncthreads();
@@ -97,9 +119,11 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraArgs p, Dow
 // After the last K step the same two stages carry on with "panels" of B: for
 // the tile's adapters one after the other, the strip's BN rows of B_a, 64
 // values wide (four adapters of rank 16, or a quarter of one of rank 256).
-// The A operand is u, straight from global memory (a few KB per tile), its
-// three bf16 parts against the same B fragment.  A 32-row block only takes the
-// adapters that its rows have.  The product of one 16-wide slice goes into an
+// The A operand is u, which is brought into the stages' other part once per
+// tile (once per 32 ranks), its three bf16 parts against the same B fragment:
+// read from global memory where it is used, u cost one latency per block and
+// slice, 6 us a panel.  A 32-row block only takes the adapters that its rows
+// have.  The product of one 16-wide slice goes into an
 // accumulator of its own and is added to the rows of its adapter alone: a row
 // never sees another adapter's weights (0 x inf is not 0), and its sum does
 // not depend on the rows beside it.
@@ -123,21 +147,53 @@ __device__ __forceinline__ void load_stage(const uint16_t* const* src, uint8_t* 
     __builtin_amdgcn_global_load_lds(src[q] + k0, stage + (wave + NW * q) * 1024, 16, 0, AUX);
 }
 
-template <int LOADS, int FIRST, int NW>
-__device__ __forceinline__ void load_panel(const uint16_t* const* src, uint8_t* stage, int wave) {
-#pragma unroll
-  for (int q = FIRST; q < LOADS; ++q)
-    __builtin_amdgcn_global_load_lds(src[q], stage + (wave + NW * q) * 1024, 16, 0, 0);
-}
-
 // The adapters of a tile's rows, in the rows' order.
-template <int BM>
+template <int BM, int NW>
 struct TileRuns {
   int row[BM];      // the row at each place, ~row for a bad adapter
-  int run[BM];      // the run that the place belongs to, -1 for none
+  int run[BM];      // its adapter, then the run that it belongs to (-1: none)
   int adapter[BM];  // the runs' adapters
-  int runs;
+  int wave_runs[NW];
 };
+
+// Panel `pn` of window `w`: BN rows of the adapters' B, 64 / ww runs side by
+// side, into the lm_head part of a stage.  Past the rank or the last run any
+// valid address: those values are not used.
+template <int BM, int LOADS, int A_LOADS, int NW>
+__device__ __forceinline__ void lora_panel(const LoraArgs& p, const TileRuns<BM, NW>& tr, int runs,
+                                           int rp, int ww, int w, int pn, int n0, int wave,
+                                           int lane, uint8_t* stage) {
+#pragma unroll
+  for (int q = A_LOADS; q < LOADS; ++q) {
+    const int r = 8 * (wave + NW * q) + (lane >> 3);
+    const int k = pn * kBK + ((lane & 7) ^ ((r >> 1) & 7)) * 8;
+    const int run = min(k / ww, runs - 1);
+    int k_in = w * ww + k % ww;
+    if (k_in >= p.rank) k_in = 0;
+    const uint16_t* src = p.b + static_cast<int64_t>(tr.adapter[run]) * p.stride_b +
+                          static_cast<int64_t>(min(n0 + r - BM, p.vocab - 1)) * p.ld_b + k_in;
+    __builtin_amdgcn_global_load_lds(src, stage + (wave + NW * q) * 1024, 16, 0, 0);
+  }
+}
+
+// u of BM / 2 rows from place m0 on, ranks [w ww, (w + 1) ww), into the hidden
+// part of a stage, u_chunks 16-byte chunks a row.
+template <int BM, int NW>
+__device__ __forceinline__ void lora_rows(const DownRows& d, int rp, int ww, int w, int u_chunks,
+                                          int m0, int M, int wave, int lane, uint8_t* stage) {
+  constexpr int kMost = (BM / 2 * (kParts * 4 + 1) + 63) / 64;  // wave loads at ww = 32
+  static_assert(kMost * 1024 <= BM * 128, "u of half the rows fits the hidden part");
+  const int loads = (BM / 2 * u_chunks + 63) / 64;
+  const int per_part = ww / 8;
+  for (int q = wave; q < loads; q += NW) {
+    const int i = q * 64 + lane;
+    const int place = min(m0 + i / u_chunks, M - 1);
+    const int c = min(i % u_chunks, u_chunks - 2);
+    const int k = min(w * ww + c % per_part * 8, rp - 8);
+    const __bf16* src = d.u + (static_cast<int64_t>(place) * kParts + c / per_part) * rp + k;
+    __builtin_amdgcn_global_load_lds(src, stage + q * 1024, 16, 0, 0);
+  }
+}
 
 template <int BM, int BN, int WAVES_M, int WAVES_N, int AUX>
 __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void lora_gemm_kernel(
@@ -154,9 +210,11 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void lora_gemm_kernel(
   static_assert(NW * kStoreFloats * 4 <= 2 * STAGE, "store scratch fits the stages");
   static_assert(BM <= 64 * NW, "a thread for every row of the tile");
 
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE];
-  __shared__ TileRuns<BM> tr;
-  __shared__ int wave_runs[NW];
+  // One array: with several, the compiler makes every fragment read wait for
+  // the direct loads of the next stage.
+  using Runs = TileRuns<BM, NW>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE + sizeof(Runs)];
+  Runs& tr = *reinterpret_cast<Runs*>(lds + 2 * STAGE);
 
   const int bid = blockIdx.x;
   const int tile = (bid % kXcds) * tiles_per_xcd + bid / kXcds;
@@ -179,31 +237,13 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void lora_gemm_kernel(
     else
       src[q] = p.lm_head + static_cast<int64_t>(min(n0 + r - BM, N - 1)) * p.ld_lm_head + c * 8;
   }
-  load_stage<LOADS, A_LOADS, NW, AUX>(src, lds, wave, 0);
-
-  // The tile's runs of adapters.
-  {
-    const bool in = tid < BM && m0 + tid < M;
-    const int id = in ? d.id[m0 + tid] : kNoAdapter;
-    const int last = in && tid > 0 ? d.id[m0 + tid - 1] : kNoAdapter;
-    const bool starts = id >= 0 && (tid == 0 || id != last);
-    const uint64_t mask = __ballot(starts);
-    if (lane == 0) wave_runs[wave] = __popcll(mask);
-    __syncthreads();
-    int before = 0, all = 0;
-    for (int w = 0; w < NW; ++w) {
-      before += w < wave ? wave_runs[w] : 0;
-      all += wave_runs[w];
-    }
-    const int run = before + __popcll(mask & ((2ull << lane) - 1)) - 1;
-    if (tid < BM) {
-      const int row = in ? d.row[m0 + tid] : 0;
-      tr.row[tid] = id == kBadAdapter ? ~row : row;
-      tr.run[tid] = id >= 0 ? run : -1;
-      if (starts) tr.adapter[run] = id;
-    }
-    if (tid == 0) tr.runs = all;
+  const int my_id = tid < BM && m0 + tid < M ? d.id[m0 + tid] : kNoAdapter;
+  const int my_row = tid < BM && m0 + tid < M ? d.row[m0 + tid] : 0;
+  if (tid < BM) {
+    tr.run[tid] = my_id;
+    tr.row[tid] = my_id == kBadAdapter ? ~my_row : my_row;
   }
+  load_stage<LOADS, A_LOADS, NW, AUX>(src, lds, wave, 0);
 
   f32x16 acc[TM][TN];
 #pragma unroll
@@ -278,25 +318,31 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void lora_gemm_kernel(
   }
 
   // ---- the adapters
-  const int rp = padded_rank(p.rank);
-  const int runs = tr.runs;
-  const int width = runs * rp;                  // of all the tile's adapters side by side
-  const int panels = (width + kBK - 1) / kBK;
-  // Sources of panel `pn`: the B_a values that each lane brings.  Past the
-  // rank (or the last adapter) any valid address: those are not used.
-  auto panel_sources = [&](int pn) {
-#pragma unroll
-    for (int q = A_LOADS; q < LOADS; ++q) {
-      const int r = 8 * (wave + NW * q) + chunk_row;
-      const int c = (lane & 7) ^ ((r >> 1) & 7);
-      const int k = pn * kBK + c * 8;
-      const int run = min(k / rp, runs - 1);
-      int kin = k - run * rp;
-      if (kin >= p.rank) kin = 0;
-      src[q] = p.b + static_cast<int64_t>(tr.adapter[run]) * p.stride_b +
-               static_cast<int64_t>(min(n0 + r - BM, N - 1)) * p.ld_b + kin;
+  // The tile's runs of one adapter.
+  int runs = 0;
+  {
+    const int id = tid < BM ? tr.run[tid] : kNoAdapter;
+    const bool starts = id >= 0 && (tid == 0 || id != tr.run[tid - 1]);
+    const uint64_t mask = __ballot(starts);
+    if (lane == 0) tr.wave_runs[wave] = __popcll(mask);
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < NW; ++w) {
+      before += w < wave ? tr.wave_runs[w] : 0;
+      runs += tr.wave_runs[w];
     }
-  };
+    const int run = before + __popcll(mask & ((2ull << lane) - 1)) - 1;
+    if (tid < BM) tr.run[tid] = id >= 0 ? run : -1;
+    if (starts) tr.adapter[run] = id;
+    __syncthreads();
+  }
+  // Each row's u, and each adapter's B columns, in windows of `ww` ranks.
+  const int rp = padded_rank(p.rank);
+  const int ww = rp == 16 ? 16 : 32;
+  const int panels = (runs * ww + kBK - 1) / kBK;  // of one window
+  // u of a row in LDS: kParts x ww values and one chunk of padding, which
+  // spreads a fragment's 32 rows over the banks.
+  const int u_chunks = kParts * ww / 8 + 1;
   // First and last run of each of the wave's row blocks (none: last < first).
   int first[TM], last[TM];
 #pragma unroll
@@ -306,59 +352,64 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void lora_gemm_kernel(
     first[i] = has ? __shfl(run, __ffsll(static_cast<unsigned long long>(has)) - 1) : 0;
     last[i] = has ? __shfl(run, 63 - __clzll(static_cast<long long>(has))) : -1;
   }
-  const int buf0 = ksteps & 1;
-  if (panels > 0) {
-    panel_sources(0);
-    load_panel<LOADS, A_LOADS, NW>(src, lds + buf0 * STAGE, wave);
-  }
-  for (int pn = 0; pn < panels; ++pn) {
-    const int cur = (buf0 + pn) & 1;
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    if (pn + 1 < panels) {
-      panel_sources(pn + 1);
-      load_panel<LOADS, A_LOADS, NW>(src, lds + (cur ^ 1) * STAGE, wave);
-    }
+  // Panels alternate between the stages' lm_head parts; u of the tile's first
+  // half of rows lies in the first stage's hidden part, of the second half in
+  // the other's.
+  for (int w = 0; runs > 0 && w * ww < rp; ++w) {
+    if (w > 0) __syncthreads();  // the last window's u and panels are done with
+    lora_panel<BM, LOADS, A_LOADS, NW>(p, tr, runs, rp, ww, w, 0, n0, wave, lane, lds);
+    lora_rows<BM, NW>(d, rp, ww, w, u_chunks, m0, M, wave, lane, lds);
+    lora_rows<BM, NW>(d, rp, ww, w, u_chunks, m0 + BM / 2, M, wave, lane, lds + STAGE);
+    for (int pn = 0; pn < panels; ++pn) {
+      const int cur = pn & 1;
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+      if (pn + 1 < panels)
+        lora_panel<BM, LOADS, A_LOADS, NW>(p, tr, runs, rp, ww, w, pn + 1, n0, wave, lane,
+                                           lds + (cur ^ 1) * STAGE);
 #pragma unroll
-    for (int kk = 0; kk < kBK / 16; ++kk) {
-      const int k = pn * kBK + kk * 16;
-      const int run = k / rp, kin = k - run * rp;
-      if (run >= runs) break;
-      bool any = false;
+      for (int kk = 0; kk < kBK / 16; ++kk) {
+        const int run = (pn * kBK + kk * 16) / ww, k_in = (kk * 16) % ww;
+        if (run >= runs || w * ww + k_in >= rp) continue;
+        bool any = false;
 #pragma unroll
-      for (int i = 0; i < TM; ++i) any = any || (run >= first[i] && run <= last[i]);
-      if (!any) continue;
-      bf16x8 bfr[TN];
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        bfr[j] = *reinterpret_cast<const bf16x8*>(lds + cur * STAGE + boff[j] +
-                                                  (((kk * 2 + fhalf) ^ bswz[j]) << 4));
-        if (kin + fhalf * 8 >= p.rank)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) bfr[j][e] = static_cast<__bf16>(0.0f);
-      }
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        if (run < first[i] || run > last[i]) continue;
-        const int place = min(m0 + wm0 + i * 32 + frow, M - 1);
-        const __bf16* u = d.u + static_cast<int64_t>(place) * kParts * rp + kin + fhalf * 8;
-        bf16x8 uf[kParts];
-#pragma unroll
-        for (int q = 0; q < kParts; ++q) uf[q] = *reinterpret_cast<const bf16x8*>(u + q * rp);
-        bool mine[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          mine[e] = tr.run[wm0 + i * 32 + 8 * (e >> 2) + 4 * fhalf + (e & 3)] == run;
+        for (int i = 0; i < TM; ++i) any = any || (run >= first[i] && run <= last[i]);
+        if (!any) continue;
+        bf16x8 bfr[TN];
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
-          f32x16 part;
+          bfr[j] = *reinterpret_cast<const bf16x8*>(lds + cur * STAGE + boff[j] +
+                                                    (((kk * 2 + fhalf) ^ bswz[j]) << 4));
+          if (w * ww + k_in + fhalf * 8 >= p.rank)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) part[e] = 0.0f;
+            for (int e = 0; e < 8; ++e) bfr[j][e] = static_cast<__bf16>(0.0f);
+        }
 #pragma unroll
-          for (int q = kParts - 1; q >= 0; --q)
-            part = __builtin_amdgcn_mfma_f32_32x32x16_bf16(uf[q], bfr[j], part, 0, 0, 0);
+        for (int i = 0; i < TM; ++i) {
+          if (run < first[i] || run > last[i]) continue;
+          const int at = wm0 + i * 32 + frow;
+          const uint8_t* u = lds + (at < BM / 2 ? 0 : STAGE) +
+                             ((at % (BM / 2)) * u_chunks + k_in / 8 + fhalf) * 16;
+          bf16x8 uf[kParts];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) acc[i][j][e] = mine[e] ? acc[i][j][e] + part[e] : acc[i][j][e];
+          for (int q = 0; q < kParts; ++q)
+            uf[q] = *reinterpret_cast<const bf16x8*>(u + q * ww * 2);
+          bool mine[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            mine[e] = tr.run[wm0 + i * 32 + 8 * (e >> 2) + 4 * fhalf + (e & 3)] == run;
+#pragma unroll
+          for (int j = 0; j < TN; ++j) {
+            f32x16 part;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) part[e] = 0.0f;
+#pragma unroll
+            for (int q = kParts - 1; q >= 0; --q)
+              part = __builtin_amdgcn_mfma_f32_32x32x16_bf16(uf[q], bfr[j], part, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              acc[i][j][e] = mine[e] ? acc[i][j][e] + part[e] : acc[i][j][e];
+          }
         }
       }
     }
@@ -477,7 +528,9 @@ size_t lmhead_lora_workspace_size(int64_t rows, int64_t rank) {
 hipError_t launch_lmhead_lora(const LoraArgs& p, void* ws, hipStream_t stream) {
   size_t bytes;
   const DownRows d = lay_out(ws, p.rows, p.rank, &bytes);
-  hipLaunchKernelGGL(lora_down_kernel, dim3(p.rows < (1 << 20) ? p.rows : (1 << 20)),
+  hipLaunchKernelGGL(lora_down_kernel,
+                     dim3(p.rows < (1 << 18) ? p.rows : (1 << 18),
+                          (padded_rank(p.rank) + kDownRanks - 1) / kDownRanks),
                      dim3(kDownThreads), 0, stream, p, d);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
