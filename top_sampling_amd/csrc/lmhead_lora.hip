@@ -15,19 +15,31 @@ namespace ts {
 namespace {
 
 constexpr int kNoAdapter = -1, kBadAdapter = -2;
-constexpr int kParts = 3;  // bf16 numbers that hold one fp32 u
+constexpr int kParts = 3;  // bf16 numbers that hold one fp32 value of u
+constexpr int kWindow = 16;  // ranks that are worked on at a time
 constexpr int kDownThreads = 256;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-__host__ __device__ constexpr int padded_rank(int rank) { return (rank + 15) / 16 * 16; }
+__host__ __device__ constexpr int padded_rank(int rank) {
+  return (rank + kWindow - 1) / kWindow * kWindow;
+}
 
 // What the down step leaves, rows in the order of (adapter, row).
 struct DownRows {
-  __bf16* u;     // [rows][kParts][padded rank], zeros past the rank
+  __bf16* u;     // [rows][padded rank / 16][kParts][16], zeros past the rank
   int32_t* row;  // the row at this place
   int32_t* id;   // its adapter, kNoAdapter or kBadAdapter
 };
+
+// Value k of a row of u.
+__device__ __forceinline__ float whole_u(const __bf16* u, int k) {
+  const __bf16* part = u + k / kWindow * (kParts * kWindow) + k % kWindow;
+  float sum = 0.0f;
+#pragma unroll
+  for (int q = kParts - 1; q >= 0; --q) sum += static_cast<float>(part[q * kWindow]);
+  return sum;
+}
 
 __device__ __forceinline__ int adapter_of(int id, int n_adapters) {
   if (id >= 0 && id < n_adapters) return id;
@@ -36,8 +48,8 @@ __device__ __forceinline__ int adapter_of(int id, int n_adapters) {
 
 // One workgroup per row and kDownRanks ranks, four ranks a wave; kDownStep
 // 512-wide pieces of the row are in flight at a time.
-constexpr int kDownRanks = 16;
-constexpr int kDownStep = 2;
+constexpr int kDownRanks = kWindow;
+constexpr int kDownStep = 4;
 
 __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraArgs p, DownRows out) {
   constexpr int kPerWave = kDownRanks / (kDownThreads / 64);
@@ -92,14 +104,15 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraArgs p, Dow
       out.id[place] = id;
     }
     const float scale = id >= 0 && p.scales ? p.scales[id] : 1.0f;
-    __bf16* u = out.u + static_cast<int64_t>(place) * kParts * rp;
+    __bf16* u = out.u + (static_cast<int64_t>(place) * rp + blockIdx.y * kDownRanks) * kParts +
+                wave * kPerWave;
 #pragma unroll
     for (int k = 0; k < kPerWave; ++k) {
       float rest = sum[k] * scale;
 #pragma unroll
       for (int q = 0; q < kParts; ++q) {
         const __bf16 part = static_cast<__bf16>(rest);
-        if (lane == k) u[q * rp + k0 + k] = part;
+        if (lane == k) u[q * kWindow + k] = part;
         rest -= static_cast<float>(part);
       }
     }
@@ -116,17 +129,20 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraArgs p, Dow
 // are taken in the order of their adapters, through a row list for the loads
 // and the stores, so a tile holds few adapters and each in one run of rows.
 //
-// After the last K step the same two stages carry on with "panels" of B: for
-// the tile's adapters one after the other, the strip's BN rows of B_a, 64
-// values wide (four adapters of rank 16, or a quarter of one of rank 256).
-// The A operand is u, which is brought into the stages' other part once per
-// tile (once per 32 ranks), its three bf16 parts against the same B fragment:
-// read from global memory where it is used, u cost one latency per block and
-// slice, 6 us a panel.  A 32-row block only takes the adapters that its rows
-// have.  The product of one 16-wide slice goes into an
-// accumulator of its own and is added to the rows of its adapter alone: a row
-// never sees another adapter's weights (0 x inf is not 0), and its sum does
-// not depend on the rows beside it.
+// After the last K step the same two stages carry on, in windows of 16 ranks,
+// with "panels" of B: the strip's BN rows of the B of four of the tile's
+// adapters, 16 ranks each, in the stage's lm_head part.  u of the tile's rows
+// for the same 16 ranks lies in the hidden part.  Both come a step ahead of
+// their use: read from global memory where it is used, u cost a latency per
+// block and slice (6 us a panel).  A 32-row block takes the adapters that its
+// rows have, with u of the other rows set to 0 in the A fragment.
+//
+// 0 x inf is not 0, so infinities and NaN in B are set to 0 as well, and a tile
+// that met one adds their products to the rows of that adapter alone after its
+// logits are stored.  A row never sees another adapter's weights, and what it
+// gets does not depend on the rows beside it.  (Adding every product through a
+// selection of the adapter's rows instead cost 18 us a tile of 320 x 256 with
+// nine adapters of rank 32, where the main loop takes 150.)
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef f32x4 f32x4u __attribute__((aligned(4)));
@@ -147,52 +163,77 @@ __device__ __forceinline__ void load_stage(const uint16_t* const* src, uint8_t* 
     __builtin_amdgcn_global_load_lds(src[q] + k0, stage + (wave + NW * q) * 1024, 16, 0, AUX);
 }
 
-// The adapters of a tile's rows, in the rows' order.
+// The adapters of a tile's rows.  A run is the rows of one adapter.
 template <int BM, int NW>
 struct TileRuns {
-  int row[BM];      // the row at each place, ~row for a bad adapter
-  int run[BM];      // its adapter, then the run that it belongs to (-1: none)
-  int adapter[BM];  // the runs' adapters
+  int row[BM];        // the row at each place, ~row for a bad adapter
+  int id[BM];         // its adapter
+  int adapter[BM];    // of each run
+  int start[BM + 1];  // the runs' first places, and the end of the last
   int wave_runs[NW];
+  int met_non_finite;
 };
 
-// Panel `pn` of window `w`: BN rows of the adapters' B, 64 / ww runs side by
-// side, into the lm_head part of a stage.  Past the rank or the last run any
-// valid address: those values are not used.
+// Panel `pn` of window `w`: BN rows of the B of four runs, side by side, into
+// the lm_head part of a stage.  Past the last run or the rank any valid
+// address: those values are not used.
 template <int BM, int LOADS, int A_LOADS, int NW>
 __device__ __forceinline__ void lora_panel(const LoraArgs& p, const TileRuns<BM, NW>& tr, int runs,
-                                           int rp, int ww, int w, int pn, int n0, int wave,
-                                           int lane, uint8_t* stage) {
-#pragma unroll
+                                           int w, int pn, int n0, int wave, int lane,
+                                           uint8_t* stage) {
+#pragma unroll 1
   for (int q = A_LOADS; q < LOADS; ++q) {
     const int r = 8 * (wave + NW * q) + (lane >> 3);
-    const int k = pn * kBK + ((lane & 7) ^ ((r >> 1) & 7)) * 8;
-    const int run = min(k / ww, runs - 1);
-    int k_in = w * ww + k % ww;
-    if (k_in >= p.rank) k_in = 0;
+    const int c = (lane & 7) ^ ((r >> 1) & 7);
+    const int run = min(pn * (kBK / kWindow) + (c >> 1), runs - 1);
+    const int k = w * kWindow + (c & 1) * 8;
     const uint16_t* src = p.b + static_cast<int64_t>(tr.adapter[run]) * p.stride_b +
-                          static_cast<int64_t>(min(n0 + r - BM, p.vocab - 1)) * p.ld_b + k_in;
+                          static_cast<int64_t>(min(n0 + r - BM, p.vocab - 1)) * p.ld_b +
+                          (k < p.rank ? k : 0);
     __builtin_amdgcn_global_load_lds(src, stage + (wave + NW * q) * 1024, 16, 0, 0);
   }
 }
 
-// u of BM / 2 rows from place m0 on, ranks [w ww, (w + 1) ww), into the hidden
-// part of a stage, u_chunks 16-byte chunks a row.
+// Window `w` of the tile's u into the hidden part of a stage: kUChunks 16-byte
+// chunks a row, of which the last is padding that spreads a fragment's 32 rows
+// over the banks.
+constexpr int kUChunks = kParts * kWindow / 8 + 1;
+
 template <int BM, int NW>
-__device__ __forceinline__ void lora_rows(const DownRows& d, int rp, int ww, int w, int u_chunks,
-                                          int m0, int M, int wave, int lane, uint8_t* stage) {
-  constexpr int kMost = (BM / 2 * (kParts * 4 + 1) + 63) / 64;  // wave loads at ww = 32
-  static_assert(kMost * 1024 <= BM * 128, "u of half the rows fits the hidden part");
-  const int loads = (BM / 2 * u_chunks + 63) / 64;
-  const int per_part = ww / 8;
-  for (int q = wave; q < loads; q += NW) {
+__device__ __forceinline__ void lora_rows(const DownRows& d, int rp, int w, int m0, int M,
+                                          int wave, int lane, uint8_t* stage) {
+  constexpr int kLoads = (BM * kUChunks + 63) / 64;
+  static_assert(kLoads * 1024 <= BM * 128, "u of the rows fits the hidden part");
+#pragma unroll 1
+  for (int q = wave; q < kLoads; q += NW) {
     const int i = q * 64 + lane;
-    const int place = min(m0 + i / u_chunks, M - 1);
-    const int c = min(i % u_chunks, u_chunks - 2);
-    const int k = min(w * ww + c % per_part * 8, rp - 8);
-    const __bf16* src = d.u + (static_cast<int64_t>(place) * kParts + c / per_part) * rp + k;
+    const int place = min(m0 + i / kUChunks, M - 1);
+    const int c = min(i % kUChunks, kUChunks - 2);
+    const __bf16* src =
+        d.u + (static_cast<int64_t>(place) * rp + w * kWindow) * kParts + c * 8;
     __builtin_amdgcn_global_load_lds(src, stage + q * 1024, 16, 0, 0);
   }
+}
+
+constexpr uint16_t kExponent = 0x7f80;  // of a bf16; all ones: infinity or NaN
+
+__device__ __forceinline__ bf16x8 finite_part(const bf16x8& v) {
+  typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+  u16x8 b = __builtin_bit_cast(u16x8, v);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) b[e] = (b[e] & kExponent) == kExponent ? uint16_t{0} : b[e];
+  return __builtin_bit_cast(bf16x8, b);
+}
+
+// Whether one of eight bf16 is an infinity or a NaN.
+__device__ __forceinline__ bool not_finite(const bf16x8& v) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  const u32x4 b = __builtin_bit_cast(u32x4, v);
+  // Adding 1 to an exponent of all ones carries into the sign's place.
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) any |= (b[i] & 0x7f807f80u) + 0x00800080u;
+  return (any & 0x80008000u) != 0;
 }
 
 template <int BM, int BN, int WAVES_M, int WAVES_N, int AUX>
@@ -237,12 +278,14 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void lora_gemm_kernel(
     else
       src[q] = p.lm_head + static_cast<int64_t>(min(n0 + r - BM, N - 1)) * p.ld_lm_head + c * 8;
   }
-  const int my_id = tid < BM && m0 + tid < M ? d.id[m0 + tid] : kNoAdapter;
-  const int my_row = tid < BM && m0 + tid < M ? d.row[m0 + tid] : 0;
+  const bool in = tid < BM && m0 + tid < M;
+  const int my_id = in ? d.id[m0 + tid] : kNoAdapter;
+  const int my_row = in ? d.row[m0 + tid] : 0;
   if (tid < BM) {
-    tr.run[tid] = my_id;
+    tr.id[tid] = my_id;
     tr.row[tid] = my_id == kBadAdapter ? ~my_row : my_row;
   }
+  if (tid == 0) tr.met_non_finite = 0;
   load_stage<LOADS, A_LOADS, NW, AUX>(src, lds, wave, 0);
 
   f32x16 acc[TM][TN];
@@ -318,11 +361,11 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void lora_gemm_kernel(
   }
 
   // ---- the adapters
-  // The tile's runs of one adapter.
+  // The tile's runs.
   int runs = 0;
   {
-    const int id = tid < BM ? tr.run[tid] : kNoAdapter;
-    const bool starts = id >= 0 && (tid == 0 || id != tr.run[tid - 1]);
+    const int id = tid < BM ? tr.id[tid] : kNoAdapter;
+    const bool starts = id >= 0 && (tid == 0 || id != tr.id[tid - 1]);
     const uint64_t mask = __ballot(starts);
     if (lane == 0) tr.wave_runs[wave] = __popcll(mask);
     __syncthreads();
@@ -331,86 +374,75 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void lora_gemm_kernel(
       before += w < wave ? tr.wave_runs[w] : 0;
       runs += tr.wave_runs[w];
     }
-    const int run = before + __popcll(mask & ((2ull << lane) - 1)) - 1;
-    if (tid < BM) tr.run[tid] = id >= 0 ? run : -1;
-    if (starts) tr.adapter[run] = id;
+    if (starts) {
+      const int run = before + __popcll(mask & ((1ull << lane) - 1));
+      tr.adapter[run] = id;
+      tr.start[run] = tid;
+    }
+    if (tid == 0) tr.start[runs] = min(BM, M - m0);
     __syncthreads();
   }
-  // Each row's u, and each adapter's B columns, in windows of `ww` ranks.
+  // Step q has its panel in stage q & 1, window w its u in stage w & 1.
   const int rp = padded_rank(p.rank);
-  const int ww = rp == 16 ? 16 : 32;
-  const int panels = (runs * ww + kBK - 1) / kBK;  // of one window
-  // u of a row in LDS: kParts x ww values and one chunk of padding, which
-  // spreads a fragment's 32 rows over the banks.
-  const int u_chunks = kParts * ww / 8 + 1;
-  // First and last run of each of the wave's row blocks (none: last < first).
-  int first[TM], last[TM];
-#pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int run = tr.run[wm0 + i * 32 + frow];
-    const uint64_t has = __ballot(run >= 0 && lane < 32);
-    first[i] = has ? __shfl(run, __ffsll(static_cast<unsigned long long>(has)) - 1) : 0;
-    last[i] = has ? __shfl(run, 63 - __clzll(static_cast<long long>(has))) : -1;
+  const int panels = (runs + kBK / kWindow - 1) / (kBK / kWindow);  // of one window
+  const int steps = panels * (rp / kWindow);
+  if (steps > 0) {
+    lora_panel<BM, LOADS, A_LOADS, NW>(p, tr, runs, 0, 0, n0, wave, lane, lds);
+    lora_rows<BM, NW>(d, rp, 0, m0, M, wave, lane, lds);
   }
-  // Panels alternate between the stages' lm_head parts; u of the tile's first
-  // half of rows lies in the first stage's hidden part, of the second half in
-  // the other's.
-  for (int w = 0; runs > 0 && w * ww < rp; ++w) {
-    if (w > 0) __syncthreads();  // the last window's u and panels are done with
-    lora_panel<BM, LOADS, A_LOADS, NW>(p, tr, runs, rp, ww, w, 0, n0, wave, lane, lds);
-    lora_rows<BM, NW>(d, rp, ww, w, u_chunks, m0, M, wave, lane, lds);
-    lora_rows<BM, NW>(d, rp, ww, w, u_chunks, m0 + BM / 2, M, wave, lane, lds + STAGE);
-    for (int pn = 0; pn < panels; ++pn) {
-      const int cur = pn & 1;
-      __builtin_amdgcn_s_waitcnt(0);
-      __syncthreads();
-      if (pn + 1 < panels)
-        lora_panel<BM, LOADS, A_LOADS, NW>(p, tr, runs, rp, ww, w, pn + 1, n0, wave, lane,
-                                           lds + (cur ^ 1) * STAGE);
+  for (int q = 0, w = 0, pn = 0; q < steps; ++q, ++pn) {
+    if (pn == panels) {
+      pn = 0;
+      ++w;
+    }
+    const int cur = q & 1;
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (q + 1 < steps) {
+      const bool more = pn + 1 < panels;
+      lora_panel<BM, LOADS, A_LOADS, NW>(p, tr, runs, more ? w : w + 1, more ? pn + 1 : 0, n0,
+                                         wave, lane, lds + (cur ^ 1) * STAGE);
+    }
+    if (pn == 0 && (w + 1) * kWindow < rp)
+      lora_rows<BM, NW>(d, rp, w + 1, m0, M, wave, lane, lds + ((w + 1) & 1) * STAGE);
+    const uint8_t* ub = lds + (w & 1) * STAGE + (wm0 + frow) * (kUChunks * 16) + fhalf * 16;
+    const int here = min(kBK / kWindow, runs - pn * (kBK / kWindow));
+#pragma unroll 1
+    for (int kk = 0; kk < here; ++kk) {
+      const int run = pn * (kBK / kWindow) + kk;
+      // The run's places within the wave's rows.
+      const int from = __builtin_amdgcn_readfirstlane(tr.start[run]) - wm0;
+      const int to = __builtin_amdgcn_readfirstlane(tr.start[run + 1]) - wm0;
+      if (to <= 0 || from >= WM) continue;
+      bf16x8 bfr[TN];
+      bool odd = false;
 #pragma unroll
-      for (int kk = 0; kk < kBK / 16; ++kk) {
-        const int run = (pn * kBK + kk * 16) / ww, k_in = (kk * 16) % ww;
-        if (run >= runs || w * ww + k_in >= rp) continue;
-        bool any = false;
+      for (int j = 0; j < TN; ++j) {
+        bfr[j] = *reinterpret_cast<const bf16x8*>(lds + cur * STAGE + boff[j] +
+                                                  (((kk * 2 + fhalf) ^ bswz[j]) << 4));
+        if (w * kWindow + fhalf * 8 >= p.rank) bfr[j] = bf16x8{};
+        odd = odd || not_finite(bfr[j]);
+      }
+      if (__ballot(odd) != 0) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i) any = any || (run >= first[i] && run <= last[i]);
-        if (!any) continue;
-        bf16x8 bfr[TN];
+        for (int j = 0; j < TN; ++j) bfr[j] = finite_part(bfr[j]);
+        if (lane == 0) tr.met_non_finite = 1;
+      }
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-          bfr[j] = *reinterpret_cast<const bf16x8*>(lds + cur * STAGE + boff[j] +
-                                                    (((kk * 2 + fhalf) ^ bswz[j]) << 4));
-          if (w * ww + k_in + fhalf * 8 >= p.rank)
+      for (int i = 0; i < TM; ++i) {
+        if (to <= i * 32 || from >= i * 32 + 32) continue;
+        const bool mine = i * 32 + frow >= from && i * 32 + frow < to;
+        bf16x8 uf[kParts];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) bfr[j][e] = static_cast<__bf16>(0.0f);
+        for (int t = 0; t < kParts; ++t) {
+          uf[t] = *reinterpret_cast<const bf16x8*>(ub + i * 32 * kUChunks * 16 + t * kWindow * 2);
+          if (!mine) uf[t] = bf16x8{};
         }
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-          if (run < first[i] || run > last[i]) continue;
-          const int at = wm0 + i * 32 + frow;
-          const uint8_t* u = lds + (at < BM / 2 ? 0 : STAGE) +
-                             ((at % (BM / 2)) * u_chunks + k_in / 8 + fhalf) * 16;
-          bf16x8 uf[kParts];
+        for (int t = kParts - 1; t >= 0; --t)
 #pragma unroll
-          for (int q = 0; q < kParts; ++q)
-            uf[q] = *reinterpret_cast<const bf16x8*>(u + q * ww * 2);
-          bool mine[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            mine[e] = tr.run[wm0 + i * 32 + 8 * (e >> 2) + 4 * fhalf + (e & 3)] == run;
-#pragma unroll
-          for (int j = 0; j < TN; ++j) {
-            f32x16 part;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) part[e] = 0.0f;
-#pragma unroll
-            for (int q = kParts - 1; q >= 0; --q)
-              part = __builtin_amdgcn_mfma_f32_32x32x16_bf16(uf[q], bfr[j], part, 0, 0, 0);
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              acc[i][j][e] = mine[e] ? acc[i][j][e] + part[e] : acc[i][j][e];
-          }
-        }
+          for (int j = 0; j < TN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(uf[t], bfr[j], acc[i][j], 0, 0, 0);
       }
     }
   }
@@ -456,6 +488,22 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void lora_gemm_kernel(
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     }
   }
+
+  // ---- what infinities and NaN in B add to their adapters' rows
+  __syncthreads();
+  if (tr.met_non_finite == 0) return;
+  for (int at = tid; at < BM * BN; at += 64 * NW) {
+    const int place = at / BN, v = n0 + at % BN;
+    if (m0 + place >= M || v >= N || tr.id[place] < 0) continue;
+    const __bf16* u = d.u + static_cast<int64_t>(m0 + place) * rp * kParts;
+    const uint16_t* b = p.b + static_cast<int64_t>(tr.id[place]) * p.stride_b +
+                        static_cast<int64_t>(v) * p.ld_b;
+    float sum = 0.0f;
+    for (int k = 0; k < p.rank; ++k)
+      if ((b[k] & kExponent) == kExponent)
+        sum = fmaf(whole_u(u, k), __uint_as_float(static_cast<uint32_t>(b[k]) << 16), sum);
+    p.logits[static_cast<int64_t>(tr.row[place]) * p.ld_logits + v] += sum;
+  }
 }
 
 template <int BM, int BN, int WAVES_M, int WAVES_N, int AUX>
@@ -484,16 +532,14 @@ __global__ __launch_bounds__(kUpCols) void lora_add_kernel(LoraArgs p, DownRows 
       *out = NAN;
       continue;
     }
-    const __bf16* u = d.u + static_cast<int64_t>(place) * kParts * rp;
+    const __bf16* u = d.u + static_cast<int64_t>(place) * rp * kParts;
     const uint16_t* b = p.b + static_cast<int64_t>(id) * p.stride_b + static_cast<int64_t>(v) * p.ld_b;
     float sum = 0.0f;
     for (int k = 0; k < p.rank; k += 8) {
       const bf16x8 bv = *reinterpret_cast<const bf16x8*>(b + k);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float uk = static_cast<float>(u[k + e]) + static_cast<float>(u[rp + k + e]) +
-                         static_cast<float>(u[2 * rp + k + e]);
-        sum = fmaf(uk, static_cast<float>(bv[e]), sum);
+        sum = fmaf(whole_u(u, k + e), static_cast<float>(bv[e]), sum);
       }
     }
     *out += sum;
@@ -507,8 +553,8 @@ DownRows lay_out(void* base, int64_t rows, int64_t rank, size_t* bytes) {
   size_t at = 0;
   DownRows d;
   d.u = reinterpret_cast<__bf16*>(p + at);
-  at += round256(sizeof(__bf16) * kParts * static_cast<size_t>(padded_rank(static_cast<int>(rank))) *
-                 static_cast<size_t>(rows));
+  at += round256(sizeof(__bf16) * kParts * static_cast<size_t>(rows) *
+                 static_cast<size_t>(padded_rank(static_cast<int>(rank))));
   d.row = reinterpret_cast<int32_t*>(p + at);
   at += round256(sizeof(int32_t) * static_cast<size_t>(rows));
   d.id = reinterpret_cast<int32_t*>(p + at);
