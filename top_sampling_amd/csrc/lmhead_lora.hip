@@ -46,19 +46,27 @@ __device__ __forceinline__ int adapter_of(int id, int n_adapters) {
   return id == kNoAdapter ? kNoAdapter : kBadAdapter;
 }
 
-// One workgroup per row and kDownRanks ranks, four ranks a wave; kDownStep
-// 512-wide pieces of the row are in flight at a time.
-constexpr int kDownRanks = kWindow;
-constexpr int kDownStep = 4;
+// One workgroup per row and kWindow ranks, four ranks a wave; kDownStep
+// 512-wide pieces of the row and of A are in flight at a time.  Bound by the
+// L2's delivery of A, read once per row: 640 rows of 4,096 at rank 32 take 12
+// us, 64 at rank 16 take 5.  Four rows a workgroup sharing what they have of
+// one adapter: 16 and 14 us; four and eight pieces in flight: 13 and 16 us.
+constexpr int kDownStep = 2;
 
 __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraArgs p, DownRows out) {
-  constexpr int kPerWave = kDownRanks / (kDownThreads / 64);
-  __shared__ int before_wave[kDownThreads / 64];
+  constexpr int kWaves = kDownThreads / 64;
+  constexpr int kPerWave = kWindow / kWaves;
+  __shared__ int before_wave[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int rp = padded_rank(p.rank);
-  const int k0 = blockIdx.y * kDownRanks + wave * kPerWave;
+  const int k0 = blockIdx.y * kWindow + wave * kPerWave;
   for (int r = blockIdx.x; r < p.rows; r += gridDim.x) {
     const int id = adapter_of(p.ids[r], p.n_adapters);
+    int before = 0;
+    for (int i = tid; i < p.rows; i += kDownThreads) {
+      const int other = adapter_of(p.ids[i], p.n_adapters);
+      before += other < id || (other == id && i < r);
+    }
     float sum[kPerWave] = {};
     if (id >= 0 && k0 < p.rank) {  // the rank is a multiple of 8, so of kPerWave
       const uint16_t* x = p.hidden + static_cast<int64_t>(r) * p.ld_hidden;
@@ -85,11 +93,6 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraArgs p, Dow
         }
       }
     }
-    int before = 0;
-    for (int i = tid; i < p.rows; i += kDownThreads) {
-      const int other = adapter_of(p.ids[i], p.n_adapters);
-      before += other < id || (other == id && i < r);
-    }
     for (int d = 32; d > 0; d >>= 1) {
       before += __shfl_xor(before, d, 64);
 #pragma unroll
@@ -98,13 +101,13 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraArgs p, Dow
     if (lane == 0) before_wave[wave] = before;
     __syncthreads();
     int place = 0;
-    for (int w = 0; w < kDownThreads / 64; ++w) place += before_wave[w];
+    for (int w = 0; w < kWaves; ++w) place += before_wave[w];
     if (tid == 0 && blockIdx.y == 0) {
       out.row[place] = r;
       out.id[place] = id;
     }
     const float scale = id >= 0 && p.scales ? p.scales[id] : 1.0f;
-    __bf16* u = out.u + (static_cast<int64_t>(place) * rp + blockIdx.y * kDownRanks) * kParts +
+    __bf16* u = out.u + (static_cast<int64_t>(place) * rp + blockIdx.y * kWindow) * kParts +
                 wave * kPerWave;
 #pragma unroll
     for (int k = 0; k < kPerWave; ++k) {
@@ -129,12 +132,14 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraArgs p, Dow
 // are taken in the order of their adapters, through a row list for the loads
 // and the stores, so a tile holds few adapters and each in one run of rows.
 //
-// After the last K step the same two stages carry on, in windows of 16 ranks,
-// with "panels" of B: the strip's BN rows of the B of four of the tile's
-// adapters, 16 ranks each, in the stage's lm_head part.  u of the tile's rows
-// for the same 16 ranks lies in the hidden part.  Both come a step ahead of
-// their use: read from global memory where it is used, u cost a latency per
-// block and slice (6 us a panel).  A 32-row block takes the adapters that its
+// After the last K step the same two stages carry on with "panels" of B: the
+// strip's BN rows of the B of four of the tile's adapters, in windows of 16
+// ranks, in the stage's lm_head part.  u of those adapters' rows for the same
+// 16 ranks lies in the hidden part.  Both come a step ahead of their use: read
+// from global memory where it is used, u cost a latency per block and slice
+// (6 us a panel).  The windows of one panel follow each other, as they share
+// B's cache lines (the other order took 64 rows with 64 adapters of rank 64
+// from 0.5 to 0.7 ms).  A 32-row block takes the adapters that its
 // rows have, with u of the other rows set to 0 in the A fragment.
 //
 // 0 x inf is not 0, so infinities and NaN in B are set to 0 as well, and a tile
@@ -194,18 +199,18 @@ __device__ __forceinline__ void lora_panel(const LoraArgs& p, const TileRuns<BM,
   }
 }
 
-// Window `w` of the tile's u into the hidden part of a stage: kUChunks 16-byte
-// chunks a row, of which the last is padding that spreads a fragment's 32 rows
-// over the banks.
+// Window `w` of u of the tile's places [from, to) into the hidden part of a
+// stage: kUChunks 16-byte chunks a row, of which the last is padding that
+// spreads a fragment's 32 rows over the banks.
 constexpr int kUChunks = kParts * kWindow / 8 + 1;
 
 template <int BM, int NW>
-__device__ __forceinline__ void lora_rows(const DownRows& d, int rp, int w, int m0, int M,
-                                          int wave, int lane, uint8_t* stage) {
-  constexpr int kLoads = (BM * kUChunks + 63) / 64;
-  static_assert(kLoads * 1024 <= BM * 128, "u of the rows fits the hidden part");
+__device__ __forceinline__ void lora_rows(const DownRows& d, int rp, int w, int m0, int from,
+                                          int to, int M, int wave, int lane, uint8_t* stage) {
+  static_assert((BM * kUChunks + 63) / 64 * 1024 <= BM * 128, "u of the rows fits");
+  const int end = (to * kUChunks + 63) / 64;
 #pragma unroll 1
-  for (int q = wave; q < kLoads; q += NW) {
+  for (int q = from * kUChunks / 64 + wave; q < end; q += NW) {
     const int i = q * 64 + lane;
     const int place = min(m0 + i / kUChunks, M - 1);
     const int c = min(i % kUChunks, kUChunks - 2);
@@ -236,8 +241,9 @@ __device__ __forceinline__ bool not_finite(const bf16x8& v) {
   return (any & 0x80008000u) != 0;
 }
 
-template <int BM, int BN, int WAVES_M, int WAVES_N, int AUX>
-__global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void lora_gemm_kernel(
+// WAVES: waves that a SIMD is to hold, which bounds the registers.
+template <int BM, int BN, int WAVES_M, int WAVES_N, int AUX, int WAVES>
+__global__ __launch_bounds__(64 * WAVES_M * WAVES_N, WAVES) void lora_gemm_kernel(
     LoraArgs p, DownRows d, int tiles_m, int tiles_total, int tiles_per_xcd) {
   constexpr int NW = WAVES_M * WAVES_N;
   constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
@@ -382,52 +388,49 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void lora_gemm_kernel(
     if (tid == 0) tr.start[runs] = min(BM, M - m0);
     __syncthreads();
   }
-  // Step q has its panel in stage q & 1, window w its u in stage w & 1.
+  // Step q: window w of panel pn, in stage q & 1.
+  constexpr int kRuns = kBK / kWindow;  // of a panel
   const int rp = padded_rank(p.rank);
-  const int panels = (runs + kBK / kWindow - 1) / (kBK / kWindow);  // of one window
-  const int steps = panels * (rp / kWindow);
-  if (steps > 0) {
-    lora_panel<BM, LOADS, A_LOADS, NW>(p, tr, runs, 0, 0, n0, wave, lane, lds);
-    lora_rows<BM, NW>(d, rp, 0, m0, M, wave, lane, lds);
-  }
-  for (int q = 0, w = 0, pn = 0; q < steps; ++q, ++pn) {
-    if (pn == panels) {
-      pn = 0;
-      ++w;
-    }
-    const int cur = q & 1;
+  const int steps = (runs + kRuns - 1) / kRuns * (rp / kWindow);
+  auto bring = [&](int pn, int w, int stage) {
+    uint8_t* to = lds + stage * STAGE;
+    lora_panel<BM, LOADS, A_LOADS, NW>(p, tr, runs, w, pn, n0, wave, lane, to);
+    lora_rows<BM, NW>(d, rp, w, m0, tr.start[pn * kRuns], tr.start[min(pn * kRuns + kRuns, runs)],
+                      M, wave, lane, to);
+  };
+  if (steps > 0) bring(0, 0, 0);
+  for (int q = 0, pn = 0, w = 0; q < steps; ++q) {
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
-    if (q + 1 < steps) {
-      const bool more = pn + 1 < panels;
-      lora_panel<BM, LOADS, A_LOADS, NW>(p, tr, runs, more ? w : w + 1, more ? pn + 1 : 0, n0,
-                                         wave, lane, lds + (cur ^ 1) * STAGE);
-    }
-    if (pn == 0 && (w + 1) * kWindow < rp)
-      lora_rows<BM, NW>(d, rp, w + 1, m0, M, wave, lane, lds + ((w + 1) & 1) * STAGE);
-    const uint8_t* ub = lds + (w & 1) * STAGE + (wm0 + frow) * (kUChunks * 16) + fhalf * 16;
-    const int here = min(kBK / kWindow, runs - pn * (kBK / kWindow));
-#pragma unroll 1
-    for (int kk = 0; kk < here; ++kk) {
-      const int run = pn * (kBK / kWindow) + kk;
-      // The run's places within the wave's rows.
-      const int from = __builtin_amdgcn_readfirstlane(tr.start[run]) - wm0;
-      const int to = __builtin_amdgcn_readfirstlane(tr.start[run + 1]) - wm0;
-      if (to <= 0 || from >= WM) continue;
-      bf16x8 bfr[TN];
-      bool odd = false;
+    const int last_w = w * kWindow + kWindow >= rp;
+    if (q + 1 < steps) bring(last_w ? pn + 1 : pn, last_w ? 0 : w + 1, (q + 1) & 1);
+    const uint8_t* stage = lds + (q & 1) * STAGE;
+    const uint8_t* ub = stage + (wm0 + frow) * (kUChunks * 16) + fhalf * 16;
+    // Where the panel's runs start and end within the wave's rows.
+    const int starts = tr.start[min(pn * kRuns + min(lane, kRuns), runs)] - wm0;
+    bf16x8 bfr[kRuns][TN];
+    bool odd = false;
+#pragma unroll
+    for (int kk = 0; kk < kRuns; ++kk)
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
-        bfr[j] = *reinterpret_cast<const bf16x8*>(lds + cur * STAGE + boff[j] +
-                                                  (((kk * 2 + fhalf) ^ bswz[j]) << 4));
-        if (w * kWindow + fhalf * 8 >= p.rank) bfr[j] = bf16x8{};
-        odd = odd || not_finite(bfr[j]);
+        bfr[kk][j] = *reinterpret_cast<const bf16x8*>(stage + boff[j] +
+                                                      (((kk * 2 + fhalf) ^ bswz[j]) << 4));
+        if (w * kWindow + fhalf * 8 >= p.rank) bfr[kk][j] = bf16x8{};
+        odd = odd || not_finite(bfr[kk][j]);
       }
-      if (__ballot(odd) != 0) {
+    if (__ballot(odd) != 0) {
 #pragma unroll
-        for (int j = 0; j < TN; ++j) bfr[j] = finite_part(bfr[j]);
-        if (lane == 0) tr.met_non_finite = 1;
-      }
+      for (int kk = 0; kk < kRuns; ++kk)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) bfr[kk][j] = finite_part(bfr[kk][j]);
+      if (lane == 0) tr.met_non_finite = 1;
+    }
+#pragma unroll
+    for (int kk = 0; kk < kRuns; ++kk) {
+      const int from = __builtin_amdgcn_readlane(starts, kk);
+      const int to = __builtin_amdgcn_readlane(starts, kk + 1);
+      if (to <= 0 || from >= WM || from == to) continue;
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
         if (to <= i * 32 || from >= i * 32 + 32) continue;
@@ -442,9 +445,11 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void lora_gemm_kernel(
         for (int t = kParts - 1; t >= 0; --t)
 #pragma unroll
           for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(uf[t], bfr[j], acc[i][j], 0, 0, 0);
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(uf[t], bfr[kk][j], acc[i][j], 0, 0, 0);
       }
     }
+    pn = last_w ? pn + 1 : pn;
+    w = last_w ? 0 : w + 1;
   }
 
   // ---- the logits, a row segment at a time through a scratch of the wave's
@@ -506,13 +511,13 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void lora_gemm_kernel(
   }
 }
 
-template <int BM, int BN, int WAVES_M, int WAVES_N, int AUX>
+template <int BM, int BN, int WAVES_M, int WAVES_N, int AUX, int WAVES>
 hipError_t launch_fused(const LoraArgs& p, const DownRows& d, hipStream_t stream) {
   const int tiles_m = (p.rows + BM - 1) / BM;
   const int tiles_n = (p.vocab + BN - 1) / BN;
   const int total = tiles_m * tiles_n;
   const int per_xcd = (total + kXcds - 1) / kXcds;
-  hipLaunchKernelGGL((lora_gemm_kernel<BM, BN, WAVES_M, WAVES_N, AUX>), dim3(per_xcd * kXcds),
+  hipLaunchKernelGGL((lora_gemm_kernel<BM, BN, WAVES_M, WAVES_N, AUX, WAVES>), dim3(per_xcd * kXcds),
                      dim3(64 * WAVES_M * WAVES_N), 0, stream, p, d, tiles_m, total, per_xcd);
   return hipGetLastError();
 }
@@ -575,8 +580,7 @@ hipError_t launch_lmhead_lora(const LoraArgs& p, void* ws, hipStream_t stream) {
   size_t bytes;
   const DownRows d = lay_out(ws, p.rows, p.rank, &bytes);
   hipLaunchKernelGGL(lora_down_kernel,
-                     dim3(p.rows < (1 << 18) ? p.rows : (1 << 18),
-                          (padded_rank(p.rank) + kDownRanks - 1) / kDownRanks),
+                     dim3(p.rows < (1 << 18) ? p.rows : (1 << 18), padded_rank(p.rank) / kWindow),
                      dim3(kDownThreads), 0, stream, p, d);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -585,10 +589,15 @@ hipError_t launch_lmhead_lora(const LoraArgs& p, void* ws, hipStream_t stream) {
     // 128 rows one row tile reads the lm_head once: past the caches.
     const int64_t pad256 = (p.rows + int64_t{255}) / 256 * 256;
     const int64_t pad320 = (p.rows + int64_t{319}) / 320 * 320;
-    if (p.rows <= 64) return launch_fused<64, 128, 1, 4, 2>(p, d, stream);
-    if (p.rows <= 128) return launch_fused<128, 128, 2, 4, 2>(p, d, stream);
-    if (pad320 < pad256) return launch_fused<320, 256, 2, 4, 0>(p, d, stream);
-    return launch_fused<256, 256, 2, 4, 0>(p, d, stream);
+    if (p.rows <= 64) return launch_fused<64, 128, 1, 4, 2, 3>(p, d, stream);
+    if (p.rows <= 128) return launch_fused<128, 128, 2, 4, 2, 4>(p, d, stream);
+    // A short vocabulary slice makes too few 256-wide tiles for the card: 122 of
+    // them (256 x 31,040, H 2,560) take 76 us, the 486 smaller tiles 62; from
+    // three quarters of the card on it turns (235 tiles: 100 against 119 us).
+    if ((pad256 / 256) * ((p.vocab + 255) / 256) < 192)
+      return launch_fused<128, 128, 2, 4, 0, 4>(p, d, stream);
+    if (pad320 < pad256) return launch_fused<320, 256, 2, 4, 0, 2>(p, d, stream);
+    return launch_fused<256, 256, 2, 4, 0, 2>(p, d, stream);
   }
   e = launch_lmhead_gemm(p.hidden, p.ld_hidden, p.lm_head, p.ld_lm_head, p.logits, p.ld_logits,
                          p.rows, p.vocab, p.hidden_dim, stream);
