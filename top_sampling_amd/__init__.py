@@ -445,15 +445,23 @@ class PreferenceLoss:
 
 class _OnDevice:
     """Makes the device of a call's tensors and its stream current, so that
-    outputs and workspaces are allocated for that stream."""
+    outputs and workspaces are allocated for that stream.  Where they are
+    already, which is the usual call, nothing is switched (switching takes
+    longer than a small kernel)."""
+
+    __slots__ = ("pointer", "_guard")
 
     def __init__(self, device, stream):
         torch = _torch()
         if device.type != "cuda":
             raise ValueError("tensors must be on the GPU")
+        self._guard = None
         if stream is None:
-            stream = torch.cuda.current_stream(device)
-        elif not hasattr(stream, "cuda_stream"):
+            if device.index != torch.cuda.current_device():
+                self._guard = torch.cuda.device(device)
+            self.pointer = torch._C._cuda_getCurrentRawStream(device.index)
+            return
+        if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), device=device)
         elif stream.device != device:
             raise ValueError("the stream belongs to another device than the tensors")
@@ -461,18 +469,19 @@ class _OnDevice:
         self._guard = torch.cuda.stream(stream)
 
     def __enter__(self):
-        self._guard.__enter__()
+        if self._guard is not None:
+            self._guard.__enter__()
         return self.pointer
 
     def __exit__(self, *exc):
-        self._guard.__exit__(*exc)
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
 
 
 def _check_vector(t, name, n, device, dtype=None):
-    torch = _torch()
-    dtype = dtype or torch.float32
     if t is None:
         return
+    dtype = dtype or _torch().float32
     if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values")
     if t.device != device:
@@ -505,8 +514,10 @@ def _grad_rows(grad_logits, logits):
     return max(int(grad_logits.stride(0)), int(grad_logits.shape[1]))
 
 
-def _check_workspace(workspace, device):
+def _workspace(workspace, need, device):
     torch = _torch()
+    if workspace is None:
+        return torch.empty(max(256, need), dtype=torch.uint8, device=device)
     if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
             workspace.device != device:
         raise ValueError("workspace must be a contiguous uint8 tensor on the logits' device")
@@ -531,14 +542,11 @@ def token_logprobs(logits, token_ids, temperature: float = 1.0, entropies: bool 
     rows, vocab = logits.shape
     dev = logits.device
     with _OnDevice(dev, stream) as s:
-        if workspace is None:
-            workspace = torch.empty(max(256, token_logprobs_workspace_bytes(rows, vocab)),
-                                    dtype=torch.uint8, device=dev)
-        _check_workspace(workspace, dev)
+        workspace = _workspace(workspace, token_logprobs_workspace_bytes(rows, vocab), dev)
         out = TokenLogprobs(
             torch.empty(rows, dtype=torch.float32, device=dev),
             torch.empty(rows, dtype=torch.float32, device=dev) if entropies else None,
-            torch.empty(rows, 2, dtype=torch.float32, device=dev),
+            torch.empty((rows, 2), dtype=torch.float32, device=dev),
             torch.empty(rows, dtype=torch.int32, device=dev))
         _check(lib.token_logprobs(
             _ptr(logits), kind, rows, vocab, ld, _ptr(token_ids), temperature, _ptr(out.logprobs),
@@ -592,18 +600,13 @@ def policy_loss(logits, token_ids, old_logprobs, advantages, ref_logprobs=None, 
                        (grad_loss, "grad_loss", 1)):
         _check_vector(t, name, n, dev)
     with _OnDevice(dev, stream) as s:
-        if workspace is None:
-            workspace = torch.empty(max(256, token_logprobs_workspace_bytes(rows, vocab)),
-                                    dtype=torch.uint8, device=dev)
-        _check_workspace(workspace, dev)
+        workspace = _workspace(workspace, token_logprobs_workspace_bytes(rows, vocab), dev)
         if grad_logits is None and backward:
             grad_logits = torch.empty(rows, vocab, dtype=logits.dtype, device=dev)
         ldg = _grad_rows(grad_logits, logits) if grad_logits is not None else 0
         out = PolicyLoss(
             torch.empty((), dtype=torch.float32, device=dev),
-            torch.empty(rows, dtype=torch.float32, device=dev),
-            torch.empty(rows, dtype=torch.float32, device=dev),
-            torch.empty(rows, dtype=torch.float32, device=dev),
+            *torch.empty((3, rows), dtype=torch.float32, device=dev).unbind(0),
             torch.empty(rows, dtype=torch.int32, device=dev), grad_logits)
         params = _PolicyParams(temperature, clip_low, clip_high, kl_coef)
         _check(lib.policy_loss(
@@ -636,11 +639,8 @@ def preference_loss(logits, token_ids, seq_offsets, ref_logprobs=None, pair_weig
                        (pair_weights, "pair_weights", n_pairs), (grad_loss, "grad_loss", 1)):
         _check_vector(t, name, n, dev)
     with _OnDevice(dev, stream) as s:
-        if workspace is None:
-            workspace = torch.empty(
-                max(256, preference_loss_workspace_bytes(rows, vocab, n_pairs)),
-                dtype=torch.uint8, device=dev)
-        _check_workspace(workspace, dev)
+        workspace = _workspace(workspace, preference_loss_workspace_bytes(rows, vocab, n_pairs),
+                               dev)
         if grad_logits is None and backward:
             grad_logits = torch.empty(rows, vocab, dtype=logits.dtype, device=dev)
         ldg = _grad_rows(grad_logits, logits) if grad_logits is not None else 0
@@ -705,10 +705,7 @@ def lmhead_logits_local_lora(hidden, lm_head, lora_a, lora_b, adapter_ids, adapt
         if out.shape != (rows, vocab) or out.dtype != torch.float32 or out.device != dev or \
                 (vocab > 1 and out.stride(1) != 1):
             raise ValueError("out must be fp32 [rows, V_local] with unit column stride")
-        if workspace is None:
-            workspace = torch.empty(max(256, lmhead_lora_workspace_bytes(rows, rank)),
-                                    dtype=torch.uint8, device=dev)
-        _check_workspace(workspace, dev)
+        workspace = _workspace(workspace, lmhead_lora_workspace_bytes(rows, rank), dev)
         _check(lib.lmhead_logits_local_lora(
             _ptr(hidden), rows, h, row_stride(hidden, h), _ptr(lm_head), vocab,
             row_stride(lm_head, h), _ptr(lora_a), adapter_stride(lora_a), row_stride(lora_a, h),

@@ -405,7 +405,7 @@ template <typename T>
 __global__ __launch_bounds__(kThreads) void policy_rows_kernel(
     const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,
     const float* __restrict__ weights, Scale sc, const Part* __restrict__ parts, int chunks,
-    PolicyArgs p, RowGrad* __restrict__ grads, double* __restrict__ losses) {
+    PolicyArgs p, RowGrad* __restrict__ grads, double* losses, int sum_here) {
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsPerGroup + threadIdx.x / kRowLanes;
        row < rows; row += static_cast<int64_t>(gridDim.x) * kRowsPerGroup) {
     const int r = static_cast<int>(row);
@@ -454,6 +454,11 @@ __global__ __launch_bounds__(kThreads) void policy_rows_kernel(
       const double up = p.grad_loss ? static_cast<double>(*p.grad_loss) : 1.0;
       grads[r] = row_grad(st, up * w * g, sc);
     }
+  }
+  if (sum_here) {
+    __syncthreads();
+    const double s = group_sum(losses, rows);
+    if (threadIdx.x == 0) *p.loss = static_cast<float>(s);
   }
 }
 
@@ -779,12 +784,16 @@ hipError_t policy_loss_t(const TokenRows& t, const PolicyArgs& p, const GradRows
   const bool back = d.x != nullptr;
   hipError_t e = launch_stats<T, false>(t, sc, cut, w, RowInit{}, stream);
   if (e != hipSuccess) return e;
+  // Without a gradient and with one workgroup of rows, that one adds up the
+  // loss; with a gradient the last pass does, otherwise a kernel of its own.
+  const bool sum_here = !back && t.rows <= kRowsPerGroup;
   hipLaunchKernelGGL((policy_rows_kernel<T>),
                      dim3(grid_of((t.rows + kRowsPerGroup - 1) / kRowsPerGroup)), dim3(kThreads),
                      0, stream, static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, t.tokens,
-                     t.weights, sc, w.parts, cut.chunks, p, back ? w.grads : nullptr, w.losses);
+                     t.weights, sc, w.parts, cut.chunks, p, back ? w.grads : nullptr, w.losses,
+                     sum_here);
   e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || sum_here) return e;
   return back ? launch_grad<T>(t, sc, cut, w, d, t.rows, p.loss, stream)
               : launch_sum(w.losses, t.rows, p.loss, stream);
 }
