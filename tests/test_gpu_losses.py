@@ -252,7 +252,38 @@ def test_policy_loss(rows, vocab, pad, dtype):
         assert fwd.grad_logits is None and not got.row_status.any()
         for o in (got, fwd):
             check_policy(o, want, x, temperature, dtype, rows, f(w), f(adv), kl_coef, scale)
-        assert torch.equal(got.logprobs, fwd.logprobs) and torch.equal(got.ratios, fwd.ratios)
+
+
+@pytest.mark.parametrize("dtype,rows,vocab,pad", [
+    # rows held on the chip as a whole, with a part that is read again, of
+    # more than that twice over, and unaligned
+    ("fp32", 96, 33000, 0), ("fp32", 96, 114688, 0), ("fp32", 97, 120001, 0),
+    ("bf16", 128, 131077, 3), ("bf16", 130, 262144, 0), ("fp32", 3, 32768, 0),
+    # two passes
+    ("fp32", 95, 33001, 0), ("bf16", 127, 40000, 1), ("fp32", 2, 300000, 0),
+])
+def test_policy_loss_long_rows(dtype, rows, vocab, pad):
+    import torch
+
+    import top_sampling_amd as ts
+
+    logits, x = make_logits(rows, vocab, dtype, pad, rows + vocab)
+    tok = allowed_tokens(x, 6)
+    old, rf, adv, w = policy_inputs(rows, x, tok, 0.8, 8)
+    kw = dict(clip_low=0.2, clip_high=0.28, kl_coef=0.1, temperature=0.8)
+    f = lambda a: a.astype(np.float64)  # noqa: E731
+    want = ref.policy(x, tok, f(old), f(adv), f(rf), f(w), **kw)
+    args = (to_dev(tok, torch.int32), to_dev(old), to_dev(adv), to_dev(rf), to_dev(w))
+    wide = torch.full((rows, vocab + 1), 7.0, dtype=logits.dtype, device=logits.device)
+    got = ts.policy_loss(logits, *args, grad_logits=wide[:, :vocab], **kw)
+    torch.cuda.synchronize()
+    assert (wide[:, vocab:] == 7.0).all()
+    check_policy(got, want, x, 0.8, dtype, rows, f(w), f(adv), 0.1)
+    again = ts.policy_loss(logits, *args, backward=True, **kw)
+    assert torch.equal(again.grad_logits, got.grad_logits) and torch.equal(again.loss, got.loss)
+    same = logits.clone()
+    ts.policy_loss(same, *args, grad_logits=same, **kw)
+    assert torch.equal(same, got.grad_logits)
 
 
 def test_policy_clip_limits_and_no_weights():

@@ -311,11 +311,20 @@ struct RowStats {
   int status;
 };
 
+// Status and log-probability from the joined statistics and the token's logit.
+__device__ __forceinline__ void finish_row(RowStats& r, int token, int vocab, float xt,
+                                           const Scale& sc) {
+  r.status = token >= vocab ? TS_ROW_BAD_PARAMS
+                            : (fabsf(r.m) < INFINITY ? TS_ROW_OK : TS_ROW_BAD_LOGITS);
+  r.lp = r.status == TS_ROW_OK ? (static_cast<double>(xt) - r.m) * sc.inv_t - log(r.s) : NAN;
+}
+
 // A row's records joined by kRowLanes lanes; the row is not left out.
 template <bool ENT, typename T>
 __device__ __forceinline__ RowStats join_row(const T* x, int64_t ld, int vocab, int token, int row,
                                              const Part* parts, int chunks, const Scale& sc) {
   const int lane = threadIdx.x % kRowLanes;
+  const float xt = static_cast<float>(x[static_cast<int64_t>(row) * ld + min(token, vocab - 1)]);
   RowStats r;
   r.m = -INFINITY;
   r.s = r.u = 0.0;
@@ -330,17 +339,7 @@ __device__ __forceinline__ RowStats join_row(const T* x, int64_t ld, int vocab, 
     r.m = top;
   }
   join_lanes<ENT>(r.m, r.s, r.u, kRowLanes, sc);
-  if (token >= vocab) {
-    r.status = TS_ROW_BAD_PARAMS;
-    r.lp = NAN;
-  } else if (!(fabsf(r.m) < INFINITY)) {
-    r.status = TS_ROW_BAD_LOGITS;
-    r.lp = NAN;
-  } else {
-    r.status = TS_ROW_OK;
-    const float xt = static_cast<float>(x[static_cast<int64_t>(row) * ld + token]);
-    r.lp = (static_cast<double>(xt) - r.m) * sc.inv_t - log(r.s);
-  }
+  finish_row(r, token, vocab, xt, sc);
   return r;
 }
 
@@ -401,6 +400,58 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(const double* __restrict_
   if (threadIdx.x == 0) *out = static_cast<float>(s);
 }
 
+// What a left-out row of the policy loss writes, and one that takes part; both
+// by one thread.  The latter returns the row's gradient record.
+__device__ __forceinline__ void policy_left_out(const PolicyArgs& p, int r, double* losses) {
+  losses[r] = 0.0;
+  if (p.logprobs) p.logprobs[r] = 0.0f;
+  if (p.ratios) p.ratios[r] = 1.0f;
+  if (p.kl) p.kl[r] = 0.0f;
+  if (p.row_status) p.row_status[r] = TS_ROW_OK;
+}
+
+// The row's own inputs, read ahead of the statistics.
+struct PolicyRow {
+  float weight, advantage, old_lp, ref_lp, grad_loss;
+};
+
+__device__ __forceinline__ PolicyRow policy_row_inputs(const PolicyArgs& p, const float* weights,
+                                                       int r) {
+  return PolicyRow{weights ? weights[r] : 1.0f, p.advantages[r], p.old_logprobs[r],
+                   p.ref_logprobs ? p.ref_logprobs[r] : 0.0f, p.grad_loss ? *p.grad_loss : 1.0f};
+}
+
+__device__ __forceinline__ RowGrad policy_row(const PolicyArgs& p, const PolicyRow& in,
+                                              const RowStats& st, const Scale& sc, int r,
+                                              double* losses) {
+  const double w = in.weight, adv = in.advantage;
+  const double ratio = exp(st.lp - static_cast<double>(in.old_lp));
+  const double low = 1.0 - p.clip_low, high = 1.0 + p.clip_high;
+  // min(r A, clip(r) A): the bound that holds against the advantage's sign is
+  // the only one that can bind.  A = 0 gives 0 at any ratio.
+  const bool inside = adv >= 0.0 ? !(ratio > high) : !(ratio < low);
+  double gain = 0.0, g = 0.0;
+  if (adv != 0.0) {
+    gain = (inside ? ratio : (adv >= 0.0 ? high : low)) * adv;
+    g = inside ? -adv * ratio : 0.0;
+  }
+  double kl = 0.0;
+  if (p.ref_logprobs != nullptr) {
+    const double gap = static_cast<double>(in.ref_lp) - st.lp;
+    const double em = expm1(gap);
+    kl = em - gap;
+    if (p.kl_coef != 0.0) g -= p.kl_coef * em;
+  }
+  double loss = -gain;
+  if (p.kl_coef != 0.0) loss += p.kl_coef * kl;
+  losses[r] = st.status == TS_ROW_OK ? w * loss : NAN;
+  if (p.logprobs) p.logprobs[r] = static_cast<float>(st.lp);
+  if (p.ratios) p.ratios[r] = static_cast<float>(ratio);
+  if (p.kl) p.kl[r] = static_cast<float>(kl);
+  if (p.row_status) p.row_status[r] = st.status;
+  return row_grad(st, static_cast<double>(in.grad_loss) * w * g, sc);
+}
+
 template <typename T>
 __global__ __launch_bounds__(kThreads) void policy_rows_kernel(
     const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,
@@ -412,48 +463,16 @@ __global__ __launch_bounds__(kThreads) void policy_rows_kernel(
     const bool writes = threadIdx.x % kRowLanes == 0;
     if (left_out(tokens, weights, r)) {
       if (writes) {
-        losses[r] = 0.0;
+        policy_left_out(p, r, losses);
         if (grads) grads[r] = RowGrad{0.0f, 0.0f, 0.0f, 0.0f};
-        if (p.logprobs) p.logprobs[r] = 0.0f;
-        if (p.ratios) p.ratios[r] = 1.0f;
-        if (p.kl) p.kl[r] = 0.0f;
-        if (p.row_status) p.row_status[r] = TS_ROW_OK;
       }
       continue;
     }
+    const PolicyRow in = policy_row_inputs(p, weights, r);
     const RowStats st = join_row<false>(x, ld, vocab, tokens[r], r, parts, chunks, sc);
     if (!writes) continue;
-    const double w = weights ? static_cast<double>(weights[r]) : 1.0;
-    const double adv = p.advantages[r];
-    const double ratio = exp(st.lp - static_cast<double>(p.old_logprobs[r]));
-    const double low = 1.0 - p.clip_low;
-    const double high = 1.0 + p.clip_high;
-    // min(r A, clip(r) A): the bound that holds against the advantage's sign
-    // is the only one that can bind.  A = 0 gives 0 at any ratio.
-    const bool inside = adv >= 0.0 ? !(ratio > high) : !(ratio < low);
-    double gain = 0.0, g = 0.0;
-    if (adv != 0.0) {
-      gain = (inside ? ratio : (adv >= 0.0 ? high : low)) * adv;
-      g = inside ? -adv * ratio : 0.0;
-    }
-    double kl = 0.0;
-    if (p.ref_logprobs != nullptr) {
-      const double gap = static_cast<double>(p.ref_logprobs[r]) - st.lp;
-      const double em = expm1(gap);
-      kl = em - gap;
-      if (p.kl_coef != 0.0) g -= p.kl_coef * em;
-    }
-    double loss = -gain;
-    if (p.kl_coef != 0.0) loss += p.kl_coef * kl;
-    losses[r] = st.status == TS_ROW_OK ? w * loss : NAN;
-    if (p.logprobs) p.logprobs[r] = static_cast<float>(st.lp);
-    if (p.ratios) p.ratios[r] = static_cast<float>(ratio);
-    if (p.kl) p.kl[r] = static_cast<float>(kl);
-    if (p.row_status) p.row_status[r] = st.status;
-    if (grads != nullptr) {
-      const double up = p.grad_loss ? static_cast<double>(*p.grad_loss) : 1.0;
-      grads[r] = row_grad(st, up * w * g, sc);
-    }
+    const RowGrad g = policy_row(p, in, st, sc, r, losses);
+    if (grads) grads[r] = g;
   }
   if (sum_here) {
     __syncthreads();
@@ -682,6 +701,190 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(
   }
 }
 
+// -------------------------------------------------- policy loss in one read
+// One workgroup per row, alone on its CU, which holds the row between the
+// statistics and the gradient: every exponential goes into a register or into
+// LDS, relative to the thread's maximum at that point, and the gradient pass
+// only scales it.  160 registers and 64 LDS words a thread hold 114,688
+// entries; what a longer row has beyond them is read a second time.  In two
+// passes the second read costs as much as the first, out of the Infinity Cache
+// too: reads and writes together pass at 6.5-6.8 TB/s.  Loss and gradient of
+// 640 x 151,936 fp32 in two passes and in one: 192 and 157 us (one read and
+// one write take 120 at that rate, the quarter that is read again 15); 1,024 x
+// 151,936 bf16: 155 and 129; 1,021 x 100,277 bf16: 113 and 103.  Loads one
+// batch ahead are best (1,024 x 151,936: two ahead 142 us, all at once 150; the
+// batches' exponentials then run after the loads and not under them),
+// as are ten register batches (eleven spill).
+constexpr int kOneThreads = 512;
+constexpr int kOneVals = 16;                         // entries of a thread's batch
+constexpr int kRegBatches = 10;
+constexpr int kLdsBatches = 4;
+
+template <typename T>
+__global__ __launch_bounds__(kOneThreads, 2) void policy_row_at_once_kernel(
+    const T* x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,
+    const float* __restrict__ weights, Scale sc, PolicyArgs p, T* d, int64_t ldd,
+    double* __restrict__ losses) {
+  constexpr int VN = Vec<T>::n;
+  constexpr int NV = kOneVals / VN;  // vectors of a thread's batch
+  using V = typename Vec<T>::Type;
+  __shared__ f32x4 held_lds[kLdsBatches * kOneVals / 4][kOneThreads];
+  __shared__ Part wave_part[kOneThreads / 64];
+  __shared__ RowGrad row_record;
+  const int whole = vocab / VN;
+  const int batches = (whole + NV * kOneThreads - 1) / (NV * kOneThreads);
+
+  // No loop over rows: with one the compiler keeps the batches' registers
+  // across rows, and 700 of them spill.
+  const int r = blockIdx.x;
+  const int64_t row = r;
+  // The thread's number, unknown to the compiler as such: it would work out
+  // the places of all batches ahead and keep them in registers.
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const T* rx = x + row * ld;
+  T* rd = d + row * ldd;
+  const int token = tokens[r];
+  if (left_out(tokens, weights, r)) {
+    if (tid == 0) policy_left_out(p, r, losses);
+    row_grad_pass<T, false, kOneThreads>(rx, rd, vocab, 0, whole, true, token,
+                                         RowGrad{0.0f, 0.0f, 0.0f, 0.0f}, sc);
+    return;
+  }
+  const PolicyRow in = policy_row_inputs(p, weights, r);
+  const float xt = static_cast<float>(rx[min(token, vocab - 1)]);
+
+  float m = -INFINITY;
+  double s = 0.0, u = 0.0;
+  auto load = [&](int b, V (&raw)[NV]) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = min((b * NV + j) * kOneThreads + tid, whole - 1);
+      raw[j] = *reinterpret_cast<const V*>(rx + static_cast<int64_t>(i) * VN);
+    }
+  };
+  // Batch b's exponentials, relative to the maximum it leaves in m, and the
+  // next batch's loads.
+  V raw[NV];
+  auto add = [&](int b, float (&e)[kOneVals]) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const bool in_row = (b * NV + j) * kOneThreads + tid < whole;
+#pragma unroll
+      for (int k = 0; k < VN; ++k)
+        e[j * VN + k] = in_row ? static_cast<float>(raw[j][k]) : -INFINITY;
+    }
+    if (b + 1 < batches) load(b + 1, raw);
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < kOneVals; k += 2) top = max_nan(max_nan(top, e[k]), e[k + 1]);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    s *= static_cast<double>(exp_t(fmaxf(m - ref, sc.floor), sc));
+    m = top;
+#pragma unroll
+    for (int k = 0; k < kOneVals; ++k) e[k] = exp_t(e[k] - ref, sc);
+    float sum[kOneVals / 2];
+#pragma unroll
+    for (int k = 0; k < kOneVals / 2; ++k) sum[k] = e[k] + e[k + kOneVals / 2];
+#pragma unroll
+    for (int n = kOneVals / 4; n > 0; n >>= 1)
+#pragma unroll
+      for (int k = 0; k < n; ++k) sum[k] += sum[k + n];
+    s += sum[0];
+  };
+
+  constexpr int kKept = kRegBatches + kLdsBatches;
+  float held[kRegBatches][kOneVals], top_at[kKept];
+  if (batches > 0) load(0, raw);
+#pragma unroll
+  for (int b = 0; b < kRegBatches; ++b) {
+    if (b < batches) {
+      add(b, held[b]);
+      top_at[b] = m;
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < kLdsBatches; ++q) {
+    const int b = kRegBatches + q;
+    if (b < batches) {
+      float e[kOneVals];
+      add(b, e);
+      top_at[b] = m;
+#pragma unroll
+      for (int k = 0; k < kOneVals / 4; ++k)
+        held_lds[q * (kOneVals / 4) + k][tid] = f32x4{e[4 * k], e[4 * k + 1], e[4 * k + 2],
+                                                      e[4 * k + 3]};
+    }
+  }
+  for (int b = kKept; b < batches; ++b) {
+    float e[kOneVals];
+    add(b, e);
+  }
+  const int tail_at = whole * VN + tid;
+  float tail_x = -INFINITY;
+  if (tail_at < vocab) {
+    tail_x = static_cast<float>(rx[tail_at]);
+    const float top = max_nan(m, tail_x), ref = top == -INFINITY ? 0.0f : top;
+    s = s * exp_t(fmaxf(m - ref, sc.floor), sc) + exp_t(fmaxf(tail_x - ref, sc.floor), sc);
+    m = top;
+  }
+  join_group<false, kOneThreads>(m, s, u, sc, wave_part);
+  if (tid == 0) {
+    RowStats st;
+    st.m = m;
+    st.s = s;
+    finish_row(st, token, vocab, xt, sc);
+    row_record = policy_row(p, in, st, sc, r, losses);
+  }
+  __syncthreads();
+  const RowGrad g = row_record;
+
+  // The gradient, the read-again batches first: their end is in the L2.
+  asm volatile("" : "+v"(tid));
+  const int token_vec = token / VN, token_e = token % VN;
+  const bool zero = g.a == 0.0f && g.own == 0.0f;
+  auto store = [&](int b, const float (&e)[kOneVals], float top) {
+    const float scale = zero ? 0.0f : exp_t(fmaxf(top - g.m, sc.floor), sc) * g.a;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = (b * NV + j) * kOneThreads + tid;
+      V o;
+#pragma unroll
+      for (int k = 0; k < VN; ++k) o[k] = static_cast<T>(e[j * VN + k] * scale);
+      if (i == token_vec) {
+#pragma unroll
+        for (int k = 0; k < VN; ++k) o[k] = k == token_e ? static_cast<T>(g.own) : o[k];
+      }
+      if (i < whole)
+        __builtin_nontemporal_store(o, reinterpret_cast<V*>(rd + static_cast<int64_t>(i) * VN));
+    }
+  };
+  if (batches > kKept)
+    row_grad_pass<T, false, kOneThreads>(rx, rd, vocab, kKept * NV * kOneThreads, whole, false,
+                                         token, g, sc);
+  if (tail_at < vocab)
+    rd[tail_at] = static_cast<T>(zero ? 0.0f
+                                      : tail_at == token ? g.own : exp_t(tail_x - g.m, sc) * g.a);
+#pragma unroll
+  for (int q = kLdsBatches - 1; q >= 0; --q) {
+    const int b = kRegBatches + q;
+    if (b < batches) {
+      float e[kOneVals];
+#pragma unroll
+      for (int k = 0; k < kOneVals / 4; ++k) {
+        const f32x4 v = held_lds[q * (kOneVals / 4) + k][tid];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) e[4 * k + t] = v[t];
+      }
+      store(b, e, top_at[b]);
+    }
+  }
+#pragma unroll
+  for (int b = kRegBatches - 1; b >= 0; --b) {
+    if (b < batches) store(b, held[b], top_at[b]);
+  }
+}
+
 // -------------------------------------------------------------- workspace
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -782,6 +985,19 @@ hipError_t policy_loss_t(const TokenRows& t, const PolicyArgs& p, const GradRows
   const Cut cut = cut_rows(t.rows, t.vocab, Vec<T>::n);
   const Workspace w = lay_out(ws, t.rows, t.vocab, 0);
   const bool back = d.x != nullptr;
+  // A row per workgroup keeps a CU busy for 5 us and 0.15 ns an entry, whatever
+  // the number of rows; in two passes the rows are cut up over the card.  With
+  // gradient, two passes and one, us: 8 rows of 32,000 10.4 and 10.4, of 151,936
+  // 13.8 and 26.6; fp32, 64 rows of 151,936 26 and 28, 96 35 and 29; bf16, 96
+  // rows of 151,936 23 and 26, 128 27.6 and 26.4.
+  if (back && t.rows <= (1 << 22) &&
+      (t.vocab <= 32768 || t.rows >= (t.bf16 ? 128 : 96))) {
+    hipLaunchKernelGGL((policy_row_at_once_kernel<T>), dim3(t.rows), dim3(kOneThreads), 0,
+                       stream, static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, t.tokens,
+                       t.weights, sc, p, static_cast<T*>(d.x), d.ld, w.losses);
+    const hipError_t one = hipGetLastError();
+    return one != hipSuccess ? one : launch_sum(w.losses, t.rows, p.loss, stream);
+  }
   hipError_t e = launch_stats<T, false>(t, sc, cut, w, RowInit{}, stream);
   if (e != hipSuccess) return e;
   // Without a gradient and with one workgroup of rows, that one adds up the
