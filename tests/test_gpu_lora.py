@@ -96,6 +96,13 @@ CASES = [
     (320, 128, 400, 16, 1, 0, "one"), (640, 256, 700, 32, 16, 0, "runs"),
     (641, 128, 100, 48, 7, 0, "random"), (50, 128, 90, 16, 4, 0, "bad"),
     (700, 64, 33, 8, 6, 0, "bad"),
+    # wider vocabularies, for every tile shape: 64 x 128 with three stages and
+    # with two, 128 x 128 with two, of few tiles and of many, 256 and 320 rows
+    (60, 128, 25001, 16, 9, 0, "random"), (90, 192, 22300, 40, 12, 0, "runs"),
+    (64, 320, 33100, 24, 64, 0, "random"), (5, 64, 40000, 8, 2, 0, "bad"),
+    (100, 128, 66000, 16, 7, 0, "random"), (133, 192, 31040, 64, 9, 0, "bad"),
+    (256, 128, 60001, 32, 256, 0, "random"), (320, 128, 60000, 24, 20, 1, "runs"),
+    (310, 64, 60100, 8, 3, 0, "bad"), (250, 64, 60002, 16, 1, 0, "none"),
     # hidden sizes that are no multiple of 64
     (5, 72, 33, 8, 2, 0, "random"), (70, 200, 300, 24, 9, 1, "runs"), (260, 136, 140, 64, 5, 0, "bad"),
 ]

@@ -241,8 +241,21 @@ __device__ __forceinline__ bool not_finite(const bf16x8& v) {
   return (any & 0x80008000u) != 0;
 }
 
+// Waits until at most N of the wave's loads are on their way and its LDS reads
+// are done, then for the other waves.  Neither a fence nor __syncthreads(), which
+// would wait for the direct loads of the later stages as well.
+template <int N>
+__device__ __forceinline__ void wait_stage() {
+  static_assert(N < 64, "vmcnt has six bits");
+  // vmcnt in bits 3:0 and 15:14, lgkmcnt 0, expcnt left at its maximum.
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);
+  asm volatile("s_barrier" ::: "memory");
+}
+
+// STAGES: LDS stages, of which all but one are loaded ahead.
 // WAVES: waves that a SIMD is to hold, which bounds the registers.
-template <int BM, int BN, int WAVES_M, int WAVES_N, int AUX, int WAVES>
+template <int BM, int BN, int WAVES_M, int WAVES_N, int AUX, int STAGES, int WAVES>
 __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, WAVES) void lora_gemm_kernel(
     LoraArgs p, DownRows d, int tiles_m, int tiles_total, int tiles_per_xcd) {
   constexpr int NW = WAVES_M * WAVES_N;
@@ -254,14 +267,14 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, WAVES) void lora_gemm_kerne
   constexpr int A_LOADS = BM / 8 / NW;
   static_assert(ROWS / 8 % NW == 0 && BM / 8 % NW == 0, "blocks split evenly over the waves");
   static_assert(WM % 32 == 0 && WN % 32 == 0, "wave tile of whole 32x32 blocks");
-  static_assert(NW * kStoreFloats * 4 <= 2 * STAGE, "store scratch fits the stages");
+  static_assert(NW * kStoreFloats * 4 <= STAGES * STAGE, "store scratch fits the stages");
   static_assert(BM <= 64 * NW, "a thread for every row of the tile");
 
   // One array: with several, the compiler makes every fragment read wait for
   // the direct loads of the next stage.
   using Runs = TileRuns<BM, NW>;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE + sizeof(Runs)];
-  Runs& tr = *reinterpret_cast<Runs*>(lds + 2 * STAGE);
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES * STAGE + sizeof(Runs)];
+  Runs& tr = *reinterpret_cast<Runs*>(lds + STAGES * STAGE);
 
   const int bid = blockIdx.x;
   const int tile = (bid % kXcds) * tiles_per_xcd + bid / kXcds;
@@ -292,7 +305,10 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, WAVES) void lora_gemm_kerne
     tr.row[tid] = my_id == kBadAdapter ? ~my_row : my_row;
   }
   if (tid == 0) tr.met_non_finite = 0;
-  load_stage<LOADS, A_LOADS, NW, AUX>(src, lds, wave, 0);
+  const int ksteps = p.hidden_dim / kBK;
+#pragma unroll
+  for (int st = 0; st < STAGES - 1; ++st)
+    if (st < ksteps) load_stage<LOADS, A_LOADS, NW, AUX>(src, lds + st * STAGE, wave, st * kBK);
 
   f32x16 acc[TM][TN];
 #pragma unroll
@@ -328,13 +344,23 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, WAVES) void lora_gemm_kerne
   };
 
   constexpr int kPerRead = (TM * TN) / (TM + TN) > 0 ? (TM * TN) / (TM + TN) : 1;
-  const int ksteps = p.hidden_dim / kBK;
-  for (int ks = 0; ks < ksteps; ++ks) {
-    const int cur = ks & 1;
-    __builtin_amdgcn_s_waitcnt(0);  // this step's loads have landed in LDS
-    __syncthreads();                // ... for every wave; the other buffer is free
-    if (ks + 1 < ksteps)
-      load_stage<LOADS, A_LOADS, NW, AUX>(src, lds + (cur ^ 1) * STAGE, wave, (ks + 1) * kBK);
+  for (int ks = 0, cur = 0; ks < ksteps; ++ks, cur = cur + 1 == STAGES ? 0 : cur + 1) {
+    // This step's loads have landed in LDS for every wave, and the stage of the
+    // step before is free.
+    if constexpr (STAGES == 2) {
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+    } else {
+      // A wave's loads land in order, LOADS of them a stage; the later stages
+      // may be on their way, near the end only some of them are.
+      if (ks + STAGES - 2 < ksteps)
+        wait_stage<LOADS * (STAGES - 2)>();
+      else
+        wait_stage<0>();
+    }
+    if (ks + STAGES - 1 < ksteps)
+      load_stage<LOADS, A_LOADS, NW, AUX>(
+          src, lds + (cur == 0 ? STAGES - 1 : cur - 1) * STAGE, wave, (ks + STAGES - 1) * kBK);
     bf16x8 af[2][TM], bfr[2][TN];
     frags(cur, 0, af[0], bfr[0]);
 #pragma unroll
@@ -388,23 +414,31 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, WAVES) void lora_gemm_kerne
     if (tid == 0) tr.start[runs] = min(BM, M - m0);
     __syncthreads();
   }
-  // Step q: window w of panel pn, in stage q & 1.
+  // Step q: a window of a panel, in stage q % STAGES.  Half of the stages are
+  // worked on while the other half is filled.
   constexpr int kRuns = kBK / kWindow;  // of a panel
+  constexpr int kGroup = STAGES / 2;
   const int rp = padded_rank(p.rank);
-  const int steps = (runs + kRuns - 1) / kRuns * (rp / kWindow);
-  auto bring = [&](int pn, int w, int stage) {
-    uint8_t* to = lds + stage * STAGE;
-    lora_panel<BM, LOADS, A_LOADS, NW>(p, tr, runs, w, pn, n0, wave, lane, to);
-    lora_rows<BM, NW>(d, rp, w, m0, tr.start[pn * kRuns], tr.start[min(pn * kRuns + kRuns, runs)],
-                      M, wave, lane, to);
-  };
-  if (steps > 0) bring(0, 0, 0);
-  for (int q = 0, pn = 0, w = 0; q < steps; ++q) {
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    const int last_w = w * kWindow + kWindow >= rp;
-    if (q + 1 < steps) bring(last_w ? pn + 1 : pn, last_w ? 0 : w + 1, (q + 1) & 1);
-    const uint8_t* stage = lds + (q & 1) * STAGE;
+  const int windows = rp / kWindow;
+  const int steps = (runs + kRuns - 1) / kRuns * windows;
+  for (int q = -kGroup; q < steps; ++q) {
+    if (q % kGroup == 0) {
+      if (q >= 0) {
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+      }
+#pragma unroll 1
+      for (int t = q + kGroup; t < min(q + 2 * kGroup, steps); ++t) {
+        const int pn = t / windows, w = t - pn * windows;
+        uint8_t* to = lds + (t % STAGES) * STAGE;
+        lora_panel<BM, LOADS, A_LOADS, NW>(p, tr, runs, w, pn, n0, wave, lane, to);
+        lora_rows<BM, NW>(d, rp, w, m0, tr.start[pn * kRuns],
+                          tr.start[min(pn * kRuns + kRuns, runs)], M, wave, lane, to);
+      }
+    }
+    if (q < 0) continue;
+    const int pn = q / windows, w = q - pn * windows;
+    const uint8_t* stage = lds + (q % STAGES) * STAGE;
     const uint8_t* ub = stage + (wm0 + frow) * (kUChunks * 16) + fhalf * 16;
     // Where the panel's runs start and end within the wave's rows.
     const int starts = tr.start[min(pn * kRuns + min(lane, kRuns), runs)] - wm0;
@@ -448,8 +482,6 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, WAVES) void lora_gemm_kerne
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(uf[t], bfr[kk][j], acc[i][j], 0, 0, 0);
       }
     }
-    pn = last_w ? pn + 1 : pn;
-    w = last_w ? 0 : w + 1;
   }
 
   // ---- the logits, a row segment at a time through a scratch of the wave's
@@ -511,13 +543,13 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, WAVES) void lora_gemm_kerne
   }
 }
 
-template <int BM, int BN, int WAVES_M, int WAVES_N, int AUX, int WAVES>
+template <int BM, int BN, int WAVES_M, int WAVES_N, int AUX, int STAGES, int WAVES>
 hipError_t launch_fused(const LoraArgs& p, const DownRows& d, hipStream_t stream) {
   const int tiles_m = (p.rows + BM - 1) / BM;
   const int tiles_n = (p.vocab + BN - 1) / BN;
   const int total = tiles_m * tiles_n;
   const int per_xcd = (total + kXcds - 1) / kXcds;
-  hipLaunchKernelGGL((lora_gemm_kernel<BM, BN, WAVES_M, WAVES_N, AUX, WAVES>), dim3(per_xcd * kXcds),
+  hipLaunchKernelGGL((lora_gemm_kernel<BM, BN, WAVES_M, WAVES_N, AUX, STAGES, WAVES>), dim3(per_xcd * kXcds),
                      dim3(64 * WAVES_M * WAVES_N), 0, stream, p, d, tiles_m, total, per_xcd);
   return hipGetLastError();
 }
@@ -589,15 +621,25 @@ hipError_t launch_lmhead_lora(const LoraArgs& p, void* ws, hipStream_t stream) {
     // 128 rows one row tile reads the lm_head once: past the caches.
     const int64_t pad256 = (p.rows + int64_t{255}) / 256 * 256;
     const int64_t pad320 = (p.rows + int64_t{319}) / 320 * 320;
-    if (p.rows <= 64) return launch_fused<64, 128, 1, 4, 2, 3>(p, d, stream);
-    if (p.rows <= 128) return launch_fused<128, 128, 2, 4, 2, 4>(p, d, stream);
+    // Few tiles: a CU brings in 63 GB/s at most, so 64 x 128 tiles that are
+    // fewer than half the CUs take four times as many, narrow ones (4 rows of
+    // 4,288 and 2,613 columns: 36 us with 21 tiles, 27 with 82; 61 rows and
+    // 25,129 columns, 197 tiles: 54, 83 with 786), and up to one or two a CU a
+    // third stage (90 rows, 22,324 columns: 57 us as 175 tiles of 128 x 128
+    // with two stages, 46 as 350 with three).
+    const int64_t small = (p.rows + int64_t{63}) / 64 * ((p.vocab + int64_t{127}) / 128);
+    if (small <= 128) return launch_fused<32, 32, 1, 1, 0, 6, 1>(p, d, stream);
+    if (small <= 256 || (p.rows > 64 && small <= 512))
+      return launch_fused<64, 128, 1, 4, 0, 3, 2>(p, d, stream);
+    if (p.rows <= 64) return launch_fused<64, 128, 1, 4, 2, 2, 3>(p, d, stream);
+    if (p.rows <= 128) return launch_fused<128, 128, 2, 4, 2, 2, 4>(p, d, stream);
     // A short vocabulary slice makes too few 256-wide tiles for the card: 122 of
     // them (256 x 31,040, H 2,560) take 76 us, the 486 smaller tiles 62; from
     // three quarters of the card on it turns (235 tiles: 100 against 119 us).
     if ((pad256 / 256) * ((p.vocab + 255) / 256) < 192)
-      return launch_fused<128, 128, 2, 4, 0, 4>(p, d, stream);
-    if (pad320 < pad256) return launch_fused<320, 256, 2, 4, 0, 2>(p, d, stream);
-    return launch_fused<256, 256, 2, 4, 0, 2>(p, d, stream);
+      return launch_fused<128, 128, 2, 4, 0, 2, 4>(p, d, stream);
+    if (pad320 < pad256) return launch_fused<320, 256, 2, 4, 0, 2, 2>(p, d, stream);
+    return launch_fused<256, 256, 2, 4, 0, 2, 2>(p, d, stream);
   }
   e = launch_lmhead_gemm(p.hidden, p.ld_hidden, p.lm_head, p.ld_lm_head, p.logits, p.ld_logits,
                          p.rows, p.vocab, p.hidden_dim, stream);
