@@ -111,7 +111,7 @@ SHAPES = [
     # rows, vocab, pad: one and two tokens, odd sizes, below and above a
     # vector, a slab (1,024 vectors) and a chunk, unaligned row starts
     (1, 1, 0), (1, 2, 0), (5, 3, 1), (7, 9, 0), (6, 255, 0), (13, 1000, 24), (12, 4096, 0),
-    (6, 4097, 0), (37, 8192, 3), (8, 30011, 0), (3, 151936, 0), (70, 16390, 5), (1100, 257, 0),
+    (6, 4097, 0), (37, 8192, 3), (8, 30011, 0), (3, 151936, 0), (70, 16390, 5), (1100, 257, 0), (200, 40001, 0),
 ]
 
 
@@ -321,7 +321,7 @@ def pref_offsets(rows, pairs, seed):
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("rows,vocab,pad,pairs", [
     (1, 1, 0, 1), (2, 2, 0, 1), (5, 3, 1, 2), (13, 1000, 24, 3), (37, 4097, 0, 9),
-    (8, 30011, 0, 1), (300, 600, 0, 2), (1100, 257, 0, 40),
+    (8, 30011, 0, 1), (300, 600, 0, 2), (1100, 257, 0, 40), (20, 70001, 0, 3), (200, 40001, 2, 4),
 ])
 def test_preference_loss(rows, vocab, pad, pairs, dtype):
     import torch

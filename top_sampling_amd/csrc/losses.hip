@@ -38,6 +38,7 @@ constexpr int kSlab = kThreads * kBatch;        // vectors a workgroup takes at 
 constexpr int kMaxChunkSlabs = 2;               // longest chunk, in slabs
 constexpr int kTargetGroups = 1024;             // workgroups wanted for few rows
 constexpr int kMaxGrid = 1 << 23;               // workgroups of one launch (grid-stride beyond)
+constexpr int kShortRow = 32768;                // entries: see whole_rows()
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -124,6 +125,22 @@ Cut cut_rows(int64_t rows, int64_t vocab, int vec) {
   c.len = static_cast<int>(len);
   c.chunks = static_cast<int>((nvec + len - 1) / len);
   return c;
+}
+
+// Whether the statistics take a row per workgroup instead of a chunk.  Short
+// rows do at any number, as that saves the records and a launch (2,000
+// entries: 4 against 6 us, 32,000 and 500 rows 13 against 17).  Long ones take a
+// CU too long unless there are enough of them: bf16, 128 rows of 151,936 17
+// against 15 us, 256 18 against 22, 1,024 62 against 70; fp32, 512 rows of
+// 60,000 25 against 27, 640 of 151,936 73 both ways, 800 97 against 89.
+bool whole_rows(int64_t rows, int64_t vocab, int vec) {
+  return vocab <= kShortRow || (rows >= 192 && (vec > 4 || vocab <= 2 * kShortRow));
+}
+
+// The statistics' chunks.
+Cut cut_stats(int64_t rows, int64_t vocab, int vec) {
+  if (!whole_rows(rows, vocab, vec)) return cut_rows(rows, vocab, vec);
+  return Cut{static_cast<int>(vocab / vec), 1};
 }
 
 __device__ __forceinline__ bool left_out(const int32_t* tokens, const float* weights, int row) {
@@ -351,6 +368,27 @@ __device__ __forceinline__ RowGrad row_grad(const RowStats& r, double g, const S
                  static_cast<float>(g * sc.inv_t * -expm1(r.lp))};
 }
 
+// What a row of token_logprobs writes, left out and not; by one thread.
+__device__ __forceinline__ void score_left_out(const ScoreOut& o, int64_t r) {
+  o.logprobs[r] = 0.0f;
+  if (o.entropies) o.entropies[r] = 0.0f;
+  if (o.row_stats) o.row_stats[2 * r] = o.row_stats[2 * r + 1] = 0.0f;
+  if (o.row_status) o.row_status[r] = TS_ROW_OK;
+}
+
+__device__ __forceinline__ void score_row(const ScoreOut& o, const RowStats& st, const Scale& sc,
+                                          int64_t r) {
+  const bool ok = st.status == TS_ROW_OK;
+  o.logprobs[r] = static_cast<float>(st.lp);
+  if (o.entropies)
+    o.entropies[r] = ok ? static_cast<float>(log(st.s) - st.u * sc.inv_t / st.s) : NAN;
+  if (o.row_stats) {
+    o.row_stats[2 * r] = ok ? st.m : NAN;
+    o.row_stats[2 * r + 1] = ok ? static_cast<float>(st.s) : NAN;
+  }
+  if (o.row_status) o.row_status[r] = st.status;
+}
+
 template <bool ENT, typename T>
 __global__ __launch_bounds__(kThreads) void score_rows_kernel(
     const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,
@@ -360,24 +398,38 @@ __global__ __launch_bounds__(kThreads) void score_rows_kernel(
     const int r = static_cast<int>(row);
     const bool writes = threadIdx.x % kRowLanes == 0;
     if (tokens[r] < 0) {
-      if (writes) {
-        o.logprobs[r] = 0.0f;
-        if (ENT) o.entropies[r] = 0.0f;
-        if (o.row_stats) o.row_stats[2 * row] = o.row_stats[2 * row + 1] = 0.0f;
-        if (o.row_status) o.row_status[r] = TS_ROW_OK;
-      }
+      if (writes) score_left_out(o, row);
       continue;
     }
     const RowStats st = join_row<ENT>(x, ld, vocab, tokens[r], r, parts, chunks, sc);
-    if (!writes) continue;
-    const bool ok = st.status == TS_ROW_OK;
-    o.logprobs[r] = static_cast<float>(st.lp);
-    if (ENT) o.entropies[r] = ok ? static_cast<float>(log(st.s) - st.u * sc.inv_t / st.s) : NAN;
-    if (o.row_stats) {
-      o.row_stats[2 * row] = ok ? st.m : NAN;
-      o.row_stats[2 * row + 1] = ok ? static_cast<float>(st.s) : NAN;
+    if (writes) score_row(o, st, sc, row);
+  }
+}
+
+// A workgroup takes a row as a whole, in one launch instead of two.
+template <bool ENT, typename T>
+__global__ __launch_bounds__(kThreads) void score_whole_kernel(
+    const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,
+    Scale sc, ScoreOut o) {
+  __shared__ Part wave_part[kThreads / 64];
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    const int token = tokens[r];
+    if (token < 0) {
+      if (threadIdx.x == 0) score_left_out(o, r);
+      continue;
     }
-    if (o.row_status) o.row_status[r] = st.status;
+    const T* rx = x + r * ld;
+    const float xt = static_cast<float>(rx[min(token, vocab - 1)]);
+    RowStats st;
+    st.m = -INFINITY;
+    st.s = st.u = 0.0;
+    row_stats<T, ENT, kThreads>(rx, vocab, 0, vocab / Vec<T>::n, true, sc, st.m, st.s, st.u);
+    join_group<ENT, kThreads>(st.m, st.s, st.u, sc, wave_part);
+    if (threadIdx.x == 0) {
+      finish_row(st, token, vocab, xt, sc);
+      score_row(o, st, sc, r);
+    }
+    __syncthreads();
   }
 }
 
@@ -481,6 +533,35 @@ __global__ __launch_bounds__(kThreads) void policy_rows_kernel(
   }
 }
 
+// The loss alone, a row per workgroup.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void policy_whole_kernel(
+    const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,
+    const float* __restrict__ weights, Scale sc, PolicyArgs p, double* losses) {
+  __shared__ Part wave_part[kThreads / 64];
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const int r = static_cast<int>(row);
+    const int token = tokens[r];
+    if (left_out(tokens, weights, r)) {
+      if (threadIdx.x == 0) policy_left_out(p, r, losses);
+      continue;
+    }
+    const PolicyRow in = policy_row_inputs(p, weights, r);
+    const T* rx = x + row * ld;
+    const float xt = static_cast<float>(rx[min(token, vocab - 1)]);
+    RowStats st;
+    st.m = -INFINITY;
+    st.s = st.u = 0.0;
+    row_stats<T, false, kThreads>(rx, vocab, 0, vocab / Vec<T>::n, true, sc, st.m, st.s, st.u);
+    join_group<false, kThreads>(st.m, st.s, st.u, sc, wave_part);
+    if (threadIdx.x == 0) {
+      finish_row(st, token, vocab, xt, sc);
+      policy_row(p, in, st, sc, r, losses);
+    }
+    __syncthreads();
+  }
+}
+
 // One workgroup per pair: the log-ratio sums of its two sequences, the pair's
 // loss, and the gradient records of its rows.
 __device__ __forceinline__ void seq_bounds(const int32_t* offsets, int seq, int rows, int& from,
@@ -489,13 +570,16 @@ __device__ __forceinline__ void seq_bounds(const int32_t* offsets, int seq, int 
   to = min(max(offsets[seq + 1], from), rows);
 }
 
+constexpr int kPairThreads = 1024;
+constexpr int kPairRows = kPairThreads / kRowLanes;
+
 template <typename T>
-__global__ __launch_bounds__(kThreads) void preference_pairs_kernel(
+__global__ __launch_bounds__(kPairThreads) void preference_pairs_kernel(
     const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,
     Scale sc, const Part* __restrict__ parts, int chunks, PreferenceArgs p,
     RowGrad* __restrict__ grads, double* __restrict__ losses) {
-  __shared__ double wave_sum[2][kThreads / 64];
-  __shared__ int wave_n[2][kThreads / 64];
+  __shared__ double wave_sum[2][kPairThreads / 64];
+  __shared__ int wave_n[2][kPairThreads / 64];
   __shared__ double coef[2];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int group = tid / kRowLanes;
@@ -506,7 +590,7 @@ __global__ __launch_bounds__(kThreads) void preference_pairs_kernel(
       seq_bounds(p.seq_offsets, pair + side * p.n_pairs, rows, from, to);
       double sum = 0.0;
       int n = 0;
-      for (int row = from + group; row < to; row += kRowsPerGroup) {
+      for (int row = from + group; row < to; row += kPairRows) {
         if (tokens[row] < 0) continue;
         const RowStats st = join_row<false>(x, ld, vocab, tokens[row], row, parts, chunks, sc);
         if (!writes) continue;
@@ -531,7 +615,7 @@ __global__ __launch_bounds__(kThreads) void preference_pairs_kernel(
       for (int side = 0; side < 2; ++side) {
         double s = 0.0;
         int n = 0;
-        for (int w = 0; w < kThreads / 64; ++w) {
+        for (int w = 0; w < kPairThreads / 64; ++w) {
           s += wave_sum[side][w];
           n += wave_n[side][w];
         }
@@ -566,7 +650,7 @@ __global__ __launch_bounds__(kThreads) void preference_pairs_kernel(
         int from, to;
         seq_bounds(p.seq_offsets, pair + side * p.n_pairs, rows, from, to);
         const double k = coef[side];
-        for (int row = from + group; row < to; row += kRowsPerGroup) {
+        for (int row = from + group; row < to; row += kPairRows) {
           if (tokens[row] < 0) continue;
           RowGrad r = grads[row];
           if (k == 0.0) {
@@ -944,6 +1028,16 @@ hipError_t token_logprobs_t(const TokenRows& t, const ScoreOut& o, void* ws, hip
   const Scale sc = make_scale(t.temperature);
   const Cut cut = cut_rows(t.rows, t.vocab, Vec<T>::n);
   const Workspace w = lay_out(ws, t.rows, t.vocab, 0);
+  if (whole_rows(t.rows, t.vocab, Vec<T>::n)) {
+    const dim3 grid(grid_of(t.rows));
+    if (o.entropies != nullptr)
+      hipLaunchKernelGGL((score_whole_kernel<true, T>), grid, dim3(kThreads), 0, stream,
+                         static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, t.tokens, sc, o);
+    else
+      hipLaunchKernelGGL((score_whole_kernel<false, T>), grid, dim3(kThreads), 0, stream,
+                         static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, t.tokens, sc, o);
+    return hipGetLastError();
+  }
   const dim3 grid(grid_of((t.rows + kRowsPerGroup - 1) / kRowsPerGroup));
   if (o.entropies != nullptr) {
     const hipError_t e = launch_stats<T, true>(t, sc, cut, w, RowInit{}, stream);
@@ -991,10 +1085,17 @@ hipError_t policy_loss_t(const TokenRows& t, const PolicyArgs& p, const GradRows
   // 13.8 and 26.6; fp32, 64 rows of 151,936 26 and 28, 96 35 and 29; bf16, 96
   // rows of 151,936 23 and 26, 128 27.6 and 26.4.
   if (back && t.rows <= (1 << 22) &&
-      (t.vocab <= 32768 || t.rows >= (t.bf16 ? 128 : 96))) {
+      (t.vocab <= kShortRow || t.rows >= (t.bf16 ? 128 : 96))) {
     hipLaunchKernelGGL((policy_row_at_once_kernel<T>), dim3(t.rows), dim3(kOneThreads), 0,
                        stream, static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, t.tokens,
                        t.weights, sc, p, static_cast<T*>(d.x), d.ld, w.losses);
+    const hipError_t one = hipGetLastError();
+    return one != hipSuccess ? one : launch_sum(w.losses, t.rows, p.loss, stream);
+  }
+  if (!back && whole_rows(t.rows, t.vocab, Vec<T>::n)) {
+    hipLaunchKernelGGL((policy_whole_kernel<T>), dim3(grid_of(t.rows)), dim3(kThreads), 0, stream,
+                       static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, t.tokens, t.weights, sc,
+                       p, w.losses);
     const hipError_t one = hipGetLastError();
     return one != hipSuccess ? one : launch_sum(w.losses, t.rows, p.loss, stream);
   }
@@ -1019,19 +1120,20 @@ hipError_t preference_loss_t(const TokenRows& t, const PreferenceArgs& p, const 
                              void* ws, hipStream_t stream) {
   const Scale sc = make_scale(t.temperature);
   const Cut cut = cut_rows(t.rows, t.vocab, Vec<T>::n);
+  const Cut stats = cut_stats(t.rows, t.vocab, Vec<T>::n);
   const Workspace w = lay_out(ws, t.rows, t.vocab, p.n_pairs);
   const bool back = d.x != nullptr && t.rows > 0;
   hipError_t e = hipSuccess;
   if (t.rows > 0) {
     const RowInit init{back ? w.grads : nullptr, p.logprobs, p.row_status, p.seq_offsets,
                        2 * p.n_pairs};
-    e = launch_stats<T, false>(t, sc, cut, w, init, stream);
+    e = launch_stats<T, false>(t, sc, stats, w, init, stream);
     if (e != hipSuccess) return e;
   }
   if (p.n_pairs > 0) {
-    hipLaunchKernelGGL((preference_pairs_kernel<T>), dim3(grid_of(p.n_pairs)), dim3(kThreads), 0,
+    hipLaunchKernelGGL((preference_pairs_kernel<T>), dim3(grid_of(p.n_pairs)), dim3(kPairThreads), 0,
                        stream, static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, t.tokens, sc,
-                       w.parts, cut.chunks, p, back ? w.grads : nullptr, w.losses);
+                       w.parts, stats.chunks, p, back ? w.grads : nullptr, w.losses);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
