@@ -580,3 +580,75 @@ def test_long_rows_pass_32_bits():
     want = ts.token_logprobs_backward(logits, tk, b, g)
     got = ts.token_logprobs_backward(big, tk, a, g, grad_logits=big)
     assert torch.equal(got, want)
+
+
+def test_longest_row():
+    """One row of 2^31 - 1 entries (4 GB in bf16), the last ones short of a
+    vector: the largest accepted size."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    vocab = 2 ** 31 - 1
+    dev = torch.device("cuda:0")
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GB of GPU memory")
+    x = torch.zeros(1, vocab, dtype=torch.bfloat16, device=dev)
+    x[0, -1], x[0, 5] = 20.0, 18.0
+    token = torch.tensor([vocab - 1], dtype=torch.int32, device=dev)
+    total = vocab - 2 + np.exp(20.0) + np.exp(18.0)
+    lp = 20.0 - np.log(total)
+    out = ts.token_logprobs(x, token)
+    assert abs(out.logprobs.item() - lp) < LSE + U * abs(lp)
+    one = torch.ones(1, device=dev)
+    grad = ts.token_logprobs_backward(x, token, out, one)
+    # a probability is off by 2 LSE of itself, and then rounded to bf16
+    for at, want in ((vocab - 1, 1 - np.exp(lp)), (vocab - 2, -1 / total), (5, -np.exp(18) / total),
+                     (0, -1 / total), (2 ** 30 + 1, -1 / total)):
+        assert abs(grad[0, at].item() - want) <= abs(want) * (2.0 ** -8 + 4 * LSE), at
+    pol = ts.policy_loss(x, token, out.logprobs, one, grad_logits=x)
+    torch.cuda.synchronize()
+    assert abs(pol.loss.item() + 1) < 4 * LSE
+    assert abs(x[0, -1].item() + (1 - np.exp(lp))) <= 2.0 ** -8 + 4 * LSE
+    assert abs(x[0, 7].item() * total - 1) <= 2.0 ** -8 + 4 * LSE
+
+
+def test_graphs_that_share_a_workspace():
+    """Two captured calls with one workspace, replayed in turn on one stream:
+    nothing is kept in it from call to call."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    dev = torch.device("cuda:0")
+    g = torch.Generator(device=dev)
+    g.manual_seed(2)
+    rows, vocab = 24, 40001
+    x = torch.randn(rows, vocab, generator=g, device=dev)
+    tokens = torch.randint(0, vocab, (rows,), generator=g, device=dev, dtype=torch.int32)
+    old = -torch.rand(rows, generator=g, device=dev) - 10
+    adv = torch.randn(rows, generator=g, device=dev)
+    offsets = torch.tensor([0, 7, 12, 20, 24], dtype=torch.int32, device=dev)
+    ws = torch.empty(ts.preference_loss_workspace_bytes(rows, vocab, 2), dtype=torch.uint8,
+                     device=dev)
+    calls = (lambda: ts.policy_loss(x, tokens, old, adv, backward=True, workspace=ws),
+             lambda: ts.preference_loss(x, tokens, offsets, backward=True, workspace=ws))
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for call in calls:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(call())
+        graphs.append(graph)
+    for i in range(3):
+        x.mul_(0.9)
+        ws.fill_(255)
+        for graph in graphs:
+            graph.replay()
+        got = [(o.loss.clone(), o.grad_logits.clone()) for o in outs]
+        want = [call() for call in calls]
+        torch.cuda.synchronize()
+        for (loss, grad), w in zip(got, want):
+            assert torch.equal(loss, w.loss) and torch.equal(grad, w.grad_logits), i

@@ -12,14 +12,19 @@
 // and the entry of the token itself is written as a value of its own, from
 // 1 - p_t = -expm1(lp), which keeps its digits when p_t is near 1.
 //
-// All of it is bound by the logits' bytes: about eight instructions an
-// element against four (two) bytes read.  Three kernels:
+// All of it is bound by the logits' bytes: about ten instructions an element
+// (the exponential counts for four) against four or two bytes read.
 //   stats  one pass over the logits with a running maximum and sum per
 //          thread; a row is cut into chunks so that a few rows fill the card
 //          too; one record per (row, chunk)
 //   rows   joins a row's records and does the per-row arithmetic in double
 //          (a ratio next to a clip border decides a whole gradient row)
 //   grad   reads the logits again and writes the gradient
+//   whole  short or many rows without a gradient: stats and rows in one, a
+//          row per workgroup
+//   policy_row_at_once  the policy loss with its gradient in one read
+// Measured alone: stats reads 640 x 151,936 fp32 in 63 us (6.2 TB/s), grad
+// reads and writes 256 x 248,320 bf16 in 40 us (6.3 TB/s).
 // exp(x / T) is taken as exp2((x - m) c) with c = log2(e) / T held as two
 // floats, so a temperature's rounding does not tilt the whole sum.
 #include <float.h>
@@ -64,19 +69,19 @@ struct Vec<__bf16> {
 struct Scale {
   float c_hi, c_lo;  // log2(e) / T in two floats, both above 0
   float floor;       // x - m below this gives exp2 = 0
-  double c, inv_t;
+  double inv_t;
 };
 
 Scale make_scale(double temperature) {
   Scale s;
-  s.c = M_LOG2E / temperature;
-  s.c_hi = static_cast<float>(s.c);
-  if (s.c_hi >= s.c) s.c_hi = nextafterf(s.c_hi, 0.0f);
+  const double c = M_LOG2E / temperature;
+  s.c_hi = static_cast<float>(c);
+  if (s.c_hi >= c) s.c_hi = nextafterf(s.c_hi, 0.0f);
   // A temperature beyond 1e30 leaves normal numbers here, and e_j at 1.
   s.c_hi = std::max(s.c_hi, FLT_MIN);
-  s.c_lo = std::max(static_cast<float>(s.c - static_cast<double>(s.c_hi)), FLT_MIN);
+  s.c_lo = std::max(static_cast<float>(c - static_cast<double>(s.c_hi)), FLT_MIN);
   s.inv_t = 1.0 / temperature;
-  s.floor = static_cast<float>(std::max(-200.0 / s.c, -static_cast<double>(FLT_MAX)));
+  s.floor = static_cast<float>(std::max(-200.0 / c, -static_cast<double>(FLT_MAX)));
   return s;
 }
 
@@ -260,20 +265,18 @@ __device__ __forceinline__ void row_stats(const T* row, int vocab, int v0, int v
     s += tree_sum(w);
     if (ENT) u += tree_sum(ut);
   }
-  const int at = vocab / VN * VN + tid;
-  if (tail && at < vocab) {
-    const float x = static_cast<float>(row[at]);
+  if (tail && tid < vocab % VN) {
+    const float x = static_cast<float>(row[vocab - vocab % VN + tid]);
     const float top = max_nan(m, x), ref = top == -INFINITY ? 0.0f : top;
-    const float shift = fmaxf(m - ref, sc.floor), t = fmaxf(x - ref, sc.floor);
+    const float shift = fmaxf(m - ref, sc.floor), t = x - ref;
     const double f = exp_t(shift, sc), ex = exp_t(t, sc);
-    if (ENT) u = f * (u + shift * s) + ex * t;
+    if (ENT) u = f * (u + shift * s) + ex * fmaxf(t, sc.floor);
     s = f * s + ex;
     m = top;
   }
 }
 
-// The workgroup's (m, s, u) joined; threads below THREADS / 64 of the first
-// wave have the result.
+// The workgroup's (m, s, u) joined; the first threads have the result.
 template <bool ENT, int THREADS>
 __device__ __forceinline__ void join_group(float& m, double& s, double& u, const Scale& sc,
                                            Part* wave_part) {
@@ -705,9 +708,10 @@ __device__ __forceinline__ void row_grad_pass(const T* row, T* out, int vocab, i
     const float ex = exp_t(t, sc);
     return is_token ? g.own : (ENT ? ex * fmaf(g.b, t, g.a) : ex * g.a);
   };
-  const int at = vocab / VN * VN + tid;
-  if (tail && at < vocab)
+  if (tail && tid < vocab % VN) {
+    const int at = vocab - vocab % VN + tid;
     out[at] = static_cast<T>(zero ? 0.0f : entry(static_cast<float>(row[at]), at == token));
+  }
   if (v0 >= end) return;
   // The token's vector, and its place in there, if it is one of these.
   const int token_vec = token >= 0 ? token / VN : -1, token_e = token >= 0 ? token % VN : 0;
@@ -904,12 +908,13 @@ __global__ __launch_bounds__(kOneThreads, 2) void policy_row_at_once_kernel(
     float e[kOneVals];
     add(b, e);
   }
-  const int tail_at = whole * VN + tid;
+  const bool in_tail = tid < vocab % VN;
+  const int tail_at = in_tail ? whole * VN + tid : 0;
   float tail_x = -INFINITY;
-  if (tail_at < vocab) {
+  if (in_tail) {
     tail_x = static_cast<float>(rx[tail_at]);
     const float top = max_nan(m, tail_x), ref = top == -INFINITY ? 0.0f : top;
-    s = s * exp_t(fmaxf(m - ref, sc.floor), sc) + exp_t(fmaxf(tail_x - ref, sc.floor), sc);
+    s = s * exp_t(fmaxf(m - ref, sc.floor), sc) + exp_t(tail_x - ref, sc);
     m = top;
   }
   join_group<false, kOneThreads>(m, s, u, sc, wave_part);
@@ -946,7 +951,7 @@ __global__ __launch_bounds__(kOneThreads, 2) void policy_row_at_once_kernel(
   if (batches > kKept)
     row_grad_pass<T, false, kOneThreads>(rx, rd, vocab, kKept * NV * kOneThreads, whole, false,
                                          token, g, sc);
-  if (tail_at < vocab)
+  if (in_tail)
     rd[tail_at] = static_cast<T>(zero ? 0.0f
                                       : tail_at == token ? g.own : exp_t(tail_x - g.m, sc) * g.a);
 #pragma unroll
