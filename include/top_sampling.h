@@ -152,11 +152,13 @@ int lmhead_logits_local(const void* hidden, int64_t rows, int64_t hidden_dim,
  * Adapters of several ranks are padded with zeros to the largest.  Products
  * and sums are fp32; the inner sums are not rounded to bf16.
  * Requirements (else TS_EUNSUPPORTED): those of lmhead_logits_local, rank a
- * multiple of 8 up to TS_MAX_LORA_RANK, ld_a, ld_b and the strides multiples
- * of 8, lora_a and lora_b 16-byte aligned.  n_adapters == 0 or rank == 0 is
- * TS_EINVAL.
+ * multiple of 8 up to TS_MAX_LORA_RANK, rows up to TS_MAX_LORA_ROWS, ld_a, ld_b
+ * and the strides multiples of 8, lora_a and lora_b 16-byte aligned.
+ * n_adapters == 0 or rank == 0 is TS_EINVAL.
  */
-#define TS_MAX_LORA_RANK 256   /* largest accepted adapter rank              */
+#define TS_MAX_LORA_RANK 256       /* largest accepted adapter rank          */
+#define TS_MAX_LORA_ROWS 1048576   /* largest accepted row count (the rows
+                                      are put in order by comparison)        */
 size_t lmhead_lora_workspace_bytes(int64_t rows, int64_t rank);
 int lmhead_logits_local_lora(const void* hidden, int64_t rows, int64_t hidden_dim,
                              int64_t ld_hidden, const void* lm_head, int64_t vocab_local,

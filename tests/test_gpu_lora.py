@@ -183,6 +183,28 @@ def test_rows_do_not_reach_each_other(hidden):
     assert torch.isnan(got[ids == 1]).all() and torch.isnan(got[11]).all()
 
 
+@pytest.mark.parametrize("hidden", [128, 136])
+def test_infinite_inner_sums(hidden):
+    """An infinity in A makes u infinite, and the logits infinite with B's sign
+    (NaN where B is 0), as the formula has it."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    rows, vocab, rank, n = 40, 150, 8, 2
+    x, w, a, b, _ = make(rows, hidden, vocab, rank, n, 9)
+    a[1, 5, 7] = float("inf")
+    x[:, 7] = x[:, 7].abs() + 0.5
+    b[1, 3:9] = 0
+    ids = torch.arange(rows, dtype=torch.int32, device=_dev()) % 2
+    got = ts.lmhead_logits_local_lora(x, w, a, b, ids).cpu()
+    sign = b[1, :, 5].float().cpu()
+    assert torch.isfinite(got[::2]).all()
+    want = torch.where(sign == 0, float("nan"), sign * float("inf"))
+    assert torch.equal(torch.isnan(got[1::2]), torch.isnan(want).expand(rows // 2, -1))
+    assert torch.equal(got[1::2].nan_to_num(0.0), want.expand(rows // 2, -1).nan_to_num(0.0))
+
+
 def test_streams_and_graph():
     import torch
 

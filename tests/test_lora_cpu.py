@@ -34,7 +34,8 @@ def _lora(**kw):
     (dict(n=-1), ts.TS_EINVAL), (dict(n=0), ts.TS_EINVAL), (dict(rank=0), ts.TS_EINVAL),
     (dict(rank=-8), ts.TS_EINVAL), (dict(rank=12, ldb=16), ts.TS_EUNSUPPORTED),
     (dict(rank=264, ldb=264), ts.TS_EUNSUPPORTED), (dict(rows=1 << 31), ts.TS_EUNSUPPORTED),
-    (dict(n=1 << 31), ts.TS_EUNSUPPORTED), (dict(h=0), ts.TS_EINVAL),
+    (dict(n=1 << 31), ts.TS_EUNSUPPORTED),
+    (dict(rows=ts.TS_MAX_LORA_ROWS + 1), ts.TS_EUNSUPPORTED), (dict(h=0), ts.TS_EINVAL),
     (dict(x=None), ts.TS_EINVAL), (dict(w=None), ts.TS_EINVAL), (dict(a=None), ts.TS_EINVAL),
     (dict(b=None), ts.TS_EINVAL), (dict(ids=None), ts.TS_EINVAL), (dict(out=None), ts.TS_EINVAL),
     (dict(ldx=248), ts.TS_EINVAL), (dict(ldw=248), ts.TS_EINVAL), (dict(lda=248), ts.TS_EINVAL),
@@ -62,6 +63,17 @@ def test_workspace_query():
     assert ts.lmhead_lora_workspace_bytes(4, 1000) == 0
     # three bf16 parts of every u, the row and its adapter
     assert ts.lmhead_lora_workspace_bytes(640, 16) >= 640 * (3 * 16 * 2 + 8)
+
+
+def test_header_constants_match_binding():
+    import os
+    import re
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "include", "top_sampling.h")).read()
+    for name in ("TS_MAX_LORA_RANK", "TS_MAX_LORA_ROWS", "TS_PREFERENCE_MEAN"):
+        assert re.search(rf"#define {name} {getattr(ts, name)}\b", text), name
+    assert re.search(rf"TS_F32 = {ts.TS_F32}, TS_BF16 = {ts.TS_BF16}\b", text)
 
 
 def test_binding_refusals():

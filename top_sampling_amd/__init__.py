@@ -49,6 +49,7 @@ PARAMS_BYTES = 24
 TS_F32, TS_BF16 = 0, 1
 TS_PREFERENCE_MEAN = 1
 TS_MAX_LORA_RANK = 256
+TS_MAX_LORA_ROWS = 1 << 20
 
 # (name, restype, argtypes) of every symbol the headers declare
 # (include/top_sampling.h and the measurement aids of top_sampling_measure.h).

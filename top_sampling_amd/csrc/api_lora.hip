@@ -26,7 +26,7 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 extern "C" {
 
 size_t lmhead_lora_workspace_bytes(int64_t rows, int64_t rank) {
-  if (rows < 0 || rank < 0 || rows > kMaxDim || rank > TS_MAX_LORA_RANK) return 0;
+  if (rows < 0 || rank < 0 || rows > TS_MAX_LORA_ROWS || rank > TS_MAX_LORA_RANK) return 0;
   return ts::lmhead_lora_workspace_size(rows, rank);
 }
 
@@ -48,6 +48,8 @@ int lmhead_logits_local_lora(const void* hidden, int64_t rows, int64_t hidden_di
   if (rank > TS_MAX_LORA_RANK || rank % 8)
     return fail(TS_EUNSUPPORTED, "rank %lld is not a multiple of 8 up to %d (pad with zeros)",
                 (long long)rank, TS_MAX_LORA_RANK);
+  if (rows > TS_MAX_LORA_ROWS)
+    return fail(TS_EUNSUPPORTED, "rows %lld above %d", (long long)rows, TS_MAX_LORA_ROWS);
   if (rows == 0 || vocab_local == 0) return TS_OK;
   if (hidden_dim == 0) return fail(TS_EINVAL, "hidden_dim == 0 with a non-empty output");
   if (!hidden || !lm_head || !lora_a || !lora_b || !adapter_ids || !logits)

@@ -72,11 +72,12 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraArgs p, Dow
       const uint16_t* x = p.hidden + static_cast<int64_t>(r) * p.ld_hidden;
       const uint16_t* a = p.a + static_cast<int64_t>(id) * p.stride_a +
                           static_cast<int64_t>(k0) * p.ld_a;
-      for (int h0 = lane * 8; h0 < p.hidden_dim; h0 += kDownStep * 512) {
+      const unsigned hidden = p.hidden_dim;  // h0 may pass 2^31
+      for (unsigned h0 = lane * 8; h0 < hidden; h0 += kDownStep * 512) {
         bf16x8 xv[kDownStep], av[kDownStep][kPerWave];
 #pragma unroll
         for (int q = 0; q < kDownStep; ++q) {
-          const int h = min(h0 + q * 512, p.hidden_dim - 8);
+          const unsigned h = min(h0 + q * 512, hidden - 8);
           xv[q] = *reinterpret_cast<const bf16x8*>(x + h);
 #pragma unroll
           for (int k = 0; k < kPerWave; ++k)
@@ -84,7 +85,7 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraArgs p, Dow
         }
 #pragma unroll
         for (int q = 0; q < kDownStep; ++q) {
-          if (h0 + q * 512 >= p.hidden_dim) continue;
+          if (h0 + q * 512 >= hidden) continue;
 #pragma unroll
           for (int k = 0; k < kPerWave; ++k)
 #pragma unroll
@@ -116,7 +117,8 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraArgs p, Dow
       for (int q = 0; q < kParts; ++q) {
         const __bf16 part = static_cast<__bf16>(rest);
         if (lane == k) u[q * kWindow + k] = part;
-        rest -= static_cast<float>(part);
+        // Of an infinity nothing is left (the difference would be NaN).
+        rest = fabsf(static_cast<float>(part)) < INFINITY ? rest - static_cast<float>(part) : 0.0f;
       }
     }
     __syncthreads();
@@ -193,7 +195,7 @@ __device__ __forceinline__ void lora_panel(const LoraArgs& p, const TileRuns<BM,
     const int run = min(pn * (kBK / kWindow) + (c >> 1), runs - 1);
     const int k = w * kWindow + (c & 1) * 8;
     const uint16_t* src = p.b + static_cast<int64_t>(tr.adapter[run]) * p.stride_b +
-                          static_cast<int64_t>(min(n0 + r - BM, p.vocab - 1)) * p.ld_b +
+                          static_cast<int64_t>(n0 + min(r - BM, p.vocab - 1 - n0)) * p.ld_b +
                           (k < p.rank ? k : 0);
     __builtin_amdgcn_global_load_lds(src, stage + (wave + NW * q) * 1024, 16, 0, 0);
   }
@@ -295,7 +297,7 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, WAVES) void lora_gemm_kerne
     if (q < A_LOADS)
       src[q] = p.hidden + static_cast<int64_t>(d.row[min(m0 + r, M - 1)]) * p.ld_hidden + c * 8;
     else
-      src[q] = p.lm_head + static_cast<int64_t>(min(n0 + r - BM, N - 1)) * p.ld_lm_head + c * 8;
+      src[q] = p.lm_head + static_cast<int64_t>(n0 + min(r - BM, N - 1 - n0)) * p.ld_lm_head + c * 8;
   }
   const bool in = tid < BM && m0 + tid < M;
   const int my_id = in ? d.id[m0 + tid] : kNoAdapter;
@@ -479,7 +481,8 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, WAVES) void lora_gemm_kerne
         for (int t = kParts - 1; t >= 0; --t)
 #pragma unroll
           for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(uf[t], bfr[kk][j], acc[i][j], 0, 0, 0);
+            acc[i][j] =
+                __builtin_amdgcn_mfma_f32_32x32x16_bf16(uf[t], bfr[kk][j], acc[i][j], 0, 0, 0);
       }
     }
   }
@@ -498,26 +501,26 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, WAVES) void lora_gemm_kerne
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-      const int col = n0 + wn0 + j * 32 + c0;
+      const int col = wn0 + j * 32 + c0, left = N - n0;  // from n0 on
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int rr = (lane >> 3) + 8 * q;
         const int at = wm0 + i * 32 + rr;
         f32x4 v = *reinterpret_cast<const f32x4*>(scr + rr * kStoreStride + c0);
-        if (m0 + at >= M || col >= N) continue;
+        if (m0 + at >= M || col >= left) continue;
         int row = tr.row[at];
         if (row < 0) {
           row = ~row;
 #pragma unroll
           for (int t = 0; t < 4; ++t) v[t] = NAN;
         }
-        float* dst = p.logits + static_cast<int64_t>(row) * p.ld_logits + col;
-        if (col + 3 < N) {
+        float* dst = p.logits + static_cast<int64_t>(row) * p.ld_logits + n0 + col;
+        if (col + 3 < left) {
           *reinterpret_cast<f32x4u*>(dst) = v;
         } else {
 #pragma unroll
           for (int t = 0; t < 4; ++t)
-            if (col + t < N) dst[t] = v[t];
+            if (col + t < left) dst[t] = v[t];
         }
       }
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -530,8 +533,9 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, WAVES) void lora_gemm_kerne
   __syncthreads();
   if (tr.met_non_finite == 0) return;
   for (int at = tid; at < BM * BN; at += 64 * NW) {
-    const int place = at / BN, v = n0 + at % BN;
-    if (m0 + place >= M || v >= N || tr.id[place] < 0) continue;
+    const int place = at / BN;
+    if (m0 + place >= M || at % BN >= N - n0 || tr.id[place] < 0) continue;
+    const int v = n0 + at % BN;
     const __bf16* u = d.u + static_cast<int64_t>(m0 + place) * rp * kParts;
     const uint16_t* b = p.b + static_cast<int64_t>(tr.id[place]) * p.stride_b +
                         static_cast<int64_t>(v) * p.ld_b;
@@ -546,11 +550,12 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, WAVES) void lora_gemm_kerne
 template <int BM, int BN, int WAVES_M, int WAVES_N, int AUX, int STAGES, int WAVES>
 hipError_t launch_fused(const LoraArgs& p, const DownRows& d, hipStream_t stream) {
   const int tiles_m = (p.rows + BM - 1) / BM;
-  const int tiles_n = (p.vocab + BN - 1) / BN;
+  const int tiles_n = (p.vocab - 1) / BN + 1;
   const int total = tiles_m * tiles_n;
   const int per_xcd = (total + kXcds - 1) / kXcds;
-  hipLaunchKernelGGL((lora_gemm_kernel<BM, BN, WAVES_M, WAVES_N, AUX, STAGES, WAVES>), dim3(per_xcd * kXcds),
-                     dim3(64 * WAVES_M * WAVES_N), 0, stream, p, d, tiles_m, total, per_xcd);
+  hipLaunchKernelGGL((lora_gemm_kernel<BM, BN, WAVES_M, WAVES_N, AUX, STAGES, WAVES>),
+                     dim3(per_xcd * kXcds), dim3(64 * WAVES_M * WAVES_N), 0, stream, p, d, tiles_m,
+                     total, per_xcd);
   return hipGetLastError();
 }
 
@@ -560,7 +565,7 @@ constexpr int kUpCols = 256;
 // logits += B_a u, one workgroup per row and kUpCols columns.
 __global__ __launch_bounds__(kUpCols) void lora_add_kernel(LoraArgs p, DownRows d) {
   const int rp = padded_rank(p.rank);
-  const int v = blockIdx.x * kUpCols + threadIdx.x;
+  const int64_t v = static_cast<int64_t>(blockIdx.x) * kUpCols + threadIdx.x;
   for (int place = blockIdx.y; place < p.rows; place += gridDim.y) {
     const int id = d.id[place];
     if (id == kNoAdapter || v >= p.vocab) continue;
@@ -570,7 +575,7 @@ __global__ __launch_bounds__(kUpCols) void lora_add_kernel(LoraArgs p, DownRows 
       continue;
     }
     const __bf16* u = d.u + static_cast<int64_t>(place) * rp * kParts;
-    const uint16_t* b = p.b + static_cast<int64_t>(id) * p.stride_b + static_cast<int64_t>(v) * p.ld_b;
+    const uint16_t* b = p.b + static_cast<int64_t>(id) * p.stride_b + v * p.ld_b;
     float sum = 0.0f;
     for (int k = 0; k < p.rank; k += 8) {
       const bf16x8 bv = *reinterpret_cast<const bf16x8*>(b + k);
@@ -636,7 +641,7 @@ hipError_t launch_lmhead_lora(const LoraArgs& p, void* ws, hipStream_t stream) {
     // A short vocabulary slice makes too few 256-wide tiles for the card: 122 of
     // them (256 x 31,040, H 2,560) take 76 us, the 486 smaller tiles 62; from
     // three quarters of the card on it turns (235 tiles: 100 against 119 us).
-    if ((pad256 / 256) * ((p.vocab + 255) / 256) < 192)
+    if ((pad256 / 256) * ((p.vocab + int64_t{255}) / 256) < 192)
       return launch_fused<128, 128, 2, 4, 0, 2, 4>(p, d, stream);
     if (pad320 < pad256) return launch_fused<320, 256, 2, 4, 0, 2, 2>(p, d, stream);
     return launch_fused<256, 256, 2, 4, 0, 2, 2>(p, d, stream);
@@ -645,7 +650,7 @@ hipError_t launch_lmhead_lora(const LoraArgs& p, void* ws, hipStream_t stream) {
                          p.rows, p.vocab, p.hidden_dim, stream);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(lora_add_kernel,
-                     dim3((p.vocab + kUpCols - 1) / kUpCols, p.rows < 65535 ? p.rows : 65535),
+                     dim3((p.vocab + int64_t{kUpCols} - 1) / kUpCols, p.rows < 65535 ? p.rows : 65535),
                      dim3(kUpCols), 0, stream, p, d);
   return hipGetLastError();
 }
