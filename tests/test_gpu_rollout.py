@@ -1,0 +1,131 @@
+"""The adapter, sampler, scoring and loss calls together, as a fine-tuning step
+of adapters makes them: rows of several requests are projected each under its
+adapter, a token is sampled for every row, the reference scores it without
+adapters, and a loss's gradient comes back for the logits.  Every step is
+checked against the float64 oracle on the step's own inputs."""
+import numpy as np
+import pytest
+
+import workloads
+from oracle import losses as ref
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+LSE = 1.2e-5  # of a log-probability, derived in test_gpu_losses.py
+
+
+def _setup(rows, hidden, vocab, rank, n, seed):
+    import torch
+
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    dev = torch.device("cuda:0")
+    g = torch.Generator(device=dev)
+    g.manual_seed(seed)
+
+    def bf(*shape, std):
+        return (torch.randn(*shape, generator=g, device=dev) * std).to(torch.bfloat16)
+
+    x, w = bf(rows, hidden, std=1.0), bf(vocab, hidden, std=0.08)
+    a, b = bf(n, rank, hidden, std=hidden ** -0.5), bf(n, vocab, rank, std=0.2)
+    ids = torch.randint(-1, n, (rows,), generator=g, device=dev, dtype=torch.int32)
+    scales = torch.rand(n, generator=g, device=dev) + 0.5
+    return dev, g, x, w, a, b, ids, scales
+
+
+def _params(rows, dev, temperature):
+    import top_sampling_amd as ts
+
+    p = np.zeros(rows, dtype=workloads.PARAMS_DTYPE)
+    p["temperature"], p["top_p"] = temperature, 1.0
+    p["seed"] = np.arange(rows) + 17
+    return ts.params_to_device(p, dev)
+
+
+def f64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+@pytest.mark.parametrize("rows,hidden,vocab", [(24, 128, 4097), (200, 192, 33003)])
+def test_policy_step(rows, hidden, vocab):
+    import torch
+
+    import top_sampling_amd as ts
+
+    dev, g, x, w, a, b, ids, scales = _setup(rows, hidden, vocab, 16, 5, rows)
+    temperature = 0.9
+    # rollout
+    logits = ts.lmhead_logits_local_lora(x, w, a, b, ids, scales)
+    drawn = ts.sampler_sample(logits, _params(rows, dev, temperature), processed=True)
+    assert (drawn.token_ids >= 0).all() and (drawn.row_status == 0).all()
+    # the sampler's log-probabilities of what it drew are those of scoring it:
+    # the sampler's own bound is 1e-4
+    scored = ts.token_logprobs(logits, drawn.token_ids, temperature)
+    assert (scored.logprobs - drawn.token_logprobs).abs().max() < 1e-4 + LSE
+    # reference: the same rows without adapters
+    base = ts.lmhead_logits_local(x, w)
+    none = torch.full_like(ids, -1)
+    assert torch.equal(base, ts.lmhead_logits_local_lora(x, w, a, b, none, scales))
+    reference = ts.token_logprobs(base, drawn.token_ids, temperature).logprobs
+    # the policy has moved since: every adapter a little
+    b2 = (b.float() * 1.05).to(torch.bfloat16)
+    now = ts.lmhead_logits_local_lora(x, w, a, b2, ids, scales)
+    adv = torch.randn(rows, generator=g, device=dev)
+    live = (torch.rand(rows, generator=g, device=dev) < 0.9).float()
+    weights = live / live.sum()
+    kw = dict(clip_low=0.2, clip_high=0.28, kl_coef=0.05, temperature=temperature)
+    got = ts.policy_loss(now, drawn.token_ids, drawn.token_logprobs, adv, reference, weights,
+                         backward=True, **kw)
+    torch.cuda.synchronize()
+    tokens = drawn.token_ids.cpu().numpy()
+    want = ref.policy(f64(now), tokens, f64(drawn.token_logprobs), f64(adv), f64(reference),
+                      f64(weights), **kw)
+    lp = want["logprobs"]
+    assert (np.abs(f64(got.logprobs) - lp) <= LSE + U * np.abs(lp)).all()
+    # rows whose ratio is nearer to a border than its error may take either side
+    near = np.minimum(np.abs(want["ratios"] - 0.8), np.abs(want["ratios"] - 1.28)) < 1e-4
+    size = f64(weights) * (np.abs(f64(adv)) * want["ratios"] + 0.05 * 4)
+    tol = size[:, None] * 3 * LSE / temperature + np.abs(want["grad"]) * 4e-5
+    off = np.abs(f64(got.grad_logits) - want["grad"]) - tol
+    assert (off[~near] <= 0).all()
+    # the loss along a direction, by differences: its fp32 value is off by
+    # 2 U |loss| + LSE sum(size), over a step of 2 h; the third derivative
+    # adds h^2.
+    d = torch.randn(rows, vocab, generator=g, device=dev)
+    h = 1e-2
+    up, down = (ts.policy_loss(now + s * h * d, drawn.token_ids, drawn.token_logprobs, adv,
+                               reference, weights, **{**kw, "clip_low": np.inf,
+                                                      "clip_high": np.inf}).loss.item()
+                for s in (1, -1))
+    free = ts.policy_loss(now, drawn.token_ids, drawn.token_logprobs, adv, reference, weights,
+                          backward=True, **{**kw, "clip_low": np.inf, "clip_high": np.inf})
+    slope = (free.grad_logits.double() * d.double()).sum().item()
+    bound = (2 * U * abs(up) + LSE * size.sum()) / h + 10 * h * h * size.sum()
+    assert abs((up - down) / (2 * h) - slope) <= bound
+
+
+def test_preference_step_in_place():
+    import torch
+
+    import top_sampling_amd as ts
+
+    rows, hidden, vocab, pairs = 60, 128, 5001, 3
+    dev, g, x, w, a, b, ids, scales = _setup(rows, hidden, vocab, 24, 4, 3)
+    logits = ts.lmhead_logits_local_lora(x, w, a, b, ids, scales)
+    tokens = torch.randint(0, vocab, (rows,), generator=g, device=dev, dtype=torch.int32)
+    tokens[::7] = -1  # prompt rows
+    reference = ts.token_logprobs(ts.lmhead_logits_local(x, w), tokens).logprobs
+    offsets = torch.tensor([0, 11, 19, 30, 30, 52, 60], dtype=torch.int32, device=dev)
+    x64 = f64(logits)
+    want = ref.preference(x64, tokens.cpu().numpy(), offsets.tolist(), f64(reference), beta=0.2,
+                          mean=True)
+    got = ts.preference_loss(logits, tokens, offsets, reference, beta=0.2, mean=True,
+                             grad_logits=logits)
+    torch.cuda.synchronize()
+    assert got.grad_logits is logits
+    assert abs(got.loss.item() - want["loss"]) < 0.2 * 2 * LSE + 2 * U * want["loss"]
+    tol = np.abs(want["grad"]) * 6e-5 + 0.2 / 3 * 4 * LSE * (want["grad"] != 0) * \
+        np.exp(ref.log_softmax(x64, 1.0)).clip(1e-9)
+    tol[np.arange(rows), tokens.cpu().numpy().clip(0)] += 0.2 / 3 * 4 * LSE
+    assert (np.abs(f64(logits) - want["grad"]) <= tol).all()
+    assert not logits[::7].any()
