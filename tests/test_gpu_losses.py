@@ -279,11 +279,17 @@ def test_policy_loss_long_rows(dtype, rows, vocab, pad):
     torch.cuda.synchronize()
     assert (wide[:, vocab:] == 7.0).all()
     check_policy(got, want, x, 0.8, dtype, rows, f(w), f(adv), 0.1)
+    first = [t.clone() for t in (got.grad_logits, got.loss)]
+    same = ts.policy_loss(logits, *args, grad_logits=wide[:, :vocab], **kw)
+    assert torch.equal(same.grad_logits, first[0]) and torch.equal(same.loss, first[1])
+    # In this gradient the rows start elsewhere in their cache lines, so the
+    # sums run in another order: both are within the bound, not bit for bit one.
     again = ts.policy_loss(logits, *args, backward=True, **kw)
-    assert torch.equal(again.grad_logits, got.grad_logits) and torch.equal(again.loss, got.loss)
+    check_policy(again, want, x, 0.8, dtype, rows, f(w), f(adv), 0.1)
     same = logits.clone()
+    beside = ts.policy_loss(same, *args, backward=True, **kw)
     ts.policy_loss(same, *args, grad_logits=same, **kw)
-    assert torch.equal(same, got.grad_logits)
+    assert torch.equal(same, beside.grad_logits)
 
 
 def test_policy_clip_limits_and_no_weights():
@@ -652,3 +658,63 @@ def test_graphs_that_share_a_workspace():
         torch.cuda.synchronize()
         for (loss, grad), w in zip(got, want):
             assert torch.equal(loss, w.loss) and torch.equal(grad, w.grad_logits), i
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("vocab", [1, 6, 40, 71, 131, 1000, 33001])
+def test_every_alignment(dtype, vocab):
+    """Rows that start anywhere in a cache line, the gradient's elsewhere than
+    the logits'; what lies between the rows is left alone."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    rows = 3
+    kind = torch.float32 if dtype == "fp32" else torch.bfloat16
+    g = torch.Generator(device="cpu")
+    g.manual_seed(vocab)
+    x0 = torch.randn(rows, vocab, generator=g).mul(3).to(kind)
+    tok = torch.tensor([0, vocab - 1, vocab // 2], dtype=torch.int32, device=_dev())
+    x = x0.double().numpy()
+    e = np.exp(x - x.max(-1, keepdims=True))
+    prob = e / e.sum(-1, keepdims=True)
+    lp = np.log(prob[np.arange(rows), tok.cpu().numpy()])
+    adv = torch.tensor([1.0, -2.0, 0.5], device=_dev())
+    want = prob.copy()
+    want[np.arange(rows), tok.cpu().numpy()] -= 1.0
+    # 1 - p of a likely token comes from its log-probability
+    tol = grad_tol(want, x, 1.0, dtype, 4 * LSE) + 4 * LSE * (want < 0)
+    old = to_dev(lp)
+    for at, stride, grad_at, grad_stride in ((0, 0, 0, 0), (1, 0, 1, 0), (5, 3, 0, 1), (63, 0, 2, 7),
+                                             (32, 64 - vocab % 64, 31, 64 - vocab % 64),
+                                             (7, 1, 7, 1)):
+        say("alignment", dtype, vocab, at, stride, grad_at, grad_stride)
+        ld, ldg = vocab + stride, vocab + grad_stride
+        wide = torch.full((at + rows * ld + 70,), 7.0, dtype=kind, device=_dev())
+        logits = wide[at:].as_strided((rows, vocab), (ld, 1), at)
+        logits.copy_(x0)
+        out = ts.token_logprobs(logits, tok)
+        close(out.logprobs, lp, LSE + U * np.abs(lp), "logprobs")
+        buf = torch.full((grad_at + rows * ldg + 70,), 7.0, dtype=kind, device=_dev())
+        grad = buf.as_strided((rows, vocab), (ldg, 1), grad_at)
+        ts.token_logprobs_backward(logits, tok, out, -torch.ones_like(adv), grad_logits=grad)
+        close(grad, want, tol, "backward")
+        grad.fill_(7.0)
+        pol = ts.policy_loss(logits, tok, old, adv, clip_low=np.inf, clip_high=np.inf,
+                             grad_logits=grad)
+        close(pol.logprobs, lp, LSE + U * np.abs(lp), "policy logprobs")
+        a = adv.cpu().double().numpy()[:, None]
+        close(grad, a * want, np.abs(a) * (tol + np.abs(want) * 2 * LSE), "policy")
+        pair = ts.preference_loss(logits, tok, torch.tensor([0, 1, 3], dtype=torch.int32,
+                                                            device=_dev()), grad_logits=grad)
+        close(pair.logprobs, lp, LSE + U * np.abs(lp), "preference logprobs")
+        rho = 0.1 * (lp[0] - lp[1] - lp[2])
+        k = 0.1 / (1 + np.exp(rho)) * np.array([[1.0], [-1.0], [-1.0]])
+        close(grad, k * want, np.abs(k) * (tol + np.abs(want) * 4 * LSE), "preference")
+        grad.fill_(7.0)
+        assert (buf == 7.0).all()
+        inplace = ts.token_logprobs_backward(logits, tok, out, -torch.ones_like(adv),
+                                             grad_logits=logits)
+        close(inplace, want, tol, "in place")
+        logits.fill_(7.0)
+        assert (wide == 7.0).all()

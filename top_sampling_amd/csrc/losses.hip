@@ -181,6 +181,40 @@ __device__ __forceinline__ float tree_sum(float (&w)[kBatch][VN]) {
   return v[0];
 }
 
+// A row as vectors: `edge` entries at its two ends, and between them `whole`
+// vectors from entry `head` on, which starts a cache line of `lines`, the
+// gradient's row.  With vectors from entry 0 on a row of odd length has every
+// store across a line's border.  From 0 and from a line on, 1,021 x 100,277:
+// loss and gradient, bf16 104 and 87 us (87 too where the rows are whole lines
+// apart), fp32 180 and 164; backward pass of the log-probabilities, bf16 84
+// and 74, fp32 152 and 142.  From a 16-byte border on: bf16 98 and 75, fp32 179
+// and 150.
+// Loads alone only mind bf16's 2-byte borders (log-probabilities, bf16 47 and
+// 42 us, fp32 74 both ways), so the statistics of fp32 rows, whose last digits
+// depend on how a row is cut, are taken from entry 0 on.
+struct Shape {
+  int head, whole, edge;
+
+  // The place of edge entry i.
+  template <typename T>
+  __device__ __forceinline__ int at(int i) const {
+    return i < head ? i : i + whole * Vec<T>::n;
+  }
+};
+
+constexpr int kLine = 128;
+
+template <typename T>
+__device__ __forceinline__ Shape row_shape(const T* lines, int vocab) {
+  constexpr int PER = kLine / sizeof(T);
+  const int past = static_cast<int>(reinterpret_cast<uintptr_t>(lines) / sizeof(T) % PER);
+  Shape f;
+  f.head = min((PER - past) % PER, vocab);
+  f.whole = (vocab - f.head) / Vec<T>::n;
+  f.edge = vocab - f.whole * Vec<T>::n;
+  return f;
+}
+
 // ------------------------------------------------------------------- stats
 // What the pass sets for every row before the later kernels fill in the rows
 // that take part (any pointer may be null), and the rows that do: with
@@ -193,7 +227,7 @@ struct RowInit {
   int n_seqs;
 };
 
-// A slab of a row's whole vectors, kThreads x kBatch of them from v on; past
+// A slab of a row's whole vectors, THREADS x kBatch of them from v on; past
 // `end` the loads repeat the last vector and are not used.
 template <typename T, int THREADS>
 struct Slab {
@@ -215,22 +249,24 @@ struct Slab {
   }
 };
 
-// A thread's share of vectors [v0, v1) of a row joined into m, s, u; `tail`:
-// also the row's last entries, short of a vector.  The next slab's loads are
-// in flight while a slab is added up.
+// A thread's share of vectors [v0, v1) of a row joined into m, s, u; `edge`:
+// also the entries at the row's ends.  The next slab's loads are in flight
+// while a slab is added up.
 template <typename T, bool ENT, int THREADS>
-__device__ __forceinline__ void row_stats(const T* row, int vocab, int v0, int v1, bool tail,
+__device__ __forceinline__ void row_stats(const T* row, int vocab, int v0, int v1, bool edge,
                                           const Scale& sc, float& m, double& s, double& u) {
   constexpr int VN = Vec<T>::n;
   const int tid = threadIdx.x;
-  const int end = min(v1, vocab / VN);
+  const Shape f = sizeof(T) < 4 ? row_shape(row, vocab) : Shape{0, vocab / VN, vocab % VN};
+  const T* body = row + f.head;
+  const int end = min(v1, f.whole);
   Slab<T, THREADS> next;
-  if (v0 < end) next.load(row, v0, end);
+  if (v0 < end) next.load(body, v0, end);
   for (int v = v0; v < end; v += THREADS * kBatch) {
     float w[kBatch][VN], ut[kBatch][VN];
     next.unpack(w);
     if (v + THREADS * kBatch < end) {
-      next.load(row, v + THREADS * kBatch, end);
+      next.load(body, v + THREADS * kBatch, end);
     }
     if (v + THREADS * kBatch > end) {
 #pragma unroll
@@ -246,9 +282,9 @@ __device__ __forceinline__ void row_stats(const T* row, int vocab, int v0, int v
       for (int e = 0; e < VN; e += 2) top = max_nan(max_nan(top, w[j][e]), w[j][e + 1]);
     const float ref = top == -INFINITY ? 0.0f : top;
     const float shift = fmaxf(m - ref, sc.floor);
-    const double f = exp_t(shift, sc);
-    if (ENT) u = f * (u + shift * s);
-    s *= f;
+    const double keep = exp_t(shift, sc);
+    if (ENT) u = keep * (u + shift * s);
+    s *= keep;
     m = top;
     // A batch is added up as a tree, and the batches in double: behind a term
     // near 1, terms below half an fp32 step would all be lost one by one, and
@@ -265,13 +301,13 @@ __device__ __forceinline__ void row_stats(const T* row, int vocab, int v0, int v
     s += tree_sum(w);
     if (ENT) u += tree_sum(ut);
   }
-  if (tail && tid < vocab % VN) {
-    const float x = static_cast<float>(row[vocab - vocab % VN + tid]);
+  if (edge && tid < f.edge) {
+    const float x = static_cast<float>(row[f.template at<T>(tid)]);
     const float top = max_nan(m, x), ref = top == -INFINITY ? 0.0f : top;
     const float shift = fmaxf(m - ref, sc.floor), t = x - ref;
-    const double f = exp_t(shift, sc), ex = exp_t(t, sc);
-    if (ENT) u = f * (u + shift * s) + ex * fmaxf(t, sc.floor);
-    s = f * s + ex;
+    const double keep = exp_t(shift, sc), ex = exp_t(t, sc);
+    if (ENT) u = keep * (u + shift * s) + ex * fmaxf(t, sc.floor);
+    s = keep * s + ex;
     m = top;
   }
 }
@@ -690,31 +726,36 @@ __device__ __forceinline__ RowGrad score_row_grad(const ScoreGrad& g, int row, b
                  static_cast<float>(own * sc.inv_t)};
 }
 
-// The gradient of vectors [v0, v1) of a row (and with `tail` of its last
-// entries), slab by slab from the last to the first: the end of what the
+// The gradient of vectors [v0, v1) of a row (and with `edge` of the entries at
+// its ends), slab by slab from the last to the first: the end of what the
 // statistics pass read is still in the caches.  The stores go past them.
 template <typename T, bool ENT, int THREADS>
 __device__ __forceinline__ void row_grad_pass(const T* row, T* out, int vocab, int v0, int v1,
-                                              bool tail, int token, const RowGrad& g,
+                                              bool edge, int token, const RowGrad& g,
                                               const Scale& sc) {
   constexpr int VN = Vec<T>::n;
+  const Shape f = row_shape(out, vocab);
   constexpr int SLAB = THREADS * kBatch;
   using V = typename Vec<T>::Type;
   const int tid = threadIdx.x;
-  const int end = min(v1, vocab / VN);
+  const int end = min(v1, f.whole);
   const bool zero = g.a == 0.0f && g.b == 0.0f && g.own == 0.0f;
   auto entry = [&](float x, bool is_token) {
     const float t = ENT ? fmaxf(x - g.m, sc.floor) : x - g.m;
     const float ex = exp_t(t, sc);
     return is_token ? g.own : (ENT ? ex * fmaf(g.b, t, g.a) : ex * g.a);
   };
-  if (tail && tid < vocab % VN) {
-    const int at = vocab - vocab % VN + tid;
+  if (edge && tid < f.edge) {
+    const int at = f.template at<T>(tid);
     out[at] = static_cast<T>(zero ? 0.0f : entry(static_cast<float>(row[at]), at == token));
   }
   if (v0 >= end) return;
+  row += f.head;
+  out += f.head;
   // The token's vector, and its place in there, if it is one of these.
-  const int token_vec = token >= 0 ? token / VN : -1, token_e = token >= 0 ? token % VN : 0;
+  const bool in_body = token >= f.head;
+  const int token_vec = in_body ? (token - f.head) / VN : -1;
+  const int token_e = in_body ? (token - f.head) % VN : 0;
   int v = v0 + (end - 1 - v0) / SLAB * SLAB;
   Slab<T, THREADS> next;
   if (!zero) next.load(row, v, end);
@@ -776,7 +817,9 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(
       const bool skip = token < 0;
       // The gradient may replace the logits, so the token's own logit is only
       // read by the workgroup that also writes it.
-      const int owner = min(token / VN / cut.len, cut.chunks - 1);
+      const Shape f = row_shape(rd, vocab);
+      const int vec = (token - f.head) / VN;
+      const int owner = token < f.head || vec >= f.whole ? cut.chunks - 1 : vec / cut.len;
       const bool mine = token >= 0 && token < vocab && owner == chunk;
       const float xt = mine ? static_cast<float>(rx[token]) : 0.0f;
       g = score_row_grad(sg, row, skip, xt, sc);
@@ -793,19 +836,21 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(
 // One workgroup per row, alone on its CU, which holds the row between the
 // statistics and the gradient: every exponential goes into a register or into
 // LDS, relative to the thread's maximum at that point, and the gradient pass
-// only scales it.  160 registers and 64 LDS words a thread hold 114,688
+// only scales it.  144 registers and 64 LDS words a thread hold 106,496
 // entries; what a longer row has beyond them is read a second time.  In two
 // passes the second read costs as much as the first, out of the Infinity Cache
 // too: reads and writes together pass at 6.5-6.8 TB/s.  Loss and gradient of
 // 640 x 151,936 fp32 in two passes and in one: 192 and 157 us (one read and
-// one write take 120 at that rate, the quarter that is read again 15); 1,024 x
-// 151,936 bf16: 155 and 129; 1,021 x 100,277 bf16: 113 and 103.  Loads one
-// batch ahead are best (1,024 x 151,936: two ahead 142 us, all at once 150; the
-// batches' exponentials then run after the loads and not under them),
-// as are ten register batches (eleven spill).
+// one write take 120 at that rate, the three tenths that are read again 18);
+// 1,024 x 151,936 bf16: 155 and 127.  Loads one batch ahead are best (1,024 x
+// 151,936: two ahead 142 us, all at once 150; the batches' exponentials then
+// run after the loads and not under them), as are nine register batches (with
+// ten, which spill two registers in bf16, 1,021 x 100,277 takes 91 us, not 87).
+// Holding the logits and not the exponentials, twice as many in bf16 and so two
+// workgroups a CU, is no faster (129 us), and slower for short rows.
 constexpr int kOneThreads = 512;
 constexpr int kOneVals = 16;                         // entries of a thread's batch
-constexpr int kRegBatches = 10;
+constexpr int kRegBatches = 9;
 constexpr int kLdsBatches = 4;
 
 template <typename T>
@@ -819,7 +864,8 @@ __global__ __launch_bounds__(kOneThreads, 2) void policy_row_at_once_kernel(
   __shared__ f32x4 held_lds[kLdsBatches * kOneVals / 4][kOneThreads];
   __shared__ Part wave_part[kOneThreads / 64];
   __shared__ RowGrad row_record;
-  const int whole = vocab / VN;
+  const Shape f = row_shape(d + static_cast<int64_t>(blockIdx.x) * ldd, vocab);
+  const int whole = f.whole;
   const int batches = (whole + NV * kOneThreads - 1) / (NV * kOneThreads);
 
   // No loop over rows: with one the compiler keeps the batches' registers
@@ -842,13 +888,14 @@ __global__ __launch_bounds__(kOneThreads, 2) void policy_row_at_once_kernel(
   const PolicyRow in = policy_row_inputs(p, weights, r);
   const float xt = static_cast<float>(rx[min(token, vocab - 1)]);
 
+  const char* body = reinterpret_cast<const char*>(rx + f.head);
   float m = -INFINITY;
   double s = 0.0, u = 0.0;
   auto load = [&](int b, V (&raw)[NV]) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = min((b * NV + j) * kOneThreads + tid, whole - 1);
-      raw[j] = *reinterpret_cast<const V*>(rx + static_cast<int64_t>(i) * VN);
+      raw[j] = *reinterpret_cast<const V*>(body + static_cast<uint32_t>(i) * 16u);
     }
   };
   // Batch b's exponentials, relative to the maximum it leaves in m, and the
@@ -908,13 +955,13 @@ __global__ __launch_bounds__(kOneThreads, 2) void policy_row_at_once_kernel(
     float e[kOneVals];
     add(b, e);
   }
-  const bool in_tail = tid < vocab % VN;
-  const int tail_at = in_tail ? whole * VN + tid : 0;
-  float tail_x = -INFINITY;
-  if (in_tail) {
-    tail_x = static_cast<float>(rx[tail_at]);
-    const float top = max_nan(m, tail_x), ref = top == -INFINITY ? 0.0f : top;
-    s = s * exp_t(fmaxf(m - ref, sc.floor), sc) + exp_t(tail_x - ref, sc);
+  const bool in_edge = tid < f.edge;
+  const int edge_at = in_edge ? f.template at<T>(tid) : 0;
+  float edge_x = -INFINITY;
+  if (in_edge) {
+    edge_x = static_cast<float>(rx[edge_at]);
+    const float top = max_nan(m, edge_x), ref = top == -INFINITY ? 0.0f : top;
+    s = s * exp_t(fmaxf(m - ref, sc.floor), sc) + exp_t(edge_x - ref, sc);
     m = top;
   }
   join_group<false, kOneThreads>(m, s, u, sc, wave_part);
@@ -930,7 +977,10 @@ __global__ __launch_bounds__(kOneThreads, 2) void policy_row_at_once_kernel(
 
   // The gradient, the read-again batches first: their end is in the L2.
   asm volatile("" : "+v"(tid));
-  const int token_vec = token / VN, token_e = token % VN;
+  const bool in_body = token >= f.head;
+  const int token_vec = in_body ? (token - f.head) / VN : -1;
+  const int token_e = in_body ? (token - f.head) % VN : 0;
+  char* out = reinterpret_cast<char*>(rd + f.head);
   const bool zero = g.a == 0.0f && g.own == 0.0f;
   auto store = [&](int b, const float (&e)[kOneVals], float top) {
     const float scale = zero ? 0.0f : exp_t(fmaxf(top - g.m, sc.floor), sc) * g.a;
@@ -945,15 +995,15 @@ __global__ __launch_bounds__(kOneThreads, 2) void policy_row_at_once_kernel(
         for (int k = 0; k < VN; ++k) o[k] = k == token_e ? static_cast<T>(g.own) : o[k];
       }
       if (i < whole)
-        __builtin_nontemporal_store(o, reinterpret_cast<V*>(rd + static_cast<int64_t>(i) * VN));
+        __builtin_nontemporal_store(o, reinterpret_cast<V*>(out + static_cast<uint32_t>(i) * 16u));
     }
   };
   if (batches > kKept)
     row_grad_pass<T, false, kOneThreads>(rx, rd, vocab, kKept * NV * kOneThreads, whole, false,
                                          token, g, sc);
-  if (in_tail)
-    rd[tail_at] = static_cast<T>(zero ? 0.0f
-                                      : tail_at == token ? g.own : exp_t(tail_x - g.m, sc) * g.a);
+  if (in_edge)
+    rd[edge_at] = static_cast<T>(zero ? 0.0f
+                                      : edge_at == token ? g.own : exp_t(edge_x - g.m, sc) * g.a);
 #pragma unroll
   for (int q = kLdsBatches - 1; q >= 0; --q) {
     const int b = kRegBatches + q;
@@ -1089,7 +1139,7 @@ hipError_t policy_loss_t(const TokenRows& t, const PolicyArgs& p, const GradRows
   // gradient, two passes and one, us: 8 rows of 32,000 10.4 and 10.4, of 151,936
   // 13.8 and 26.6; fp32, 64 rows of 151,936 26 and 28, 96 35 and 29; bf16, 96
   // rows of 151,936 23 and 26, 128 27.6 and 26.4.
-  if (back && t.rows <= (1 << 22) &&
+  if (back && t.rows <= (1 << 22) && t.vocab <= (1 << 29) &&
       (t.vocab <= kShortRow || t.rows >= (t.bf16 ? 128 : 96))) {
     hipLaunchKernelGGL((policy_row_at_once_kernel<T>), dim3(t.rows), dim3(kOneThreads), 0,
                        stream, static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, t.tokens,
