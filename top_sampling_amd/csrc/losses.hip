@@ -20,8 +20,8 @@
 //   rows   joins a row's records and does the per-row arithmetic in double
 //          (a ratio next to a clip border decides a whole gradient row)
 //   grad   reads the logits again and writes the gradient
-//   whole  short or many rows without a gradient: stats and rows in one, a
-//          row per workgroup
+//   whole  short or many rows: stats and rows in one, a row per workgroup
+//   pairs  the preference loss's sums over its sequences
 //   policy_row_at_once  the policy loss with its gradient in one read
 // Measured alone: stats reads 640 x 151,936 fp32 in 63 us (6.2 TB/s), grad
 // reads and writes 256 x 248,320 bf16 in 40 us (6.3 TB/s).
@@ -142,15 +142,18 @@ bool whole_rows(int64_t rows, int64_t vocab, int vec) {
   return vocab <= kShortRow || (rows >= 192 && (vec > 4 || vocab <= 2 * kShortRow));
 }
 
-// The statistics' chunks.
-Cut cut_stats(int64_t rows, int64_t vocab, int vec) {
-  if (!whole_rows(rows, vocab, vec)) return cut_rows(rows, vocab, vec);
-  return Cut{static_cast<int>(vocab / vec), 1};
-}
+// Which rows of a call take part; the others are not read.
+struct RowsIn {
+  const int32_t* tokens;   // a negative one leaves its row out,
+  const float* weights;    // as a weight of 0 does,
+  const int32_t* offsets;  // and a place outside [offsets[0], offsets[n_seqs])
+  int n_seqs;
 
-__device__ __forceinline__ bool left_out(const int32_t* tokens, const float* weights, int row) {
-  return tokens[row] < 0 || (weights != nullptr && weights[row] == 0.0f);
-}
+  __device__ __forceinline__ bool left_out(int row) const {
+    return tokens[row] < 0 || (weights != nullptr && weights[row] == 0.0f) ||
+           (offsets != nullptr && (row < offsets[0] || row >= offsets[n_seqs]));
+  }
+};
 
 // Joins (m, s, u) of a group of `width` lanes (a power of two); every lane
 // gets the result.  An empty part has m = -inf and s = u = 0.
@@ -216,17 +219,6 @@ __device__ __forceinline__ Shape row_shape(const T* lines, int vocab) {
 }
 
 // ------------------------------------------------------------------- stats
-// What the pass sets for every row before the later kernels fill in the rows
-// that take part (any pointer may be null), and the rows that do: with
-// `offsets`, only those of [offsets[0], offsets[n_seqs]).
-struct RowInit {
-  RowGrad* grads;
-  float* logprobs;
-  int32_t* row_status;
-  const int32_t* offsets;
-  int n_seqs;
-};
-
 // A slab of a row's whole vectors, THREADS x kBatch of them from v on; past
 // `end` the loads repeat the last vector and are not used.
 template <typename T, int THREADS>
@@ -332,20 +324,14 @@ __device__ __forceinline__ void join_group(float& m, double& s, double& u, const
 
 template <typename T, bool ENT>
 __global__ __launch_bounds__(kThreads) void stats_kernel(
-    const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,
-    const float* __restrict__ weights, Scale sc, Cut cut, Part* __restrict__ parts, RowInit init) {
+    const T* __restrict__ x, int64_t ld, int rows, int vocab, RowsIn in, Scale sc, Cut cut,
+    Part* __restrict__ parts) {
   __shared__ Part wave_part[kThreads / 64];
   const int tid = threadIdx.x;
   const int64_t total = static_cast<int64_t>(rows) * cut.chunks;
   for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
     const int row = static_cast<int>(b / cut.chunks), chunk = static_cast<int>(b % cut.chunks);
-    if (chunk == 0 && tid == 0) {
-      if (init.grads) init.grads[row] = RowGrad{0.0f, 0.0f, 0.0f, 0.0f};
-      if (init.logprobs) init.logprobs[row] = 0.0f;
-      if (init.row_status) init.row_status[row] = TS_ROW_OK;
-    }
-    if (left_out(tokens, weights, row)) continue;
-    if (init.offsets && (row < init.offsets[0] || row >= init.offsets[init.n_seqs])) continue;
+    if (in.left_out(row)) continue;
     float m = -INFINITY;
     double s = 0.0, u = 0.0;
     row_stats<T, ENT, kThreads>(x + static_cast<int64_t>(row) * ld, vocab, chunk * cut.len,
@@ -545,22 +531,22 @@ __device__ __forceinline__ RowGrad policy_row(const PolicyArgs& p, const PolicyR
 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void policy_rows_kernel(
-    const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,
-    const float* __restrict__ weights, Scale sc, const Part* __restrict__ parts, int chunks,
-    PolicyArgs p, RowGrad* __restrict__ grads, double* losses, int sum_here) {
+    const T* __restrict__ x, int64_t ld, int rows, int vocab, RowsIn rows_in, Scale sc,
+    const Part* __restrict__ parts, int chunks, PolicyArgs p, RowGrad* __restrict__ grads,
+    double* losses, int sum_here) {
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsPerGroup + threadIdx.x / kRowLanes;
        row < rows; row += static_cast<int64_t>(gridDim.x) * kRowsPerGroup) {
     const int r = static_cast<int>(row);
     const bool writes = threadIdx.x % kRowLanes == 0;
-    if (left_out(tokens, weights, r)) {
+    if (rows_in.left_out(r)) {
       if (writes) {
         policy_left_out(p, r, losses);
         if (grads) grads[r] = RowGrad{0.0f, 0.0f, 0.0f, 0.0f};
       }
       continue;
     }
-    const PolicyRow in = policy_row_inputs(p, weights, r);
-    const RowStats st = join_row<false>(x, ld, vocab, tokens[r], r, parts, chunks, sc);
+    const PolicyRow in = policy_row_inputs(p, rows_in.weights, r);
+    const RowStats st = join_row<false>(x, ld, vocab, rows_in.tokens[r], r, parts, chunks, sc);
     if (!writes) continue;
     const RowGrad g = policy_row(p, in, st, sc, r, losses);
     if (grads) grads[r] = g;
@@ -575,17 +561,17 @@ __global__ __launch_bounds__(kThreads) void policy_rows_kernel(
 // The loss alone, a row per workgroup.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void policy_whole_kernel(
-    const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,
-    const float* __restrict__ weights, Scale sc, PolicyArgs p, double* losses) {
+    const T* __restrict__ x, int64_t ld, int rows, int vocab, RowsIn rows_in, Scale sc,
+    PolicyArgs p, double* losses) {
   __shared__ Part wave_part[kThreads / 64];
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
     const int r = static_cast<int>(row);
-    const int token = tokens[r];
-    if (left_out(tokens, weights, r)) {
+    const int token = rows_in.tokens[r];
+    if (rows_in.left_out(r)) {
       if (threadIdx.x == 0) policy_left_out(p, r, losses);
       continue;
     }
-    const PolicyRow in = policy_row_inputs(p, weights, r);
+    const PolicyRow in = policy_row_inputs(p, rows_in.weights, r);
     const T* rx = x + row * ld;
     const float xt = static_cast<float>(rx[min(token, vocab - 1)]);
     RowStats st;
@@ -601,65 +587,124 @@ __global__ __launch_bounds__(kThreads) void policy_whole_kernel(
   }
 }
 
-// One workgroup per pair: the log-ratio sums of its two sequences, the pair's
-// loss, and the gradient records of its rows.
+// What a row of the preference loss writes, left out and not; by one thread.
+// The gradient records are for dL/dlp = 1; the pair kernel scales them.
+__device__ __forceinline__ void preference_left_out(const PreferenceArgs& p, int r, double* ratios,
+                                                    RowGrad* grads) {
+  ratios[r] = 0.0;
+  if (p.logprobs) p.logprobs[r] = 0.0f;
+  if (p.row_status) p.row_status[r] = TS_ROW_OK;
+  if (grads) grads[r] = RowGrad{0.0f, 0.0f, 0.0f, 0.0f};
+}
+
+__device__ __forceinline__ void preference_row(const PreferenceArgs& p, const RowStats& st,
+                                               const Scale& sc, int r, double* ratios,
+                                               RowGrad* grads) {
+  ratios[r] = st.lp - (p.ref_logprobs ? static_cast<double>(p.ref_logprobs[r]) : 0.0);
+  if (p.logprobs) p.logprobs[r] = static_cast<float>(st.lp);
+  if (p.row_status) p.row_status[r] = st.status;
+  if (grads) grads[r] = row_grad(st, 1.0, sc);
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void preference_rows_kernel(
+    const T* __restrict__ x, int64_t ld, int rows, int vocab, RowsIn rows_in, Scale sc,
+    const Part* __restrict__ parts, int chunks, PreferenceArgs p, RowGrad* __restrict__ grads,
+    double* __restrict__ ratios) {
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsPerGroup + threadIdx.x / kRowLanes;
+       row < rows; row += static_cast<int64_t>(gridDim.x) * kRowsPerGroup) {
+    const int r = static_cast<int>(row);
+    const bool writes = threadIdx.x % kRowLanes == 0;
+    if (rows_in.left_out(r)) {
+      if (writes) preference_left_out(p, r, ratios, grads);
+      continue;
+    }
+    const RowStats st = join_row<false>(x, ld, vocab, rows_in.tokens[r], r, parts, chunks, sc);
+    if (writes) preference_row(p, st, sc, r, ratios, grads);
+  }
+}
+
+// A row per workgroup, in one launch instead of two.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void preference_whole_kernel(
+    const T* __restrict__ x, int64_t ld, int rows, int vocab, RowsIn rows_in, Scale sc,
+    PreferenceArgs p, RowGrad* __restrict__ grads, double* __restrict__ ratios) {
+  __shared__ Part wave_part[kThreads / 64];
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const int r = static_cast<int>(row);
+    if (rows_in.left_out(r)) {
+      if (threadIdx.x == 0) preference_left_out(p, r, ratios, grads);
+      continue;
+    }
+    const int token = rows_in.tokens[r];
+    const T* rx = x + row * ld;
+    const float xt = static_cast<float>(rx[min(token, vocab - 1)]);
+    RowStats st;
+    st.m = -INFINITY;
+    st.s = st.u = 0.0;
+    row_stats<T, false, kThreads>(rx, vocab, 0, vocab / Vec<T>::n, true, sc, st.m, st.s, st.u);
+    join_group<false, kThreads>(st.m, st.s, st.u, sc, wave_part);
+    if (threadIdx.x == 0) {
+      finish_row(st, token, vocab, xt, sc);
+      preference_row(p, st, sc, r, ratios, grads);
+    }
+    __syncthreads();
+  }
+}
+
+// One workgroup per pair, half of it for each answer: the log-ratio sums of its
+// two sequences, the pair's loss, and the factors of its rows' gradient
+// records.  The rows' records are joined before, over the whole card: done here,
+// one pair of 1,000-row answers over 32,000 entries took 178 us in all, not 133,
+// and 8 pairs of 64-row answers over 151,936 entries (bf16) 164, not 156.
 __device__ __forceinline__ void seq_bounds(const int32_t* offsets, int seq, int rows, int& from,
                                            int& to) {
   from = min(max(offsets[seq], 0), rows);
   to = min(max(offsets[seq + 1], from), rows);
 }
 
-constexpr int kPairThreads = 1024;
-constexpr int kPairRows = kPairThreads / kRowLanes;
+constexpr int kPairThreads = 512;
 
-template <typename T>
 __global__ __launch_bounds__(kPairThreads) void preference_pairs_kernel(
-    const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,
-    Scale sc, const Part* __restrict__ parts, int chunks, PreferenceArgs p,
-    RowGrad* __restrict__ grads, double* __restrict__ losses) {
-  __shared__ double wave_sum[2][kPairThreads / 64];
-  __shared__ int wave_n[2][kPairThreads / 64];
+    int rows, const int32_t* __restrict__ tokens, PreferenceArgs p,
+    const double* __restrict__ ratios, RowGrad* __restrict__ grads, double* __restrict__ losses) {
+  constexpr int kWaves = kPairThreads / 64;
+  constexpr int kSide = kPairThreads / 2;  // threads of each answer
+  __shared__ double wave_sum[kWaves];
+  __shared__ int wave_n[kWaves];
   __shared__ double coef[2];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int group = tid / kRowLanes;
-  const bool writes = tid % kRowLanes == 0;
+  const int side = tid / kSide;
   for (int pair = blockIdx.x; pair < p.n_pairs; pair += gridDim.x) {
-    for (int side = 0; side < 2; ++side) {
-      int from, to;
-      seq_bounds(p.seq_offsets, pair + side * p.n_pairs, rows, from, to);
-      double sum = 0.0;
-      int n = 0;
-      for (int row = from + group; row < to; row += kPairRows) {
-        if (tokens[row] < 0) continue;
-        const RowStats st = join_row<false>(x, ld, vocab, tokens[row], row, parts, chunks, sc);
-        if (!writes) continue;
-        sum += st.lp - (p.ref_logprobs ? static_cast<double>(p.ref_logprobs[row]) : 0.0);
-        ++n;
-        if (p.logprobs) p.logprobs[row] = static_cast<float>(st.lp);
-        if (p.row_status) p.row_status[row] = st.status;
-        if (grads != nullptr) grads[row] = row_grad(st, 1.0, sc);
-      }
-      for (int d = 32; d > 0; d >>= 1) {
-        sum += __shfl_xor(sum, d, 64);
-        n += __shfl_xor(n, d, 64);
-      }
-      if (lane == 0) {
-        wave_sum[side][wave] = sum;
-        wave_n[side][wave] = n;
-      }
+    int from, to;
+    seq_bounds(p.seq_offsets, pair + side * p.n_pairs, rows, from, to);
+    double sum = 0.0;
+    int n = 0;
+    for (int64_t row = int64_t{from} + tid % kSide; row < to; row += kSide) {
+      if (tokens[row] < 0) continue;
+      sum += ratios[row];
+      ++n;
+    }
+    for (int d = 32; d > 0; d >>= 1) {
+      sum += __shfl_xor(sum, d, 64);
+      n += __shfl_xor(n, d, 64);
+    }
+    if (lane == 0) {
+      wave_sum[wave] = sum;
+      wave_n[wave] = n;
     }
     __syncthreads();
     if (tid == 0) {
       double rho[2], per[2];
-      for (int side = 0; side < 2; ++side) {
+      for (int q = 0; q < 2; ++q) {
         double s = 0.0;
-        int n = 0;
-        for (int w = 0; w < kPairThreads / 64; ++w) {
-          s += wave_sum[side][w];
-          n += wave_n[side][w];
+        int count = 0;
+        for (int w = q * kWaves / 2; w < (q + 1) * kWaves / 2; ++w) {
+          s += wave_sum[w];
+          count += wave_n[w];
         }
-        per[side] = p.mean && n > 0 ? 1.0 / n : 1.0;
-        rho[side] = s * per[side];
+        per[q] = p.mean && count > 0 ? 1.0 / count : 1.0;
+        rho[q] = s * per[q];
       }
       const double beta = p.beta, eps = p.label_smoothing;
       const double z = beta * (rho[0] - rho[1]) - p.margin;
@@ -683,23 +728,18 @@ __global__ __launch_bounds__(kPairThreads) void preference_pairs_kernel(
       }
     }
     __syncthreads();
-    if (grads != nullptr && writes) {
-      // The same lanes as above, so each scales the records that it wrote.
-      for (int side = 0; side < 2; ++side) {
-        int from, to;
-        seq_bounds(p.seq_offsets, pair + side * p.n_pairs, rows, from, to);
-        const double k = coef[side];
-        for (int row = from + group; row < to; row += kPairRows) {
-          if (tokens[row] < 0) continue;
-          RowGrad r = grads[row];
-          if (k == 0.0) {
-            r = RowGrad{0.0f, 0.0f, 0.0f, 0.0f};
-          } else {
-            r.a = static_cast<float>(r.a * k);
-            r.own = static_cast<float>(r.own * k);
-          }
-          grads[row] = r;
+    if (grads != nullptr) {
+      const double k = coef[side];
+      for (int64_t row = int64_t{from} + tid % kSide; row < to; row += kSide) {
+        if (tokens[row] < 0) continue;
+        RowGrad r = grads[row];
+        if (k == 0.0) {
+          r = RowGrad{0.0f, 0.0f, 0.0f, 0.0f};
+        } else {
+          r.a = static_cast<float>(r.a * k);
+          r.own = static_cast<float>(r.own * k);
         }
+        grads[row] = r;
       }
     }
     __syncthreads();
@@ -855,8 +895,8 @@ constexpr int kLdsBatches = 4;
 
 template <typename T>
 __global__ __launch_bounds__(kOneThreads, 2) void policy_row_at_once_kernel(
-    const T* x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,
-    const float* __restrict__ weights, Scale sc, PolicyArgs p, T* d, int64_t ldd,
+    const T* x, int64_t ld, int rows, int vocab, RowsIn rows_in, Scale sc, PolicyArgs p, T* d,
+    int64_t ldd,
     double* __restrict__ losses) {
   constexpr int VN = Vec<T>::n;
   constexpr int NV = kOneVals / VN;  // vectors of a thread's batch
@@ -878,14 +918,14 @@ __global__ __launch_bounds__(kOneThreads, 2) void policy_row_at_once_kernel(
   asm volatile("" : "+v"(tid));
   const T* rx = x + row * ld;
   T* rd = d + row * ldd;
-  const int token = tokens[r];
-  if (left_out(tokens, weights, r)) {
+  const int token = rows_in.tokens[r];
+  if (rows_in.left_out(r)) {
     if (tid == 0) policy_left_out(p, r, losses);
     row_grad_pass<T, false, kOneThreads>(rx, rd, vocab, 0, whole, true, token,
                                          RowGrad{0.0f, 0.0f, 0.0f, 0.0f}, sc);
     return;
   }
-  const PolicyRow in = policy_row_inputs(p, weights, r);
+  const PolicyRow in = policy_row_inputs(p, rows_in.weights, r);
   const float xt = static_cast<float>(rx[min(token, vocab - 1)]);
 
   const char* body = reinterpret_cast<const char*>(rx + f.head);
@@ -1030,11 +1070,12 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 struct Workspace {
   Part* parts;
   RowGrad* grads;
-  double* losses;
+  double* terms;   // of the rows: loss terms, or log ratios
+  double* losses;  // of the pairs
   size_t bytes;
 };
 
-Workspace lay_out(void* base, int64_t rows, int64_t vocab, int64_t terms) {
+Workspace lay_out(void* base, int64_t rows, int64_t vocab, int64_t n_pairs) {
   const int chunks = std::max(cut_rows(rows, vocab, Vec<float>::n).chunks,
                               cut_rows(rows, vocab, Vec<__bf16>::n).chunks);
   char* p = static_cast<char*>(base);
@@ -1044,8 +1085,10 @@ Workspace lay_out(void* base, int64_t rows, int64_t vocab, int64_t terms) {
   at += round256(sizeof(Part) * static_cast<size_t>(rows) * chunks);
   w.grads = reinterpret_cast<RowGrad*>(p + at);
   at += round256(sizeof(RowGrad) * static_cast<size_t>(rows));
+  w.terms = reinterpret_cast<double*>(p + at);
+  at += round256(sizeof(double) * static_cast<size_t>(rows));
   w.losses = reinterpret_cast<double*>(p + at);
-  at += round256(sizeof(double) * static_cast<size_t>(terms > rows ? terms : rows));
+  at += round256(sizeof(double) * static_cast<size_t>(n_pairs));
   w.bytes = at;
   return w;
 }
@@ -1056,20 +1099,21 @@ int grid_of(int64_t groups) {
 
 template <typename T, bool ENT>
 hipError_t launch_stats(const TokenRows& t, const Scale& sc, const Cut& cut, const Workspace& w,
-                        const RowInit& init, hipStream_t stream) {
+                        const RowsIn& in, hipStream_t stream) {
   hipLaunchKernelGGL((stats_kernel<T, ENT>), dim3(grid_of(int64_t{t.rows} * cut.chunks)),
                      dim3(kThreads), 0, stream, static_cast<const T*>(t.x), t.ld, t.rows, t.vocab,
-                     t.tokens, t.weights, sc, cut, w.parts, init);
+                     in, sc, cut, w.parts);
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t launch_grad(const TokenRows& t, const Scale& sc, const Cut& cut, const Workspace& w,
-                       const GradRows& d, int64_t terms, float* loss, hipStream_t stream) {
+                       const GradRows& d, const double* losses, int64_t n_losses, float* loss,
+                       hipStream_t stream) {
   hipLaunchKernelGGL((grad_kernel<T, false, false>), dim3(grid_of(int64_t{t.rows} * cut.chunks)),
                      dim3(kThreads), 0, stream, static_cast<const T*>(t.x), t.ld, t.rows, t.vocab,
-                     t.tokens, sc, cut, w.grads, ScoreGrad{}, static_cast<T*>(d.x), d.ld, w.losses,
-                     terms, loss);
+                     t.tokens, sc, cut, w.grads, ScoreGrad{}, static_cast<T*>(d.x), d.ld, losses,
+                     n_losses, loss);
   return hipGetLastError();
 }
 
@@ -1083,6 +1127,7 @@ hipError_t token_logprobs_t(const TokenRows& t, const ScoreOut& o, void* ws, hip
   const Scale sc = make_scale(t.temperature);
   const Cut cut = cut_rows(t.rows, t.vocab, Vec<T>::n);
   const Workspace w = lay_out(ws, t.rows, t.vocab, 0);
+  const RowsIn in{t.tokens, nullptr, nullptr, 0};
   if (whole_rows(t.rows, t.vocab, Vec<T>::n)) {
     const dim3 grid(grid_of(t.rows));
     if (o.entropies != nullptr)
@@ -1093,15 +1138,15 @@ hipError_t token_logprobs_t(const TokenRows& t, const ScoreOut& o, void* ws, hip
                          static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, t.tokens, sc, o);
     return hipGetLastError();
   }
-  const dim3 grid(grid_of((t.rows + kRowsPerGroup - 1) / kRowsPerGroup));
+  const dim3 grid(grid_of((t.rows + int64_t{kRowsPerGroup} - 1) / kRowsPerGroup));
   if (o.entropies != nullptr) {
-    const hipError_t e = launch_stats<T, true>(t, sc, cut, w, RowInit{}, stream);
+    const hipError_t e = launch_stats<T, true>(t, sc, cut, w, in, stream);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((score_rows_kernel<true, T>), grid, dim3(kThreads), 0, stream,
                        static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, t.tokens, sc, w.parts,
                        cut.chunks, o);
   } else {
-    const hipError_t e = launch_stats<T, false>(t, sc, cut, w, RowInit{}, stream);
+    const hipError_t e = launch_stats<T, false>(t, sc, cut, w, in, stream);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((score_rows_kernel<false, T>), grid, dim3(kThreads), 0, stream,
                        static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, t.tokens, sc, w.parts,
@@ -1133,6 +1178,7 @@ hipError_t policy_loss_t(const TokenRows& t, const PolicyArgs& p, const GradRows
   const Scale sc = make_scale(t.temperature);
   const Cut cut = cut_rows(t.rows, t.vocab, Vec<T>::n);
   const Workspace w = lay_out(ws, t.rows, t.vocab, 0);
+  const RowsIn in{t.tokens, t.weights, nullptr, 0};
   const bool back = d.x != nullptr;
   // A row per workgroup keeps a CU busy for 5 us and 0.15 ns an entry, whatever
   // the number of rows; in two passes the rows are cut up over the card.  With
@@ -1142,32 +1188,30 @@ hipError_t policy_loss_t(const TokenRows& t, const PolicyArgs& p, const GradRows
   if (back && t.rows <= (1 << 22) && t.vocab <= (1 << 29) &&
       (t.vocab <= kShortRow || t.rows >= (t.bf16 ? 128 : 96))) {
     hipLaunchKernelGGL((policy_row_at_once_kernel<T>), dim3(t.rows), dim3(kOneThreads), 0,
-                       stream, static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, t.tokens,
-                       t.weights, sc, p, static_cast<T*>(d.x), d.ld, w.losses);
+                       stream, static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, in, sc, p,
+                       static_cast<T*>(d.x), d.ld, w.terms);
     const hipError_t one = hipGetLastError();
-    return one != hipSuccess ? one : launch_sum(w.losses, t.rows, p.loss, stream);
+    return one != hipSuccess ? one : launch_sum(w.terms, t.rows, p.loss, stream);
   }
   if (!back && whole_rows(t.rows, t.vocab, Vec<T>::n)) {
     hipLaunchKernelGGL((policy_whole_kernel<T>), dim3(grid_of(t.rows)), dim3(kThreads), 0, stream,
-                       static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, t.tokens, t.weights, sc,
-                       p, w.losses);
+                       static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, in, sc, p, w.terms);
     const hipError_t one = hipGetLastError();
-    return one != hipSuccess ? one : launch_sum(w.losses, t.rows, p.loss, stream);
+    return one != hipSuccess ? one : launch_sum(w.terms, t.rows, p.loss, stream);
   }
-  hipError_t e = launch_stats<T, false>(t, sc, cut, w, RowInit{}, stream);
+  hipError_t e = launch_stats<T, false>(t, sc, cut, w, in, stream);
   if (e != hipSuccess) return e;
   // Without a gradient and with one workgroup of rows, that one adds up the
   // loss; with a gradient the last pass does, otherwise a kernel of its own.
   const bool sum_here = !back && t.rows <= kRowsPerGroup;
   hipLaunchKernelGGL((policy_rows_kernel<T>),
-                     dim3(grid_of((t.rows + kRowsPerGroup - 1) / kRowsPerGroup)), dim3(kThreads),
-                     0, stream, static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, t.tokens,
-                     t.weights, sc, w.parts, cut.chunks, p, back ? w.grads : nullptr, w.losses,
-                     sum_here);
+                     dim3(grid_of((t.rows + int64_t{kRowsPerGroup} - 1) / kRowsPerGroup)), dim3(kThreads),
+                     0, stream, static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, in, sc, w.parts,
+                     cut.chunks, p, back ? w.grads : nullptr, w.terms, sum_here);
   e = hipGetLastError();
   if (e != hipSuccess || sum_here) return e;
-  return back ? launch_grad<T>(t, sc, cut, w, d, t.rows, p.loss, stream)
-              : launch_sum(w.losses, t.rows, p.loss, stream);
+  return back ? launch_grad<T>(t, sc, cut, w, d, w.terms, t.rows, p.loss, stream)
+              : launch_sum(w.terms, t.rows, p.loss, stream);
 }
 
 template <typename T>
@@ -1175,24 +1219,33 @@ hipError_t preference_loss_t(const TokenRows& t, const PreferenceArgs& p, const 
                              void* ws, hipStream_t stream) {
   const Scale sc = make_scale(t.temperature);
   const Cut cut = cut_rows(t.rows, t.vocab, Vec<T>::n);
-  const Cut stats = cut_stats(t.rows, t.vocab, Vec<T>::n);
   const Workspace w = lay_out(ws, t.rows, t.vocab, p.n_pairs);
+  const RowsIn in{t.tokens, nullptr, p.seq_offsets, 2 * p.n_pairs};
   const bool back = d.x != nullptr && t.rows > 0;
+  RowGrad* grads = back ? w.grads : nullptr;
   hipError_t e = hipSuccess;
-  if (t.rows > 0) {
-    const RowInit init{back ? w.grads : nullptr, p.logprobs, p.row_status, p.seq_offsets,
-                       2 * p.n_pairs};
-    e = launch_stats<T, false>(t, sc, stats, w, init, stream);
+  if (t.rows > 0 && whole_rows(t.rows, t.vocab, Vec<T>::n)) {
+    hipLaunchKernelGGL((preference_whole_kernel<T>), dim3(grid_of(t.rows)), dim3(kThreads), 0,
+                       stream, static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, in, sc, p, grads,
+                       w.terms);
+    e = hipGetLastError();
+  } else if (t.rows > 0) {
+    e = launch_stats<T, false>(t, sc, cut, w, in, stream);
     if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((preference_rows_kernel<T>),
+                       dim3(grid_of((t.rows + int64_t{kRowsPerGroup} - 1) / kRowsPerGroup)),
+                       dim3(kThreads), 0, stream, static_cast<const T*>(t.x), t.ld, t.rows,
+                       t.vocab, in, sc, w.parts, cut.chunks, p, grads, w.terms);
+    e = hipGetLastError();
   }
+  if (e != hipSuccess) return e;
   if (p.n_pairs > 0) {
-    hipLaunchKernelGGL((preference_pairs_kernel<T>), dim3(grid_of(p.n_pairs)), dim3(kPairThreads), 0,
-                       stream, static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, t.tokens, sc,
-                       w.parts, stats.chunks, p, back ? w.grads : nullptr, w.losses);
+    hipLaunchKernelGGL(preference_pairs_kernel, dim3(grid_of(p.n_pairs)), dim3(kPairThreads), 0,
+                       stream, t.rows, t.tokens, p, w.terms, grads, w.losses);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  return back ? launch_grad<T>(t, sc, cut, w, d, p.n_pairs, p.loss, stream)
+  return back ? launch_grad<T>(t, sc, cut, w, d, w.losses, p.n_pairs, p.loss, stream)
               : launch_sum(w.losses, p.n_pairs, p.loss, stream);
 }
 
