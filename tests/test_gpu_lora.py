@@ -103,6 +103,10 @@ CASES = [
     (100, 128, 66000, 16, 7, 0, "random"), (133, 192, 31040, 64, 9, 0, "bad"),
     (256, 128, 60001, 32, 256, 0, "random"), (320, 128, 60000, 24, 20, 1, "runs"),
     (310, 64, 60100, 8, 3, 0, "bad"), (250, 64, 60002, 16, 1, 0, "none"),
+    # 192 x 128, 192 x 256, one round of 128 x 128, two row tiles of 320
+    (150, 128, 22100, 16, 9, 0, "random"), (190, 192, 60001, 24, 40, 1, "bad"),
+    (192, 64, 40010, 72, 192, 0, "random"), (300, 64, 18993, 8, 30, 0, "random"),
+    (640, 64, 30001, 16, 64, 0, "runs"),
     # hidden sizes that are no multiple of 64
     (5, 72, 33, 8, 2, 0, "random"), (70, 200, 300, 24, 9, 1, "runs"), (260, 136, 140, 64, 5, 0, "bad"),
 ]

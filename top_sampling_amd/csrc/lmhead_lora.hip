@@ -9,6 +9,8 @@
 // u is held as three bf16 numbers whose sum is its fp32 value, so that the
 // matrix cores' products with B lose nothing: rounding u to bf16 once would
 // leave 2^-9 of the adapter's share in the fp32 logits.
+#include <algorithm>
+
 #include "lmhead_lora.hpp"
 
 namespace ts {
@@ -129,20 +131,24 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraArgs p, Dow
 // The projection with the up step inside (hidden size a multiple of 64).
 //
 // The main loop is lmhead_logits_local's: v_mfma_f32_32x32x16_bf16, 64-wide K
-// steps through two LDS stages filled by direct loads, the XOR swizzle of the
-// 16-byte chunks, row tiles of an lm_head strip back to back on one XCD.  Rows
+// steps through LDS stages filled by direct loads (two, or more where a CU has
+// few waves), the XOR swizzle of the 16-byte chunks, row tiles of an lm_head
+// strip back to back on one XCD.  Rows
 // are taken in the order of their adapters, through a row list for the loads
 // and the stores, so a tile holds few adapters and each in one run of rows.
 //
-// After the last K step the same two stages carry on with "panels" of B: the
+// After the last K step the same stages carry on with "panels" of B: the
 // strip's BN rows of the B of four of the tile's adapters, in windows of 16
 // ranks, in the stage's lm_head part.  u of those adapters' rows for the same
-// 16 ranks lies in the hidden part.  Both come a step ahead of their use: read
-// from global memory where it is used, u cost a latency per block and slice
-// (6 us a panel).  The windows of one panel follow each other, as they share
-// B's cache lines (the other order took 64 rows with 64 adapters of rank 64
-// from 0.5 to 0.7 ms).  A 32-row block takes the adapters that its
-// rows have, with u of the other rows set to 0 in the A fragment.
+// 16 ranks lies in the hidden part.  Both come ahead of their use, the first
+// ones under the last K steps: read from global memory where it is used, u cost
+// a latency per block and slice (6 us a panel), and panels that were loaded
+// after the K steps, two stages at a time, cost 64 rows with 64 adapters of
+// rank 64 over 18,992 columns 122 us, not 115, with 32 of rank 16 over 151,936
+// columns 259, not 253.  The windows of one panel follow each other, as they
+// share B's cache lines (the other order took 64 rows with 64 adapters of rank
+// 64 from 0.5 to 0.7 ms).  A 32-row block takes the adapters that its rows have,
+// with u of the other rows set to 0 in the A fragment.
 //
 // 0 x inf is not 0, so infinities and NaN in B are set to 0 as well, and a tile
 // that met one adds their products to the rows of that adapter alone after its
@@ -201,18 +207,17 @@ __device__ __forceinline__ void lora_panel(const LoraArgs& p, const TileRuns<BM,
   }
 }
 
-// Window `w` of u of the tile's places [from, to) into the hidden part of a
-// stage: kUChunks 16-byte chunks a row, of which the last is padding that
-// spreads a fragment's 32 rows over the banks.
+// Window `w` of u of the tile's rows into the hidden part of a stage, kUChunks
+// 16-byte chunks a row, of which the last is padding that spreads a fragment's
+// 32 rows over the banks.  Blocks [from, to) of 64 chunks each.
 constexpr int kUChunks = kParts * kWindow / 8 + 1;
 
 template <int BM, int NW>
 __device__ __forceinline__ void lora_rows(const DownRows& d, int rp, int w, int m0, int from,
                                           int to, int M, int wave, int lane, uint8_t* stage) {
-  static_assert((BM * kUChunks + 63) / 64 * 1024 <= BM * 128, "u of the rows fits");
-  const int end = (to * kUChunks + 63) / 64;
+  static_assert((BM * kUChunks + 63) / 64 <= BM / 8, "u of the rows fits");
 #pragma unroll 1
-  for (int q = from * kUChunks / 64 + wave; q < end; q += NW) {
+  for (int q = from + wave; q < to; q += NW) {
     const int i = q * 64 + lane;
     const int place = min(m0 + i / kUChunks, M - 1);
     const int c = min(i % kUChunks, kUChunks - 2);
@@ -345,24 +350,29 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, WAVES) void lora_gemm_kerne
       bfr[j] = *reinterpret_cast<const bf16x8*>(base + boff[j] + ((chunk ^ bswz[j]) << 4));
   };
 
-  constexpr int kPerRead = (TM * TN) / (TM + TN) > 0 ? (TM * TN) / (TM + TN) : 1;
-  for (int ks = 0, cur = 0; ks < ksteps; ++ks, cur = cur + 1 == STAGES ? 0 : cur + 1) {
-    // This step's loads have landed in LDS for every wave, and the stage of the
-    // step before is free.
+  // Waits until the step's loads have landed in LDS for every wave; the stage of
+  // the step before is free then.  A wave's loads land in order, LOADS of them a
+  // step; `full`: the later STAGES - 2 steps are all on their way.
+  auto wait_step = [&](bool full) {
     if constexpr (STAGES == 2) {
       __builtin_amdgcn_s_waitcnt(0);
       __syncthreads();
     } else {
-      // A wave's loads land in order, LOADS of them a stage; the later stages
-      // may be on their way, near the end only some of them are.
-      if (ks + STAGES - 2 < ksteps)
+      if (full)
         wait_stage<LOADS * (STAGES - 2)>();
       else
         wait_stage<0>();
     }
-    if (ks + STAGES - 1 < ksteps)
-      load_stage<LOADS, A_LOADS, NW, AUX>(
-          src, lds + (cur == 0 ? STAGES - 1 : cur - 1) * STAGE, wave, (ks + STAGES - 1) * kBK);
+  };
+
+  // MFMAs between two fragment reads, or reads after each MFMA where those are
+  // fewer.
+  constexpr int kMfmas = TM * TN, kReads = TM + TN;
+  constexpr bool kMoreReads = kMfmas < kReads;
+  constexpr int kGroupMfmas = kMoreReads ? 1 : kMfmas / kReads;
+  constexpr int kGroupReads = kMoreReads ? (kReads + kMfmas - 1) / kMfmas : 1;
+  constexpr int kGroups = kMoreReads ? kMfmas : kReads;
+  auto k_step = [&](int cur) __attribute__((always_inline)) {
     bf16x8 af[2][TM], bfr[2][TN];
     frags(cur, 0, af[0], bfr[0]);
 #pragma unroll
@@ -377,32 +387,41 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, WAVES) void lora_gemm_kerne
     }
     // This step's first fragments, then per 16-wide slice its MFMAs with the
     // next slice's fragment reads spread between them.
-    __builtin_amdgcn_sched_group_barrier(0x100, TM + TN, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
 #pragma unroll
     for (int kk = 0; kk < kBK / 16; ++kk) {
       if (kk + 1 < kBK / 16) {
 #pragma unroll
-        for (int t = 0; t < TM + TN; ++t) {
-          __builtin_amdgcn_sched_group_barrier(0x008, kPerRead, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        for (int t = 0; t < kGroups; ++t) {
+          __builtin_amdgcn_sched_group_barrier(0x008, kGroupMfmas, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, kGroupReads, 0);
         }
-        if (TM * TN > kPerRead * (TM + TN))
-          __builtin_amdgcn_sched_group_barrier(0x008, TM * TN - kPerRead * (TM + TN), 0);
+        if (kMfmas > kGroupMfmas * kGroups)
+          __builtin_amdgcn_sched_group_barrier(0x008, kMfmas - kGroupMfmas * kGroups, 0);
       } else {
-        __builtin_amdgcn_sched_group_barrier(0x008, TM * TN, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, kMfmas, 0);
       }
     }
+  };
+  int step = 0, cur = 0;  // the step worked on, and its stage
+  auto after = [](int stage) { return stage + 1 == STAGES ? 0 : stage + 1; };
+  for (; step < ksteps - (STAGES - 1); ++step, cur = after(cur)) {
+    wait_step(true);
+    load_stage<LOADS, A_LOADS, NW, AUX>(src, lds + (cur == 0 ? STAGES - 1 : cur - 1) * STAGE, wave,
+                                        (step + STAGES - 1) * kBK);
+    k_step(cur);
   }
 
   // ---- the adapters
-  // The tile's runs.
+  // The tile's runs.  Its barriers leave the loads on their way.
   int runs = 0;
   {
+    wait_stage<63>();
     const int id = tid < BM ? tr.id[tid] : kNoAdapter;
     const bool starts = id >= 0 && (tid == 0 || id != tr.id[tid - 1]);
     const uint64_t mask = __ballot(starts);
     if (lane == 0) tr.wave_runs[wave] = __popcll(mask);
-    __syncthreads();
+    wait_stage<63>();
     int before = 0;
     for (int w = 0; w < NW; ++w) {
       before += w < wave ? tr.wave_runs[w] : 0;
@@ -414,33 +433,43 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, WAVES) void lora_gemm_kerne
       tr.start[run] = tid;
     }
     if (tid == 0) tr.start[runs] = min(BM, M - m0);
-    __syncthreads();
+    wait_stage<63>();
   }
-  // Step q: a window of a panel, in stage q % STAGES.  Half of the stages are
-  // worked on while the other half is filled.
+  // The steps after the K steps: a window of a panel each, its first ones loaded
+  // under the last K steps.
   constexpr int kRuns = kBK / kWindow;  // of a panel
-  constexpr int kGroup = STAGES / 2;
   const int rp = padded_rank(p.rank);
   const int windows = rp / kWindow;
-  const int steps = (runs + kRuns - 1) / kRuns * windows;
-  for (int q = -kGroup; q < steps; ++q) {
-    if (q % kGroup == 0) {
-      if (q >= 0) {
-        __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();
-      }
-#pragma unroll 1
-      for (int t = q + kGroup; t < min(q + 2 * kGroup, steps); ++t) {
-        const int pn = t / windows, w = t - pn * windows;
-        uint8_t* to = lds + (t % STAGES) * STAGE;
-        lora_panel<BM, LOADS, A_LOADS, NW>(p, tr, runs, w, pn, n0, wave, lane, to);
-        lora_rows<BM, NW>(d, rp, w, m0, tr.start[pn * kRuns],
-                          tr.start[min(pn * kRuns + kRuns, runs)], M, wave, lane, to);
-      }
-    }
-    if (q < 0) continue;
+  const int total = ksteps + (runs + kRuns - 1) / kRuns * windows;
+  int issued = ksteps;
+  auto issue = [&](uint8_t* to) {
+    const int q = issued - ksteps;
     const int pn = q / windows, w = q - pn * windows;
-    const uint8_t* stage = lds + (q % STAGES) * STAGE;
+    lora_panel<BM, LOADS, A_LOADS, NW>(p, tr, runs, w, pn, n0, wave, lane, to);
+    // With more stages the waits count on LOADS loads a step; otherwise only
+    // the rows that have the panel's adapters.
+    const int from = STAGES > 2 ? 0 : tr.start[pn * kRuns] * kUChunks / 64;
+    const int end = STAGES > 2 ? BM / 8
+                               : (tr.start[min(pn * kRuns + kRuns, runs)] * kUChunks + 63) / 64;
+    lora_rows<BM, NW>(d, rp, w, m0, from, end, M, wave, lane, to);
+    ++issued;
+  };
+  while (issued < min(total, STAGES - 1)) issue(lds + issued * STAGE);
+  auto next_step = [&]() {
+    wait_step(issued - step == STAGES - 1);
+    if (issued < total) issue(lds + (cur == 0 ? STAGES - 1 : cur - 1) * STAGE);
+  };
+#pragma unroll 1
+  for (; step < ksteps; ++step, cur = after(cur)) {
+    next_step();
+    k_step(cur);
+  }
+#pragma unroll 1
+  for (; step < total; ++step, cur = after(cur)) {
+    next_step();
+    const int q = step - ksteps;
+    const int pn = q / windows, w = q - pn * windows;
+    const uint8_t* stage = lds + cur * STAGE;
     const uint8_t* ub = stage + (wm0 + frow) * (kUChunks * 16) + fhalf * 16;
     // Where the panel's runs start and end within the wave's rows.
     const int starts = tr.start[min(pn * kRuns + min(lane, kRuns), runs)] - wm0;
@@ -622,10 +651,6 @@ hipError_t launch_lmhead_lora(const LoraArgs& p, void* ws, hipStream_t stream) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (p.hidden_dim % kBK == 0) {
-    // The tile that pads the rows least, as for the shared projection.  Up to
-    // 128 rows one row tile reads the lm_head once: past the caches.
-    const int64_t pad256 = (p.rows + int64_t{255}) / 256 * 256;
-    const int64_t pad320 = (p.rows + int64_t{319}) / 320 * 320;
     // Few tiles: a CU brings in 63 GB/s at most, so 64 x 128 tiles that are
     // fewer than half the CUs take four times as many, narrow ones (4 rows of
     // 4,288 and 2,613 columns: 36 us with 21 tiles, 27 with 82; 61 rows and
@@ -636,15 +661,34 @@ hipError_t launch_lmhead_lora(const LoraArgs& p, void* ws, hipStream_t stream) {
     if (small <= 128) return launch_fused<32, 32, 1, 1, 0, 6, 1>(p, d, stream);
     if (small <= 256 || (p.rows > 64 && small <= 512))
       return launch_fused<64, 128, 1, 4, 0, 3, 2>(p, d, stream);
+    // Up to 128 rows one row tile reads the lm_head once: past the caches.
     if (p.rows <= 64) return launch_fused<64, 128, 1, 4, 2, 2, 3>(p, d, stream);
     if (p.rows <= 128) return launch_fused<128, 128, 2, 4, 2, 2, 4>(p, d, stream);
-    // A short vocabulary slice makes too few 256-wide tiles for the card: 122 of
-    // them (256 x 31,040, H 2,560) take 76 us, the 486 smaller tiles 62; from
-    // three quarters of the card on it turns (235 tiles: 100 against 119 us).
-    if ((pad256 / 256) * ((p.vocab + int64_t{255}) / 256) < 192)
-      return launch_fused<128, 128, 2, 4, 0, 2, 4>(p, d, stream);
-    if (pad320 < pad256) return launch_fused<320, 256, 2, 4, 0, 2, 2>(p, d, stream);
-    return launch_fused<256, 256, 2, 4, 0, 2, 2>(p, d, stream);
+    // More rows: the tile whose rounds over the card take least, by what a round
+    // of it takes in 10 ns a K step (us, H = 4,096, but 2,560 of 133 and 256
+    // rows; 192n is 192 x 128):
+    //   rows x columns     128   192n   192   256   320
+    //   133 x  31,040       71     60    78    89   101
+    //   256 x  31,040       58     81    69    75    86
+    //   300 x  18,992       82    117    90   111   129
+    //   512 x  18,992      117    119   100   109   128
+    //   640 x  18,992      164    213   220   154   163
+    //   640 x  31,040      228    256   209   234   164
+    //   160 x 151,936      441    366   371   390   433
+    //   384 x 151,936      608    649   553   645   760
+    auto rounds = [&](int64_t bm, int64_t bn, int64_t at_once, int64_t cost) {
+      const int64_t tiles = (p.rows + bm - 1) / bm * ((p.vocab + bn - 1) / bn);
+      return (tiles + at_once - 1) / at_once * cost;
+    };
+    const int64_t t128 = rounds(128, 128, 512, 140), t192n = rounds(192, 128, 256, 120);
+    const int64_t t192 = rounds(192, 256, 256, 180), t256 = rounds(256, 256, 256, 205);
+    const int64_t t320 = rounds(320, 256, 256, 245);
+    const int64_t least = std::min({t128, t192n, t192, t256, t320});
+    if (t320 == least) return launch_fused<320, 256, 2, 4, 0, 2, 2>(p, d, stream);
+    if (t256 == least) return launch_fused<256, 256, 2, 4, 0, 2, 2>(p, d, stream);
+    if (t192 == least) return launch_fused<192, 256, 2, 4, 0, 2, 2>(p, d, stream);
+    if (t192n == least) return launch_fused<192, 128, 2, 4, 0, 3, 2>(p, d, stream);
+    return launch_fused<128, 128, 2, 4, 0, 2, 4>(p, d, stream);
   }
   e = launch_lmhead_gemm(p.hidden, p.ld_hidden, p.lm_head, p.ld_lm_head, p.logits, p.ld_logits,
                          p.rows, p.vocab, p.hidden_dim, stream);
