@@ -113,6 +113,7 @@ def _load() -> ctypes.CDLL:
 
 
 lib = _load()
+import torch  # noqa: E402  (_load has loaded it)
 
 
 class TopSamplingError(RuntimeError):
@@ -148,7 +149,7 @@ def _stream_ptr(stream) -> int:
 
 
 def _ptr(t) -> int | None:
-    return None if t is None else int(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 # ---------------------------------------------------------------- projection
@@ -444,6 +445,10 @@ class PreferenceLoss:
     grad_logits: object  # the logits' type [rows, vocab], or None
 
 
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
 class _OnDevice:
     """Makes the device of a call's tensors and its stream current, so that
     outputs and workspaces are allocated for that stream.  Where they are
@@ -453,14 +458,13 @@ class _OnDevice:
     __slots__ = ("pointer", "_guard")
 
     def __init__(self, device, stream):
-        torch = _torch()
         if device.type != "cuda":
             raise ValueError("tensors must be on the GPU")
         self._guard = None
         if stream is None:
-            if device.index != torch.cuda.current_device():
+            if device.index != _current_device():
                 self._guard = torch.cuda.device(device)
-            self.pointer = torch._C._cuda_getCurrentRawStream(device.index)
+            self.pointer = _current_stream(device.index)
             return
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), device=device)
@@ -479,10 +483,12 @@ class _OnDevice:
             self._guard.__exit__(*exc)
 
 
-def _check_vector(t, name, n, device, dtype=None):
+_LOGITS_TYPES = {torch.float32: TS_F32, torch.bfloat16: TS_BF16}
+
+
+def _check_vector(t, name, n, device, dtype=torch.float32):
     if t is None:
         return
-    dtype = dtype or _torch().float32
     if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values")
     if t.device != device:
@@ -491,9 +497,8 @@ def _check_vector(t, name, n, device, dtype=None):
 
 def _token_rows(logits, token_ids):
     """Checks logits and token ids; returns (type code, leading dimension)."""
-    torch = _torch()
-    types = {torch.float32: TS_F32, torch.bfloat16: TS_BF16}
-    if logits.dim() != 2 or logits.dtype not in types:
+    kind = _LOGITS_TYPES.get(logits.dtype)
+    if logits.dim() != 2 or kind is None:
         raise ValueError("logits must be fp32 or bf16 [rows, vocab]")
     rows, vocab = logits.shape
     if vocab > 1 and logits.stride(1) != 1:
@@ -501,7 +506,7 @@ def _token_rows(logits, token_ids):
     if rows > 1 and logits.stride(0) < vocab:
         raise ValueError("logits rows overlap")
     _check_vector(token_ids, "token_ids", rows, logits.device, torch.int32)
-    return types[logits.dtype], max(int(logits.stride(0)), int(vocab))
+    return kind, max(logits.stride(0), vocab)
 
 
 def _grad_rows(grad_logits, logits):
@@ -512,11 +517,10 @@ def _grad_rows(grad_logits, logits):
         raise ValueError("grad_logits must have unit column stride")
     if grad_logits.shape[0] > 1 and grad_logits.stride(0) < grad_logits.shape[1]:
         raise ValueError("grad_logits rows overlap")
-    return max(int(grad_logits.stride(0)), int(grad_logits.shape[1]))
+    return max(grad_logits.stride(0), grad_logits.shape[1])
 
 
 def _workspace(workspace, need, device):
-    torch = _torch()
     if workspace is None:
         return torch.empty(max(256, need), dtype=torch.uint8, device=device)
     if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
@@ -538,7 +542,6 @@ def token_logprobs(logits, token_ids, temperature: float = 1.0, entropies: bool 
     """Log-probability of ``token_ids[r]`` (int32; negative: row left out)
     under ``softmax(logits[r] / temperature)``, fp32 or bf16 ``logits [rows,
     vocab]``, and with ``entropies`` that distribution's entropy."""
-    torch = _torch()
     kind, ld = _token_rows(logits, token_ids)
     rows, vocab = logits.shape
     dev = logits.device
@@ -563,7 +566,6 @@ def token_logprobs_backward(logits, token_ids, forward: TokenLogprobs, grad_logp
     ``grad_entropies`` (or None), with the ``TokenLogprobs`` that
     ``token_logprobs`` gave for the same logits, tokens and temperature.
     ``grad_logits`` may be ``logits`` itself."""
-    torch = _torch()
     kind, ld = _token_rows(logits, token_ids)
     rows, vocab = logits.shape
     dev = logits.device
@@ -592,7 +594,6 @@ def policy_loss(logits, token_ids, old_logprobs, advantages, ref_logprobs=None, 
     ``backward``, or a ``grad_logits`` buffer (``logits`` itself is allowed),
     the same call writes ``grad_loss`` (a device scalar, None for 1) times
     the gradient of the logits."""
-    torch = _torch()
     kind, ld = _token_rows(logits, token_ids)
     rows, vocab = logits.shape
     dev = logits.device
@@ -605,10 +606,10 @@ def policy_loss(logits, token_ids, old_logprobs, advantages, ref_logprobs=None, 
         if grad_logits is None and backward:
             grad_logits = torch.empty(rows, vocab, dtype=logits.dtype, device=dev)
         ldg = _grad_rows(grad_logits, logits) if grad_logits is not None else 0
-        out = PolicyLoss(
-            torch.empty((), dtype=torch.float32, device=dev),
-            *torch.empty((3, rows), dtype=torch.float32, device=dev).unbind(0),
-            torch.empty(rows, dtype=torch.int32, device=dev), grad_logits)
+        logprobs, ratios, kl, status = torch.empty((4, rows), dtype=torch.float32,
+                                                   device=dev).unbind(0)
+        out = PolicyLoss(torch.empty((), dtype=torch.float32, device=dev), logprobs, ratios, kl,
+                         status.view(torch.int32), grad_logits)
         params = _PolicyParams(temperature, clip_low, clip_high, kl_coef)
         _check(lib.policy_loss(
             _ptr(logits), kind, rows, vocab, ld, _ptr(token_ids), ctypes.addressof(params),
@@ -628,7 +629,6 @@ def preference_loss(logits, token_ids, seq_offsets, ref_logprobs=None, pair_weig
     answers first, then the rejected ones in the same order.  ``mean`` divides
     each sequence's sum by its tokens.  ``backward``, ``grad_loss`` and
     ``grad_logits`` as in ``policy_loss``."""
-    torch = _torch()
     kind, ld = _token_rows(logits, token_ids)
     rows, vocab = logits.shape
     dev = logits.device
@@ -673,7 +673,6 @@ def lmhead_logits_local_lora(hidden, lm_head, lora_a, lora_b, adapter_ids, adapt
     row's own ``A = lora_a[id]``, ``B = lora_b[id]`` (bf16 ``[n, rank, H]`` and
     ``[n, V_local, rank]``, inner stride 1) and ``adapter_scales[id]`` (fp32,
     None for 1); id -1 has no adapter."""
-    torch = _torch()
     if hidden.dim() != 2 or lm_head.dim() != 2 or lora_a.dim() != 3 or lora_b.dim() != 3:
         raise ValueError("hidden and lm_head must be 2-D, lora_a and lora_b 3-D")
     rows, h = hidden.shape
