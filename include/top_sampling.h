@@ -406,7 +406,8 @@ int sampler_assemble_and_sample(const float* const* slices, const int64_t* slice
  *                initialisation, ordered on one stream by whoever shares it.
  * Sums over the vocabulary are fp32 per thread and double from there on;
  * per-row arithmetic is double, outputs are rounded once.  Results do not
- * depend on the order in which workgroups run.  rows == 0 writes nothing but
+ * depend on the order in which workgroups run; the order of a row's sum goes by
+ * the call's sizes and by where in a cache line its row starts.  rows == 0 writes nothing but
  * a loss of 0.  rows, vocab < 2^31.
  */
 enum { TS_F32 = 0, TS_BF16 = 1 };
