@@ -718,3 +718,41 @@ def test_every_alignment(dtype, vocab):
         close(inplace, want, tol, "in place")
         logits.fill_(7.0)
         assert (wide == 7.0).all()
+
+
+def test_many_rows():
+    """More rows than one launch has workgroups for, two logits each: loss
+    sums, and rows past 2^22."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    rows = (1 << 23) + 1001
+    x = torch.zeros(rows, 2, device=_dev())
+    g = torch.Generator(device=_dev())
+    g.manual_seed(1)
+    x[:, 1] = torch.randn(rows, generator=g, device=_dev())
+    tok = (torch.arange(rows, device=_dev()) % 2).int()
+    lp = torch.log_softmax(x.double(), -1).gather(1, tok.long()[:, None])[:, 0]
+    out = ts.token_logprobs(x, tok)
+    assert ((out.logprobs.double() - lp).abs() <= LSE + U * lp.abs()).all()
+    adv = torch.where(tok == 0, 1.0, -0.5)
+    w = torch.full((rows,), 1.0 / rows, device=_dev())
+    one = torch.softmax(x.double(), -1)
+    one.scatter_add_(1, tok.long()[:, None], torch.full_like(lp, -1.0)[:, None])
+    want = one * adv.double()[:, None] * w.double()[:, None]
+    for back in (False, True):
+        pol = ts.policy_loss(x, tok, lp.float(), adv, weights=w, backward=back)
+        # each ratio is off by 2 LSE, and the old log-probabilities' rounding
+        assert abs(pol.loss.item() + adv.double().mean().item()) <= 3 * LSE
+    assert ((pol.grad_logits.double() - want).abs() <= 8 * LSE / rows).all()
+    half = rows // 2
+    off = torch.tensor([0, half, rows], dtype=torch.int32, device=_dev())
+    pair = ts.preference_loss(x, tok, off, mean=True, backward=True)
+    z = 0.1 * (lp[:half].mean() - lp[half:].mean()).item()
+    assert abs(pair.loss.item() - np.log1p(np.exp(-z))) <= 0.1 * 2 * LSE + 2 * U
+    k = -0.1 / (1 + np.exp(z)) / half
+    assert ((pair.grad_logits[:half].double() + k * one[:half]).abs() <= 8 * LSE * -k).all()
+    # rows are consecutive entries: a left-out end stays zero
+    tok[-3:] = -1
+    assert not ts.token_logprobs(x, tok).logprobs[-3:].any()

@@ -462,6 +462,7 @@ __global__ __launch_bounds__(kThreads) void score_whole_kernel(
 __device__ __forceinline__ double group_sum(const double* v, int64_t n) {
   __shared__ double wave_sum[kThreads / 64];
   double s = 0.0;
+#pragma unroll 8
   for (int64_t i = threadIdx.x; i < n; i += kThreads) s += v[i];
   for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d, 64);
   if ((threadIdx.x & 63) == 0) wave_sum[threadIdx.x >> 6] = s;
@@ -873,40 +874,44 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(
 }
 
 // -------------------------------------------------- policy loss in one read
-// One workgroup per row, alone on its CU, which holds the row between the
-// statistics and the gradient: every exponential goes into a register or into
-// LDS, relative to the thread's maximum at that point, and the gradient pass
-// only scales it.  144 registers and 64 LDS words a thread hold 106,496
-// entries; what a longer row has beyond them is read a second time.  In two
-// passes the second read costs as much as the first, out of the Infinity Cache
-// too: reads and writes together pass at 6.5-6.8 TB/s.  Loss and gradient of
-// 640 x 151,936 fp32 in two passes and in one: 192 and 157 us (one read and
-// one write take 120 at that rate, the three tenths that are read again 18);
-// 1,024 x 151,936 bf16: 155 and 127.  Loads one batch ahead are best (1,024 x
-// 151,936: two ahead 142 us, all at once 150; the batches' exponentials then
-// run after the loads and not under them), as are nine register batches (with
-// ten, which spill two registers in bf16, 1,021 x 100,277 takes 91 us, not 87).
-// Holding the logits and not the exponentials, twice as many in bf16 and so two
-// workgroups a CU, is no faster (129 us), and slower for short rows.
-constexpr int kOneThreads = 512;
-constexpr int kOneVals = 16;                         // entries of a thread's batch
-constexpr int kRegBatches = 9;
-constexpr int kLdsBatches = 4;
+// One workgroup per row, which holds the row between the statistics and the
+// gradient: every exponential goes into a register (REGS batches) or into LDS
+// (LDS batches), relative to the thread's maximum at that point, and the
+// gradient pass only scales it.
+//   Long rows have a CU to themselves: 144 registers and 64 LDS words a thread
+// hold 106,496 entries; what a longer row has beyond them is read a second
+// time.  In two passes the second read costs as much as the first, out of the
+// Infinity Cache too: reads and writes together pass at 6.5-6.8 TB/s.  Loss and
+// gradient of 640 x 151,936 fp32 in two passes and in one: 192 and 157 us (one
+// read and one write take 120 at that rate, the three tenths that are read
+// again 18); 1,024 x 151,936 bf16: 155 and 127.  Loads one batch ahead are best
+// (1,024 x 151,936: two ahead 142 us, all at once 150; the batches' exponentials
+// then run after the loads and not under them), as are nine register batches
+// (with ten, which spill two registers in bf16, 1,021 x 100,277 takes 91 us, not
+// 87).  Holding the logits and not the exponentials, twice as many in bf16 and
+// so two workgroups a CU, is no faster (129 us), and slower for short rows.
+//   Short rows have two (up to 32,768 entries) or four (16,384) workgroups on a
+// CU, so that one's reads run under another's writes and row arithmetic.  With a
+// CU to themselves and without, us: 1,000 x 32,000 fp32 48 and 43, bf16 33 and
+// 25; 1,000 x 4,096 fp32 19 and 10; 8,192 x 16,384 bf16 165 and 82; 8 x 32,000
+// 10.1 and 10.0.  Half of their batches in LDS leave the registers that four
+// workgroups can have (all in registers: 1,000 x 32,000 bf16 41 us).
+constexpr int kTinyRow = 16384;
+constexpr int kOneVals = 16;  // entries of a thread's batch
 
-template <typename T>
-__global__ __launch_bounds__(kOneThreads, 2) void policy_row_at_once_kernel(
+template <typename T, int THREADS, int REGS, int LDS, int WAVES>
+__global__ __launch_bounds__(THREADS, WAVES) void policy_row_at_once_kernel(
     const T* x, int64_t ld, int rows, int vocab, RowsIn rows_in, Scale sc, PolicyArgs p, T* d,
-    int64_t ldd,
-    double* __restrict__ losses) {
+    int64_t ldd, double* __restrict__ losses) {
   constexpr int VN = Vec<T>::n;
   constexpr int NV = kOneVals / VN;  // vectors of a thread's batch
   using V = typename Vec<T>::Type;
-  __shared__ f32x4 held_lds[kLdsBatches * kOneVals / 4][kOneThreads];
-  __shared__ Part wave_part[kOneThreads / 64];
+  __shared__ f32x4 held_lds[LDS * kOneVals / 4][THREADS];
+  __shared__ Part wave_part[THREADS / 64];
   __shared__ RowGrad row_record;
   const Shape f = row_shape(d + static_cast<int64_t>(blockIdx.x) * ldd, vocab);
   const int whole = f.whole;
-  const int batches = (whole + NV * kOneThreads - 1) / (NV * kOneThreads);
+  const int batches = (whole + NV * THREADS - 1) / (NV * THREADS);
 
   // No loop over rows: with one the compiler keeps the batches' registers
   // across rows, and 700 of them spill.
@@ -921,7 +926,7 @@ __global__ __launch_bounds__(kOneThreads, 2) void policy_row_at_once_kernel(
   const int token = rows_in.tokens[r];
   if (rows_in.left_out(r)) {
     if (tid == 0) policy_left_out(p, r, losses);
-    row_grad_pass<T, false, kOneThreads>(rx, rd, vocab, 0, whole, true, token,
+    row_grad_pass<T, false, THREADS>(rx, rd, vocab, 0, whole, true, token,
                                          RowGrad{0.0f, 0.0f, 0.0f, 0.0f}, sc);
     return;
   }
@@ -934,7 +939,7 @@ __global__ __launch_bounds__(kOneThreads, 2) void policy_row_at_once_kernel(
   auto load = [&](int b, V (&raw)[NV]) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int i = min((b * NV + j) * kOneThreads + tid, whole - 1);
+      const int i = min((b * NV + j) * THREADS + tid, whole - 1);
       raw[j] = *reinterpret_cast<const V*>(body + static_cast<uint32_t>(i) * 16u);
     }
   };
@@ -944,7 +949,7 @@ __global__ __launch_bounds__(kOneThreads, 2) void policy_row_at_once_kernel(
   auto add = [&](int b, float (&e)[kOneVals]) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const bool in_row = (b * NV + j) * kOneThreads + tid < whole;
+      const bool in_row = (b * NV + j) * THREADS + tid < whole;
 #pragma unroll
       for (int k = 0; k < VN; ++k)
         e[j * VN + k] = in_row ? static_cast<float>(raw[j][k]) : -INFINITY;
@@ -968,19 +973,19 @@ __global__ __launch_bounds__(kOneThreads, 2) void policy_row_at_once_kernel(
     s += sum[0];
   };
 
-  constexpr int kKept = kRegBatches + kLdsBatches;
-  float held[kRegBatches][kOneVals], top_at[kKept];
+  constexpr int kKept = REGS + LDS;
+  float held[REGS][kOneVals], top_at[kKept];
   if (batches > 0) load(0, raw);
 #pragma unroll
-  for (int b = 0; b < kRegBatches; ++b) {
+  for (int b = 0; b < REGS; ++b) {
     if (b < batches) {
       add(b, held[b]);
       top_at[b] = m;
     }
   }
 #pragma unroll
-  for (int q = 0; q < kLdsBatches; ++q) {
-    const int b = kRegBatches + q;
+  for (int q = 0; q < LDS; ++q) {
+    const int b = REGS + q;
     if (b < batches) {
       float e[kOneVals];
       add(b, e);
@@ -1004,7 +1009,7 @@ __global__ __launch_bounds__(kOneThreads, 2) void policy_row_at_once_kernel(
     s = s * exp_t(fmaxf(m - ref, sc.floor), sc) + exp_t(edge_x - ref, sc);
     m = top;
   }
-  join_group<false, kOneThreads>(m, s, u, sc, wave_part);
+  join_group<false, THREADS>(m, s, u, sc, wave_part);
   if (tid == 0) {
     RowStats st;
     st.m = m;
@@ -1026,7 +1031,7 @@ __global__ __launch_bounds__(kOneThreads, 2) void policy_row_at_once_kernel(
     const float scale = zero ? 0.0f : exp_t(fmaxf(top - g.m, sc.floor), sc) * g.a;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int i = (b * NV + j) * kOneThreads + tid;
+      const int i = (b * NV + j) * THREADS + tid;
       V o;
 #pragma unroll
       for (int k = 0; k < VN; ++k) o[k] = static_cast<T>(e[j * VN + k] * scale);
@@ -1039,14 +1044,14 @@ __global__ __launch_bounds__(kOneThreads, 2) void policy_row_at_once_kernel(
     }
   };
   if (batches > kKept)
-    row_grad_pass<T, false, kOneThreads>(rx, rd, vocab, kKept * NV * kOneThreads, whole, false,
+    row_grad_pass<T, false, THREADS>(rx, rd, vocab, kKept * NV * THREADS, whole, false,
                                          token, g, sc);
   if (in_edge)
     rd[edge_at] = static_cast<T>(zero ? 0.0f
                                       : edge_at == token ? g.own : exp_t(edge_x - g.m, sc) * g.a);
 #pragma unroll
-  for (int q = kLdsBatches - 1; q >= 0; --q) {
-    const int b = kRegBatches + q;
+  for (int q = LDS - 1; q >= 0; --q) {
+    const int b = REGS + q;
     if (b < batches) {
       float e[kOneVals];
 #pragma unroll
@@ -1059,7 +1064,7 @@ __global__ __launch_bounds__(kOneThreads, 2) void policy_row_at_once_kernel(
     }
   }
 #pragma unroll
-  for (int b = kRegBatches - 1; b >= 0; --b) {
+  for (int b = REGS - 1; b >= 0; --b) {
     if (b < batches) store(b, held[b], top_at[b]);
   }
 }
@@ -1182,15 +1187,21 @@ hipError_t policy_loss_t(const TokenRows& t, const PolicyArgs& p, const GradRows
   const bool back = d.x != nullptr;
   // A row per workgroup keeps a CU busy for 5 us and 0.15 ns an entry, whatever
   // the number of rows; in two passes the rows are cut up over the card.  With
-  // gradient, two passes and one, us: 8 rows of 32,000 10.4 and 10.4, of 151,936
+  // gradient, two passes and one, us: 8 rows of 32,000 10.5 and 10.0, of 151,936
   // 13.8 and 26.6; fp32, 64 rows of 151,936 26 and 28, 96 35 and 29; bf16, 96
   // rows of 151,936 23 and 26, 128 27.6 and 26.4.
   if (back && t.rows <= (1 << 22) && t.vocab <= (1 << 29) &&
       (t.vocab <= kShortRow || t.rows >= (t.bf16 ? 128 : 96))) {
-    hipLaunchKernelGGL((policy_row_at_once_kernel<T>), dim3(t.rows), dim3(kOneThreads), 0,
-                       stream, static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, in, sc, p,
-                       static_cast<T*>(d.x), d.ld, w.terms);
-    const hipError_t one = hipGetLastError();
+    auto launch = [&](auto kernel, int threads) {
+      hipLaunchKernelGGL(kernel, dim3(t.rows), dim3(threads), 0, stream,
+                         static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, in, sc, p,
+                         static_cast<T*>(d.x), d.ld, w.terms);
+      return hipGetLastError();
+    };
+    const hipError_t one =
+        t.vocab <= kTinyRow    ? launch(policy_row_at_once_kernel<T, 256, 2, 2, 4>, 256)
+        : t.vocab <= kShortRow ? launch(policy_row_at_once_kernel<T, 512, 2, 2, 4>, 512)
+                               : launch(policy_row_at_once_kernel<T, 512, 9, 4, 2>, 512);
     return one != hipSuccess ? one : launch_sum(w.terms, t.rows, p.loss, stream);
   }
   if (!back && whole_rows(t.rows, t.vocab, Vec<T>::n)) {
