@@ -513,11 +513,23 @@ def _grad_rows(grad_logits, logits):
     if grad_logits.shape != logits.shape or grad_logits.dtype != logits.dtype or \
             grad_logits.device != logits.device:
         raise ValueError("grad_logits must have the shape, type and device of logits")
-    if grad_logits.shape[1] > 1 and grad_logits.stride(1) != 1:
+    (rows, vocab), stride = grad_logits.shape, grad_logits.stride()
+    if vocab > 1 and stride[1] != 1:
         raise ValueError("grad_logits must have unit column stride")
-    if grad_logits.shape[0] > 1 and grad_logits.stride(0) < grad_logits.shape[1]:
+    if rows > 1 and stride[0] < vocab:
         raise ValueError("grad_logits rows overlap")
-    return max(grad_logits.stride(0), grad_logits.shape[1])
+    return max(stride[0], vocab)
+
+
+def _gradient(grad_logits, wanted, logits):
+    """The buffer of the logits' gradient (checked, or a new one if wanted)
+    and its leading dimension."""
+    if grad_logits is not None:
+        return grad_logits, _grad_rows(grad_logits, logits)
+    if not wanted:
+        return None, 0
+    rows, vocab = logits.shape
+    return torch.empty(rows, vocab, dtype=logits.dtype, device=logits.device), vocab
 
 
 def _workspace(workspace, need, device):
@@ -553,9 +565,9 @@ def token_logprobs(logits, token_ids, temperature: float = 1.0, entropies: bool 
             torch.empty((rows, 2), dtype=torch.float32, device=dev),
             torch.empty(rows, dtype=torch.int32, device=dev))
         _check(lib.token_logprobs(
-            _ptr(logits), kind, rows, vocab, ld, _ptr(token_ids), temperature, _ptr(out.logprobs),
-            _ptr(out.entropies), _ptr(out.row_stats), _ptr(out.row_status), _ptr(workspace),
-            workspace.numel(), s))
+            logits.data_ptr(), kind, rows, vocab, ld, token_ids.data_ptr(), temperature,
+            out.logprobs.data_ptr(), _ptr(out.entropies), out.row_stats.data_ptr(),
+            out.row_status.data_ptr(), workspace.data_ptr(), workspace.numel(), s))
     return out
 
 
@@ -574,13 +586,11 @@ def token_logprobs_backward(logits, token_ids, forward: TokenLogprobs, grad_logp
     _check_vector(forward.row_stats, "forward.row_stats", 2 * rows, dev)
     _check_vector(forward.entropies, "forward.entropies", rows, dev)
     with _OnDevice(dev, stream) as s:
-        if grad_logits is None:
-            grad_logits = torch.empty(rows, vocab, dtype=logits.dtype, device=dev)
-        ldg = _grad_rows(grad_logits, logits)
+        grad_logits, ldg = _gradient(grad_logits, True, logits)
         _check(lib.token_logprobs_backward(
-            _ptr(logits), kind, rows, vocab, ld, _ptr(token_ids), temperature,
+            logits.data_ptr(), kind, rows, vocab, ld, token_ids.data_ptr(), temperature,
             _ptr(forward.row_stats), _ptr(grad_logprobs), _ptr(forward.entropies),
-            _ptr(grad_entropies), _ptr(grad_logits), ldg, s))
+            _ptr(grad_entropies), grad_logits.data_ptr(), ldg, s))
     return grad_logits
 
 
@@ -603,19 +613,18 @@ def policy_loss(logits, token_ids, old_logprobs, advantages, ref_logprobs=None, 
         _check_vector(t, name, n, dev)
     with _OnDevice(dev, stream) as s:
         workspace = _workspace(workspace, token_logprobs_workspace_bytes(rows, vocab), dev)
-        if grad_logits is None and backward:
-            grad_logits = torch.empty(rows, vocab, dtype=logits.dtype, device=dev)
-        ldg = _grad_rows(grad_logits, logits) if grad_logits is not None else 0
+        grad_logits, ldg = _gradient(grad_logits, backward, logits)
         logprobs, ratios, kl, status = torch.empty((4, rows), dtype=torch.float32,
                                                    device=dev).unbind(0)
         out = PolicyLoss(torch.empty((), dtype=torch.float32, device=dev), logprobs, ratios, kl,
                          status.view(torch.int32), grad_logits)
         params = _PolicyParams(temperature, clip_low, clip_high, kl_coef)
         _check(lib.policy_loss(
-            _ptr(logits), kind, rows, vocab, ld, _ptr(token_ids), ctypes.addressof(params),
-            _ptr(old_logprobs), _ptr(ref_logprobs), _ptr(advantages), _ptr(weights),
-            _ptr(grad_loss), _ptr(out.loss), _ptr(out.logprobs), _ptr(out.ratios), _ptr(out.kl),
-            _ptr(out.row_status), _ptr(grad_logits), ldg, _ptr(workspace), workspace.numel(), s))
+            logits.data_ptr(), kind, rows, vocab, ld, token_ids.data_ptr(),
+            ctypes.addressof(params), _ptr(old_logprobs), _ptr(ref_logprobs), _ptr(advantages),
+            _ptr(weights), _ptr(grad_loss), out.loss.data_ptr(), out.logprobs.data_ptr(),
+            out.ratios.data_ptr(), out.kl.data_ptr(), out.row_status.data_ptr(),
+            _ptr(grad_logits), ldg, workspace.data_ptr(), workspace.numel(), s))
     return out
 
 
@@ -642,9 +651,7 @@ def preference_loss(logits, token_ids, seq_offsets, ref_logprobs=None, pair_weig
     with _OnDevice(dev, stream) as s:
         workspace = _workspace(workspace, preference_loss_workspace_bytes(rows, vocab, n_pairs),
                                dev)
-        if grad_logits is None and backward:
-            grad_logits = torch.empty(rows, vocab, dtype=logits.dtype, device=dev)
-        ldg = _grad_rows(grad_logits, logits) if grad_logits is not None else 0
+        grad_logits, ldg = _gradient(grad_logits, backward, logits)
         out = PreferenceLoss(
             torch.empty((), dtype=torch.float32, device=dev),
             torch.empty(n_pairs, dtype=torch.float32, device=dev),
@@ -654,10 +661,11 @@ def preference_loss(logits, token_ids, seq_offsets, ref_logprobs=None, pair_weig
         params = _PreferenceParams(temperature, beta, label_smoothing, margin,
                                    TS_PREFERENCE_MEAN if mean else 0)
         _check(lib.preference_loss(
-            _ptr(logits), kind, rows, vocab, ld, _ptr(token_ids), _ptr(seq_offsets), n_pairs,
-            ctypes.addressof(params), _ptr(ref_logprobs), _ptr(pair_weights), _ptr(grad_loss),
-            _ptr(out.loss), _ptr(out.pair_losses), _ptr(out.rewards), _ptr(out.logprobs),
-            _ptr(out.row_status), _ptr(grad_logits), ldg, _ptr(workspace), workspace.numel(), s))
+            logits.data_ptr(), kind, rows, vocab, ld, token_ids.data_ptr(),
+            seq_offsets.data_ptr(), n_pairs, ctypes.addressof(params), _ptr(ref_logprobs),
+            _ptr(pair_weights), _ptr(grad_loss), out.loss.data_ptr(), out.pair_losses.data_ptr(),
+            out.rewards.data_ptr(), out.logprobs.data_ptr(), out.row_status.data_ptr(),
+            _ptr(grad_logits), ldg, workspace.data_ptr(), workspace.numel(), s))
     return out
 
 
@@ -673,32 +681,29 @@ def lmhead_logits_local_lora(hidden, lm_head, lora_a, lora_b, adapter_ids, adapt
     row's own ``A = lora_a[id]``, ``B = lora_b[id]`` (bf16 ``[n, rank, H]`` and
     ``[n, V_local, rank]``, inner stride 1) and ``adapter_scales[id]`` (fp32,
     None for 1); id -1 has no adapter."""
-    if hidden.dim() != 2 or lm_head.dim() != 2 or lora_a.dim() != 3 or lora_b.dim() != 3:
+    shapes = hidden.shape, lm_head.shape, lora_a.shape, lora_b.shape
+    if tuple(map(len, shapes)) != (2, 2, 3, 3):
         raise ValueError("hidden and lm_head must be 2-D, lora_a and lora_b 3-D")
-    rows, h = hidden.shape
-    vocab = lm_head.shape[0]
-    n, rank = lora_a.shape[:2]
-    if lm_head.shape[1] != h or lora_a.shape[2] != h or tuple(lora_b.shape) != (n, vocab, rank):
+    (rows, h), (vocab, h_w), (n, rank, h_a), shape_b = shapes
+    if h_w != h or h_a != h or shape_b != (n, vocab, rank):
         raise ValueError("sizes do not fit: hidden [rows, H], lm_head [V, H], lora_a [n, rank, H], "
                          "lora_b [n, V, rank]")
     dev = hidden.device
+    ld = []
     for t, name in ((hidden, "hidden"), (lm_head, "lm_head"), (lora_a, "lora_a"),
                     (lora_b, "lora_b")):
         if t.dtype != torch.bfloat16:
             raise TypeError(f"{name} must be bfloat16")
-        if t.shape[-1] > 1 and t.stride(-1) != 1:
+        stride, (count, width) = t.stride(), t.shape[-2:]
+        if width > 1 and stride[-1] != 1:
             raise ValueError(f"{name} must have unit inner stride")
         if t.device != dev:
             raise ValueError(f"{name} is on {t.device}, hidden on {dev}")
+        ld.append(stride[-2] if count > 1 else width)
+    ld_hidden, ld_lm_head, ld_a, ld_b = ld
+    stride_a, stride_b = (lora_a.stride(0), lora_b.stride(0)) if n > 1 else (0, 0)
     _check_vector(adapter_ids, "adapter_ids", rows, dev, torch.int32)
     _check_vector(adapter_scales, "adapter_scales", n, dev)
-
-    def row_stride(t, width):
-        return int(t.stride(-2)) if t.shape[-2] > 1 else width
-
-    def adapter_stride(t):
-        return int(t.stride(0)) if n > 1 else 0
-
     with _OnDevice(dev, stream) as s:
         if out is None:
             out = torch.empty(rows, vocab, dtype=torch.float32, device=dev)
@@ -707,11 +712,10 @@ def lmhead_logits_local_lora(hidden, lm_head, lora_a, lora_b, adapter_ids, adapt
             raise ValueError("out must be fp32 [rows, V_local] with unit column stride")
         workspace = _workspace(workspace, lmhead_lora_workspace_bytes(rows, rank), dev)
         _check(lib.lmhead_logits_local_lora(
-            _ptr(hidden), rows, h, row_stride(hidden, h), _ptr(lm_head), vocab,
-            row_stride(lm_head, h), _ptr(lora_a), adapter_stride(lora_a), row_stride(lora_a, h),
-            _ptr(lora_b), adapter_stride(lora_b), row_stride(lora_b, rank), n, rank,
-            _ptr(adapter_scales), _ptr(adapter_ids), _ptr(out), row_stride(out, vocab),
-            _ptr(workspace), workspace.numel(), s))
+            hidden.data_ptr(), rows, h, ld_hidden, lm_head.data_ptr(), vocab, ld_lm_head,
+            lora_a.data_ptr(), stride_a, ld_a, lora_b.data_ptr(), stride_b, ld_b, n, rank,
+            _ptr(adapter_scales), _ptr(adapter_ids), out.data_ptr(),
+            out.stride(0) if rows > 1 else vocab, workspace.data_ptr(), workspace.numel(), s))
     return out
 
 

@@ -302,7 +302,8 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, WAVES) void lora_gemm_kerne
     if (q < A_LOADS)
       src[q] = p.hidden + static_cast<int64_t>(d.row[min(m0 + r, M - 1)]) * p.ld_hidden + c * 8;
     else
-      src[q] = p.lm_head + static_cast<int64_t>(n0 + min(r - BM, N - 1 - n0)) * p.ld_lm_head + c * 8;
+      src[q] = p.lm_head + static_cast<int64_t>(n0 + min(r - BM, N - 1 - n0)) * p.ld_lm_head +
+               c * 8;
   }
   const bool in = tid < BM && m0 + tid < M;
   const int my_id = in ? d.id[m0 + tid] : kNoAdapter;
@@ -694,7 +695,8 @@ hipError_t launch_lmhead_lora(const LoraArgs& p, void* ws, hipStream_t stream) {
                          p.rows, p.vocab, p.hidden_dim, stream);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(lora_add_kernel,
-                     dim3((p.vocab + int64_t{kUpCols} - 1) / kUpCols, p.rows < 65535 ? p.rows : 65535),
+                     dim3((p.vocab + int64_t{kUpCols} - 1) / kUpCols,
+                          p.rows < 65535 ? p.rows : 65535),
                      dim3(kUpCols), 0, stream, p, d);
   return hipGetLastError();
 }

@@ -1216,8 +1216,8 @@ hipError_t policy_loss_t(const TokenRows& t, const PolicyArgs& p, const GradRows
   // loss; with a gradient the last pass does, otherwise a kernel of its own.
   const bool sum_here = !back && t.rows <= kRowsPerGroup;
   hipLaunchKernelGGL((policy_rows_kernel<T>),
-                     dim3(grid_of((t.rows + int64_t{kRowsPerGroup} - 1) / kRowsPerGroup)), dim3(kThreads),
-                     0, stream, static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, in, sc, w.parts,
+                     dim3(grid_of((t.rows + int64_t{kRowsPerGroup} - 1) / kRowsPerGroup)),
+                     dim3(kThreads), 0, stream, static_cast<const T*>(t.x), t.ld, t.rows, t.vocab, in, sc, w.parts,
                      cut.chunks, p, back ? w.grads : nullptr, w.terms, sum_here);
   e = hipGetLastError();
   if (e != hipSuccess || sum_here) return e;
