@@ -187,6 +187,30 @@ def test_rows_do_not_reach_each_other(hidden):
     assert torch.isnan(got[ids == 1]).all() and torch.isnan(got[11]).all()
 
 
+@pytest.mark.parametrize("rows,vocab", [(5, 300), (60, 25001), (64, 33100), (90, 22300), (100, 66000),
+                                        (150, 22100), (190, 60001), (300, 18993), (256, 60001),
+                                        (640, 30001)])
+def test_infinities_in_b(rows, vocab):
+    """On every tile shape: an infinity in an adapter's B makes that entry of
+    its rows infinite with u's sign, and changes no other bit."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    rank, n = 24, 7
+    x, w, a, b, scales = make(rows, 64, vocab, rank, n, rows)
+    ids = torch.from_numpy(some_ids("random", rows, n, 2).astype(np.int32)).to(_dev())
+    clean = ts.lmhead_logits_local_lora(x, w, a, b, ids, scales)
+    cols = torch.tensor([0, 17, vocab // 2, vocab - 1], device=_dev())
+    b[1, cols, 19] = float("inf")
+    got = ts.lmhead_logits_local_lora(x, w, a, b, ids, scales)
+    own = ids == 1
+    u = x[own].double() @ a[1, 19].double()
+    want = clean.clone()
+    want[own.nonzero(), cols] = (u.sign() * float("inf")).float()[:, None]
+    assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("hidden", [128, 136])
 def test_infinite_inner_sums(hidden):
     """An infinity in A makes u infinite, and the logits infinite with B's sign

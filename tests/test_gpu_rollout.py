@@ -129,3 +129,37 @@ def test_preference_step_in_place():
     tol[np.arange(rows), tokens.cpu().numpy().clip(0)] += 0.2 / 3 * 4 * LSE
     assert (np.abs(f64(logits) - want["grad"]) <= tol).all()
     assert not logits[::7].any()
+
+
+def test_two_streams_at_once():
+    """The same calls on two streams beside each other, and on the default
+    stream by its number, give the results of one after the other."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    dev, g, x, w, a, b, ids, scales = _setup(100, 256, 9001, 24, 6, 8)
+    other = torch.randn(100, 256, generator=g, device=dev).to(torch.bfloat16)
+    tok = torch.randint(0, 9001, (100,), generator=g, device=dev, dtype=torch.int32)
+    old = -torch.rand(100, generator=g, device=dev) - 8
+    adv = torch.randn(100, generator=g, device=dev)
+    off = torch.tensor([0, 30, 50, 80, 100], dtype=torch.int32, device=dev)
+
+    def step(x, stream):
+        logits = ts.lmhead_logits_local_lora(x, w, a, b, ids, scales, stream=stream)
+        pol = ts.policy_loss(logits, tok, old, adv, backward=True, stream=stream)
+        pref = ts.preference_loss(logits, tok, off, backward=True, stream=stream)
+        score = ts.token_logprobs(logits, tok, entropies=True, stream=stream)
+        return [logits, pol.loss, pol.grad_logits, pref.loss, pref.grad_logits, score.entropies]
+
+    want = [step(x, None), step(other, None)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        got = [step(x, streams[0]), step(other, streams[1])]
+        torch.cuda.synchronize()
+        for one, two in zip(got, want):
+            assert all(torch.equal(p, q) for p, q in zip(one, two))
+    numbered = step(x, torch.cuda.default_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(numbered, want[0]))
