@@ -96,13 +96,16 @@ CASES = [
     (320, 128, 400, 16, 1, 0, "one"), (640, 256, 700, 32, 16, 0, "runs"),
     (641, 128, 100, 48, 7, 0, "random"), (50, 128, 90, 16, 4, 0, "bad"),
     (700, 64, 33, 8, 6, 0, "bad"),
-    # wider vocabularies, for every tile shape: 64 x 128 with three stages and
-    # with two, 128 x 128 with two, of few tiles and of many, 256 and 320 rows
+    # wider vocabularies, for every tile shape: 64 x 128 and 128 x 128 with many
+    # stages and with two, of few tiles and of many, 256 and 320 rows
     (60, 128, 25001, 16, 9, 0, "random"), (90, 192, 22300, 40, 12, 0, "runs"),
     (64, 320, 33100, 24, 64, 0, "random"), (5, 64, 40000, 8, 2, 0, "bad"),
     (100, 128, 66000, 16, 7, 0, "random"), (133, 192, 31040, 64, 9, 0, "bad"),
     (256, 128, 60001, 32, 256, 0, "random"), (320, 128, 60000, 24, 20, 1, "runs"),
     (310, 64, 60100, 8, 3, 0, "bad"), (250, 64, 60002, 16, 1, 0, "none"),
+    # 64 x 64, 128 x 128 with many rows
+    (60, 192, 10001, 16, 9, 0, "random"), (130, 64, 3333, 24, 130, 1, "bad"),
+    (320, 448, 9500, 40, 30, 0, "runs"), (64, 64, 11000, 256, 64, 0, "random"),
     # 192 x 128, 192 x 256, one round of 128 x 128, two row tiles of 320
     (150, 128, 22100, 16, 9, 0, "random"), (190, 192, 60001, 24, 40, 1, "bad"),
     (192, 64, 40010, 72, 192, 0, "random"), (300, 64, 18993, 8, 30, 0, "random"),

@@ -652,16 +652,25 @@ hipError_t launch_lmhead_lora(const LoraArgs& p, void* ws, hipStream_t stream) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (p.hidden_dim % kBK == 0) {
-    // Few tiles: a CU brings in 63 GB/s at most, so 64 x 128 tiles that are
-    // fewer than half the CUs take four times as many, narrow ones (4 rows of
-    // 4,288 and 2,613 columns: 36 us with 21 tiles, 27 with 82; 61 rows and
-    // 25,129 columns, 197 tiles: 54, 83 with 786), and up to one or two a CU a
-    // third stage (90 rows, 22,324 columns: 57 us as 175 tiles of 128 x 128
-    // with two stages, 46 as 350 with three).
-    const int64_t small = (p.rows + int64_t{63}) / 64 * ((p.vocab + int64_t{127}) / 128);
-    if (small <= 128) return launch_fused<32, 32, 1, 1, 0, 6, 1>(p, d, stream);
-    if (small <= 256 || (p.rows > 64 && small <= 512))
-      return launch_fused<64, 128, 1, 4, 0, 3, 2>(p, d, stream);
+    auto tiles = [&](int64_t bm, int64_t bn) {
+      return (p.rows + bm - 1) / bm * ((p.vocab + bn - 1) / bn);
+    };
+    // Few tiles: the smallest that makes no more than one a CU (a few more of 32 x
+    // 32), one workgroup a CU with as many stages as help.  H = 4,096, weights not
+    // in the caches, us:
+    //   rows x columns    32 x 32  64 x 64  64 x 128  128 x 128  next below
+    //     4 x  4,748         28       30        37         45
+    //    64 x  4,748         35       38        48         52
+    //    64 x  9,496         43       41        50         53
+    //    64 x 16,384         75       49        56         58
+    //   128 x 16,384         94       70        54         65         66
+    //    64 x 18,992         76       69        62         64         82
+    //   128 x 25,000        125      106        83         69         72
+    //   320 x  9,496        111       79        75         56         64
+    if (tiles(32, 32) <= 300) return launch_fused<32, 32, 1, 1, 0, 6, 1>(p, d, stream);
+    if (tiles(64, 64) <= 256) return launch_fused<64, 64, 2, 2, 0, 6, 1>(p, d, stream);
+    if (tiles(64, 128) <= 256) return launch_fused<64, 128, 2, 4, 0, 5, 2>(p, d, stream);
+    if (tiles(128, 128) <= 256) return launch_fused<128, 128, 2, 4, 0, 4, 2>(p, d, stream);
     // Up to 128 rows one row tile reads the lm_head once: past the caches.
     if (p.rows <= 64) return launch_fused<64, 128, 1, 4, 2, 2, 3>(p, d, stream);
     if (p.rows <= 128) return launch_fused<128, 128, 2, 4, 2, 2, 4>(p, d, stream);
@@ -669,17 +678,17 @@ hipError_t launch_lmhead_lora(const LoraArgs& p, void* ws, hipStream_t stream) {
     // of it takes in 10 ns a K step (us, H = 4,096, but 2,560 of 133 and 256
     // rows; 192n is 192 x 128):
     //   rows x columns     128   192n   192   256   320
-    //   133 x  31,040       71     60    78    89   101
-    //   256 x  31,040       58     81    69    75    86
-    //   300 x  18,992       82    117    90   111   129
-    //   512 x  18,992      117    119   100   109   128
-    //   640 x  18,992      164    213   220   154   163
-    //   640 x  31,040      228    256   209   234   164
+    //   133 x  31,040       79     67    95    97   104
+    //   256 x  31,040       76     91    82    88    92
+    //   300 x  18,992       92    125   101   114   133
+    //   512 x  18,992      150    130   110   121   136
+    //   640 x  18,992      171    219   225   154   168
+    //   192 x  40,000      153    136   121   126   137
+    //   640 x  31,040      230    262   218   245   175
     //   160 x 151,936      441    366   371   390   433
     //   384 x 151,936      608    649   553   645   760
     auto rounds = [&](int64_t bm, int64_t bn, int64_t at_once, int64_t cost) {
-      const int64_t tiles = (p.rows + bm - 1) / bm * ((p.vocab + bn - 1) / bn);
-      return (tiles + at_once - 1) / at_once * cost;
+      return (tiles(bm, bn) + at_once - 1) / at_once * cost;
     };
     const int64_t t128 = rounds(128, 128, 512, 140), t192n = rounds(192, 128, 256, 120);
     const int64_t t192 = rounds(192, 256, 256, 180), t256 = rounds(256, 256, 256, 205);
