@@ -578,7 +578,7 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, WAVES) void lora_gemm_kerne
 }
 
 template <int BM, int BN, int WAVES_M, int WAVES_N, int AUX, int STAGES, int WAVES>
-hipError_t launch_fused(const LoraArgs& p, const DownRows& d, hipStream_t stream) {
+hipError_t launch_tile(const LoraArgs& p, const DownRows& d, hipStream_t stream) {
   const int tiles_m = (p.rows + BM - 1) / BM;
   const int tiles_n = (p.vocab - 1) / BN + 1;
   const int total = tiles_m * tiles_n;
@@ -587,6 +587,17 @@ hipError_t launch_fused(const LoraArgs& p, const DownRows& d, hipStream_t stream
                      dim3(per_xcd * kXcds), dim3(64 * WAVES_M * WAVES_N), 0, stream, p, d, tiles_m,
                      total, per_xcd);
   return hipGetLastError();
+}
+
+// One row tile reads the lm_head once, past the caches (AUX 2), as the weights
+// of a model's layers come between two calls: 4 x 18,992 (H = 4,096) 42 us
+// instead of 48, 64 x 16,384 43 instead of 49, 128 x 31,040 74 and 80, 160 x
+// 60,000 132 and 149, 256 x 151,936 397 and 414.  With several row tiles those
+// after the first find it in the L2.
+template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, int WAVES>
+hipError_t launch_fused(const LoraArgs& p, const DownRows& d, hipStream_t stream) {
+  return p.rows <= BM ? launch_tile<BM, BN, WAVES_M, WAVES_N, 2, STAGES, WAVES>(p, d, stream)
+                      : launch_tile<BM, BN, WAVES_M, WAVES_N, 0, STAGES, WAVES>(p, d, stream);
 }
 
 // ------------------------------------------- other hidden sizes: a second pass
@@ -655,25 +666,26 @@ hipError_t launch_lmhead_lora(const LoraArgs& p, void* ws, hipStream_t stream) {
     auto tiles = [&](int64_t bm, int64_t bn) {
       return (p.rows + bm - 1) / bm * ((p.vocab + bn - 1) / bn);
     };
-    // Few tiles: the smallest that makes no more than one a CU (a few more of 32 x
-    // 32), one workgroup a CU with as many stages as help.  H = 4,096, weights not
-    // in the caches, us:
+    // Few tiles: the smallest that makes no more than one a CU, with as many
+    // stages as help.  H = 4,096, weights not in the caches, us:
     //   rows x columns    32 x 32  64 x 64  64 x 128  128 x 128  next below
     //     4 x  4,748         28       30        37         45
-    //    64 x  4,748         35       38        48         52
-    //    64 x  9,496         43       41        50         53
-    //    64 x 16,384         75       49        56         58
+    //    32 x  9,496         35       34        42         49
+    //    64 x 16,384         73       43        50         53
     //   128 x 16,384         94       70        54         65         66
-    //    64 x 18,992         76       69        62         64         82
+    //    64 x 18,992         77       67        52         55         82
     //   128 x 25,000        125      106        83         69         72
     //   320 x  9,496        111       79        75         56         64
-    if (tiles(32, 32) <= 300) return launch_fused<32, 32, 1, 1, 0, 6, 1>(p, d, stream);
-    if (tiles(64, 64) <= 256) return launch_fused<64, 64, 2, 2, 0, 6, 1>(p, d, stream);
-    if (tiles(64, 128) <= 256) return launch_fused<64, 128, 2, 4, 0, 5, 2>(p, d, stream);
-    if (tiles(128, 128) <= 256) return launch_fused<128, 128, 2, 4, 0, 4, 2>(p, d, stream);
-    // Up to 128 rows one row tile reads the lm_head once: past the caches.
-    if (p.rows <= 64) return launch_fused<64, 128, 1, 4, 2, 2, 3>(p, d, stream);
-    if (p.rows <= 128) return launch_fused<128, 128, 2, 4, 2, 2, 4>(p, d, stream);
+    if (tiles(32, 32) <= 256) return launch_fused<32, 32, 1, 1, 6, 1>(p, d, stream);
+    if (tiles(64, 64) <= 256) return launch_fused<64, 64, 2, 2, 6, 1>(p, d, stream);
+    if (tiles(64, 128) <= 256) return launch_fused<64, 128, 2, 4, 5, 2>(p, d, stream);
+    if (tiles(128, 128) <= 256) return launch_fused<128, 128, 2, 4, 4, 2>(p, d, stream);
+    // One row tile and many columns: several workgroups a CU.  x 151,936, three
+    // stages and two, us: 8 rows 209 and 228, 32 rows 226 and 266, 48 rows 234
+    // and 253, 64 rows 243 and 234.
+    if (p.rows <= 48) return launch_tile<64, 128, 2, 4, 2, 3, 4>(p, d, stream);
+    if (p.rows <= 64) return launch_tile<64, 128, 1, 4, 2, 2, 3>(p, d, stream);
+    if (p.rows <= 128) return launch_tile<128, 128, 2, 4, 2, 2, 4>(p, d, stream);
     // More rows: the tile whose rounds over the card take least, by what a round
     // of it takes in 10 ns a K step (us, H = 4,096, but 2,560 of 133 and 256
     // rows; 192n is 192 x 128):
@@ -694,11 +706,11 @@ hipError_t launch_lmhead_lora(const LoraArgs& p, void* ws, hipStream_t stream) {
     const int64_t t192 = rounds(192, 256, 256, 180), t256 = rounds(256, 256, 256, 205);
     const int64_t t320 = rounds(320, 256, 256, 245);
     const int64_t least = std::min({t128, t192n, t192, t256, t320});
-    if (t320 == least) return launch_fused<320, 256, 2, 4, 0, 2, 2>(p, d, stream);
-    if (t256 == least) return launch_fused<256, 256, 2, 4, 0, 2, 2>(p, d, stream);
-    if (t192 == least) return launch_fused<192, 256, 2, 4, 0, 2, 2>(p, d, stream);
-    if (t192n == least) return launch_fused<192, 128, 2, 4, 0, 3, 2>(p, d, stream);
-    return launch_fused<128, 128, 2, 4, 0, 2, 4>(p, d, stream);
+    if (t320 == least) return launch_fused<320, 256, 2, 4, 2, 2>(p, d, stream);
+    if (t256 == least) return launch_fused<256, 256, 2, 4, 2, 2>(p, d, stream);
+    if (t192 == least) return launch_fused<192, 256, 2, 4, 2, 2>(p, d, stream);
+    if (t192n == least) return launch_fused<192, 128, 2, 4, 3, 2>(p, d, stream);
+    return launch_tile<128, 128, 2, 4, 0, 2, 4>(p, d, stream);
   }
   e = launch_lmhead_gemm(p.hidden, p.ld_hidden, p.lm_head, p.ld_lm_head, p.logits, p.ld_logits,
                          p.rows, p.vocab, p.hidden_dim, stream);
