@@ -400,8 +400,9 @@ int sampler_assemble_and_sample(const float* const* slices, const int64_t* slice
  *   grad_logits  [rows, vocab] in the logits' type, leading dimension
  *                ld_grad >= vocab.  It may be the logits themselves (same
  *                pointer and leading dimension: the gradient replaces them);
- *                any other overlap is TS_EINVAL.  Columns past vocab are not
- *                written.
+ *                any other overlap is TS_EINVAL (columns of one buffer beside
+ *                the logits' columns, with the same leading dimension, are
+ *                none).  Columns past vocab are not written.
  *   workspace    as for sampler_sample: 256-byte aligned scratch, no
  *                initialisation, ordered on one stream by whoever shares it.
  * Sums over the vocabulary are fp32 per thread and double from there on;

@@ -756,3 +756,30 @@ def test_many_rows():
     # rows are consecutive entries: a left-out end stays zero
     tok[-3:] = -1
     assert not ts.token_logprobs(x, tok).logprobs[-3:].any()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows", [5, 130])
+def test_gradient_beside_the_logits(rows, dtype):
+    """Logits and gradient as columns of one buffer, in either order."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    vocab = 33003
+    logits, x = make_logits(rows, vocab, dtype, 0, 3, masks=False)
+    tok = to_dev(allowed_tokens(x, 4), torch.int32)
+    old = to_dev(np.full(rows, -9.0))
+    adv = to_dev(np.linspace(-1, 1, rows))
+    for left, right in ((0, vocab + 2), (vocab + 3, 1)):
+        wide = torch.full((rows, 2 * vocab + 5), 7.0, dtype=logits.dtype, device=_dev())
+        here, grad = wide[:, left:left + vocab], wide[:, right:right + vocab]
+        here.copy_(logits)
+        apart = torch.empty_like(wide)[:, right:right + vocab]
+        want = ts.policy_loss(here, tok, old, adv, grad_logits=apart)
+        got = ts.policy_loss(here, tok, old, adv, grad_logits=grad)
+        assert torch.equal(grad, apart) and torch.equal(got.loss, want.loss)
+        assert torch.equal(here, logits)
+        grad.fill_(7.0)
+        here.fill_(7.0)
+        assert (wide == 7.0).all()

@@ -136,6 +136,10 @@ def _back(**kw):
     (dict(d=FAKE + 400), ts.TS_EINVAL),           # overlaps, other rows
     (dict(d=FAKE, ldd=128), ts.TS_EINVAL),        # the same start, another stride
     (dict(d=FAKE * 2 + 2), ts.TS_EUNSUPPORTED),
+    # columns of one buffer that touch the logits' on either side
+    (dict(ld=250, ldd=250, d=FAKE + 4 * 99), ts.TS_EINVAL),
+    (dict(ld=250, ldd=250, d=FAKE + 4 * 151), ts.TS_EINVAL),
+    (dict(ld=250, ldd=250, d=FAKE - 4 * 99), ts.TS_EINVAL),
 ])
 def test_token_logprobs_backward_refusals(kw, code):
     assert _back(**kw) == code

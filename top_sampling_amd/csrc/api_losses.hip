@@ -75,6 +75,12 @@ int grad_rows(ts::GradRows& d, const ts::TokenRows& t, void* grad_logits, int64_
   const char* b = static_cast<const char*>(grad_logits);
   const char* a_end = a + (static_cast<int64_t>(t.rows - 1) * t.ld + t.vocab) * size;
   const char* b_end = b + (static_cast<int64_t>(t.rows - 1) * ld_grad + t.vocab) * size;
+  // Columns side by side in one buffer do not overlap either.
+  if (t.rows > 1 && ld_grad == t.ld) {
+    int64_t gap = (b - a) / static_cast<int64_t>(size) % ld_grad;
+    if (gap < 0) gap += ld_grad;
+    if (gap >= t.vocab && gap <= ld_grad - t.vocab) return TS_OK;
+  }
   if (a < b_end && b < a_end)
     return fail(TS_EINVAL, "grad_logits overlaps logits without being the same rows");
   return TS_OK;
