@@ -559,11 +559,11 @@ def token_logprobs(logits, token_ids, temperature: float = 1.0, entropies: bool 
     dev = logits.device
     with _OnDevice(dev, stream) as s:
         workspace = _workspace(workspace, token_logprobs_workspace_bytes(rows, vocab), dev)
-        out = TokenLogprobs(
-            torch.empty(rows, dtype=torch.float32, device=dev),
-            torch.empty(rows, dtype=torch.float32, device=dev) if entropies else None,
-            torch.empty((rows, 2), dtype=torch.float32, device=dev),
-            torch.empty(rows, dtype=torch.int32, device=dev))
+        stats, logprobs, status, h = torch.empty(
+            (4 + bool(entropies)) * rows, dtype=torch.float32,
+            device=dev).split_with_sizes((2 * rows, rows, rows, rows if entropies else 0))
+        out = TokenLogprobs(logprobs, h if entropies else None, stats.view(rows, 2),
+                            status.view(torch.int32))
         _check(lib.token_logprobs(
             logits.data_ptr(), kind, rows, vocab, ld, token_ids.data_ptr(), temperature,
             out.logprobs.data_ptr(), _ptr(out.entropies), out.row_stats.data_ptr(),
@@ -614,10 +614,11 @@ def policy_loss(logits, token_ids, old_logprobs, advantages, ref_logprobs=None, 
     with _OnDevice(dev, stream) as s:
         workspace = _workspace(workspace, token_logprobs_workspace_bytes(rows, vocab), dev)
         grad_logits, ldg = _gradient(grad_logits, backward, logits)
-        logprobs, ratios, kl, status = torch.empty((4, rows), dtype=torch.float32,
-                                                   device=dev).unbind(0)
-        out = PolicyLoss(torch.empty((), dtype=torch.float32, device=dev), logprobs, ratios, kl,
-                         status.view(torch.int32), grad_logits)
+        loss, logprobs, ratios, kl, status = torch.empty(
+            1 + 4 * rows, dtype=torch.float32,
+            device=dev).split_with_sizes((1, rows, rows, rows, rows))
+        out = PolicyLoss(loss.view(()), logprobs, ratios, kl, status.view(torch.int32),
+                         grad_logits)
         params = _PolicyParams(temperature, clip_low, clip_high, kl_coef)
         _check(lib.policy_loss(
             logits.data_ptr(), kind, rows, vocab, ld, token_ids.data_ptr(),
@@ -652,12 +653,11 @@ def preference_loss(logits, token_ids, seq_offsets, ref_logprobs=None, pair_weig
         workspace = _workspace(workspace, preference_loss_workspace_bytes(rows, vocab, n_pairs),
                                dev)
         grad_logits, ldg = _gradient(grad_logits, backward, logits)
-        out = PreferenceLoss(
-            torch.empty((), dtype=torch.float32, device=dev),
-            torch.empty(n_pairs, dtype=torch.float32, device=dev),
-            torch.empty(2 * n_pairs, dtype=torch.float32, device=dev),
-            torch.empty(rows, dtype=torch.float32, device=dev),
-            torch.empty(rows, dtype=torch.int32, device=dev), grad_logits)
+        loss, pair_losses, rewards, logprobs, status = torch.empty(
+            1 + 3 * n_pairs + 2 * rows, dtype=torch.float32,
+            device=dev).split_with_sizes((1, n_pairs, 2 * n_pairs, rows, rows))
+        out = PreferenceLoss(loss.view(()), pair_losses, rewards, logprobs,
+                             status.view(torch.int32), grad_logits)
         params = _PreferenceParams(temperature, beta, label_smoothing, margin,
                                    TS_PREFERENCE_MEAN if mean else 0)
         _check(lib.preference_loss(
