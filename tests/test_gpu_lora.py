@@ -110,6 +110,9 @@ CASES = [
     (150, 128, 22100, 16, 9, 0, "random"), (190, 192, 60001, 24, 40, 1, "bad"),
     (192, 64, 40010, 72, 192, 0, "random"), (300, 64, 18993, 8, 30, 0, "random"),
     (640, 64, 30001, 16, 64, 0, "runs"),
+    # several row tiles of 64 x 128, 192 x 128, 192 x 256 and 256 x 256
+    (90, 64, 9500, 16, 9, 0, "random"), (370, 128, 16001, 24, 30, 0, "random"),
+    (384, 64, 60001, 16, 7, 0, "bad"), (512, 64, 31000, 8, 5, 0, "runs"),
     # hidden sizes that are no multiple of 64
     (5, 72, 33, 8, 2, 0, "random"), (70, 200, 300, 24, 9, 1, "runs"), (260, 136, 140, 64, 5, 0, "bad"),
 ]
@@ -190,9 +193,9 @@ def test_rows_do_not_reach_each_other(hidden):
     assert torch.isnan(got[ids == 1]).all() and torch.isnan(got[11]).all()
 
 
-@pytest.mark.parametrize("rows,vocab", [(5, 300), (60, 25001), (64, 33100), (90, 22300), (100, 66000),
-                                        (150, 22100), (190, 60001), (300, 18993), (256, 60001),
-                                        (640, 30001)])
+@pytest.mark.parametrize("rows,vocab", [(5, 300), (5, 40000), (60, 10001), (60, 25001), (64, 33100),
+                                        (90, 22300), (100, 66000), (150, 22100), (190, 60001),
+                                        (300, 18993), (256, 60001), (640, 30001)])
 def test_infinities_in_b(rows, vocab):
     """On every tile shape: an infinity in an adapter's B makes that entry of
     its rows infinite with u's sign, and changes no other bit."""
