@@ -491,7 +491,9 @@ int policy_loss(const void* logits, int32_t logits_type, int64_t rows, int64_t v
  *            - label_smoothing ln sigmoid(-z)
  *   loss   = sum over pairs of pair_weights l,
  * and, with grad_logits, grad_loss times its gradient.  An empty sequence
- * has rho = 0.  Rows before the first and after the last sequence take no
+ * has rho = 0.  A term of factor 0 is 0 at any z: a token of probability 0 in
+ * the rejected answer alone (z = inf) adds no loss and no gradient at
+ * label_smoothing 0.  Rows before the first and after the last sequence take no
  * part (log-probability and gradient row 0).  A pair of weight 0 adds
  * nothing to the loss and the gradient.
  *   seq_offsets    int32 [2 n_pairs + 1], non-decreasing; used clamped to

@@ -116,7 +116,9 @@ def preference(x, tokens, offsets, ref=None, pair_weights=None, *, beta=0.1, lab
     rho = rho / count
     z = beta * (rho[:pairs] - rho[pairs:]) - margin
     ls = lambda v: -np.logaddexp(0.0, -v)  # noqa: E731  ln sigmoid
-    each = -(1 - label_smoothing) * ls(z) - label_smoothing * ls(-z)
+    # a term of factor 0 is 0, also at an infinite z
+    each = sum((-k * ls(v) for k, v in ((1 - label_smoothing, z), (label_smoothing, -z)) if k != 0),
+               np.zeros(pairs))
     dz = -(1 - label_smoothing) * np.exp(ls(-z)) + label_smoothing * np.exp(ls(z))
     g = np.zeros(len(x))
     for i in range(2 * pairs):

@@ -783,3 +783,57 @@ def test_gradient_beside_the_logits(rows, dtype):
         grad.fill_(7.0)
         here.fill_(7.0)
         assert (wide == 7.0).all()
+
+
+def entry_tol(want, x, tok, coef, temperature, dtype):
+    """Of a loss's gradient: grad_tol's relative part, and the error `coef` of
+    each row's coefficient times what multiplies it, the entry's own
+    probability, or 1 - p_t <= 1 at the token."""
+    scale = np.exp(ref.log_softmax(x, temperature))
+    scale[np.arange(len(x)), np.maximum(tok, 0)] = 1.0
+    return grad_tol(want, x, temperature, dtype, 2 * LSE) + coef[:, None] * scale
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("smoothing", [0.0, 0.1, 1.0])
+@pytest.mark.parametrize("mean", [False, True])
+def test_preference_answers_with_a_masked_token(dtype, smoothing, mean):
+    """A token of probability 0 in the rejected answer of a pair and in the
+    chosen one: z is +-inf, and a term of factor 0 stays 0."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    for vocab in (700, 40001):  # whole rows, and in chunks
+        say("masked token", dtype, smoothing, mean, vocab)
+        rows, pairs, beta = 12, 3, 0.3
+        logits, x = make_logits(rows, vocab, dtype, 0, 21, masks=False)
+        tok = allowed_tokens(x, 7, skip=0.0)
+        off = np.arange(0, 13, 2, dtype=np.int32)
+        for r in (2, 9):  # the chosen and the rejected answer of pair 1
+            logits[r, int(tok[r])] = -float("inf")
+        x = logits.cpu().double().numpy()
+        for masked, left_out in ((9, 2), (2, 9)):
+            t = tok.copy()
+            t[left_out] = -1
+            kw = dict(beta=beta, label_smoothing=smoothing, mean=mean)
+            want = ref.preference(x, t, off, **kw)
+            got = ts.preference_loss(logits, to_dev(t, torch.int32), to_dev(off, torch.int32),
+                                     backward=True, **kw)
+            fwd = ts.preference_loss(logits, to_dev(t, torch.int32), to_dev(off, torch.int32),
+                                     **kw)
+            torch.cuda.synchronize()
+            # by hand: z = +inf, then -inf
+            lost = (smoothing if masked == 9 else 1 - smoothing) > 0
+            assert want["pair_losses"][1] == (np.inf if lost else 0.0)
+            # at most four rows in a z, and values below 16
+            z_tol = 4 * beta * LSE
+            for o in (got, fwd):
+                close(o.pair_losses, want["pair_losses"], z_tol + 16 * U, "pair losses")
+                close(o.loss, want["loss"], z_tol + 16 * U, "loss")
+                close(o.rewards, want["rewards"], z_tol + 16 * U, "rewards")
+                assert not o.row_status.any()
+            k = np.full(rows, beta / pairs * (z_tol + 2 * LSE))
+            close(got.grad_logits, want["grad"], entry_tol(want["grad"], x, t, k, 1.0, dtype),
+                  "gradient")
+            assert torch.isfinite(got.grad_logits).all()

@@ -238,3 +238,19 @@ def test_binding_refusals():
         ts._grad_rows(torch.zeros(3, 7), x)
     with pytest.raises(ValueError, match="grad_logits"):
         ts._grad_rows(torch.zeros(1, 8).expand(3, 8), x)
+
+
+def test_preference_terms_of_factor_0():
+    """A masked token in one answer: z is +-inf, and only a term whose factor
+    is above 0 can make the loss infinite."""
+    x = np.zeros((2, 4))
+    x[1, 3] = -np.inf
+    tok = np.array([0, 3])
+    for order, sign in (([0, 1], 1), ([1, 0], -1)):
+        rows = np.array(order)
+        for eps in (0.0, 0.1, 1.0):
+            got = ref.preference(x[rows], tok[rows], [0, 1, 2], label_smoothing=eps)
+            # -(1 - eps) ln sigmoid(z) is 0 at z = inf, and so the other way
+            factor = eps if sign > 0 else 1 - eps
+            assert got["pair_losses"][0] == got["loss"] == (np.inf if factor else 0.0)
+            assert np.isfinite(got["grad"]).all() and got["grad"].any() == (factor > 0)

@@ -710,7 +710,10 @@ __global__ __launch_bounds__(kPairThreads) void preference_pairs_kernel(
       const double beta = p.beta, eps = p.label_smoothing;
       const double z = beta * (rho[0] - rho[1]) - p.margin;
       const double soft = log1p(exp(-fabs(z)));  // -ln sigmoid(|z|)
-      const double loss = (1.0 - eps) * (soft + fmax(-z, 0.0)) + eps * (soft + fmax(z, 0.0));
+      // A term of factor 0 is left out: at an infinite z (a token of probability
+      // 0 in one answer) it would be 0 x inf.
+      const double loss = (eps != 1.0 ? (1.0 - eps) * (soft + fmax(-z, 0.0)) : 0.0) +
+                          (eps != 0.0 ? eps * (soft + fmax(z, 0.0)) : 0.0);
       const double weight = p.pair_weights ? static_cast<double>(p.pair_weights[pair])
                                            : 1.0 / p.n_pairs;
       // dl/dz = -(1 - eps) sigmoid(-z) + eps sigmoid(z)
