@@ -454,6 +454,9 @@ int token_logprobs_backward(const void* logits, int32_t logits_type, int64_t row
  * The weights hold the average the caller wants (1 / tokens, 1 / (sequences x
  * length), ...).  A row of weight 0, like one of a negative token id, is left
  * out.  A = 0 gives s = 0 at any ratio.
+ * A token of probability 0 (lp = -inf) with a finite ref has r = 0 and kl =
+ * inf; with kl_coef > 0 the loss is inf then and, as the row's dloss/dlp is,
+ * no entry of its gradient row is finite.
  *   params         HOST struct; clip_low and clip_high >= 0, inf for no clip
  *   old_logprobs   fp32 [rows]: log-probabilities when the tokens were drawn
  *   ref_logprobs   fp32 [rows], or NULL if kl_coef == 0

@@ -86,7 +86,7 @@ def policy(x, tokens, old, adv, ref=None, weights=None, *, clip_low=0.2, clip_hi
         g[r] = -slope
         if ref is not None:
             gap = ref[r] - lp[r]
-            kl[r] = np.exp(gap) - gap - 1
+            kl[r] = np.exp(gap) - gap - 1 if gap < np.inf else gap
             if kl_coef:
                 term += kl_coef * kl[r]
                 g[r] += kl_coef * (1 - np.exp(gap))

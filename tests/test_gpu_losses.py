@@ -837,3 +837,50 @@ def test_preference_answers_with_a_masked_token(dtype, smoothing, mean):
             close(got.grad_logits, want["grad"], entry_tol(want["grad"], x, t, k, 1.0, dtype),
                   "gradient")
             assert torch.isfinite(got.grad_logits).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows,vocab", [(6, 700), (6, 40001), (130, 33001)])
+def test_policy_token_masked_since_it_was_drawn(rows, vocab, dtype):
+    """A token of probability 0 with a finite reference: the ratio is 0 and the
+    KL term infinite, and nothing of it reaches another row."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    logits, x = make_logits(rows, vocab, dtype, 0, 22, masks=False)
+    tok = allowed_tokens(x, 7, skip=0.0)
+    old, rf, adv, _ = policy_inputs(rows, x, tok, 1.0, 3)
+    w = np.full(rows, 1.0 / rows, np.float32)
+    logits[4, int(tok[4])] = -float("inf")
+    x = logits.cpu().double().numpy()
+    f = lambda a: a.astype(np.float64)  # noqa: E731
+    args = (to_dev(tok, torch.int32), to_dev(old), to_dev(adv), to_dev(rf), to_dev(w))
+    others = np.arange(rows) != 4
+    for kl_coef in (0.0, 0.2):
+        say("masked token", dtype, rows, vocab, kl_coef)
+        kw = dict(clip_low=0.2, clip_high=0.28, kl_coef=kl_coef)
+        with np.errstate(invalid="ignore"):
+            want = ref.policy(x, tok, f(old), f(adv), f(rf), f(w), **kw)
+        coef = f(w) * (np.abs(f(adv)) * want["ratios"] + kl_coef * 8) * 2 * LSE
+        for back in (False, True):
+            got = ts.policy_loss(logits, *args, backward=back, **kw)
+            torch.cuda.synchronize()
+            assert not got.row_status.any()
+            assert got.logprobs[4] == -float("inf") and got.ratios[4] == 0.0
+            assert got.kl[4] == float("inf") and want["kl"][4] == np.inf
+            close(got.kl[to_dev(others, torch.bool)], want["kl"][others], 8 * LSE + U * 8, "kl")
+            if kl_coef:
+                assert got.loss == float("inf") and want["loss"] == np.inf
+            else:
+                close(got.loss, want["loss"], coef.sum() + 2 * U * abs(want["loss"]), "loss")
+        # dloss/dlp of the row is infinite with the KL term, and 0 without
+        assert want["grad"][4].any() == (kl_coef > 0)
+        if kl_coef:
+            assert not torch.isfinite(got.grad_logits[4]).any()
+            assert not np.isfinite(want["grad"][4]).any()
+        else:
+            assert not got.grad_logits[4].any()
+        tol = entry_tol(want["grad"], x, tok, coef, 1.0, dtype)
+        close(got.grad_logits[to_dev(others, torch.bool)], want["grad"][others], tol[others],
+              "gradient")

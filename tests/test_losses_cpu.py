@@ -254,3 +254,16 @@ def test_preference_terms_of_factor_0():
             factor = eps if sign > 0 else 1 - eps
             assert got["pair_losses"][0] == got["loss"] == (np.inf if factor else 0.0)
             assert np.isfinite(got["grad"]).all() and got["grad"].any() == (factor > 0)
+
+
+@pytest.mark.parametrize("kl_coef", [0.0, 0.3])
+def test_policy_kl_of_a_masked_token(kl_coef):
+    """lp = -inf and a finite reference: e^g - g - 1 at g = inf is inf."""
+    x = np.zeros((1, 3))
+    x[0, 1] = -np.inf
+    a = (x, np.array([1]), np.array([-1.0]), np.array([2.0]), np.array([-1.5]))
+    with np.errstate(invalid="ignore"):
+        got = ref.policy(*a, kl_coef=kl_coef)
+    assert got["kl"][0] == np.inf and got["ratios"][0] == 0.0
+    assert got["loss"] == (np.inf if kl_coef else 0.0)
+    assert not (np.isfinite(got["grad"]).any() if kl_coef else got["grad"].any())

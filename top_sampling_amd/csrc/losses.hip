@@ -517,7 +517,8 @@ __device__ __forceinline__ RowGrad policy_row(const PolicyArgs& p, const PolicyR
   if (p.ref_logprobs != nullptr) {
     const double gap = static_cast<double>(in.ref_lp) - st.lp;
     const double em = expm1(gap);
-    kl = em - gap;
+    // A token of probability 0 (gap = inf) has the limit, not inf - inf.
+    kl = gap == INFINITY ? gap : em - gap;
     if (p.kl_coef != 0.0) g -= p.kl_coef * em;
   }
   double loss = -gain;
