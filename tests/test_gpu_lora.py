@@ -301,3 +301,53 @@ def test_sampler_reports_a_bad_adapter():
     out = ts.sampler_sample(logits, ts.params_to_device(params, _dev()))
     torch.cuda.synchronize()
     assert out.row_status.tolist() == [0, ts.TS_ROW_BAD_LOGITS, 0, 0, ts.TS_ROW_BAD_LOGITS, 0]
+
+
+@pytest.mark.parametrize("rows,vocab", [(5, 300), (5, 40000), (60, 10001), (60, 25001), (64, 33100),
+                                        (90, 22300), (100, 66000), (150, 22100), (190, 60001),
+                                        (300, 18993), (256, 60001), (640, 30001)])
+@pytest.mark.parametrize("hidden", [64, 72])
+def test_infinite_inner_sums_and_infinities_in_b(rows, vocab, hidden):
+    """On every tile shape, and in the second pass of other hidden sizes: an
+    infinite u and infinite entries of B, of the same rank and of others, give
+    what the formula has, the sum of the products' infinities (NaN where two of
+    them differ in sign, or where one meets a 0)."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    rank, n = 24, 7
+    x, w, a, b, scales = make(rows, hidden, vocab, rank, n, rows)
+    ids = torch.from_numpy(some_ids("random", rows, n, 2).astype(np.int32)).to(_dev())
+    a[1, 5, 7] = float("inf")
+    x[:, 7] = x[:, 7].abs() + 0.5
+    # column 0: B infinite at the rank of the infinite u; 17: at another rank
+    # whose u is finite; the middle: both; the last: infinite at the first, and
+    # 0 at the infinite u's
+    mid, end = vocab // 2, vocab - 1
+    b[1, 0, 5] = -float("inf")
+    b[1, 17, 19] = float("inf")
+    b[1, mid, 5], b[1, mid, 19] = float("inf"), float("inf")
+    b[1, end, 0], b[1, end, 5] = float("inf"), 0.0
+    got = ts.lmhead_logits_local_lora(x, w, a, b, ids, scales)
+    torch.cuda.synchronize()
+    own = ids == 1
+    # the same rows' finite u, from the formula in float64
+    u = x[own].double() @ a[1].double().t()
+    assert torch.isinf(u[:, 5]).all() and torch.isfinite(u[:, [0, 19]]).all()
+    terms = u[:, None, :] * b[1].double()[None, [0, 17, mid, end, 1]]
+    want = torch.where(torch.isfinite(terms), 0.0, terms).sum(-1)
+    # a base sum is finite: infinities decide
+    at = got[own][:, [0, 17, mid, end, 1]].double()
+    assert torch.equal(torch.isnan(at), torch.isnan(want))
+    assert torch.equal(at.nan_to_num(0.0), want.nan_to_num(0.0))
+    # every other column has the sign of B's entry at the infinite u
+    rest = torch.ones(vocab, dtype=torch.bool, device=_dev())
+    rest[[0, 17, mid, end]] = False
+    sign = b[1, rest, 5].float()
+    sign = torch.where(sign == 0, float("nan"), sign * float("inf")).expand(int(own.sum()), -1)
+    assert torch.equal(got[own][:, rest].nan_to_num(0.0), sign.nan_to_num(0.0))
+    # and rows of other adapters keep their bits (x[:, 7] is theirs too)
+    a[1, 5, 7], b[1] = 0.0, 0.0
+    clean = ts.lmhead_logits_local_lora(x, w, a, b, ids, scales)
+    assert torch.equal(got[~own], clean[~own])

@@ -152,7 +152,10 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraArgs p, Dow
 //
 // 0 x inf is not 0, so infinities and NaN in B are set to 0 as well, and a tile
 // that met one adds their products to the rows of that adapter alone after its
-// logits are stored.  A row never sees another adapter's weights, and what it
+// logits are stored.  An infinite u would make NaN of those zeros, so where B
+// has such entries u's own are set to 0 too, and their products come later with
+// B's (a product that the matrix cores had already is infinite or NaN, and the
+// same added again changes nothing).  A row never sees another adapter's weights, and what it
 // gets does not depend on the rows beside it.  (Adding every product through a
 // selection of the adapter's rows instead cost 18 us a tile of 320 x 256 with
 // nine adapters of rank 32, where the main loop takes 150.)
@@ -485,7 +488,8 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, WAVES) void lora_gemm_kerne
         if (w * kWindow + fhalf * 8 >= p.rank) bfr[kk][j] = bf16x8{};
         odd = odd || not_finite(bfr[kk][j]);
       }
-    if (__ballot(odd) != 0) {
+    const bool any_odd = __ballot(odd) != 0;
+    if (any_odd) {
 #pragma unroll
       for (int kk = 0; kk < kRuns; ++kk)
 #pragma unroll
@@ -506,6 +510,10 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, WAVES) void lora_gemm_kerne
         for (int t = 0; t < kParts; ++t) {
           uf[t] = *reinterpret_cast<const bf16x8*>(ub + i * 32 * kUChunks * 16 + t * kWindow * 2);
           if (!mine) uf[t] = bf16x8{};
+        }
+        if (any_odd) {
+#pragma unroll
+          for (int t = 0; t < kParts; ++t) uf[t] = finite_part(uf[t]);
         }
 #pragma unroll
         for (int t = kParts - 1; t >= 0; --t)
@@ -559,7 +567,7 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, WAVES) void lora_gemm_kerne
     }
   }
 
-  // ---- what infinities and NaN in B add to their adapters' rows
+  // ---- what infinities and NaN in B and in u add to their adapters' rows
   __syncthreads();
   if (tr.met_non_finite == 0) return;
   for (int at = tid; at < BM * BN; at += 64 * NW) {
@@ -570,9 +578,11 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, WAVES) void lora_gemm_kerne
     const uint16_t* b = p.b + static_cast<int64_t>(tr.id[place]) * p.stride_b +
                         static_cast<int64_t>(v) * p.ld_b;
     float sum = 0.0f;
-    for (int k = 0; k < p.rank; ++k)
-      if ((b[k] & kExponent) == kExponent)
-        sum = fmaf(whole_u(u, k), __uint_as_float(static_cast<uint32_t>(b[k]) << 16), sum);
+    for (int k = 0; k < p.rank; ++k) {
+      const float uk = whole_u(u, k);
+      if ((b[k] & kExponent) == kExponent || !(fabsf(uk) < INFINITY))
+        sum = fmaf(uk, __uint_as_float(static_cast<uint32_t>(b[k]) << 16), sum);
+    }
     p.logits[static_cast<int64_t>(tr.row[place]) * p.ld_logits + v] += sum;
   }
 }
