@@ -884,3 +884,75 @@ def test_policy_token_masked_since_it_was_drawn(rows, vocab, dtype):
         tol = entry_tol(want["grad"], x, tok, coef, 1.0, dtype)
         close(got.grad_logits[to_dev(others, torch.bool)], want["grad"][others], tol[others],
               "gradient")
+
+
+def confident_rows(rows, vocab, dtype, seed):
+    """Logits whose token has 1 - p of 1e-9 .. 1e-6: the rest of the mass all
+    over the row, or all within eight entries of the token."""
+    import torch
+
+    g = np.random.default_rng(seed)
+    x = np.empty((rows, vocab), np.float32)
+    tok = g.integers(0, vocab, rows).astype(np.int32)
+    tok[:2] = 0, vocab - 1
+    for r in range(rows):
+        d = 10.0 ** g.uniform(-9, -6)
+        if r % 2:
+            x[r] = g.normal(np.log(d / vocab), 1.0, vocab)
+        else:
+            x[r] = g.normal(-60.0, 1.0, vocab)
+            lo, hi = max(0, tok[r] - 8), min(vocab, tok[r] + 9)
+            x[r, lo:hi] = np.log(d / (hi - lo)) + g.normal(0, 0.5, hi - lo)
+        x[r, tok[r]] = 0.0
+    t = torch.from_numpy(x).to(_dev(), torch.float32 if dtype == "fp32" else torch.bfloat16)
+    return t, t.cpu().double().numpy(), tok
+
+
+# Of d = 1 - p of a token: every e_j has LSE at most, so their sum has; the
+# values are rounded to fp32 once.
+DIGITS = LSE + 2 * U
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows,vocab", [(6, 2), (9, 40), (40, 300), (30, 16390), (6, 33001),
+                                        (12, 151936), (200, 40001), (140, 120001)])
+def test_digits_next_to_probability_1(rows, vocab, dtype):
+    """Where p is near 1, log-probability, entropy and the token's own gradient
+    entry are right relative to 1 - p, not just next to 1."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    say("digits", dtype, rows, vocab)
+    logits, x, tok = confident_rows(rows, vocab, dtype, rows + vocab)
+    lp, ent = ref.score(x, tok)
+    assert (np.abs(lp) < 1e-5).all()
+    at = np.arange(rows)
+    tk = to_dev(tok, torch.int32)
+    out = ts.token_logprobs(logits, tk, entropies=True)
+    plain = ts.token_logprobs(logits, tk)
+    torch.cuda.synchronize()
+    close(out.logprobs, lp, DIGITS * np.abs(lp), "logprobs with entropies")
+    close(plain.logprobs, lp, DIGITS * np.abs(lp), "logprobs")
+    # H = ln S + E[max - z], both positive; the mean's terms have LSE too
+    close(out.entropies, ent, 3 * DIGITS * ent, "entropies")
+    g = np.random.default_rng(5).normal(1, 0.2, rows).astype(np.float32)
+    old, adv = to_dev(lp), to_dev(-g)
+    wide = dict(clip_low=np.inf, clip_high=np.inf)
+    want = ref.policy(x, tok, lp.astype(np.float32).astype(np.float64), -g.astype(np.float64),
+                      **wide)
+    pol = ts.policy_loss(logits, tk, old, adv, backward=True, **wide)
+    fwd = ts.policy_loss(logits, tk, old, adv, **wide)
+    close(pol.logprobs, lp, DIGITS * np.abs(lp), "policy logprobs")
+    close(fwd.logprobs, lp, DIGITS * np.abs(lp), "policy logprobs without gradient")
+    # 1 - p, the ratio (LSE of nearly 0) and the rounding to the type
+    tol = np.abs(want["grad"][at, tok]) * (2 * DIGITS + 2 * U + HALF[dtype])
+    close(pol.grad_logits[to_dev(at, torch.int64), tk.long()], want["grad"][at, tok], tol,
+          "policy gradient")
+    off = np.array([0, rows // 2, rows], np.int32)
+    want = ref.preference(x, tok, off)
+    pref = ts.preference_loss(logits, tk, to_dev(off, torch.int32), backward=True)
+    close(pref.logprobs, lp, DIGITS * np.abs(lp), "preference logprobs")
+    tol = np.abs(want["grad"][at, tok]) * (2 * DIGITS + 2 * U + HALF[dtype])
+    close(pref.grad_logits[to_dev(at, torch.int64), tk.long()], want["grad"][at, tok], tol,
+          "preference gradient")
