@@ -431,6 +431,11 @@ enum { TS_F32 = 0, TS_BF16 = 1 };
  * token_ids, temperature and the logits are the forward call's.  A row whose
  * gradients are both 0 gives a row of zeros without reading its logits.  No
  * workspace.
+ *
+ * token_logprobs_backward_ex: the same with the forward pass's logprobs (fp32
+ * [rows] or NULL).  The token's own entry holds 1 - p_t, and the sum in
+ * row_stats, rounded to fp32, has no digits of that below 2^-24; with logprobs
+ * the entry is right relative to 1 - p_t.
  */
 size_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab);
 int token_logprobs(const void* logits, int32_t logits_type, int64_t rows, int64_t vocab,
@@ -442,6 +447,12 @@ int token_logprobs_backward(const void* logits, int32_t logits_type, int64_t row
                             const float* row_stats, const float* grad_logprobs,
                             const float* entropies, const float* grad_entropies,
                             void* grad_logits, int64_t ld_grad, void* stream);
+int token_logprobs_backward_ex(const void* logits, int32_t logits_type, int64_t rows,
+                               int64_t vocab, int64_t ld_logits, const int32_t* token_ids,
+                               double temperature, const float* row_stats, const float* logprobs,
+                               const float* grad_logprobs, const float* entropies,
+                               const float* grad_entropies, void* grad_logits, int64_t ld_grad,
+                               void* stream);
 
 /*
  * policy_loss: the clipped policy loss with a KL term,

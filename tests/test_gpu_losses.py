@@ -956,3 +956,78 @@ def test_digits_next_to_probability_1(rows, vocab, dtype):
     tol = np.abs(want["grad"][at, tok]) * (2 * DIGITS + 2 * U + HALF[dtype])
     close(pref.grad_logits[to_dev(at, torch.int64), tk.long()], want["grad"][at, tok], tol,
           "preference gradient")
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows,vocab", [(6, 2), (9, 40), (40, 300), (30, 16390), (12, 151936),
+                                        (200, 40001)])
+def test_backward_digits_next_to_probability_1(rows, vocab, dtype):
+    """The token's own gradient entry from the forward pass's results, relative
+    to 1 - p; and the entries of a row add up to about 0."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    say("digits backward", dtype, rows, vocab)
+    logits, x, tok = confident_rows(rows, vocab, dtype, rows + vocab)
+    at = np.arange(rows)
+    rng = np.random.default_rng(5)
+    g = rng.normal(1, 0.2, rows).astype(np.float32)
+    # of the same sign as g: the two terms of the entry do not cancel, as
+    # -h p (ln p + H) has the sign of -h
+    h = -rng.uniform(0.1, 0.3, rows).astype(np.float32)
+    tk = to_dev(tok, torch.int32)
+    for ent, gh in ((False, None), (True, None), (True, h)):
+        fwd = ts.token_logprobs(logits, tk, entropies=ent)
+        got = ts.token_logprobs_backward(logits, tk, fwd, to_dev(g),
+                                         None if gh is None else to_dev(gh))
+        torch.cuda.synchronize()
+        want = ref.score_gradient(x, tok, 1.0, g.astype(np.float64),
+                                  None if gh is None else gh.astype(np.float64))
+        own = want[at, tok]
+        # 1 - p and H, each with its digits, and two roundings of fp32 inputs
+        tol = np.abs(own) * (4 * DIGITS + 4 * U + HALF[dtype])
+        close(got[to_dev(at, torch.int64), tk.long()], own, tol, ("own entry", ent, gh is None))
+
+
+def test_backward_without_the_log_probabilities():
+    """The C entry that takes none gives the same away from probability 1."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    logits, x = make_logits(9, 4099, "fp32", 0, 1, masks=False)
+    tk = to_dev(allowed_tokens(x, 2), torch.int32)
+    g = torch.randn(9, device=_dev())
+    fwd = ts.token_logprobs(logits, tk, 0.8, entropies=True)
+    with_lp = ts.token_logprobs_backward(logits, tk, fwd, g, g, 0.8)
+    d = torch.full_like(logits, 7.0)
+    s = torch.cuda.current_stream().cuda_stream
+    assert ts.lib.token_logprobs_backward(
+        logits.data_ptr(), ts.TS_F32, 9, 4099, 4099, tk.data_ptr(), 0.8, fwd.row_stats.data_ptr(),
+        g.data_ptr(), fwd.entropies.data_ptr(), g.data_ptr(), d.data_ptr(), 4099, s) == ts.TS_OK
+    torch.cuda.synchronize()
+    assert torch.equal(d, with_lp)
+
+
+def test_backward_after_the_log_probabilities_were_changed():
+    """A caller that scales or masks the forward pass's log-probabilities in
+    place gets the gradient at the rows' own ones."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    logits, x, tok = confident_rows(12, 4099, "fp32", 3)
+    logits[6:] *= 0.3  # p from 1 down to 0.9 or less
+    x = logits.cpu().double().numpy()
+    tk, g = to_dev(tok, torch.int32), torch.ones(12, device=_dev())
+    want = ref.score_gradient(x, tok, 1.0, np.ones(12))
+    at = np.arange(12)
+    for change in (lambda v: v.neg_(), lambda v: v.sub_(0.01), lambda v: v.fill_(float("nan"))):
+        fwd = ts.token_logprobs(logits, tk)
+        change(fwd.logprobs)
+        got = ts.token_logprobs_backward(logits, tk, fwd, g)
+        own = want[at, tok]
+        # as without them: 1 - p is off by the rounding of S in fp32
+        close(got[to_dev(at, torch.int64), tk.long()], own, np.abs(own) * DIGITS * 4 + 2 * U,
+              "own entry")

@@ -267,3 +267,17 @@ def test_policy_kl_of_a_masked_token(kl_coef):
     assert got["kl"][0] == np.inf and got["ratios"][0] == 0.0
     assert got["loss"] == (np.inf if kl_coef else 0.0)
     assert not (np.isfinite(got["grad"]).any() if kl_coef else got["grad"].any())
+
+
+@pytest.mark.parametrize("kw,code", BAD_ROWS + [
+    (dict(stats=None), ts.TS_EINVAL), (dict(g=None), ts.TS_EINVAL), (dict(d=None), ts.TS_EINVAL),
+    (dict(gh=FAKE), ts.TS_EINVAL), (dict(ldd=99), ts.TS_EINVAL),
+    (dict(lp=FAKE + 2), ts.TS_EUNSUPPORTED), (dict(stats=FAKE + 2), ts.TS_EUNSUPPORTED),
+    (dict(d=FAKE + 400), ts.TS_EINVAL),
+])
+def test_token_logprobs_backward_ex_refusals(kw, code):
+    a = dict(x=FAKE, kind=0, rows=4, vocab=100, ld=100, tok=FAKE, t=1.0, stats=FAKE, lp=FAKE,
+             g=FAKE, ent=None, gh=None, d=FAKE * 2, ldd=100)
+    a.update(kw)
+    assert ts.lib.token_logprobs_backward_ex(*a.values(), None) == code
+    assert ts.lib.ts_last_error()

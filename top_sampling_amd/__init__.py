@@ -18,7 +18,7 @@ Calls mirror the C entry points:
                                  slices in place (no stitched buffer)
   sampler_sample_ex              slices plus flags (processed log-probabilities)
   sampler_workspace_bytes(_slices)  workspace size queries
-  token_logprobs(_backward)      log-probability and entropy of given tokens,
+  token_logprobs(_backward[_ex]) log-probability and entropy of given tokens,
                                  and the gradient of a function of them
   policy_loss                    clipped policy loss with a KL term
   preference_loss                loss of paired log ratios
@@ -85,6 +85,8 @@ SYMBOLS = {
                                       _VP, _SZ, _VP]),
     "token_logprobs_backward": (ctypes.c_int, [_VP, _I32, _I64, _I64, _I64, _VP, _F64, _VP, _VP,
                                                _VP, _VP, _VP, _I64, _VP]),
+    "token_logprobs_backward_ex": (ctypes.c_int, [_VP, _I32, _I64, _I64, _I64, _VP, _F64, _VP, _VP,
+                                                  _VP, _VP, _VP, _VP, _I64, _VP]),
     "policy_loss": (ctypes.c_int, [_VP, _I32, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
                                    _VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP, _SZ, _VP]),
     "preference_loss_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
@@ -576,7 +578,8 @@ def token_logprobs_backward(logits, token_ids, forward: TokenLogprobs, grad_logp
                             stream=None):
     """Gradient of the logits from ``grad_logprobs`` (fp32 ``[rows]``) and
     ``grad_entropies`` (or None), with the ``TokenLogprobs`` that
-    ``token_logprobs`` gave for the same logits, tokens and temperature.
+    ``token_logprobs`` gave for the same logits, tokens and temperature (calls
+    ``token_logprobs_backward_ex`` with its log-probabilities).
     ``grad_logits`` may be ``logits`` itself."""
     kind, ld = _token_rows(logits, token_ids)
     rows, vocab = logits.shape
@@ -584,13 +587,14 @@ def token_logprobs_backward(logits, token_ids, forward: TokenLogprobs, grad_logp
     _check_vector(grad_logprobs, "grad_logprobs", rows, dev)
     _check_vector(grad_entropies, "grad_entropies", rows, dev)
     _check_vector(forward.row_stats, "forward.row_stats", 2 * rows, dev)
+    _check_vector(forward.logprobs, "forward.logprobs", rows, dev)
     _check_vector(forward.entropies, "forward.entropies", rows, dev)
     with _OnDevice(dev, stream) as s:
         grad_logits, ldg = _gradient(grad_logits, True, logits)
-        _check(lib.token_logprobs_backward(
+        _check(lib.token_logprobs_backward_ex(
             logits.data_ptr(), kind, rows, vocab, ld, token_ids.data_ptr(), temperature,
-            _ptr(forward.row_stats), _ptr(grad_logprobs), _ptr(forward.entropies),
-            _ptr(grad_entropies), grad_logits.data_ptr(), ldg, s))
+            _ptr(forward.row_stats), _ptr(forward.logprobs), _ptr(grad_logprobs),
+            _ptr(forward.entropies), _ptr(grad_entropies), grad_logits.data_ptr(), ldg, s))
     return grad_logits
 
 

@@ -141,6 +141,17 @@ int token_logprobs_backward(const void* logits, int32_t logits_type, int64_t row
                             const float* row_stats, const float* grad_logprobs,
                             const float* entropies, const float* grad_entropies,
                             void* grad_logits, int64_t ld_grad, void* stream) {
+  return token_logprobs_backward_ex(logits, logits_type, rows, vocab, ld_logits, token_ids,
+                                    temperature, row_stats, nullptr, grad_logprobs, entropies,
+                                    grad_entropies, grad_logits, ld_grad, stream);
+}
+
+int token_logprobs_backward_ex(const void* logits, int32_t logits_type, int64_t rows,
+                               int64_t vocab, int64_t ld_logits, const int32_t* token_ids,
+                               double temperature, const float* row_stats, const float* logprobs,
+                               const float* grad_logprobs, const float* entropies,
+                               const float* grad_entropies, void* grad_logits, int64_t ld_grad,
+                               void* stream) {
   ts::TokenRows t;
   int st = token_rows(t, logits, logits_type, rows, vocab, ld_logits, token_ids, temperature);
   if (st != TS_OK || rows == 0) return st;
@@ -148,12 +159,12 @@ int token_logprobs_backward(const void* logits, int32_t logits_type, int64_t row
     return fail(TS_EINVAL, "NULL row_stats/grad_logprobs/grad_logits");
   if (grad_entropies && !entropies)
     return fail(TS_EINVAL, "grad_entropies without the forward pass's entropies");
-  if (!all_aligned4({row_stats, grad_logprobs, entropies, grad_entropies}))
+  if (!all_aligned4({row_stats, logprobs, grad_logprobs, entropies, grad_entropies}))
     return fail(TS_EUNSUPPORTED, "misaligned input");
   ts::GradRows d;
   st = grad_rows(d, t, grad_logits, ld_grad);
   if (st != TS_OK) return st;
-  const ts::ScoreGrad g{row_stats, grad_logprobs, grad_entropies ? entropies : nullptr,
+  const ts::ScoreGrad g{row_stats, logprobs, grad_logprobs, grad_entropies ? entropies : nullptr,
                         grad_entropies};
   return hip_status(
       ts::launch_token_logprobs_backward(t, g, d, static_cast<hipStream_t>(stream)),

@@ -10,7 +10,8 @@
 //           = e_j (a + b (x_j - m)) + 1[j = t] g / T,
 //   a = -(g + h (H - ln S)) / (S T),   b = -h / (S T^2),
 // and the entry of the token itself is written as a value of its own, from
-// 1 - p_t = -expm1(lp), which keeps its digits when p_t is near 1.
+// 1 - p_t = -expm1(lp), which keeps its digits when p_t is near 1 as lp does (see
+// TokenBatch; a backward pass has it from the forward pass's log-probabilities).
 //
 // All of it is bound by the logits' bytes: about ten instructions an element
 // (the exponential counts for four) against four or two bytes read.
@@ -837,19 +838,28 @@ __global__ __launch_bounds__(kPairThreads) void preference_pairs_kernel(
 
 // -------------------------------------------------------------------- grad
 // A row's record from the forward pass's statistics and the caller's
-// gradients of the log-probability and the entropy.
-__device__ __forceinline__ RowGrad score_row_grad(const ScoreGrad& g, int row, bool skip, float xt,
-                                                  const Scale& sc) {
+// gradients of the log-probability and the entropy.  The token's entry is only
+// worked out by the workgroup that writes it (`mine`), from its logit xt.
+__device__ __forceinline__ RowGrad score_row_grad(const ScoreGrad& g, int row, bool skip,
+                                                  bool mine, float xt, const Scale& sc) {
   const double dg = g.grad_logprobs[row];
   const double dh = g.grad_entropies ? static_cast<double>(g.grad_entropies[row]) : 0.0;
   if (skip || (dg == 0.0 && dh == 0.0)) return RowGrad{0.0f, 0.0f, 0.0f, 0.0f};
   const float m = g.row_stats[2 * static_cast<int64_t>(row)];
   const double s = g.row_stats[2 * static_cast<int64_t>(row) + 1];
   const double ln_s = log(s);
-  const double lp = (static_cast<double>(xt) - m) * sc.inv_t - ln_s;
   const double h = g.entropies && dh != 0.0 ? static_cast<double>(g.entropies[row]) : 0.0;
-  double own = dg * -expm1(lp);
-  if (dh != 0.0 && lp > -1e30) own -= dh * exp(lp) * (lp + h);
+  double own = 0.0;
+  if (mine) {
+    double lp = (static_cast<double>(xt) - m) * sc.inv_t - ln_s;
+    // Next to 1, S in fp32 has lost the digits of 1 - p, which the forward pass's
+    // log-probability has.  The two differ by the roundings of S and of that one,
+    // 2^-24 and 2^-28; one that is further off was changed since and is not used.
+    const double kept = g.logprobs ? g.logprobs[row] : NAN;
+    if (lp > -1.0 / 16 && fabs(kept - lp) < 0x1p-23) lp = kept;
+    own = dg * -expm1(lp);
+    if (dh != 0.0 && lp > -1e30) own -= dh * exp(lp) * (lp + h);
+  }
   return RowGrad{m, static_cast<float>(-(dg + (dh != 0.0 ? dh * (h - ln_s) : 0.0)) * sc.inv_t / s),
                  static_cast<float>(-dh * sc.inv_t * sc.inv_t / s),
                  static_cast<float>(own * sc.inv_t)};
@@ -951,7 +961,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(
       const int owner = token < f.head || vec >= f.whole ? cut.chunks - 1 : vec / cut.len;
       const bool mine = token >= 0 && token < vocab && owner == chunk;
       const float xt = mine ? static_cast<float>(rx[token]) : 0.0f;
-      g = score_row_grad(sg, row, skip, xt, sc);
+      g = score_row_grad(sg, row, skip, mine, xt, sc);
       __syncthreads();
     } else {
       g = grads[row];

@@ -33,6 +33,7 @@ struct ScoreOut {
 
 struct ScoreGrad {
   const float* row_stats;
+  const float* logprobs;        // may be null
   const float* grad_logprobs;
   const float* entropies;       // null iff grad_entropies is
   const float* grad_entropies;
