@@ -1031,3 +1031,83 @@ def test_backward_after_the_log_probabilities_were_changed():
         # as without them: 1 - p is off by the rounding of S in fp32
         close(got[to_dev(at, torch.int64), tk.long()], own, np.abs(own) * DIGITS * 4 + 2 * U,
               "own entry")
+
+
+def check_entries(got, want, x, tok, coef, temperature, dtype):
+    """The gradient entry by entry, at a tolerance that entries taken as 0
+    would not pass."""
+    tol = entry_tol(want, x, tok, coef, temperature, dtype)
+    close(got, want, tol, "gradient")
+    other = np.abs(want) > 2.0 ** -100
+    other[np.arange(len(x)), np.maximum(tok, 0)] = False
+    if other.any():
+        assert (tol < np.abs(want))[other].mean() > 0.99
+
+
+LONG = [
+    # one read: held on the chip, with a part that is read again, more than that
+    # twice over, short rows; and two passes
+    ("fp32", 96, 33000, 0), ("fp32", 96, 114688, 0), ("fp32", 97, 120001, 0),
+    ("bf16", 128, 131077, 3), ("bf16", 130, 262144, 0), ("fp32", 3, 32768, 0),
+    ("fp32", 95, 33001, 0), ("bf16", 127, 40000, 1), ("fp32", 2, 300000, 0),
+]
+ENTRIES = [(d, *s) for d in ("fp32", "bf16") for s in SHAPES]
+
+
+@pytest.mark.parametrize("dtype,rows,vocab,pad", ENTRIES + LONG)
+def test_policy_gradient_entries(dtype, rows, vocab, pad):
+    import torch
+
+    import top_sampling_amd as ts
+
+    say("policy entries", dtype, rows, vocab, pad)
+    logits, x = make_logits(rows, vocab, dtype, pad, rows * 3 + vocab)
+    tok = allowed_tokens(x, 6)
+    temperature = 0.8
+    old, rf, adv, w = policy_inputs(rows, x, tok, temperature, 8)
+    f = lambda a: a.astype(np.float64)  # noqa: E731
+    args = (to_dev(tok, torch.int32), to_dev(old), to_dev(adv), to_dev(rf), to_dev(w))
+    for kl_coef in (0.0, 0.1):
+        kw = dict(clip_low=0.2, clip_high=0.28, kl_coef=kl_coef, temperature=temperature)
+        want = ref.policy(x, tok, f(old), f(adv), f(rf), f(w), **kw)
+        got = ts.policy_loss(logits, *args, backward=True, **kw)
+        torch.cuda.synchronize()
+        # dloss/dlp: the ratio is off by LSE of itself, exp(gap) too; a clipped
+        # ratio does not enter
+        r = want["ratios"]
+        inside = np.where(adv >= 0, r <= 1.28, r >= 0.8)
+        gap = np.where(want["kl"] > 0, f(rf) - want["logprobs"], 0.0)
+        coef = f(w) * (np.abs(f(adv)) * r * inside + kl_coef * np.exp(gap)) * 2 * LSE / temperature
+        check_entries(got.grad_logits, want["grad"], x, tok, coef, temperature, dtype)
+
+
+@pytest.mark.parametrize("dtype,rows,vocab,pad", ENTRIES + [
+    ("fp32", 20, 70001, 0), ("bf16", 200, 40001, 2), ("bf16", 40, 120001, 0)])
+def test_preference_gradient_entries(dtype, rows, vocab, pad):
+    import torch
+
+    import top_sampling_amd as ts
+
+    say("preference entries", dtype, rows, vocab, pad)
+    logits, x = make_logits(rows, vocab, dtype, pad, rows * 5 + vocab)
+    tok = allowed_tokens(x, 7)
+    pairs, beta, temperature = max(1, rows // 9), 0.3, 0.8
+    off = pref_offsets(rows, pairs, 11)
+    lp, _ = ref.score(x, tok, temperature)
+    rf = (lp + np.random.default_rng(9).normal(0, 0.2, rows)).astype(np.float32)
+    for mean in (False, True):
+        kw = dict(beta=beta, label_smoothing=0.1, mean=mean, temperature=temperature)
+        want = ref.preference(x, tok, off, rf.astype(np.float64), **kw)
+        got = ts.preference_loss(logits, to_dev(tok, torch.int32), to_dev(off, torch.int32),
+                                 to_dev(rf), backward=True, **kw)
+        torch.cuda.synchronize()
+        # z: LSE a row, sums over the live rows; |d2l / dz2| <= 1/4
+        live = tok >= 0
+        n = np.array([live[off[i]:off[i + 1]].sum() for i in range(2 * pairs)])
+        rho_tol = beta * LSE * (np.minimum(n, 1) if mean else n)
+        dz_tol = (rho_tol[:pairs] + rho_tol[pairs:]) / 4
+        coef = np.zeros(rows)
+        for i in range(2 * pairs):
+            coef[off[i]:off[i + 1]] = beta / pairs * (dz_tol[i % pairs] + 2 * LSE) / \
+                (max(1, n[i]) if mean else 1) / temperature
+        check_entries(got.grad_logits, want["grad"], x, tok, coef, temperature, dtype)

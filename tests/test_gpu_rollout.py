@@ -163,3 +163,44 @@ def test_two_streams_at_once():
     numbered = step(x, torch.cuda.default_stream().cuda_stream)
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(numbered, want[0]))
+
+
+@pytest.mark.parametrize("rows,hidden,vocab", [(24, 128, 4097), (200, 192, 33003)])
+def test_step_gradient_entries(rows, hidden, vocab):
+    """The gradients of both losses on projected logits, entry by entry: the
+    error of a row's coefficient counts with the entry's own probability, so
+    entries taken as 0 would not pass."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    dev, g, x, w, a, b, ids, scales = _setup(rows, hidden, vocab, 16, 5, rows)
+    logits = ts.lmhead_logits_local_lora(x, w, a, b, ids, scales)
+    tok = torch.randint(0, vocab, (rows,), generator=g, device=dev, dtype=torch.int32)
+    tok[::9] = -1
+    reference = ts.token_logprobs(ts.lmhead_logits_local(x, w), tok).logprobs
+    old = reference + 0.05
+    adv = torch.randn(rows, generator=g, device=dev)
+    free = dict(clip_low=np.inf, clip_high=np.inf, kl_coef=0.05)
+    x64, tokens = f64(logits), tok.cpu().numpy()
+    p = np.exp(ref.log_softmax(x64, 1.0))
+    p[np.arange(rows), tokens.clip(0)] = 1.0
+    off = [0, rows // 4, rows // 2, rows // 2, rows]
+    want = ref.policy(x64, tokens, f64(old), f64(adv), f64(reference), **free)
+    got = ts.policy_loss(logits, tok, old, adv, reference, backward=True, **free)
+    # exp(reference - lp) is at most the largest of these
+    kl = np.exp(np.abs(f64(reference) - want["logprobs"]))
+    coef = (np.abs(f64(adv)) * want["ratios"] + 0.05 * kl) * 2 * LSE
+    pair = ref.preference(x64, tokens, off, f64(reference), mean=True)
+    pref = ts.preference_loss(logits, tok, torch.tensor(off, dtype=torch.int32, device=dev),
+                              reference, mean=True, backward=True)
+    size = np.array([0.1 / 2 / max(1, (tokens[lo:hi] >= 0).sum())
+                     for lo, hi in zip(off, off[1:])])
+    torch.cuda.synchronize()
+    for have, expect, c in ((got, want, coef), (pref, pair, np.repeat(size, np.diff(off)) * 3 * LSE)):
+        # an entry's own exponential is off by 2 U |z - max z| + 6 U, |..| < 100
+        tol = np.abs(expect["grad"]) * (2 * LSE + 206 * U) + c[:, None] * p + 2.0 ** -120
+        assert (np.abs(f64(have.grad_logits) - expect["grad"]) <= tol).all()
+        other = np.abs(expect["grad"]) > 2.0 ** -100
+        other[np.arange(rows), tokens.clip(0)] = False
+        assert (tol < np.abs(expect["grad"]))[other].mean() > 0.99
