@@ -1111,3 +1111,37 @@ def test_preference_gradient_entries(dtype, rows, vocab, pad):
             coef[off[i]:off[i + 1]] = beta / pairs * (dz_tol[i % pairs] + 2 * LSE) / \
                 (max(1, n[i]) if mean else 1) / temperature
         check_entries(got.grad_logits, want["grad"], x, tok, coef, temperature, dtype)
+
+
+def test_more_pairs_than_one_launch_has_workgroups_for():
+    """Past 2^23 pairs, where a workgroup a pair is more threads than a launch
+    has: nearly all are empty, the first and the last hold a row each side."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    pairs = (1 << 23) + 5
+    x, _ = make_logits(4, 300, "fp32", 0, 3, masks=False)
+    tok = torch.tensor([5, 17, 200, 299], dtype=torch.int32, device=_dev())
+    # rows 0 and 1: chosen answers of pairs 0 and pairs - 1; 2 and 3: rejected
+    off = torch.zeros(2 * pairs + 1, dtype=torch.int32, device=_dev())
+    off[1:] = 1
+    off[pairs:] = 2
+    off[pairs + 1:] = 3
+    off[2 * pairs:] = 4
+    say("pairs", pairs)
+    got = ts.preference_loss(x, tok, off, beta=0.5, backward=True)
+    torch.cuda.synchronize()
+    lp, _ = ref.score(x.cpu().double().numpy(), tok.cpu().numpy())
+    z = 0.5 * np.array([lp[0] - lp[2], lp[1] - lp[3]])
+    each = np.log1p(np.exp(-z))
+    close(got.pair_losses[[0, pairs - 1]], each, LSE + 2 * U * np.abs(each), "ends")
+    assert ((got.pair_losses[1:-1] - np.float32(np.log(2))).abs() <= 2 * U).all()
+    assert not got.rewards[1:pairs - 1].any() and not got.rewards[pairs + 1:-1].any()
+    assert abs(got.loss.item() - np.log(2)) <= 2 * U + np.abs(each).max() / pairs
+    want = ref.preference(x.cpu().double().numpy(), tok.cpu().numpy(), [0, 1, 2, 3, 4], beta=0.5)
+    scale = 2.0 / pairs  # of the two pairs' mean
+    x64 = x.cpu().double().numpy()
+    coef = np.full(4, 0.5 / pairs * 3 * LSE)
+    close(got.grad_logits, want["grad"] * scale,
+          entry_tol(want["grad"] * scale, x64, tok.cpu().numpy(), coef, 1.0, "fp32"), "gradient")

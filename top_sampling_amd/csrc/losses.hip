@@ -43,7 +43,8 @@ constexpr int kBatch = 4;                       // 16-byte vectors a thread has 
 constexpr int kSlab = kThreads * kBatch;        // vectors a workgroup takes at a time
 constexpr int kMaxChunkSlabs = 2;               // longest chunk, in slabs
 constexpr int kTargetGroups = 1024;             // workgroups wanted for few rows
-constexpr int kMaxGrid = 1 << 23;               // workgroups of one launch (grid-stride beyond)
+constexpr int64_t kMaxThreads = int64_t{1} << 31;  // of one launch (grid-stride beyond): HIP
+                                                   // counts a dimension's threads in 32 bits
 constexpr int kShortRow = 32768;                // entries: see whole_rows()
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -1200,8 +1201,8 @@ Workspace lay_out(void* base, int64_t rows, int64_t vocab, int64_t n_pairs) {
   return w;
 }
 
-int grid_of(int64_t groups) {
-  return static_cast<int>(groups < kMaxGrid ? (groups > 0 ? groups : 1) : kMaxGrid);
+int grid_of(int64_t groups, int threads = kThreads) {
+  return static_cast<int>(std::clamp<int64_t>(groups, 1, kMaxThreads / threads));
 }
 
 template <typename T, bool ENT>
@@ -1353,8 +1354,9 @@ hipError_t preference_loss_t(const TokenRows& t, const PreferenceArgs& p, const 
   }
   if (e != hipSuccess) return e;
   if (p.n_pairs > 0) {
-    hipLaunchKernelGGL(preference_pairs_kernel, dim3(grid_of(p.n_pairs)), dim3(kPairThreads), 0,
-                       stream, t.rows, t.tokens, p, w.terms, grads, w.losses);
+    hipLaunchKernelGGL(preference_pairs_kernel, dim3(grid_of(p.n_pairs, kPairThreads)),
+                       dim3(kPairThreads), 0, stream, t.rows, t.tokens, p, w.terms, grads,
+                       w.losses);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
