@@ -99,3 +99,18 @@ def test_binding_refusals():
         call(x, w, a, b, ids.long())
     with pytest.raises(ValueError, match="adapter_scales"):
         call(x, w, a, b, ids, torch.ones(3))
+
+
+@pytest.mark.parametrize("rows,vocab,hidden,fits", [
+    (1, (1 << 30) - 1024, 64, True), (1, (1 << 30) - 1023, 64, False), (64, 1 << 30, 64, False),
+    (65, (1 << 30) - 1024, 64, True), (129, 1 << 29, 64, False), (129, (1 << 29) - 512, 64, True),
+    (ts.TS_MAX_LORA_ROWS, 1 << 20, 64, False), (1, (1 << 31) - 1, 64, False),
+    (1, (1 << 31) - 257, 72, True), (1, (1 << 31) - 256, 72, False), (65, 1 << 31, 72, False),
+    (257, (1 << 31) - 4096, 72, True), (513, (1 << 31) - 4096, 72, False),
+])
+def test_more_tiles_than_a_launch_has(rows, vocab, hidden, fits):
+    """Refused before anything is enqueued; a size that fits gets as far as the
+    missing workspace."""
+    code = _lora(rows=rows, vocab=vocab, h=hidden, ldo=vocab, sb=0, ws=None)
+    assert code == (ts.TS_EWORKSPACE if fits else ts.TS_EUNSUPPORTED)
+    assert ts.lib.ts_last_error()

@@ -69,6 +69,9 @@ int lmhead_logits_local_lora(const void* hidden, int64_t rows, int64_t hidden_di
       !aligned(adapter_scales, 4))
     return fail(TS_EUNSUPPORTED, "hidden, lm_head, lora_a and lora_b must be 16-byte aligned, "
                 "logits, adapter_ids and adapter_scales 4-byte aligned");
+  if (!ts::lmhead_lora_fits(rows, vocab_local, hidden_dim))
+    return fail(TS_EUNSUPPORTED, "more tiles of logits than a launch has workgroups for "
+                "(rows=%lld vocab_local=%lld)", (long long)rows, (long long)vocab_local);
   const size_t need = ts::lmhead_lora_workspace_size(rows, rank);
   if (!workspace || workspace_bytes < need)
     return fail(TS_EWORKSPACE, "workspace of %zu bytes needed, %zu given", need,

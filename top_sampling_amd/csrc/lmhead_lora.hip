@@ -664,6 +664,18 @@ size_t lmhead_lora_workspace_size(int64_t rows, int64_t rank) {
   return bytes;
 }
 
+// HIP counts a launch's threads in 32 bits.  The smallest tiles that many
+// columns can get are 64 x 128 and 128 x 128 with eight waves, those of the
+// second pass's projection 64, 128 and 256 x 256 with four, which also adds a
+// tile to the columns in an int.
+bool lmhead_lora_fits(int64_t rows, int64_t vocab, int64_t hidden_dim) {
+  const bool fused = hidden_dim % kBK == 0;
+  const int64_t bm = rows <= 64 ? 64 : (fused || rows <= 128 ? 128 : 256), bn = fused ? 128 : 256;
+  const int64_t tiles = (rows + bm - 1) / bm * ((vocab + bn - 1) / bn);
+  return (tiles + kXcds - 1) / kXcds * kXcds * (fused ? 512 : 256) < int64_t{1} << 32 &&
+         (fused || vocab <= 0x7fffffff - bn);
+}
+
 hipError_t launch_lmhead_lora(const LoraArgs& p, void* ws, hipStream_t stream) {
   size_t bytes;
   const DownRows d = lay_out(ws, p.rows, p.rank, &bytes);

@@ -22,6 +22,8 @@ struct LoraArgs {
   int rows, vocab, hidden_dim, n_adapters, rank;
 };
 
+// Whether a launch has room for these sizes' tiles.
+bool lmhead_lora_fits(int64_t rows, int64_t vocab, int64_t hidden_dim);
 size_t lmhead_lora_workspace_size(int64_t rows, int64_t rank);
 hipError_t launch_lmhead_lora(const LoraArgs& p, void* ws, hipStream_t stream);
 
