@@ -1145,3 +1145,51 @@ def test_more_pairs_than_one_launch_has_workgroups_for():
     coef = np.full(4, 0.5 / pairs * 3 * LSE)
     close(got.grad_logits, want["grad"] * scale,
           entry_tol(want["grad"] * scale, x64, tok.cpu().numpy(), coef, 1.0, "fp32"), "gradient")
+
+
+def test_outputs_stand_on_their_own():
+    """What a user's program does with a call's outputs: a loss returned by an
+    autograd function and scaled in place, and one output changed in place
+    while a graph still holds another."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    dev = torch.device("cuda:0")
+    x = torch.randn(6, 500, device=dev)
+    tok = torch.arange(6, dtype=torch.int32, device=dev)
+    f = torch.randn(6, device=dev)
+    off = torch.tensor([0, 3, 6], dtype=torch.int32, device=dev)
+
+    def calls(v):
+        return (ts.policy_loss(v, tok, -f.abs() - 5, f, backward=True),
+                ts.preference_loss(v, tok, off, backward=True))
+
+    for i in range(2):
+        class Loss(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, v):
+                out = calls(v)[i]
+                ctx.save_for_backward(out.grad_logits)
+                return out.loss
+
+            @staticmethod
+            def backward(ctx, g):
+                return g * ctx.saved_tensors[0]
+
+        leaf = x.clone().requires_grad_()
+        loss = Loss.apply(leaf)
+        loss /= 4
+        loss.backward()
+        assert torch.equal(leaf.grad, calls(x)[i].grad_logits / 4)
+
+    w = torch.ones(6, device=dev, requires_grad=True)
+    for out in (*calls(x), ts.token_logprobs(x, tok, entropies=True)):
+        held = (w * out.logprobs).sum()
+        for other in (getattr(out, "loss", None), getattr(out, "entropies", None), out.row_status):
+            if other is not None:
+                other.zero_()
+        held.backward()
+        changed = out.logprobs
+        changed.mul_(w)
+        assert changed.requires_grad

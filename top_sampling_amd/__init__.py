@@ -460,13 +460,14 @@ class _OnDevice:
     __slots__ = ("pointer", "_guard")
 
     def __init__(self, device, stream):
-        if device.type != "cuda":
+        index = device.index
+        if index is None:
             raise ValueError("tensors must be on the GPU")
         self._guard = None
         if stream is None:
-            if device.index != _current_device():
+            if index != _current_device():
                 self._guard = torch.cuda.device(device)
-            self.pointer = _current_stream(device.index)
+            self.pointer = _current_stream(index)
             return
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), device=device)
@@ -491,7 +492,7 @@ _LOGITS_TYPES = {torch.float32: TS_F32, torch.bfloat16: TS_BF16}
 def _check_vector(t, name, n, device, dtype=torch.float32):
     if t is None:
         return
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the logits on {device}")
@@ -500,15 +501,17 @@ def _check_vector(t, name, n, device, dtype=torch.float32):
 def _token_rows(logits, token_ids):
     """Checks logits and token ids; returns (type code, leading dimension)."""
     kind = _LOGITS_TYPES.get(logits.dtype)
-    if logits.dim() != 2 or kind is None:
+    shape = logits.shape
+    if len(shape) != 2 or kind is None:
         raise ValueError("logits must be fp32 or bf16 [rows, vocab]")
-    rows, vocab = logits.shape
-    if vocab > 1 and logits.stride(1) != 1:
+    rows, vocab = shape
+    ld, step = logits.stride()
+    if vocab > 1 and step != 1:
         raise ValueError("logits must have unit column stride")
-    if rows > 1 and logits.stride(0) < vocab:
+    if rows > 1 and ld < vocab:
         raise ValueError("logits rows overlap")
     _check_vector(token_ids, "token_ids", rows, logits.device, torch.int32)
-    return kind, max(logits.stride(0), vocab)
+    return kind, max(ld, vocab)
 
 
 def _grad_rows(grad_logits, logits):
@@ -543,6 +546,15 @@ def _workspace(workspace, need, device):
     return workspace
 
 
+def _outputs(sizes, device):
+    """fp32 tensors of these sizes, and the first one's address.  One allocation
+    holds them side by side, which takes less time than one each.  They are no
+    views (this split makes none) and each has a version of its own, so that one
+    can be changed in place while a graph holds another."""
+    base = torch.empty(sum(sizes), dtype=torch.float32, device=device)
+    return base.unsafe_split_with_sizes(sizes), base.data_ptr()
+
+
 def token_logprobs_workspace_bytes(rows: int, vocab: int) -> int:
     return int(lib.token_logprobs_workspace_bytes(rows, vocab))
 
@@ -555,21 +567,21 @@ def token_logprobs(logits, token_ids, temperature: float = 1.0, entropies: bool 
                    workspace=None, stream=None) -> TokenLogprobs:
     """Log-probability of ``token_ids[r]`` (int32; negative: row left out)
     under ``softmax(logits[r] / temperature)``, fp32 or bf16 ``logits [rows,
-    vocab]``, and with ``entropies`` that distribution's entropy."""
+    vocab]``, and with ``entropies`` that distribution's entropy.  The outputs
+    share one allocation."""
     kind, ld = _token_rows(logits, token_ids)
     rows, vocab = logits.shape
     dev = logits.device
     with _OnDevice(dev, stream) as s:
         workspace = _workspace(workspace, token_logprobs_workspace_bytes(rows, vocab), dev)
-        stats, logprobs, status, h = torch.empty(
-            (4 + bool(entropies)) * rows, dtype=torch.float32,
-            device=dev).split_with_sizes((2 * rows, rows, rows, rows if entropies else 0))
-        out = TokenLogprobs(logprobs, h if entropies else None, stats.view(rows, 2),
-                            status.view(torch.int32))
+        (stats, logprobs, status, h), at = _outputs(
+            (2 * rows, rows, rows, rows if entropies else 0), dev)
+        out = TokenLogprobs(logprobs, h if entropies else None, stats.view(rows, 2).data,
+                            status.view(torch.int32).data)
         _check(lib.token_logprobs(
             logits.data_ptr(), kind, rows, vocab, ld, token_ids.data_ptr(), temperature,
-            out.logprobs.data_ptr(), _ptr(out.entropies), out.row_stats.data_ptr(),
-            out.row_status.data_ptr(), workspace.data_ptr(), workspace.numel(), s))
+            at + 8 * rows, at + 16 * rows if entropies else None, at, at + 12 * rows,
+            workspace.data_ptr(), workspace.numel(), s))
     return out
 
 
@@ -607,29 +619,29 @@ def policy_loss(logits, token_ids, old_logprobs, advantages, ref_logprobs=None, 
     ``[rows]``) holds the average wanted; None sums the rows.  With
     ``backward``, or a ``grad_logits`` buffer (``logits`` itself is allowed),
     the same call writes ``grad_loss`` (a device scalar, None for 1) times
-    the gradient of the logits."""
+    the gradient of the logits.  The outputs but ``grad_logits`` share one
+    allocation: clone a loss that is kept for long."""
     kind, ld = _token_rows(logits, token_ids)
     rows, vocab = logits.shape
     dev = logits.device
-    for t, name, n in ((old_logprobs, "old_logprobs", rows), (advantages, "advantages", rows),
-                       (ref_logprobs, "ref_logprobs", rows), (weights, "weights", rows),
-                       (grad_loss, "grad_loss", 1)):
-        _check_vector(t, name, n, dev)
+    _check_vector(old_logprobs, "old_logprobs", rows, dev)
+    _check_vector(advantages, "advantages", rows, dev)
+    _check_vector(ref_logprobs, "ref_logprobs", rows, dev)
+    _check_vector(weights, "weights", rows, dev)
+    _check_vector(grad_loss, "grad_loss", 1, dev)
     with _OnDevice(dev, stream) as s:
         workspace = _workspace(workspace, token_logprobs_workspace_bytes(rows, vocab), dev)
         grad_logits, ldg = _gradient(grad_logits, backward, logits)
-        loss, logprobs, ratios, kl, status = torch.empty(
-            1 + 4 * rows, dtype=torch.float32,
-            device=dev).split_with_sizes((1, rows, rows, rows, rows))
-        out = PolicyLoss(loss.view(()), logprobs, ratios, kl, status.view(torch.int32),
-                         grad_logits)
+        (loss, logprobs, ratios, kl, status), at = _outputs((1, rows, rows, rows, rows), dev)
+        out = PolicyLoss(loss.view(()).data, logprobs, ratios, kl,
+                         status.view(torch.int32).data, grad_logits)
         params = _PolicyParams(temperature, clip_low, clip_high, kl_coef)
         _check(lib.policy_loss(
             logits.data_ptr(), kind, rows, vocab, ld, token_ids.data_ptr(),
             ctypes.addressof(params), _ptr(old_logprobs), _ptr(ref_logprobs), _ptr(advantages),
-            _ptr(weights), _ptr(grad_loss), out.loss.data_ptr(), out.logprobs.data_ptr(),
-            out.ratios.data_ptr(), out.kl.data_ptr(), out.row_status.data_ptr(),
-            _ptr(grad_logits), ldg, workspace.data_ptr(), workspace.numel(), s))
+            _ptr(weights), _ptr(grad_loss), at, at + 4, at + 4 * (1 + rows),
+            at + 4 * (1 + 2 * rows), at + 4 * (1 + 3 * rows), _ptr(grad_logits), ldg,
+            workspace.data_ptr(), workspace.numel(), s))
     return out
 
 
@@ -641,8 +653,8 @@ def preference_loss(logits, token_ids, seq_offsets, ref_logprobs=None, pair_weig
     """Loss of paired log ratios (see ``preference_loss`` in top_sampling.h).
     ``seq_offsets`` (int32 ``[2 n_pairs + 1]``) bounds the sequences, chosen
     answers first, then the rejected ones in the same order.  ``mean`` divides
-    each sequence's sum by its tokens.  ``backward``, ``grad_loss`` and
-    ``grad_logits`` as in ``policy_loss``."""
+    each sequence's sum by its tokens.  ``backward``, ``grad_loss``,
+    ``grad_logits`` and the outputs' memory as in ``policy_loss``."""
     kind, ld = _token_rows(logits, token_ids)
     rows, vocab = logits.shape
     dev = logits.device
@@ -650,26 +662,25 @@ def preference_loss(logits, token_ids, seq_offsets, ref_logprobs=None, pair_weig
         raise ValueError("seq_offsets must hold 2 n_pairs + 1 values")
     n_pairs = seq_offsets.numel() // 2
     _check_vector(seq_offsets, "seq_offsets", 2 * n_pairs + 1, dev, torch.int32)
-    for t, name, n in ((ref_logprobs, "ref_logprobs", rows),
-                       (pair_weights, "pair_weights", n_pairs), (grad_loss, "grad_loss", 1)):
-        _check_vector(t, name, n, dev)
+    _check_vector(ref_logprobs, "ref_logprobs", rows, dev)
+    _check_vector(pair_weights, "pair_weights", n_pairs, dev)
+    _check_vector(grad_loss, "grad_loss", 1, dev)
     with _OnDevice(dev, stream) as s:
         workspace = _workspace(workspace, preference_loss_workspace_bytes(rows, vocab, n_pairs),
                                dev)
         grad_logits, ldg = _gradient(grad_logits, backward, logits)
-        loss, pair_losses, rewards, logprobs, status = torch.empty(
-            1 + 3 * n_pairs + 2 * rows, dtype=torch.float32,
-            device=dev).split_with_sizes((1, n_pairs, 2 * n_pairs, rows, rows))
-        out = PreferenceLoss(loss.view(()), pair_losses, rewards, logprobs,
-                             status.view(torch.int32), grad_logits)
+        (loss, pair_losses, rewards, logprobs, status), at = _outputs(
+            (1, n_pairs, 2 * n_pairs, rows, rows), dev)
+        out = PreferenceLoss(loss.view(()).data, pair_losses, rewards, logprobs,
+                             status.view(torch.int32).data, grad_logits)
         params = _PreferenceParams(temperature, beta, label_smoothing, margin,
                                    TS_PREFERENCE_MEAN if mean else 0)
         _check(lib.preference_loss(
             logits.data_ptr(), kind, rows, vocab, ld, token_ids.data_ptr(),
             seq_offsets.data_ptr(), n_pairs, ctypes.addressof(params), _ptr(ref_logprobs),
-            _ptr(pair_weights), _ptr(grad_loss), out.loss.data_ptr(), out.pair_losses.data_ptr(),
-            out.rewards.data_ptr(), out.logprobs.data_ptr(), out.row_status.data_ptr(),
-            _ptr(grad_logits), ldg, workspace.data_ptr(), workspace.numel(), s))
+            _ptr(pair_weights), _ptr(grad_loss), at, at + 4, at + 4 * (1 + n_pairs),
+            at + 4 * (1 + 3 * n_pairs), at + 4 * (1 + 3 * n_pairs + rows), _ptr(grad_logits),
+            ldg, workspace.data_ptr(), workspace.numel(), s))
     return out
 
 
