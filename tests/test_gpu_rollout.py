@@ -204,3 +204,16 @@ def test_step_gradient_entries(rows, hidden, vocab):
         other = np.abs(expect["grad"]) > 2.0 ** -100
         other[np.arange(rows), tokens.clip(0)] = False
         assert (tol < np.abs(expect["grad"]))[other].mean() > 0.99
+
+
+def test_current_stream_both_ways():
+    """torch's short way to the current device and stream and the public one."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    side = torch.cuda.Stream()
+    for stream in (torch.cuda.default_stream(), side):
+        with torch.cuda.stream(stream):
+            assert ts._current_device() == ts._public_current_device() == 0
+            assert ts._current_stream(0) == ts._public_current_stream(0) == stream.cuda_stream

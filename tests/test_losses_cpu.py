@@ -281,3 +281,23 @@ def test_token_logprobs_backward_ex_refusals(kw, code):
     a.update(kw)
     assert ts.lib.token_logprobs_backward_ex(*a.values(), None) == code
     assert ts.lib.ts_last_error()
+
+
+def test_import_without_private_torch_names():
+    """The package imports where torch has neither of the two private calls it
+    prefers (a build without a GPU), and uses the public ones."""
+    import os
+    import subprocess
+    import sys
+
+    code = ("import torch\n"
+            "for n in ('_cuda_getDevice', '_cuda_getCurrentRawStream'):\n"
+            "    delattr(torch._C, n)\n"
+            "import top_sampling_amd as ts\n"
+            "class S: cuda_stream = 77\n"
+            "torch.cuda.current_stream = lambda device: S() if device == 3 else None\n"
+            "torch.cuda.current_device = lambda: 5\n"
+            "assert ts._current_device() == 5 and ts._current_stream(3) == 77\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr[-2000:]

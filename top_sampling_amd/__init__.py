@@ -447,8 +447,17 @@ class PreferenceLoss:
     grad_logits: object  # the logits' type [rows, vocab], or None
 
 
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+def _public_current_device():
+    return torch.cuda.current_device()
+
+
+def _public_current_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# torch's own short ways to the two, where it has them (1 us less a call).
+_current_device = getattr(torch._C, "_cuda_getDevice", _public_current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_current_stream)
 
 
 class _OnDevice:
