@@ -401,7 +401,8 @@ int sampler_assemble_and_sample(const float* const* slices, const int64_t* slice
  *                NaN, and so is a loss it takes part in.
  *   grad_logits  [rows, vocab] in the logits' type, leading dimension
  *                ld_grad >= vocab.  It may be the logits themselves (same
- *                pointer and leading dimension: the gradient replaces them);
+ *                pointer and, with more than one row, leading dimension: the
+ *                gradient replaces them);
  *                any other overlap is TS_EINVAL (columns of one buffer beside
  *                the logits' columns, with the same leading dimension, are
  *                none).  Columns past vocab are not written.

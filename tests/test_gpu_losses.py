@@ -1193,3 +1193,24 @@ def test_outputs_stand_on_their_own():
         changed = out.logprobs
         changed.mul_(w)
         assert changed.requires_grad
+
+
+def test_one_row_in_place_by_another_view():
+    """One row of a wider buffer, and the same row as a view of its own."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    wide = torch.randn(3, 700, device=_dev())
+    tok = torch.tensor([5], dtype=torch.int32, device=_dev())
+    one = torch.ones(1, device=_dev())
+    row, same = wide[1:2, :640], wide[1, :640].clone()[None]
+    want = ts.policy_loss(same, tok, -one, one, backward=True).grad_logits
+    alias = wide[1, :640].unsqueeze(0)
+    assert alias.data_ptr() == row.data_ptr() and alias.stride(0) != row.stride(0)
+    before = wide.clone()
+    ts.policy_loss(row, tok, -one, one, grad_logits=alias)
+    torch.cuda.synchronize()
+    # the row starts elsewhere in its cache line than the clone
+    assert ((row - want).abs() <= 4 * LSE * want.abs() + 2 * LSE * (want < 0)).all()
+    assert torch.equal(wide[[0, 2]], before[[0, 2]]) and torch.equal(wide[:, 640:], before[:, 640:])

@@ -301,3 +301,12 @@ def test_import_without_private_torch_names():
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_one_row_has_no_leading_dimension():
+    """A single row's gradient may replace it whatever the strides say; gets as
+    far as the missing workspace."""
+    assert _policy(rows=1, d=FAKE, ldd=128, ws=None) == ts.TS_EWORKSPACE
+    assert _preference(rows=1, ld=300, d=FAKE, ldd=100, ws=None) == ts.TS_EWORKSPACE
+    assert _policy(rows=2, d=FAKE, ldd=128, ws=None) == ts.TS_EINVAL
+    assert _policy(rows=1, d=FAKE + 4, ldd=128, ws=None) == ts.TS_EINVAL

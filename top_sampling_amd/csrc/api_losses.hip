@@ -70,7 +70,7 @@ int grad_rows(ts::GradRows& d, const ts::TokenRows& t, void* grad_logits, int64_
     return fail(TS_EINVAL, "ld_grad %lld < vocab %d", (long long)ld_grad, t.vocab);
   const size_t size = t.bf16 ? 2 : 4;
   if (!aligned(grad_logits, size)) return fail(TS_EUNSUPPORTED, "grad_logits misaligned");
-  if (grad_logits == t.x && ld_grad == t.ld) return TS_OK;
+  if (grad_logits == t.x && (ld_grad == t.ld || t.rows == 1)) return TS_OK;
   const char* a = static_cast<const char*>(t.x);
   const char* b = static_cast<const char*>(grad_logits);
   const char* a_end = a + (static_cast<int64_t>(t.rows - 1) * t.ld + t.vocab) * size;
