@@ -394,7 +394,8 @@ int sampler_assemble_and_sample(const float* const* slices, const int64_t* slice
  *                is 0 and its gradient row is 0, whatever the row holds.
  *   temperature  finite, >= TS_GREEDY_EPS (else TS_EINVAL).  Log-probabilities
  *                are those of logits / temperature; 1 gives the sampler's raw
- *                log_softmax.
+ *                log_softmax.  A logit further below the row's largest than fp32
+ *                reaches has probability 0 at any temperature.
  *   row_status   int32 [rows] or NULL: TS_ROW_BAD_PARAMS for a token id >=
  *                vocab, TS_ROW_BAD_LOGITS for a row with a NaN or +inf logit
  *                or no finite one.  Such a row's outputs and gradient row are

@@ -1214,3 +1214,42 @@ def test_one_row_in_place_by_another_view():
     # the row starts elsewhere in its cache line than the clone
     assert ((row - want).abs() <= 4 * LSE * want.abs() + 2 * LSE * (want < 0)).all()
     assert torch.equal(wide[[0, 2]], before[[0, 2]]) and torch.equal(wide[:, 640:], before[:, 640:])
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("temperature", [1e20, 1e30, 1e35, 1e37, 1e38])
+def test_largest_temperatures(temperature, dtype):
+    """Logits as large as the temperature: log2(e) / T is a number below
+    fp32's normal ones, the sums of logits pass its range, and 1 / T^2 is 0."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    say("temperature", temperature, dtype)
+    g = np.random.default_rng(4)
+    for vocab in (3000, 40001):
+        rows = 5
+        x = (g.uniform(-1.6, 1.6, (rows, vocab)) * temperature).astype(np.float32)
+        x[1, g.random(vocab) < 0.5] = -np.inf
+        logits = torch.from_numpy(x).to(_dev(),
+                                        torch.float32 if dtype == "fp32" else torch.bfloat16)
+        x = logits.cpu().double().numpy()
+        tok = np.array([g.choice(np.flatnonzero(np.isfinite(r))) for r in x]).astype(np.int32)
+        tk = to_dev(tok, torch.int32)
+        lp, ent = ref.score(x, tok, temperature)
+        out = ts.token_logprobs(logits, tk, temperature, entropies=True)
+        close(out.logprobs, lp, LSE + U * np.abs(lp), "logprobs")
+        close(out.entropies, ent, LSE * 32, "entropies")
+        if temperature > 1e30:  # the gradients are below fp32's normal numbers
+            continue
+        a, h = g.normal(size=rows).astype(np.float32), g.normal(size=rows).astype(np.float32)
+        want = ref.score_gradient(x, tok, temperature, a.astype(np.float64),
+                                  h.astype(np.float64))
+        got = ts.token_logprobs_backward(logits, tk, out, to_dev(a), to_dev(h), temperature)
+        # as in test_token_logprobs; |ln p| + H < 4 + 2 ln(vocab)
+        p = np.exp(ref.log_softmax(x, temperature))
+        size = p * (np.abs(a) + np.abs(h) * 32)[:, None]
+        size[np.arange(rows), tok] += np.abs(a) * LSE
+        tol = grad_tol(want, x, temperature, dtype, 2 * LSE) + size * 2 * LSE / temperature
+        close(got, want, tol, "gradient")
+        assert not got[1, np.flatnonzero(np.isinf(x[1]))].any()

@@ -4,11 +4,11 @@
 // For a row x of logits, a token t and a temperature T:
 //   m = max_j x_j,  e_j = exp((x_j - m) / T),  S = sum_j e_j,  p_j = e_j / S
 //   lp = (x_t - m) / T - ln S                              (log-probability)
-//   H  = ln S - (1 / (S T)) sum_j e_j (x_j - m)            (entropy)
+//   H  = ln S - (1 / S) sum_j e_j ln e_j                   (entropy)
 // A scalar that depends on the row through g = dL/dlp and h = dL/dH has
 //   dL/dx_j = [g (1[j = t] - p_j) - h p_j (lp_j + H)] / T
-//           = e_j (a + b (x_j - m)) + 1[j = t] g / T,
-//   a = -(g + h (H - ln S)) / (S T),   b = -h / (S T^2),
+//           = e_j (a + b log2 e_j) + 1[j = t] g / T,
+//   a = -(g + h (H - ln S)) / (S T),   b = -h ln 2 / (S T),
 // and the entry of the token itself is written as a value of its own, from
 // 1 - p_t = -expm1(lp), which keeps its digits when p_t is near 1 as lp does (see
 // TokenBatch; a backward pass has it from the forward pass's log-probabilities).
@@ -27,7 +27,9 @@
 // Measured alone: stats reads 640 x 151,936 fp32 in 63 us (6.2 TB/s), grad
 // reads and writes 256 x 248,320 bf16 in 40 us (6.3 TB/s).
 // exp(x / T) is taken as exp2((x - m) c) with c = log2(e) / T held as two
-// floats, so a temperature's rounding does not tilt the whole sum.
+// floats, so a temperature's rounding does not tilt the whole sum.  The entropy
+// goes by that exponent and not by x - m, whose sums pass fp32's range, and 1 /
+// T^2 its least number, where logits and temperature are large.
 #include <float.h>
 #include <math.h>
 
@@ -79,9 +81,11 @@ Scale make_scale(double temperature) {
   const double c = M_LOG2E / temperature;
   s.c_hi = static_cast<float>(c);
   if (s.c_hi >= c) s.c_hi = nextafterf(s.c_hi, 0.0f);
-  // A temperature beyond 1e30 leaves normal numbers here, and e_j at 1.
-  s.c_hi = std::max(s.c_hi, FLT_MIN);
-  s.c_lo = std::max(static_cast<float>(c - static_cast<double>(s.c_hi)), FLT_MIN);
+  // Beyond temperatures of 1e30 these leave the normal numbers.  They stay above
+  // 0, at least 2^-149, which is 2^-21 in the exponent of the largest logits.
+  constexpr float kLeast = 0x1p-149f;
+  s.c_hi = std::max(s.c_hi, kLeast);
+  s.c_lo = std::max(static_cast<float>(c - static_cast<double>(s.c_hi)), kLeast);
   s.inv_t = 1.0 / temperature;
   s.floor = static_cast<float>(std::max(-200.0 / c, -static_cast<double>(FLT_MAX)));
   return s;
@@ -89,9 +93,16 @@ Scale make_scale(double temperature) {
 
 // exp((x - m) / T) of t = x - m.  Both products of t = -inf are -inf, so a
 // token that is not allowed gives exp2(-inf) = 0 without a test.
-__device__ __forceinline__ float exp_t(float t, const Scale& s) {
-  return __builtin_amdgcn_exp2f(fmaf(t, s.c_hi, t * s.c_lo));
+__device__ __forceinline__ float log2_t(float t, const Scale& s) {
+  return fmaf(t, s.c_hi, t * s.c_lo);
 }
+
+__device__ __forceinline__ float exp_t(float t, const Scale& s) {
+  return __builtin_amdgcn_exp2f(log2_t(t, s));
+}
+
+// A log2 e_j below this is taken as this: e_j is 0, and 0 x -inf is not.
+constexpr float kLeastLog2 = -200.0f;
 
 // The running maximum keeps a NaN (and +inf), so a bad logit shows in it.
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -100,11 +111,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 // One chunk's share of a row.
 struct Part {
-  double s, u;  // sum of e, sum of e (x - m)
+  double s, u;  // sum of e, sum of e log2 e
   float m, pad;
 };
 
-// What the gradient pass needs of a row: entry j is e_j (a + b (x_j - m)),
+// What the gradient pass needs of a row: entry j is e_j (a + b log2 e_j),
 // the token's entry is `own`.  All zero: the row's gradient is zero.
 struct RowGrad {
   float m, a, b, own;
@@ -166,7 +177,7 @@ __device__ __forceinline__ void join_lanes(float& m, double& s, double& u, int w
   for (int d = width >> 1; d > 0; d >>= 1) top = max_nan(top, __shfl_xor(top, d, width));
   const float shift = fmaxf(m - (top == -INFINITY ? 0.0f : top), sc.floor);
   const double f = exp_t(shift, sc);
-  if (ENT) u = f * (u + shift * s);
+  if (ENT) u = f * (u + log2_t(shift, sc) * s);
   s *= f;
   for (int d = width >> 1; d > 0; d >>= 1) {
     s += __shfl_xor(s, d, width);
@@ -284,7 +295,7 @@ __device__ __forceinline__ void row_stats(const T* row, int vocab, int v0, int v
     const float ref = top == -INFINITY ? 0.0f : top;
     const float shift = fmaxf(m - ref, sc.floor);
     const double keep = exp_t(shift, sc);
-    if (ENT) u = keep * (u + shift * s);
+    if (ENT) u = keep * (u + log2_t(shift, sc) * s);
     s *= keep;
     m = top;
     // A batch is added up as a tree, and the batches in double: behind a term
@@ -294,10 +305,10 @@ __device__ __forceinline__ void row_stats(const T* row, int vocab, int v0, int v
     for (int j = 0; j < kBatch; ++j)
 #pragma unroll
       for (int e = 0; e < VN; ++e) {
-        const float t = w[j][e] - ref;
-        const float ex = exp_t(t, sc);
+        const float k = log2_t(w[j][e] - ref, sc);
+        const float ex = __builtin_amdgcn_exp2f(k);
         w[j][e] = ex;
-        if (ENT) ut[j][e] = ex * fmaxf(t, sc.floor);
+        if (ENT) ut[j][e] = ex * fmaxf(k, kLeastLog2);
       }
     s += tree_sum(w);
     if (ENT) u += tree_sum(ut);
@@ -305,9 +316,9 @@ __device__ __forceinline__ void row_stats(const T* row, int vocab, int v0, int v
   if (edge && tid < f.edge) {
     const float x = static_cast<float>(row[f.template at<T>(tid)]);
     const float top = max_nan(m, x), ref = top == -INFINITY ? 0.0f : top;
-    const float shift = fmaxf(m - ref, sc.floor), t = x - ref;
-    const double keep = exp_t(shift, sc), ex = exp_t(t, sc);
-    if (ENT) u = keep * (u + shift * s) + ex * fmaxf(t, sc.floor);
+    const float shift = fmaxf(m - ref, sc.floor), k = log2_t(x - ref, sc);
+    const double keep = exp_t(shift, sc), ex = __builtin_amdgcn_exp2f(k);
+    if (ENT) u = keep * (u + log2_t(shift, sc) * s) + ex * fmaxf(k, kLeastLog2);
     s = keep * s + ex;
     m = top;
   }
@@ -458,7 +469,8 @@ __device__ __forceinline__ RowStats join_row(const T* x, int64_t ld, int vocab, 
     const float ref = top == -INFINITY ? 0.0f : top;
     const float d0 = fmaxf(r.m - ref, sc.floor), d1 = fmaxf(p.m - ref, sc.floor);
     const double f0 = exp_t(d0, sc), f1 = exp_t(d1, sc);
-    if (ENT) r.u = f0 * (r.u + d0 * r.s) + f1 * (p.u + d1 * p.s);
+    if (ENT)
+      r.u = f0 * (r.u + log2_t(d0, sc) * r.s) + f1 * (p.u + log2_t(d1, sc) * p.s);
     r.s = f0 * r.s + f1 * p.s;
     r.m = top;
   }
@@ -484,12 +496,11 @@ __device__ __forceinline__ void score_left_out(const ScoreOut& o, int64_t r) {
   if (o.row_status) o.row_status[r] = TS_ROW_OK;
 }
 
-__device__ __forceinline__ void score_row(const ScoreOut& o, const RowStats& st, const Scale& sc,
-                                          int64_t r) {
+__device__ __forceinline__ void score_row(const ScoreOut& o, const RowStats& st, int64_t r) {
   const bool ok = st.status == TS_ROW_OK;
   o.logprobs[r] = static_cast<float>(st.lp);
   if (o.entropies)
-    o.entropies[r] = ok ? static_cast<float>(log(st.s) - st.u * sc.inv_t / st.s) : NAN;
+    o.entropies[r] = ok ? static_cast<float>(log(st.s) - st.u * M_LN2 / st.s) : NAN;
   if (o.row_stats) {
     o.row_stats[2 * r] = ok ? st.m : NAN;
     o.row_stats[2 * r + 1] = ok ? static_cast<float>(st.s) : NAN;
@@ -510,7 +521,7 @@ __global__ __launch_bounds__(kThreads) void score_rows_kernel(
       continue;
     }
     const RowStats st = join_row<ENT>(x, ld, vocab, tokens[r], r, parts, cut, sc);
-    if (writes) score_row(o, st, sc, row);
+    if (writes) score_row(o, st, row);
   }
 }
 
@@ -536,7 +547,7 @@ __global__ __launch_bounds__(kThreads) void score_whole_kernel(
     regain_digits(rx, vocab, token, xt, sc, st);
     if (threadIdx.x == 0) {
       finish_row(st, token, vocab, xt, sc);
-      score_row(o, st, sc, r);
+      score_row(o, st, r);
     }
     __syncthreads();
   }
@@ -862,7 +873,7 @@ __device__ __forceinline__ RowGrad score_row_grad(const ScoreGrad& g, int row, b
     if (dh != 0.0 && lp > -1e30) own -= dh * exp(lp) * (lp + h);
   }
   return RowGrad{m, static_cast<float>(-(dg + (dh != 0.0 ? dh * (h - ln_s) : 0.0)) * sc.inv_t / s),
-                 static_cast<float>(-dh * sc.inv_t * sc.inv_t / s),
+                 static_cast<float>(-dh * M_LN2 * sc.inv_t / s),
                  static_cast<float>(own * sc.inv_t)};
 }
 
@@ -881,9 +892,9 @@ __device__ __forceinline__ void row_grad_pass(const T* row, T* out, int vocab, i
   const int end = min(v1, f.whole);
   const bool zero = g.a == 0.0f && g.b == 0.0f && g.own == 0.0f;
   auto entry = [&](float x, bool is_token) {
-    const float t = ENT ? fmaxf(x - g.m, sc.floor) : x - g.m;
-    const float ex = exp_t(t, sc);
-    return is_token ? g.own : (ENT ? ex * fmaf(g.b, t, g.a) : ex * g.a);
+    const float k = log2_t(x - g.m, sc);
+    const float ex = __builtin_amdgcn_exp2f(k);
+    return is_token ? g.own : (ENT ? ex * fmaf(g.b, fmaxf(k, kLeastLog2), g.a) : ex * g.a);
   };
   if (edge && tid < f.edge) {
     const int at = f.template at<T>(tid);
