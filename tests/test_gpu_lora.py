@@ -351,3 +351,40 @@ def test_infinite_inner_sums_and_infinities_in_b(rows, vocab, hidden):
     a[1, 5, 7], b[1] = 0.0, 0.0
     clean = ts.lmhead_logits_local_lora(x, w, a, b, ids, scales)
     assert torch.equal(got[~own], clean[~own])
+
+
+@pytest.mark.parametrize("rows,hidden,vocab,rank,n", [
+    # many row tiles, ranks above 64, and more rows than a launch of the down
+    # step or of the second pass has workgroups for
+    (3000, 192, 70, 256, 9), (5001, 64, 300, 8, 40), (2050, 136, 130, 136, 3),
+    (70001, 72, 5, 16, 6), (70001, 64, 5, 16, 6), ((1 << 18) + 77, 64, 3, 8, 5),
+])
+def test_many_rows(rows, hidden, vocab, rank, n):
+    import torch
+
+    import top_sampling_amd as ts
+
+    say("lora rows", rows, hidden, vocab, rank, n)
+    x, w, a, b, scales = make(rows, hidden, vocab, rank, n, 4)
+    ids = torch.from_numpy(some_ids("bad", rows, n, 7).astype(np.int32)).to(_dev())
+    got = ts.lmhead_logits_local_lora(x, w, a, b, ids, scales)
+    torch.cuda.synchronize()
+    xs, want = x.double(), x.double() @ w.double().t()
+    u = torch.zeros(rows, rank, dtype=torch.float64, device=_dev())
+    for i in range(n):
+        mine = (ids == i).nonzero()[:, 0]
+        u[mine] = scales[i].double() * (xs[mine] @ a[i].double().t())
+        want[mine] += u[mine] @ b[i].double().t()
+    out = (ids < -1) | (ids >= n)
+    assert torch.isnan(got[out]).all()
+    # the bound of check(), row by row
+    six = 6 * 0.41 * U
+    rms = lambda m: m.double().square().mean().sqrt()  # noqa: E731
+    row = xs.square().mean(1).sqrt()
+    top = u.abs().amax(1)
+    du = torch.where((ids >= 0) & ~out, six * hidden * row * rms(a) *
+                     scales.double()[ids.clamp(0, n - 1).long()], 0.0)
+    tol = six * hidden * row * rms(w) + 6 * du * rms(b) * rank ** 0.5 + \
+        six * (rank + 4) * top * rms(b) + 8 * U * top * b.double().abs().max() * rank ** 0.5
+    off = (got.double() - want).abs() - tol[:, None] - 2 * U * want.abs()
+    assert (off[~out] <= 0).all()
