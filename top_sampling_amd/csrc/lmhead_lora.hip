@@ -50,9 +50,11 @@ __device__ __forceinline__ int adapter_of(int id, int n_adapters) {
 
 // One workgroup per row and kWindow ranks, four ranks a wave; kDownStep
 // 512-wide pieces of the row and of A are in flight at a time.  Bound by the
-// L2's delivery of A, read once per row: 640 rows of 4,096 at rank 32 take 12
-// us, 64 at rank 16 take 5.  Four rows a workgroup sharing what they have of
-// one adapter: 16 and 14 us; four and eight pieces in flight: 13 and 16 us.
+// L2's delivery of A, read once per row, and by HBM's where the projection has
+// run since A was read: 640 rows of 4,096 at rank 32 take 16 us in that order, 64
+// at rank 16 take 12.  With A in the caches they take 12 and 5; four rows a
+// workgroup sharing what they have of one adapter 16 and 14 then, and four and
+// eight pieces in flight 13 and 16 us at 640 rows.
 constexpr int kDownStep = 2;
 
 __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraArgs p, DownRows out) {
