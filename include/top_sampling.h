@@ -154,8 +154,9 @@ int lmhead_logits_local(const void* hidden, int64_t rows, int64_t hidden_dim,
  * Requirements (else TS_EUNSUPPORTED): those of lmhead_logits_local, rank a
  * multiple of 8 up to TS_MAX_LORA_RANK, rows up to TS_MAX_LORA_ROWS, ld_a, ld_b
  * and the strides multiples of 8, lora_a and lora_b 16-byte aligned, no more
- * logits than one launch has tiles for (2^30 - 1024 columns for up to 64 rows;
- * 128 rows x 128 columns count as one tile, of 2^23 - 8).
+ * logits than one launch has tiles for (hidden_dim % 64 == 0: 2^30 - 1024
+ * columns for up to 64 rows, and 2^23 - 8 tiles of 128 x 128 for more; other
+ * sizes: 2^24 - 8 tiles of up to 256 x 256, and 2^31 - 257 columns).
  * n_adapters == 0 or rank == 0 is TS_EINVAL.
  */
 #define TS_MAX_LORA_RANK 256       /* largest accepted adapter rank          */

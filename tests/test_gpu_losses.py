@@ -1023,9 +1023,11 @@ def test_backward_after_the_log_probabilities_were_changed():
     tk, g = to_dev(tok, torch.int32), torch.ones(12, device=_dev())
     want = ref.score_gradient(x, tok, 1.0, np.ones(12))
     at = np.arange(12)
-    for change in (lambda v: v.neg_(), lambda v: v.sub_(0.01), lambda v: v.fill_(float("nan"))):
+    for change in (lambda v: v.neg_(), lambda v: v.sub_(0.01), lambda v: v.fill_(float("nan")),
+                   lambda v: v.double(), lambda v: v[:5], lambda v: v[:, None].expand(12, 2)[:, 0],
+                   lambda v: v.cpu(), lambda v: None):
         fwd = ts.token_logprobs(logits, tk)
-        change(fwd.logprobs)
+        fwd.logprobs = change(fwd.logprobs)
         got = ts.token_logprobs_backward(logits, tk, fwd, g)
         own = want[at, tok]
         # as without them: 1 - p is off by the rounding of S in fp32

@@ -600,21 +600,24 @@ def token_logprobs_backward(logits, token_ids, forward: TokenLogprobs, grad_logp
     """Gradient of the logits from ``grad_logprobs`` (fp32 ``[rows]``) and
     ``grad_entropies`` (or None), with the ``TokenLogprobs`` that
     ``token_logprobs`` gave for the same logits, tokens and temperature (calls
-    ``token_logprobs_backward_ex`` with its log-probabilities).
-    ``grad_logits`` may be ``logits`` itself."""
+    ``token_logprobs_backward_ex`` with its log-probabilities where they are
+    still as that call gave them).  ``grad_logits`` may be ``logits`` itself."""
     kind, ld = _token_rows(logits, token_ids)
     rows, vocab = logits.shape
     dev = logits.device
     _check_vector(grad_logprobs, "grad_logprobs", rows, dev)
     _check_vector(grad_entropies, "grad_entropies", rows, dev)
     _check_vector(forward.row_stats, "forward.row_stats", 2 * rows, dev)
-    _check_vector(forward.logprobs, "forward.logprobs", rows, dev)
     _check_vector(forward.entropies, "forward.entropies", rows, dev)
+    logprobs = forward.logprobs
+    if logprobs is not None and (logprobs.dtype is not torch.float32 or logprobs.device != dev or
+                                 logprobs.numel() != rows or not logprobs.is_contiguous()):
+        logprobs = None  # the caller has put something of its own there
     with _OnDevice(dev, stream) as s:
         grad_logits, ldg = _gradient(grad_logits, True, logits)
         _check(lib.token_logprobs_backward_ex(
             logits.data_ptr(), kind, rows, vocab, ld, token_ids.data_ptr(), temperature,
-            _ptr(forward.row_stats), _ptr(forward.logprobs), _ptr(grad_logprobs),
+            _ptr(forward.row_stats), _ptr(logprobs), _ptr(grad_logprobs),
             _ptr(forward.entropies), _ptr(grad_entropies), grad_logits.data_ptr(), ldg, s))
     return grad_logits
 

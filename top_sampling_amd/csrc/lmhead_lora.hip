@@ -157,8 +157,8 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraArgs p, Dow
 // logits are stored.  An infinite u would make NaN of those zeros, so where B
 // has such entries u's own are set to 0 too, and their products come later with
 // B's (a product that the matrix cores had already is infinite or NaN, and the
-// same added again changes nothing).  A row never sees another adapter's weights, and what it
-// gets does not depend on the rows beside it.  (Adding every product through a
+// same added again changes nothing).  A row never sees another adapter's weights,
+// and what it gets does not depend on the rows beside it.  (Adding every product through a
 // selection of the adapter's rows instead cost 18 us a tile of 320 x 256 with
 // nine adapters of rank 32, where the main loop takes 150.)
 typedef float f32x16 __attribute__((ext_vector_type(16)));
