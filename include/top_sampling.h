@@ -515,7 +515,8 @@ int policy_loss(const void* logits, int32_t logits_type, int64_t rows, int64_t v
  * label_smoothing 0.  Rows before the first and after the last sequence take no
  * part (log-probability and gradient row 0).  A pair of weight 0 adds
  * nothing to the loss and the gradient.
- *   seq_offsets    int32 [2 n_pairs + 1], non-decreasing; used clamped to
+ *   seq_offsets    int32 [2 n_pairs + 1], non-decreasing (the rows' gradient
+ *                  is unspecified where sequences overlap); used clamped to
  *                  [0, rows]
  *   params         HOST struct; beta > 0, label_smoothing in [0, 1]
  *   ref_logprobs   fp32 [rows], or NULL for 0 (no reference)

@@ -22,7 +22,11 @@ Calls mirror the C entry points:
                                  and the gradient of a function of them
   policy_loss                    clipped policy loss with a KL term
   preference_loss                loss of paired log ratios
-and ``compute_logits_local`` returns the rank's own ``[rows, V_local]`` slice,
+``stream`` (None: the current one) is where a call's kernels run.  The scoring,
+loss and adapter calls allocate outputs and workspaces for it; inputs have to be
+ready there, and to live until the kernels have run (``record_stream`` where they
+were allocated for another one).
+``compute_logits_local`` returns the rank's own ``[rows, V_local]`` slice,
 the local-logits hook of batch-sharded sampling (page "Qwen4Exp batch-sharded
 sampling: inside vLLM PR #61018", section "Why three lines were the whole
 job").
