@@ -72,6 +72,9 @@ enum {
   TS_ROW_BAD_LOGITS = 2   /* a NaN or +inf logit, or no finite logit          */
 };
 
+/* Element types of logits and of rows to be quantized. */
+enum { TS_F32 = 0, TS_BF16 = 1 };
+
 #define TS_MAX_LOGPROBS 1024   /* largest accepted max_logprobs              */
 #define TS_MAX_SLICES 64       /* largest accepted n_slices                  */
 #define TS_GREEDY_EPS 1e-6f    /* temperatures below this sample greedily    */
@@ -209,6 +212,56 @@ int quantize_rows_e4m3(const void* in, int64_t rows, int64_t cols, int64_t ld_in
 int lmhead_logits_local_e4m3(const void* hidden, const float* hidden_scales, int64_t rows,
                              int64_t hidden_dim, int64_t ld_hidden, const void* lm_head,
                              const float* lm_head_scales, int64_t vocab_local, int64_t ld_lm_head,
+                             float* logits, int64_t ld_logits, void* stream);
+
+/*
+ * 4-bit projection.  Rows are held as OCP MX FP4 (Open Compute Project
+ * Microscaling Formats 1.0): every 32 consecutive entries of a row are a group
+ * with one scale s = 2^e, held as the byte e + 127 (E8M0; 255 is NaN), and every
+ * entry is an E2M1 code (bit 3 the sign; 0, 0.5, 1, 1.5, 2, 3, 4, 6), two codes
+ * a byte with the even column's in the low half: 4.25 bits an entry.  The entry
+ * stands for s times its code's value.  type TS_F32 or TS_BF16.
+ *
+ * quantize_groups_e2m1: for each group
+ *   e = the least integer >= -127 with max|x| <= 7 * 2^e (values above 6 s, the
+ *   largest, lose at most the half step below it), 0 for a group of zeros, and
+ *   125 at most, so that a finite x stands as a finite value;
+ *   code = the value nearest x / s, ties to the even code, the sign x's.  A group
+ *   with a NaN or an infinity gets the scale byte 255 and codes 0.
+ *   in      [rows, cols] of in_type, leading dimension ld_in (elements)
+ *   codes   [rows, cols / 2] bytes, leading dimension ld_codes (bytes)
+ *   scales  [rows, cols / 32] bytes, leading dimension ld_scales (bytes)
+ * dequantize_groups_e2m1: the values the codes stand for, in out_type; both types
+ *   hold them exactly, but for those past the largest number, which are infinite.
+ *   A group of scale byte 255 gives NaN.
+ * Requirements of both (else TS_EUNSUPPORTED): cols a multiple of 32, codes
+ * 4-byte aligned and ld_codes a multiple of 4, values aligned to their type.
+ * codes and scales must not overlap the values.
+ *
+ * lmhead_logits_local_e2m1: lmhead_logits_local with such an lm_head,
+ *   logits[r, v] = sum_h hidden[r, h] * 2^e[v, h / 32] * q[v, h],
+ *   over the rank's own vocabulary slice, never gathered.  hidden stays bf16;
+ *   every product is exact in fp32 and sums are fp32.
+ *   hidden          bf16 [rows, hidden_dim], leading dimension ld_hidden
+ *   lm_head         codes [vocab_local, hidden_dim / 2], leading dimension
+ *                   ld_lm_head (bytes)
+ *   lm_head_scales  [vocab_local, hidden_dim / 32], leading dimension ld_scales
+ *                   (bytes), any alignment
+ *   logits          fp32 [rows, vocab_local], leading dimension ld_logits
+ * Requirements (else TS_EUNSUPPORTED): hidden_dim a multiple of 32, ld_hidden of
+ * 8, ld_lm_head of 16, hidden and lm_head 16-byte aligned, logits 4-byte aligned,
+ * vocab_local up to 2^31 - 1024, and no more than 2^22 - 1 tiles of 64 x 256
+ * logits.  Other errors and the empty cases as for lmhead_logits_local.
+ */
+int quantize_groups_e2m1(const void* in, int32_t in_type, int64_t rows, int64_t cols,
+                         int64_t ld_in, void* codes, int64_t ld_codes, void* scales,
+                         int64_t ld_scales, void* stream);
+int dequantize_groups_e2m1(const void* codes, int64_t rows, int64_t cols, int64_t ld_codes,
+                           const void* scales, int64_t ld_scales, void* out, int32_t out_type,
+                           int64_t ld_out, void* stream);
+int lmhead_logits_local_e2m1(const void* hidden, int64_t rows, int64_t hidden_dim,
+                             int64_t ld_hidden, const void* lm_head, const void* lm_head_scales,
+                             int64_t vocab_local, int64_t ld_lm_head, int64_t ld_scales,
                              float* logits, int64_t ld_logits, void* stream);
 
 /*
@@ -416,8 +469,6 @@ int sampler_assemble_and_sample(const float* const* slices, const int64_t* slice
  * the call's sizes and by where in a cache line its row starts.  rows == 0 writes nothing but
  * a loss of 0.  rows, vocab < 2^31.
  */
-enum { TS_F32 = 0, TS_BF16 = 1 };
-
 /*
  * token_logprobs: lp[r] = z_t - ln sum_j exp(z_j), z = logits[r] / temperature,
  * t = token_ids[r], and optionally the entropy H[r] = -sum_j p_j ln p_j of

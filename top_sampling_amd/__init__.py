@@ -11,6 +11,10 @@ Calls mirror the C entry points:
                                  adapter
   quantize_rows_e4m3             per-row FP8 (E4M3) quantization of bf16 rows
   lmhead_logits_local_e4m3       the same projection from FP8 codes and scales
+  (de)quantize_groups_e2m1       4-bit (MX FP4) quantization of rows, a scale
+                                 per group of 32, and the values it stands for
+  lmhead_logits_local_e2m1       the projection of bf16 hidden states from a
+                                 4-bit lm_head
   sampler_assemble_vocab_slices  stitch received vocabulary slices
   sampler_sample                 per-row temperature / top-k / top-p /
                                  logprobs / Gumbel-max sampling
@@ -23,7 +27,7 @@ Calls mirror the C entry points:
   policy_loss                    clipped policy loss with a KL term
   preference_loss                loss of paired log ratios
 ``stream`` (None: the current one) is where a call's kernels run.  The scoring,
-loss and adapter calls allocate outputs and workspaces for it; inputs have to be
+loss, adapter and 4-bit calls allocate outputs and workspaces for it; inputs have to be
 ready there, and to live until the kernels have run (``record_stream`` where they
 were allocated for another one).
 ``compute_logits_local`` returns the rank's own ``[rows, V_local]`` slice,
@@ -67,6 +71,12 @@ SYMBOLS = {
                                                 _I64, _VP, _SZ, _VP]),
     "quantize_rows_e4m3": (ctypes.c_int, [_VP, _I64, _I64, _I64, _VP, _I64, _VP, _VP]),
     "lmhead_logits_local_e4m3": (ctypes.c_int, [_VP, _VP, _I64, _I64, _I64, _VP, _VP, _I64, _I64,
+                                                _VP, _I64, _VP]),
+    "quantize_groups_e2m1": (ctypes.c_int, [_VP, _I32, _I64, _I64, _I64, _VP, _I64, _VP, _I64,
+                                            _VP]),
+    "dequantize_groups_e2m1": (ctypes.c_int, [_VP, _I64, _I64, _I64, _VP, _I64, _VP, _I32, _I64,
+                                              _VP]),
+    "lmhead_logits_local_e2m1": (ctypes.c_int, [_VP, _I64, _I64, _I64, _VP, _VP, _I64, _I64, _I64,
                                                 _VP, _I64, _VP]),
     "sampler_workspace_bytes": (_SZ, [_I64, _I64, _I32]),
     "sampler_sample": (ctypes.c_int, [_VP, _I64, _I64, _I64, _VP, _I64, _I32, _VP, _VP, _VP, _VP,
@@ -747,6 +757,103 @@ def lmhead_logits_local_lora(hidden, lm_head, lora_a, lora_b, adapter_ids, adapt
             lora_a.data_ptr(), stride_a, ld_a, lora_b.data_ptr(), stride_b, ld_b, n, rank,
             _ptr(adapter_scales), _ptr(adapter_ids), out.data_ptr(),
             out.stride(0) if rows > 1 else vocab, workspace.data_ptr(), workspace.numel(), s))
+    return out
+
+
+# ------------------------------------------------------ 4-bit rows and projection
+E2M1_GROUP = 32
+
+
+def _group_rows(t, name, dtype, rows, width, device):
+    """Checks a matrix of a 4-bit call; returns its leading dimension."""
+    if t.dtype is not dtype or t.shape != (rows, width):
+        raise ValueError(f"{name} must be {dtype} [{rows}, {width}]")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    ld, step = t.stride()
+    if width > 1 and step != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    if rows > 1 and ld < width:
+        raise ValueError(f"{name} rows overlap")
+    return max(ld, width) if rows > 1 else width
+
+
+def _values_type(dtype):
+    kind = _LOGITS_TYPES.get(dtype)
+    if kind is None:
+        raise ValueError("values must be fp32 or bf16")
+    return kind
+
+
+def quantize_groups_e2m1(x, codes=None, scales=None, stream=None):
+    """fp32 or bf16 ``x [rows, cols]`` (cols a multiple of 32) as OCP MX FP4:
+    uint8 codes ``[rows, cols / 2]`` (two a byte, the even column's in the low
+    half) and a scale byte for every 32 columns, ``[rows, cols / 32]`` (see
+    ``quantize_groups_e2m1`` in top_sampling.h)."""
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, cols]")
+    kind, dev = _values_type(x.dtype), x.device
+    rows, cols = x.shape
+    if cols % E2M1_GROUP:
+        raise ValueError(f"cols {cols} is no multiple of {E2M1_GROUP}")
+    ld_x = _group_rows(x, "x", x.dtype, rows, cols, dev)
+    with _OnDevice(dev, stream) as s:
+        if codes is None:
+            codes = torch.empty(rows, cols // 2, dtype=torch.uint8, device=dev)
+        if scales is None:
+            scales = torch.empty(rows, cols // E2M1_GROUP, dtype=torch.uint8, device=dev)
+        ld_codes = _group_rows(codes, "codes", torch.uint8, rows, cols // 2, dev)
+        ld_scales = _group_rows(scales, "scales", torch.uint8, rows, cols // E2M1_GROUP, dev)
+        _check(lib.quantize_groups_e2m1(x.data_ptr(), kind, rows, cols, ld_x, codes.data_ptr(),
+                                        ld_codes, scales.data_ptr(), ld_scales, s))
+    return codes, scales
+
+
+def dequantize_groups_e2m1(codes, scales, dtype=torch.bfloat16, out=None, stream=None):
+    """The values that 4-bit ``codes [rows, cols / 2]`` and their ``scales
+    [rows, cols / 32]`` stand for, in ``dtype`` (fp32 or bf16, both exact)."""
+    if codes.dim() != 2:
+        raise ValueError("codes must be [rows, cols / 2]")
+    dev = codes.device
+    rows, cols = codes.shape[0], 2 * codes.shape[1]
+    if cols % E2M1_GROUP:
+        raise ValueError(f"cols {cols} is no multiple of {E2M1_GROUP}")
+    ld_codes = _group_rows(codes, "codes", torch.uint8, rows, cols // 2, dev)
+    ld_scales = _group_rows(scales, "scales", torch.uint8, rows, cols // E2M1_GROUP, dev)
+    kind = _values_type(dtype if out is None else out.dtype)
+    with _OnDevice(dev, stream) as s:
+        if out is None:
+            out = torch.empty(rows, cols, dtype=dtype, device=dev)
+        ld_out = _group_rows(out, "out", out.dtype, rows, cols, dev)
+        _check(lib.dequantize_groups_e2m1(codes.data_ptr(), rows, cols, ld_codes,
+                                          scales.data_ptr(), ld_scales, out.data_ptr(), kind,
+                                          ld_out, s))
+    return out
+
+
+def lmhead_logits_local_e2m1(hidden, lm_head, lm_head_scales, out=None, stream=None):
+    """``lmhead_logits_local`` with a 4-bit lm_head: fp32 ``[rows, V_local]`` of
+    bf16 ``hidden [rows, H]`` against the codes ``lm_head [V_local, H / 2]`` and
+    their ``lm_head_scales [V_local, H / 32]`` (uint8, from
+    ``quantize_groups_e2m1``).  ``out`` may be columns of a wider buffer."""
+    if hidden.dim() != 2 or lm_head.dim() != 2:
+        raise ValueError("hidden and lm_head must be 2-D")
+    dev = hidden.device
+    rows, h = hidden.shape
+    vocab = lm_head.shape[0]
+    if h % E2M1_GROUP:
+        raise ValueError(f"hidden size {h} is no multiple of {E2M1_GROUP}")
+    ld_hidden = _group_rows(hidden, "hidden", torch.bfloat16, rows, h, dev)
+    ld_lm_head = _group_rows(lm_head, "lm_head", torch.uint8, vocab, h // 2, dev)
+    ld_scales = _group_rows(lm_head_scales, "lm_head_scales", torch.uint8, vocab,
+                            h // E2M1_GROUP, dev)
+    with _OnDevice(dev, stream) as s:
+        if out is None:
+            out = torch.empty(rows, vocab, dtype=torch.float32, device=dev)
+        ld_out = _group_rows(out, "out", torch.float32, rows, vocab, dev)
+        _check(lib.lmhead_logits_local_e2m1(
+            hidden.data_ptr(), rows, h, ld_hidden, lm_head.data_ptr(), lm_head_scales.data_ptr(),
+            vocab, ld_lm_head, ld_scales, out.data_ptr(), ld_out, s))
     return out
 
 
