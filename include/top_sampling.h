@@ -438,8 +438,8 @@ int sampler_assemble_and_sample(const float* const* slices, const int64_t* slice
  * log-probabilities; the calls below take GIVEN tokens, and the definitions
  * are written out here.
  *
- * Shared by token_logprobs, token_logprobs_backward, policy_loss and
- * preference_loss:
+ * Shared by token_logprobs, token_logprobs_backward, token_logprobs_topn,
+ * token_logprobs_listed(_backward), policy_loss and preference_loss:
  *   logits       [rows, vocab], leading dimension ld_logits, of logits_type
  *                TS_F32 or TS_BF16; any alignment of the rows.  -inf marks a
  *                token that is not allowed (probability 0).
@@ -509,6 +509,66 @@ int token_logprobs_backward_ex(const void* logits, int32_t logits_type, int64_t 
                                const float* grad_logprobs, const float* entropies,
                                const float* grad_entropies, void* grad_logits, int64_t ld_grad,
                                void* stream);
+
+/*
+ * token_logprobs_topn: token_logprobs with each token's rank and the row's most
+ * likely alternatives, in the same read of the logits.  Tokens are in the order of
+ * (logit descending, id ascending), -inf last.
+ *   ranks          int32 [rows] or NULL: the token's place in that order, from 1
+ *                  (topn_ids[r, ranks[r] - 1] is the token where that is listed)
+ *   topn_ids       int32 [rows, max_logprobs]: the first max_logprobs tokens of
+ *                  the order; -1 past the vocabulary's size
+ *   topn_logprobs  fp32 [rows, max_logprobs]: their log-probabilities, at the
+ *                  call's temperature; -inf in unused places
+ * max_logprobs 0..TS_MAX_LOGPROBS; with 0 topn_ids and topn_logprobs may be NULL.
+ * token_ids may be NULL: no token is asked for (logprobs and ranks NULL) and every
+ * row takes part.  A left-out row has rank 0 and lists nothing; a bad row has rank
+ * 0, ids -1 and NaN.  entropies, row_stats and row_status as in token_logprobs;
+ * row_stats serve token_logprobs_backward and token_logprobs_listed_backward.
+ * Rows with many equal logits beside the n-th largest, and max_logprobs above
+ * 256, are read again (same results, slower).
+ */
+size_t token_logprobs_topn_workspace_bytes(int64_t rows, int64_t vocab);
+int token_logprobs_topn(const void* logits, int32_t logits_type, int64_t rows, int64_t vocab,
+                        int64_t ld_logits, const int32_t* token_ids, double temperature,
+                        int32_t max_logprobs, float* logprobs, int32_t* ranks, float* entropies,
+                        int32_t* topn_ids, float* topn_logprobs, float* row_stats,
+                        int32_t* row_status, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/*
+ * token_logprobs_listed: log-probabilities of n_listed tokens a row, such as
+ * another model's alternatives.
+ *   listed_ids  int32 [rows, n_listed], 1 <= n_listed <= TS_MAX_LISTED.  A negative
+ *               id is an unused place (log-probability 0, its gradient is not
+ *               read); a row of which all are negative is left out.  An id may be
+ *               listed several times.  An id >= vocab makes the row
+ *               TS_ROW_BAD_PARAMS.
+ *   logprobs    fp32 [rows, n_listed]
+ *   entropies, row_stats, row_status  as in token_logprobs
+ *
+ * token_logprobs_listed_backward: the gradient of the logits of any function of
+ * these, from grad_logprobs = dL/dlp (fp32 [rows, n_listed]) and, with the forward
+ * pass's entropies, grad_entropies = dL/dH (fp32 [rows] or NULL):
+ *   dL/dlogits[r, j] = (sum_{i: id_i = j} dL/dlp_i - p_j sum_i dL/dlp_i
+ *                       - dL/dH p_j (ln p_j + H)) / temperature.
+ * listed_ids, temperature and the logits are the forward call's, and row_stats
+ * and logprobs its outputs.  A row whose gradients are all 0 gives a row of zeros
+ * without reading its logits.  No workspace.
+ */
+#define TS_MAX_LISTED 1024   /* largest accepted n_listed */
+size_t token_logprobs_listed_workspace_bytes(int64_t rows, int64_t vocab);
+int token_logprobs_listed(const void* logits, int32_t logits_type, int64_t rows, int64_t vocab,
+                          int64_t ld_logits, const int32_t* listed_ids, int32_t n_listed,
+                          double temperature, float* logprobs, float* entropies, float* row_stats,
+                          int32_t* row_status, void* workspace, size_t workspace_bytes,
+                          void* stream);
+int token_logprobs_listed_backward(const void* logits, int32_t logits_type, int64_t rows,
+                                   int64_t vocab, int64_t ld_logits, const int32_t* listed_ids,
+                                   int32_t n_listed, double temperature, const float* row_stats,
+                                   const float* logprobs, const float* grad_logprobs,
+                                   const float* entropies, const float* grad_entropies,
+                                   void* grad_logits, int64_t ld_grad, void* stream);
 
 /*
  * policy_loss: the clipped policy loss with a KL term,

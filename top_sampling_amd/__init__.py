@@ -24,6 +24,10 @@ Calls mirror the C entry points:
   sampler_workspace_bytes(_slices)  workspace size queries
   token_logprobs(_backward[_ex]) log-probability and entropy of given tokens,
                                  and the gradient of a function of them
+  token_logprobs_topn            the same with the tokens' ranks and the rows'
+                                 most likely alternatives
+  token_logprobs_listed(_backward)  log-probabilities of several listed tokens
+                                 a row, and the gradient of a function of them
   policy_loss                    clipped policy loss with a KL term
   preference_loss                loss of paired log ratios
 ``stream`` (None: the current one) is where a call's kernels run.  The scoring,
@@ -57,6 +61,7 @@ PARAMS_BYTES = 24
 TS_F32, TS_BF16 = 0, 1
 TS_PREFERENCE_MEAN = 1
 TS_MAX_LORA_RANK = 256
+TS_MAX_LISTED = 1024
 TS_MAX_LORA_ROWS = 1 << 20
 
 # (name, restype, argtypes) of every symbol the headers declare
@@ -101,6 +106,15 @@ SYMBOLS = {
                                                _VP, _VP, _VP, _I64, _VP]),
     "token_logprobs_backward_ex": (ctypes.c_int, [_VP, _I32, _I64, _I64, _I64, _VP, _F64, _VP, _VP,
                                                   _VP, _VP, _VP, _VP, _I64, _VP]),
+    "token_logprobs_topn_workspace_bytes": (_SZ, [_I64, _I64]),
+    "token_logprobs_topn": (ctypes.c_int, [_VP, _I32, _I64, _I64, _I64, _VP, _F64, _I32, _VP, _VP,
+                                           _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "token_logprobs_listed_workspace_bytes": (_SZ, [_I64, _I64]),
+    "token_logprobs_listed": (ctypes.c_int, [_VP, _I32, _I64, _I64, _I64, _VP, _I32, _F64, _VP,
+                                             _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "token_logprobs_listed_backward": (ctypes.c_int, [_VP, _I32, _I64, _I64, _I64, _VP, _I32,
+                                                      _F64, _VP, _VP, _VP, _VP, _VP, _VP, _I64,
+                                                      _VP]),
     "policy_loss": (ctypes.c_int, [_VP, _I32, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
                                    _VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP, _SZ, _VP]),
     "preference_loss_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
@@ -442,6 +456,17 @@ class TokenLogprobs:
 
 
 @dataclass
+class TokenLogprobsTopn:
+    logprobs: object       # fp32 [rows], or None without tokens
+    ranks: object          # int32 [rows], or None without tokens
+    entropies: object      # fp32 [rows], or None if not asked for
+    topn_ids: object       # int32 [rows, max_logprobs]
+    topn_logprobs: object  # fp32 [rows, max_logprobs]
+    row_stats: object      # fp32 [rows, 2], for the backward passes
+    row_status: object     # int32 [rows]
+
+
+@dataclass
 class PolicyLoss:
     loss: object         # fp32 scalar
     logprobs: object     # fp32 [rows]
@@ -521,8 +546,9 @@ def _check_vector(t, name, n, device, dtype=torch.float32):
         raise ValueError(f"{name} is on {t.device}, the logits on {device}")
 
 
-def _token_rows(logits, token_ids):
-    """Checks logits and token ids; returns (type code, leading dimension)."""
+def _token_rows(logits, token_ids, each: int = 1):
+    """Checks logits and token ids (`each` a row); returns (type code, leading
+    dimension)."""
     kind = _LOGITS_TYPES.get(logits.dtype)
     shape = logits.shape
     if len(shape) != 2 or kind is None:
@@ -533,7 +559,7 @@ def _token_rows(logits, token_ids):
         raise ValueError("logits must have unit column stride")
     if rows > 1 and ld < vocab:
         raise ValueError("logits rows overlap")
-    _check_vector(token_ids, "token_ids", rows, logits.device, torch.int32)
+    _check_vector(token_ids, "token_ids", rows * each, logits.device, torch.int32)
     return kind, max(ld, vocab)
 
 
@@ -632,6 +658,105 @@ def token_logprobs_backward(logits, token_ids, forward: TokenLogprobs, grad_logp
         _check(lib.token_logprobs_backward_ex(
             logits.data_ptr(), kind, rows, vocab, ld, token_ids.data_ptr(), temperature,
             _ptr(forward.row_stats), _ptr(logprobs), _ptr(grad_logprobs),
+            _ptr(forward.entropies), _ptr(grad_entropies), grad_logits.data_ptr(), ldg, s))
+    return grad_logits
+
+
+def token_logprobs_topn_workspace_bytes(rows: int, vocab: int) -> int:
+    return int(lib.token_logprobs_topn_workspace_bytes(rows, vocab))
+
+
+def token_logprobs_listed_workspace_bytes(rows: int, vocab: int) -> int:
+    return int(lib.token_logprobs_listed_workspace_bytes(rows, vocab))
+
+
+def token_logprobs_topn(logits, token_ids, max_logprobs: int, temperature: float = 1.0,
+                        entropies: bool = False, workspace=None,
+                        stream=None) -> TokenLogprobsTopn:
+    """``token_logprobs`` with each token's rank (from 1, in the order of logit
+    descending and id ascending) and the row's first ``max_logprobs`` tokens of
+    that order with their log-probabilities.  ``token_ids`` None asks for the
+    alternatives alone, of every row.  The outputs share one allocation."""
+    kind, ld = _token_rows(logits, token_ids)
+    rows, vocab = logits.shape
+    n, dev = int(max_logprobs), logits.device
+    if n < 0 or n > TS_MAX_LOGPROBS:
+        raise ValueError(f"max_logprobs {n} outside 0..{TS_MAX_LOGPROBS}")
+    given = rows if token_ids is not None else 0
+    with _OnDevice(dev, stream) as s:
+        workspace = _workspace(workspace, token_logprobs_topn_workspace_bytes(rows, vocab), dev)
+        (stats, logprobs, ranks, status, ids, top, h), at = _outputs(
+            (2 * rows, given, given, rows, rows * n, rows * n, rows if entropies else 0), dev)
+        out = TokenLogprobsTopn(
+            logprobs if given == rows else None,
+            ranks.view(torch.int32).data if given == rows else None, h if entropies else None,
+            ids.view(torch.int32).view(rows, n).data, top.view(rows, n).data,
+            stats.view(rows, 2).data, status.view(torch.int32).data)
+        after = at + 4 * (2 * rows + 2 * given)
+        _check(lib.token_logprobs_topn(
+            logits.data_ptr(), kind, rows, vocab, ld, _ptr(token_ids), temperature, n,
+            at + 8 * rows if given else None, at + 4 * (2 * rows + given) if given else None,
+            after + 4 * (rows + 2 * rows * n) if entropies else None, after + 4 * rows,
+            after + 4 * (rows + rows * n), at, after, workspace.data_ptr(), workspace.numel(), s))
+    return out
+
+
+def token_logprobs_listed(logits, listed_ids, temperature: float = 1.0, entropies: bool = False,
+                          workspace=None, stream=None) -> TokenLogprobs:
+    """Log-probabilities of ``listed_ids [rows, n]`` (int32; negative: unused
+    place, all of a row negative: row left out) under ``softmax(logits[r] /
+    temperature)``: a ``TokenLogprobs`` whose ``logprobs`` are ``[rows, n]``.  The
+    outputs share one allocation."""
+    n = _listed(logits, listed_ids)
+    kind, ld = _token_rows(logits, listed_ids, n)
+    rows, vocab = logits.shape
+    dev = logits.device
+    with _OnDevice(dev, stream) as s:
+        workspace = _workspace(workspace, token_logprobs_listed_workspace_bytes(rows, vocab), dev)
+        (stats, logprobs, status, h), at = _outputs(
+            (2 * rows, rows * n, rows, rows if entropies else 0), dev)
+        out = TokenLogprobs(logprobs.view(rows, n).data, h if entropies else None,
+                            stats.view(rows, 2).data, status.view(torch.int32).data)
+        after = at + 4 * (2 * rows + rows * n)
+        _check(lib.token_logprobs_listed(
+            logits.data_ptr(), kind, rows, vocab, ld, listed_ids.data_ptr(), n, temperature,
+            at + 8 * rows, after + 4 * rows if entropies else None, at, after,
+            workspace.data_ptr(), workspace.numel(), s))
+    return out
+
+
+def _listed(logits, listed_ids):
+    if listed_ids.dim() != 2 or logits.dim() != 2 or listed_ids.shape[0] != logits.shape[0]:
+        raise ValueError("listed_ids must be [rows, n] and logits [rows, vocab]")
+    n = listed_ids.shape[1]
+    if n < 1 or n > TS_MAX_LISTED:
+        raise ValueError(f"{n} listed tokens a row, outside 1..{TS_MAX_LISTED}")
+    return n
+
+
+def token_logprobs_listed_backward(logits, listed_ids, forward: TokenLogprobs, grad_logprobs,
+                                   grad_entropies=None, temperature: float = 1.0,
+                                   grad_logits=None, stream=None):
+    """Gradient of the logits from ``grad_logprobs`` (fp32 ``[rows, n]``) and
+    ``grad_entropies`` (fp32 ``[rows]`` or None), with the ``TokenLogprobs`` that
+    ``token_logprobs_listed`` gave for the same logits, ids and temperature.
+    ``grad_logits`` may be ``logits`` itself."""
+    n = _listed(logits, listed_ids)
+    kind, ld = _token_rows(logits, listed_ids, n)
+    rows, vocab = logits.shape
+    dev = logits.device
+    if grad_logprobs is None or forward.logprobs is None or forward.row_stats is None:
+        raise ValueError("grad_logprobs and the forward pass's outputs are needed")
+    _check_vector(grad_logprobs, "grad_logprobs", rows * n, dev)
+    _check_vector(grad_entropies, "grad_entropies", rows, dev)
+    _check_vector(forward.row_stats, "forward.row_stats", 2 * rows, dev)
+    _check_vector(forward.logprobs, "forward.logprobs", rows * n, dev)
+    _check_vector(forward.entropies, "forward.entropies", rows, dev)
+    with _OnDevice(dev, stream) as s:
+        grad_logits, ldg = _gradient(grad_logits, True, logits)
+        _check(lib.token_logprobs_listed_backward(
+            logits.data_ptr(), kind, rows, vocab, ld, listed_ids.data_ptr(), n, temperature,
+            _ptr(forward.row_stats), _ptr(forward.logprobs), _ptr(grad_logprobs),
             _ptr(forward.entropies), _ptr(grad_entropies), grad_logits.data_ptr(), ldg, s))
     return grad_logits
 

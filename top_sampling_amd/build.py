@@ -18,7 +18,7 @@ LIB = os.path.join(PKG, "libtopsampling.so")
 SOURCES = ["api.hip", "lmhead_gemm.hip", "lmhead_fp8.hip", "sampler_fast.hip", "sampler_exact.hip",
            "assemble.hip", "clock_probe.hip", "noise_readout.hip", "noalloc.hip",
            "api_losses.hip", "losses.hip", "api_lora.hip", "lmhead_lora.hip",
-           "api_e2m1.hip", "lmhead_e2m1.hip"]
+           "api_e2m1.hip", "lmhead_e2m1.hip", "alternatives.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

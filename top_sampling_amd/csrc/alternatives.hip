@@ -1,0 +1,896 @@
+// Log-probabilities of given tokens with their rank and the row's most likely
+// alternatives, and of several listed tokens a row with the gradient of the
+// logits, on gfx950.
+//
+// With m, S, p_j and H of a row as in token_rows.hpp:
+//   rank    1 + the number of tokens before t in the order of (logit descending,
+//           id ascending); the alternatives are that order's first n tokens
+//   listed  lp_i = (x[id_i] - m) / T - ln S for the row's ids id_0 .. id_(n-1)
+//   dL/dx_j = [sum_{i: id_i = j} g_i - G p_j - h p_j (ln p_j + H)] / T,
+//           g_i = dL/dlp_i, G = sum_i g_i, h = dL/dH
+//           = e_j (a + b log2 e_j) + 1/T sum_{i: id_i = j} g_i,
+//           a = -(G + h (H - ln S)) / (S T),  b = -h ln 2 / (S T);
+//           a listed token's entry is written as a value of its own, from
+//           1 - p = -expm1(lp), as in the single-token gradient.
+// Bound by the logits' bytes: one read forwards, a read and a write backwards.
+//
+// The alternatives cost no second read: while the statistics pass has the
+// logits in registers it also writes the largest of every group of entries (16
+// or 32 of each of 8 neighbouring threads).  A lower bound of the n-th largest
+// logit follows from those alone (the n-th largest of the 256 threads' largest
+// groups), and only the groups that reach it, little more than n, are looked
+// into again.
+#include "alternatives.hpp"
+
+#include "token_rows.hpp"
+
+namespace ts {
+namespace {
+
+constexpr int kGroupLanes = 8;                          // threads that share a group
+constexpr int kSlabGroups = kThreads / kGroupLanes;     // groups of a slab
+constexpr int kGroupVecs = kGroupLanes * kBatch;        // vectors of a group
+constexpr int kListedGroups = 1024;                     // groups looked into, at most
+constexpr int kCandidates = 2048;                       // entries put in order, at most
+
+// How the statistics pass leaves the largest entries of groups: group g of slab
+// s of a row's chunk c is number (c slabs + s) kSlabGroups + g.
+struct Groups {
+  int chunks, chunk_len, slabs, per_row;
+};
+
+Groups make_groups(const Cut& cut) {
+  Groups g;
+  g.chunks = cut.chunks;
+  g.chunk_len = cut.len;
+  g.slabs = (cut.len + kSlab - 1) / kSlab;
+  g.per_row = g.chunks * g.slabs * kSlabGroups;
+  return g;
+}
+
+// A row as one chunk.
+Cut whole_cut(int64_t vocab, int vec) {
+  return Cut{static_cast<int>(std::max<int64_t>(vocab / vec, 1)), 1};
+}
+
+// The largest of a value over 8 neighbouring lanes; all of them get it.
+__device__ __forceinline__ float max_of_8(float x) {
+  auto step = [](float v, auto ctrl) {
+    return max_nan(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                                    0, __builtin_bit_cast(int, v),
+                                                    decltype(ctrl)::value, 0xF, 0xF, true)));
+  };
+  x = step(x, std::integral_constant<int, 0xB1>{});   // quad_perm [1, 0, 3, 2]
+  x = step(x, std::integral_constant<int, 0x4E>{});   // quad_perm [2, 3, 0, 1]
+  return step(x, std::integral_constant<int, 0x141>{});  // row_half_mirror
+}
+
+// What the statistics pass does beside adding up: groups, and the entries
+// before the token in the order.
+template <typename T>
+struct TopVisit {
+  static constexpr bool kOn = true;
+  float* groups;   // of the row's chunk, or null
+  int v0;          // the chunk's first vector
+  float xt;        // the token's logit, +inf if there is none
+  int token, token_vec, token_e;
+  int better;
+
+  __device__ __forceinline__ void slab(int v, int end, const float (&w)[kBatch][Vec<T>::n],
+                                       float high) {
+    if (groups != nullptr) {
+      const float top = max_of_8(high);
+      if (threadIdx.x % kGroupLanes == 0)
+        groups[(v - v0) / kSlab * kSlabGroups + threadIdx.x / kGroupLanes] = top;
+    }
+    if (__any(high >= xt)) {
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = v + j * kThreads + static_cast<int>(threadIdx.x);
+#pragma unroll
+        for (int e = 0; e < Vec<T>::n; ++e) {
+          const bool before = i < token_vec || (i == token_vec && e < token_e);
+          better += (w[j][e] > xt || (w[j][e] == xt && before && i < end)) ? 1 : 0;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void edge(int at, float x) {
+    better += (x > xt || (x == xt && at < token)) ? 1 : 0;
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ TopVisit<T> make_visit(const Shape& f, float* groups, int v0, float xt,
+                                                  int token) {
+  TopVisit<T> v;
+  v.groups = groups;
+  v.v0 = v0;
+  v.xt = xt;
+  v.token = token;
+  const bool in_body = token >= f.head;
+  v.token_vec = in_body ? (token - f.head) / Vec<T>::n : -1;
+  v.token_e = in_body ? (token - f.head) % Vec<T>::n : 0;
+  v.better = 0;
+  return v;
+}
+
+// Sum of an int over the workgroup; every thread gets it.
+__device__ __forceinline__ int group_count(int n, int* wave_n) {
+  for (int d = 32; d > 0; d >>= 1) n += __shfl_xor(n, d, 64);
+  if ((threadIdx.x & 63) == 0) wave_n[threadIdx.x >> 6] = n;
+  __syncthreads();
+  n = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) n += wave_n[w];
+  return n;
+}
+
+// float -> uint32 in the order of the numbers, -0 as 0.
+__device__ __forceinline__ uint32_t order_of(float x) {
+  uint32_t b = __float_as_uint(x);
+  b = b == 0x80000000u ? 0u : b;
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+__device__ __forceinline__ float number_of(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+// An entry's place in the order of alternatives: larger is earlier.
+__device__ __forceinline__ uint64_t entry_key(float x, int id) {
+  return static_cast<uint64_t>(order_of(x)) << 32 | (0xffffffffu - static_cast<uint32_t>(id));
+}
+
+struct TopShared {
+  uint64_t cand[kCandidates];
+  int group[kListedGroups];
+  alignas(16) uint32_t most[kThreads];
+  int hist[256];
+  int n_groups, n_cand, wave_n[kThreads / 64];
+  uint32_t bound;
+  uint64_t bound64;
+  int need, above, first_id, done;
+  Part wave_part[kThreads / 64];
+  double s, ln_s;
+};
+
+// A bound of the n-th largest key that at most kCandidates keys reach, from the
+// whole row digit by digit.  For rows that the groups do not narrow down: many
+// equal entries, or n beyond the threads.
+template <typename T>
+__device__ __forceinline__ void exact_bound(const T* row, int vocab, int n, TopShared& sh) {
+  uint64_t prefix = 0;
+  if (threadIdx.x == 0) {
+    sh.need = n;
+    sh.above = 0;
+    sh.done = 0;
+  }
+  for (int shift = 56; shift >= 0; shift -= 8) {
+    sh.hist[threadIdx.x] = 0;
+    __syncthreads();
+    for (int64_t i = threadIdx.x; i < vocab; i += kThreads) {
+      const uint64_t key = entry_key(static_cast<float>(row[i]), static_cast<int>(i));
+      if (shift == 56 || key >> (shift + 8) == prefix >> (shift + 8))
+        atomicAdd(&sh.hist[static_cast<int>(key >> shift) & 255], 1);
+    }
+    __syncthreads();
+    // The digit that holds the key: its own keys and those above reach `need`.
+    int over = 0;
+    for (int d = threadIdx.x + 1; d < 256; ++d) over += sh.hist[d];
+    const int mine = sh.hist[threadIdx.x];
+    const int need = sh.need, above = sh.above;
+    __syncthreads();
+    if (over < need && over + mine >= need) {
+      sh.bound64 = prefix | static_cast<uint64_t>(threadIdx.x) << shift;
+      sh.need = need - over;
+      sh.above = above + over;
+      sh.done = above + over + mine <= kCandidates;
+    }
+    __syncthreads();
+    prefix = sh.bound64;
+    if (sh.done) break;
+  }
+}
+
+// The n first entries of a row (n <= vocab) into sh.cand, with n_cand entries in
+// no order, all of which and no others reach a bound.  By the whole workgroup.
+template <typename T>
+__device__ __forceinline__ void find_candidates(const T* row, int vocab, const Groups& gs,
+                                                const float* groups, int n, TopShared& sh) {
+  constexpr int VN = Vec<T>::n;
+  const int tid = threadIdx.x;
+  const Shape f = stats_shape(row, vocab);
+  if (tid == 0) sh.n_groups = sh.n_cand = 0;
+  bool by_groups = n <= kThreads;
+  auto live = [&](int g) {
+    const int slab = g / kSlabGroups, c = slab / gs.slabs;
+    return c * gs.chunk_len + slab % gs.slabs * kSlab <
+           min((c + 1) * static_cast<int64_t>(gs.chunk_len), static_cast<int64_t>(f.whole));
+  };
+  if (by_groups) {
+    uint32_t most = 0;
+    for (int g = tid; g < gs.per_row; g += kThreads)
+      if (live(g)) most = max(most, order_of(groups[g]));
+    sh.most[tid] = most;
+    __syncthreads();
+    int place = 0;
+    const uint4* m4 = reinterpret_cast<const uint4*>(sh.most);
+#pragma unroll 4
+    for (int k = 0; k < kThreads / 4; ++k) {
+      const uint4 v = m4[k];
+      place += (v.x > most || (v.x == most && 4 * k < tid)) ? 1 : 0;
+      place += (v.y > most || (v.y == most && 4 * k + 1 < tid)) ? 1 : 0;
+      place += (v.z > most || (v.z == most && 4 * k + 2 < tid)) ? 1 : 0;
+      place += (v.w > most || (v.w == most && 4 * k + 3 < tid)) ? 1 : 0;
+    }
+    if (place == n - 1) sh.bound = most;
+    __syncthreads();
+    const uint32_t bound = sh.bound;
+    if (most >= bound) {
+      for (int g = tid; g < gs.per_row; g += kThreads)
+        if (live(g) && order_of(groups[g]) >= bound) {
+          const int at = atomicAdd(&sh.n_groups, 1);
+          if (at < kListedGroups) sh.group[at] = g;
+        }
+    }
+    __syncthreads();
+    by_groups = sh.n_groups <= kListedGroups;
+    if (by_groups) {
+      auto add = [&](float x, int id) {
+        if (order_of(x) < bound) return;
+        const int at = atomicAdd(&sh.n_cand, 1);
+        if (at < kCandidates) sh.cand[at] = entry_key(x, id);
+      };
+      for (int k = tid / kGroupVecs; k < sh.n_groups; k += kThreads / kGroupVecs) {
+        const int g = sh.group[k], slab = g / kSlabGroups, c = slab / gs.slabs;
+        const int j = tid % kGroupVecs / kGroupLanes;
+        const int64_t v = static_cast<int64_t>(c) * gs.chunk_len + slab % gs.slabs * kSlab +
+                          j * kThreads + g % kSlabGroups * kGroupLanes + tid % kGroupLanes;
+        if (v >= min((c + 1) * static_cast<int64_t>(gs.chunk_len), static_cast<int64_t>(f.whole)))
+          continue;
+        const typename Vec<T>::Type w =
+            *reinterpret_cast<const typename Vec<T>::Type*>(row + f.head + v * VN);
+#pragma unroll
+        for (int e = 0; e < VN; ++e)
+          add(static_cast<float>(w[e]), f.head + static_cast<int>(v) * VN + e);
+      }
+      if (tid < f.edge) {
+        const int at = f.template at<T>(tid);
+        add(static_cast<float>(row[at]), at);
+      }
+    }
+    __syncthreads();
+    if (by_groups && sh.n_cand <= kCandidates) return;
+    __syncthreads();
+    if (tid == 0) sh.n_cand = 0;
+  }
+  exact_bound(row, vocab, n, sh);
+  const uint64_t bound = sh.bound64;
+  for (int64_t i = tid; i < vocab; i += kThreads) {
+    const uint64_t key = entry_key(static_cast<float>(row[i]), static_cast<int>(i));
+    if (key >= bound) sh.cand[atomicAdd(&sh.n_cand, 1)] = key;
+  }
+  __syncthreads();
+}
+
+// A row that is left out, and one with a bad status.
+__device__ __forceinline__ void topn_no_row(const TopnOut& o, int64_t r, int status) {
+  const bool bad = status != TS_ROW_OK;
+  if (threadIdx.x == 0) {
+    if (o.logprobs) {
+      o.logprobs[r] = bad ? NAN : 0.0f;
+      if (o.ranks) o.ranks[r] = 0;
+    }
+    if (o.entropies) o.entropies[r] = bad ? NAN : 0.0f;
+    if (o.row_stats) o.row_stats[2 * r] = o.row_stats[2 * r + 1] = bad ? NAN : 0.0f;
+    if (o.row_status) o.row_status[r] = status;
+  }
+  for (int i = threadIdx.x; i < o.n; i += kThreads) {
+    o.topn_ids[r * o.n + i] = -1;
+    o.topn_logprobs[r * o.n + i] = bad ? NAN : -INFINITY;
+  }
+}
+
+// A row's outputs from its joined statistics (held by the first threads), the
+// number of entries before its token, and its groups.  By the whole workgroup.
+template <typename T>
+__device__ __forceinline__ void finish_topn(const T* row, int64_t r, int vocab, int token,
+                                            bool has_token, float xt, RowStats& st, int better,
+                                            const Groups& gs, const float* groups, const Cut& cut,
+                                            const Scale& sc, const TopnOut& o, TopShared& sh) {
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    sh.wave_part[0] = Part{st.s, st.u, st.m, 0.0f};
+    sh.first_id = has_token ? token : 0;
+  }
+  const int before = group_count(better, sh.wave_n);  // waits for the others too
+  st.m = sh.wave_part[0].m;
+  st.s = sh.wave_part[0].s;
+  st.u = sh.wave_part[0].u;
+  const int status = has_token && token >= vocab ? TS_ROW_BAD_PARAMS
+                     : fabsf(st.m) < INFINITY    ? TS_ROW_OK
+                                                 : TS_ROW_BAD_LOGITS;
+  if (status != TS_ROW_OK) {
+    topn_no_row(o, r, status);
+    return;
+  }
+  const int n = min(o.n, vocab);
+  uint64_t key = 0;
+  int place = n, rest_place = n;
+  if (n > 0) {
+    find_candidates(row, vocab, gs, groups, n, sh);
+    const int count = sh.n_cand;
+    if (tid < count) {
+      key = sh.cand[tid];
+      place = 0;
+      for (int k = 0; k < count; ++k) place += sh.cand[k] > key ? 1 : 0;
+      if (place == 0) sh.first_id = static_cast<int>(0xffffffffu - static_cast<uint32_t>(key));
+    }
+    for (int c = tid + kThreads; c < count; c += kThreads) {
+      const uint64_t other = sh.cand[c];
+      rest_place = 0;
+      for (int k = 0; k < count; ++k) rest_place += sh.cand[k] > other ? 1 : 0;
+      if (rest_place == 0)
+        sh.first_id = static_cast<int>(0xffffffffu - static_cast<uint32_t>(other));
+    }
+    __syncthreads();
+  }
+  // The digits of 1 - p of the one token that may have p next to 1.
+  if (tid < 64) {
+    const int first = sh.first_id;
+    const float x1 = n > 0 ? st.m : has_token ? xt : -INFINITY;
+    if (tid < kBatch && next_to_one(st.m, st.s, first, vocab, x1)) {
+      const Shape f = stats_shape(row, vocab);
+      TokenBatch<T, kBatch> batch;
+      batch.load(row, f, cut.chunks == 1 ? max(f.whole, 1) : cut.len, kThreads, first);
+      st.s += batch.lost(st.m, sc);
+    }
+    if (tid == 0) {
+      sh.s = st.s;
+      sh.ln_s = log(st.s);
+    }
+  }
+  __syncthreads();
+  const double ln_s = sh.ln_s;
+  if (tid == 0) {
+    if (o.logprobs) {
+      o.logprobs[r] = static_cast<float>((static_cast<double>(xt) - st.m) * sc.inv_t - ln_s);
+      if (o.ranks) o.ranks[r] = before + 1;
+    }
+    if (o.entropies) o.entropies[r] = static_cast<float>(ln_s - st.u * M_LN2 / sh.s);
+    if (o.row_stats) {
+      o.row_stats[2 * r] = st.m;
+      o.row_stats[2 * r + 1] = static_cast<float>(sh.s);
+    }
+    if (o.row_status) o.row_status[r] = TS_ROW_OK;
+  }
+  auto put = [&](int at, uint64_t k) {
+    if (at >= n) return;
+    const float x = number_of(static_cast<uint32_t>(k >> 32));
+    o.topn_ids[r * o.n + at] = static_cast<int>(0xffffffffu - static_cast<uint32_t>(k));
+    o.topn_logprobs[r * o.n + at] =
+        static_cast<float>((static_cast<double>(x) - st.m) * sc.inv_t - ln_s);
+  };
+  if (n > 0) {
+    const int count = sh.n_cand;
+    if (tid < count) put(place, key);
+    for (int c = tid + kThreads; c < count; c += kThreads) {
+      const uint64_t other = sh.cand[c];
+      int at = 0;
+      for (int k = 0; k < count; ++k) at += sh.cand[k] > other ? 1 : 0;
+      put(at, other);
+    }
+  }
+  for (int i = n + tid; i < o.n; i += kThreads) {
+    o.topn_ids[r * o.n + i] = -1;
+    o.topn_logprobs[r * o.n + i] = -INFINITY;
+  }
+}
+
+template <bool ENT, typename T>
+__global__ __launch_bounds__(kThreads) void topn_whole_kernel(
+    const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,
+    Scale sc, Cut cut, Groups gs, float* groups, TopnOut o) {
+  __shared__ TopShared sh;
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    const bool has_token = tokens != nullptr;
+    const int token = has_token ? tokens[r] : -1;
+    if (has_token && token < 0) {
+      topn_no_row(o, r, TS_ROW_OK);
+      continue;
+    }
+    const T* rx = x + r * ld;
+    const float xt = has_token ? static_cast<float>(rx[min(token, vocab - 1)]) : INFINITY;
+    float* gr = groups + r * gs.per_row;
+    TopVisit<T> visit = make_visit<T>(stats_shape(rx, vocab), o.n > 0 ? gr : nullptr, 0, xt, token);
+    RowStats st;
+    st.m = -INFINITY;
+    st.s = st.u = 0.0;
+    row_stats<T, ENT, kThreads>(rx, vocab, 0, vocab / Vec<T>::n, true, sc, st.m, st.s, st.u,
+                                &visit);
+    join_group<ENT, kThreads>(st.m, st.s, st.u, sc, sh.wave_part);
+    __syncthreads();
+    finish_topn(rx, r, vocab, token, has_token, xt, st, visit.better, gs, gr, cut, sc, o, sh);
+    __syncthreads();
+  }
+}
+
+template <bool ENT, typename T>
+__global__ __launch_bounds__(kThreads) void topn_stats_kernel(
+    const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,
+    Scale sc, Cut cut, Groups gs, float* __restrict__ groups, Part* __restrict__ parts,
+    int* __restrict__ betters, int want_groups) {
+  __shared__ Part wave_part[kThreads / 64];
+  __shared__ int wave_n[kThreads / 64];
+  const int tid = threadIdx.x;
+  const int64_t total = static_cast<int64_t>(rows) * cut.chunks;
+  for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
+    const int row = static_cast<int>(b / cut.chunks), chunk = static_cast<int>(b % cut.chunks);
+    const int token = tokens ? tokens[row] : -1;
+    if (tokens && token < 0) continue;
+    const T* rx = x + static_cast<int64_t>(row) * ld;
+    const float xt = tokens ? static_cast<float>(rx[min(token, vocab - 1)]) : INFINITY;
+    float* gr = groups + static_cast<int64_t>(row) * gs.per_row + chunk * gs.slabs * kSlabGroups;
+    TopVisit<T> visit = make_visit<T>(stats_shape(rx, vocab), want_groups ? gr : nullptr,
+                                      chunk * cut.len, xt, token);
+    float m = -INFINITY;
+    double s = 0.0, u = 0.0;
+    row_stats<T, ENT, kThreads>(rx, vocab, chunk * cut.len, (chunk + 1) * cut.len,
+                                chunk == cut.chunks - 1, sc, m, s, u, &visit);
+    join_group<ENT, kThreads>(m, s, u, sc, wave_part);
+    const int n = group_count(visit.better, wave_n);
+    if (tid == 0) {
+      parts[b] = Part{s, u, m, 0.0f};
+      betters[b] = n;
+    }
+    __syncthreads();
+  }
+}
+
+template <bool ENT, typename T>
+__global__ __launch_bounds__(kThreads) void topn_rows_kernel(
+    const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,
+    Scale sc, Cut cut, Groups gs, const float* __restrict__ groups,
+    const Part* __restrict__ parts, const int* __restrict__ betters, TopnOut o) {
+  __shared__ TopShared sh;
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    const bool has_token = tokens != nullptr;
+    const int token = has_token ? tokens[r] : -1;
+    if (has_token && token < 0) {
+      topn_no_row(o, r, TS_ROW_OK);
+      continue;
+    }
+    const T* rx = x + r * ld;
+    const float xt = has_token ? static_cast<float>(rx[min(token, vocab - 1)]) : INFINITY;
+    RowStats st;
+    st.m = -INFINITY;
+    st.s = st.u = 0.0;
+    int better = 0;
+    for (int i = threadIdx.x; i < cut.chunks; i += kThreads) {
+      const Part p = parts[r * cut.chunks + i];
+      const float top = max_nan(st.m, p.m), ref = top == -INFINITY ? 0.0f : top;
+      const float d0 = fmaxf(st.m - ref, sc.floor), d1 = fmaxf(p.m - ref, sc.floor);
+      const double f0 = exp_t(d0, sc), f1 = exp_t(d1, sc);
+      if (ENT) st.u = f0 * (st.u + log2_t(d0, sc) * st.s) + f1 * (p.u + log2_t(d1, sc) * p.s);
+      st.s = f0 * st.s + f1 * p.s;
+      st.m = top;
+      better += betters[r * cut.chunks + i];
+    }
+    join_group<ENT, kThreads>(st.m, st.s, st.u, sc, sh.wave_part);
+    __syncthreads();
+    finish_topn(rx, r, vocab, token, has_token, xt, st, better, gs,
+                groups + r * gs.per_row, cut, sc, o, sh);
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------ listed
+// Whether none of a row's ids is used; by the whole workgroup.
+__device__ __forceinline__ bool none_listed(const int32_t* ids, int n) {
+  bool any = false;
+  for (int i = threadIdx.x; i < n; i += kThreads) any |= ids[i] >= 0;
+  return __syncthreads_or(any) == 0;
+}
+
+// What a row that is left out writes, or one with a bad status; by a wave.
+__device__ __forceinline__ void listed_no_row(const ListedOut& o, const int32_t* ids, int64_t r,
+                                              int status, int lane) {
+  const float v = status == TS_ROW_OK ? 0.0f : NAN;
+  for (int i = lane; i < o.n; i += 64) o.logprobs[r * o.n + i] = ids[i] < 0 ? 0.0f : v;
+  if (lane != 0) return;
+  if (o.entropies) o.entropies[r] = v;
+  if (o.row_stats) o.row_stats[2 * r] = o.row_stats[2 * r + 1] = v;
+  if (o.row_status) o.row_status[r] = status;
+}
+
+// A row's outputs from its joined statistics, which every lane of the wave has.
+// `len`: how the row was cut.
+template <typename T>
+__device__ __forceinline__ void finish_listed(const T* row, int64_t r, int vocab,
+                                              const int32_t* ids, RowStats& st, int len,
+                                              const Scale& sc, const ListedOut& o, int lane) {
+  bool past = false;
+  int first = -1;
+  for (int i = lane; i < o.n; i += 64) {
+    const int id = ids[i];
+    past |= id >= vocab;
+    if (id >= 0 && id < vocab && static_cast<float>(row[id]) == st.m) first = id;
+  }
+  const int status = __any(past) ? TS_ROW_BAD_PARAMS
+                     : fabsf(st.m) < INFINITY ? TS_ROW_OK : TS_ROW_BAD_LOGITS;
+  if (status != TS_ROW_OK) {
+    listed_no_row(o, ids, r, status, lane);
+    return;
+  }
+  // At most one id has p next to 1; the digits of its 1 - p.
+  const uint64_t holds = __ballot(first >= 0);
+  if (holds != 0) {
+    first = __shfl(first, __ffsll(static_cast<unsigned long long>(holds)) - 1, 64);
+    if (next_to_one(st.m, st.s, first, vocab, st.m)) {
+      double more = 0.0;
+      if (lane < kBatch) {
+        TokenBatch<T, kBatch> batch;
+        batch.load(row, stats_shape(row, vocab), len, kThreads, first);
+        more = batch.lost(st.m, sc);
+      }
+      st.s += __shfl(more, 0, 64);
+    }
+  }
+  const double ln_s = log(st.s);
+  for (int i = lane; i < o.n; i += 64) {
+    const int id = ids[i];
+    o.logprobs[r * o.n + i] =
+        id < 0 ? 0.0f
+               : static_cast<float>((static_cast<double>(static_cast<float>(row[id])) - st.m) *
+                                        sc.inv_t - ln_s);
+  }
+  if (lane != 0) return;
+  if (o.entropies) o.entropies[r] = static_cast<float>(ln_s - st.u * M_LN2 / st.s);
+  if (o.row_stats) {
+    o.row_stats[2 * r] = st.m;
+    o.row_stats[2 * r + 1] = static_cast<float>(st.s);
+  }
+  if (o.row_status) o.row_status[r] = TS_ROW_OK;
+}
+
+template <bool ENT, typename T>
+__global__ __launch_bounds__(kThreads) void listed_whole_kernel(
+    const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ ids,
+    Scale sc, ListedOut o) {
+  __shared__ Part wave_part[kThreads / 64];
+  const int tid = threadIdx.x;
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    const int32_t* row_ids = ids + r * o.n;
+    if (none_listed(row_ids, o.n)) {
+      if (tid < 64) listed_no_row(o, row_ids, r, TS_ROW_OK, tid);
+      continue;
+    }
+    const T* rx = x + r * ld;
+    RowStats st;
+    st.m = -INFINITY;
+    st.s = st.u = 0.0;
+    row_stats<T, ENT, kThreads>(rx, vocab, 0, vocab / Vec<T>::n, true, sc, st.m, st.s, st.u);
+    join_group<ENT, kThreads>(st.m, st.s, st.u, sc, wave_part);
+    if (tid < 64) {
+      st.m = __shfl(st.m, 0, 64);
+      st.s = __shfl(st.s, 0, 64);
+      st.u = __shfl(st.u, 0, 64);
+      finish_listed(rx, r, vocab, row_ids, st, max(stats_shape(rx, vocab).whole, 1), sc, o, tid);
+    }
+    __syncthreads();
+  }
+}
+
+template <bool ENT, typename T>
+__global__ __launch_bounds__(kThreads) void listed_stats_kernel(
+    const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ ids,
+    int n, Scale sc, Cut cut, Part* __restrict__ parts) {
+  __shared__ Part wave_part[kThreads / 64];
+  const int64_t total = static_cast<int64_t>(rows) * cut.chunks;
+  for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
+    const int row = static_cast<int>(b / cut.chunks), chunk = static_cast<int>(b % cut.chunks);
+    if (none_listed(ids + static_cast<int64_t>(row) * n, n)) continue;
+    float m = -INFINITY;
+    double s = 0.0, u = 0.0;
+    row_stats<T, ENT, kThreads>(x + static_cast<int64_t>(row) * ld, vocab, chunk * cut.len,
+                                (chunk + 1) * cut.len, chunk == cut.chunks - 1, sc, m, s, u);
+    join_group<ENT, kThreads>(m, s, u, sc, wave_part);
+    if (threadIdx.x == 0) parts[b] = Part{s, u, m, 0.0f};
+    __syncthreads();
+  }
+}
+
+// A wave a row.
+template <bool ENT, typename T>
+__global__ __launch_bounds__(kThreads) void listed_rows_kernel(
+    const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ ids,
+    Scale sc, Cut cut, const Part* __restrict__ parts, ListedOut o) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6);
+       r < rows; r += static_cast<int64_t>(gridDim.x) * (kThreads / 64)) {
+    const int32_t* row_ids = ids + r * o.n;
+    bool any = false;
+    for (int i = lane; i < o.n; i += 64) any |= row_ids[i] >= 0;
+    if (!__any(any)) {
+      listed_no_row(o, row_ids, r, TS_ROW_OK, lane);
+      continue;
+    }
+    RowStats st;
+    st.m = -INFINITY;
+    st.s = st.u = 0.0;
+    for (int i = lane; i < cut.chunks; i += 64) {
+      const Part p = parts[r * cut.chunks + i];
+      const float top = max_nan(st.m, p.m), ref = top == -INFINITY ? 0.0f : top;
+      const float d0 = fmaxf(st.m - ref, sc.floor), d1 = fmaxf(p.m - ref, sc.floor);
+      const double f0 = exp_t(d0, sc), f1 = exp_t(d1, sc);
+      if (ENT) st.u = f0 * (st.u + log2_t(d0, sc) * st.s) + f1 * (p.u + log2_t(d1, sc) * p.s);
+      st.s = f0 * st.s + f1 * p.s;
+      st.m = top;
+    }
+    join_lanes<ENT>(st.m, st.s, st.u, 64, sc);
+    finish_listed(x + r * ld, r, vocab, row_ids, st, cut.len, sc, o, lane);
+  }
+}
+
+// The gradient's dense part of vectors [v0, v1) of a row (and with `edge` of the
+// entries at its ends), from the last slab to the first: entry j is
+// e_j (a + b log2 e_j).  `read` false: it is all `a`, which is 0.
+struct DenseGrad {
+  float m, a, b;
+};
+
+template <typename T, bool ENT>
+__device__ __forceinline__ void dense_grad(const T* row, T* out, const Shape& f, int v0, int v1,
+                                           bool edge, bool read, const DenseGrad& g,
+                                           const Scale& sc) {
+  constexpr int VN = Vec<T>::n;
+  using V = typename Vec<T>::Type;
+  const int tid = threadIdx.x;
+  const int end = min(v1, f.whole);
+  auto entry = [&](float x) {
+    const float k = log2_t(x - g.m, sc);
+    const float ex = __builtin_amdgcn_exp2f(k);
+    return ENT ? ex * fmaf(g.b, fmaxf(k, kLeastLog2), g.a) : ex * g.a;
+  };
+  if (edge && tid < f.edge) {
+    const int at = f.template at<T>(tid);
+    out[at] = static_cast<T>(read ? entry(static_cast<float>(row[at])) : 0.0f);
+  }
+  if (v0 >= end) return;
+  row += f.head;
+  out += f.head;
+  int v = v0 + (end - 1 - v0) / kSlab * kSlab;
+  Slab<T, kThreads> next;
+  if (read) next.load(row, v, end);
+  for (; v >= v0; v -= kSlab) {
+    float w[kBatch][VN];
+    if (!read) {
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+        for (int e = 0; e < VN; ++e) w[j][e] = 0.0f;
+    } else {
+      next.unpack(w);
+      if (v > v0) next.load(row, v - kSlab, end);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+        for (int e = 0; e < VN; ++e) w[j][e] = entry(w[j][e]);
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = v + j * kThreads + tid;
+      V o;
+#pragma unroll
+      for (int e = 0; e < VN; ++e) o[e] = static_cast<T>(w[j][e]);
+      if (i < end)
+        __builtin_nontemporal_store(o, reinterpret_cast<V*>(out + static_cast<int64_t>(i) * VN));
+    }
+  }
+}
+
+// A workgroup writes a chunk of a row's dense part, then the listed entries in
+// it.  Their values need no logit, only the forward pass's log-probabilities, so
+// the gradient may replace the logits.  An id that is listed several times is
+// written once, by its first place, from the sum of its gradients.
+template <typename T, bool ENT>
+__global__ __launch_bounds__(kThreads) void listed_grad_kernel(
+    const T* x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ ids, Scale sc,
+    Cut cut, ListedGrad g, T* d, int64_t ldd) {
+  __shared__ double wave_sum[kThreads / 64];
+  __shared__ int s_ids[TS_MAX_LISTED];
+  __shared__ float s_g[TS_MAX_LISTED];
+  const int tid = threadIdx.x;
+  const int64_t total = static_cast<int64_t>(rows) * cut.chunks;
+  for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
+    // Last row first, as the end of the logits is what the caches still hold.
+    const int row = rows - 1 - static_cast<int>(b / cut.chunks);
+    const int chunk = cut.chunks - 1 - static_cast<int>(b % cut.chunks);
+    const int64_t at = static_cast<int64_t>(row) * g.n;
+    const T* rx = x + static_cast<int64_t>(row) * ld;
+    T* rd = d + static_cast<int64_t>(row) * ldd;
+    double sum = 0.0;
+    const double dh_row = ENT ? static_cast<double>(g.grad_entropies[row]) : 0.0;
+    bool any = false;
+    for (int i = tid; i < g.n; i += kThreads) {
+      const int id = ids[at + i];
+      const float gi = id < 0 ? 0.0f : g.grad_logprobs[at + i];
+      s_ids[i] = id;
+      s_g[i] = gi;
+      sum += gi;
+      any |= id >= 0 && (gi != 0.0f || dh_row != 0.0);
+    }
+    for (int k = 32; k > 0; k >>= 1) sum += __shfl_xor(sum, k, 64);
+    if ((tid & 63) == 0) wave_sum[tid >> 6] = sum;
+    const bool live = __syncthreads_or(any) != 0;
+    sum = 0.0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 64; ++w) sum += wave_sum[w];
+    const double dh = ENT && live ? dh_row : 0.0;
+    const double h = ENT && dh != 0.0 ? static_cast<double>(g.entropies[row]) : 0.0;
+    DenseGrad dense{0.0f, 0.0f, 0.0f};
+    if (live) {
+      const double s = g.row_stats[2 * static_cast<int64_t>(row) + 1];
+      dense.m = g.row_stats[2 * static_cast<int64_t>(row)];
+      dense.a = static_cast<float>(-(sum + (dh != 0.0 ? dh * (h - log(s)) : 0.0)) * sc.inv_t / s);
+      dense.b = static_cast<float>(-dh * M_LN2 * sc.inv_t / s);
+    }
+    const Shape f = row_shape(rd, vocab);
+    const int v0 = chunk * cut.len;
+    const bool last = chunk == cut.chunks - 1;
+    dense_grad<T, ENT>(rx, rd, f, v0, v0 + cut.len, last,
+                       live && !(dense.a == 0.0f && dense.b == 0.0f), dense, sc);
+    __syncthreads();  // before entries of the same places
+    for (int i = tid; live && i < g.n; i += kThreads) {
+      const int id = s_ids[i];
+      if (id < 0 || id >= vocab) continue;
+      const int vec = (id - f.head) / Vec<T>::n;
+      const bool in_body = id >= f.head && vec < f.whole;
+      if (in_body ? vec < v0 || vec >= v0 + cut.len : !last) continue;
+      bool is_first = true;
+      double mine = 0.0;
+      for (int k = 0; k < g.n; ++k) {
+        const bool same = s_ids[k] == id;
+        if (same && k < i) is_first = false;
+        if (same) mine += s_g[k];
+      }
+      if (!is_first) continue;
+      // g (1 - p) of its own share, -p of the others'.
+      const double lp = g.logprobs[at + i], p = exp(lp);
+      double v = mine * -expm1(lp) - (sum - mine) * p;
+      if (ENT && dh != 0.0 && !(lp < -1e30)) v -= dh * p * (lp + h);
+      rd[id] = static_cast<T>(static_cast<float>(v * sc.inv_t));
+    }
+    __syncthreads();
+  }
+}
+
+// --------------------------------------------------------------- workspace
+struct TopnSpace {
+  Part* parts;
+  int* betters;
+  float* groups;
+  size_t bytes;
+};
+
+TopnSpace lay_out_topn(void* base, int64_t rows, int64_t vocab) {
+  size_t chunks = 0, groups = 0;
+  for (const int vec : {Vec<float>::n, Vec<__bf16>::n}) {
+    for (const Cut& cut : {cut_rows(rows, vocab, vec), whole_cut(vocab, vec)}) {
+      chunks = std::max(chunks, static_cast<size_t>(cut.chunks));
+      groups = std::max(groups, static_cast<size_t>(make_groups(cut).per_row));
+    }
+  }
+  char* p = static_cast<char*>(base);
+  size_t at = 0;
+  TopnSpace w;
+  w.parts = reinterpret_cast<Part*>(p + at);
+  at += round256(sizeof(Part) * static_cast<size_t>(rows) * chunks);
+  w.betters = reinterpret_cast<int*>(p + at);
+  at += round256(sizeof(int) * static_cast<size_t>(rows) * chunks);
+  w.groups = reinterpret_cast<float*>(p + at);
+  at += round256(sizeof(float) * static_cast<size_t>(rows) * groups);
+  w.bytes = at;
+  return w;
+}
+
+template <typename T, bool ENT>
+hipError_t topn_t(const TokenRows& t, const TopnOut& o, void* ws, hipStream_t stream) {
+  const Scale sc = make_scale(t.temperature);
+  const TopnSpace w = lay_out_topn(ws, t.rows, t.vocab);
+  const T* x = static_cast<const T*>(t.x);
+  if (whole_rows(t.rows, t.vocab, Vec<T>::n)) {
+    const Cut cut = whole_cut(t.vocab, Vec<T>::n);
+    hipLaunchKernelGGL((topn_whole_kernel<ENT, T>), dim3(grid_of(t.rows)), dim3(kThreads), 0,
+                       stream, x, t.ld, t.rows, t.vocab, t.tokens, sc, cut, make_groups(cut),
+                       w.groups, o);
+    return hipGetLastError();
+  }
+  const Cut cut = cut_rows(t.rows, t.vocab, Vec<T>::n);
+  const Groups gs = make_groups(cut);
+  hipLaunchKernelGGL((topn_stats_kernel<ENT, T>), dim3(grid_of(int64_t{t.rows} * cut.chunks)),
+                     dim3(kThreads), 0, stream, x, t.ld, t.rows, t.vocab, t.tokens, sc, cut, gs,
+                     w.groups, w.parts, w.betters, o.n > 0);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((topn_rows_kernel<ENT, T>), dim3(grid_of(t.rows)), dim3(kThreads), 0, stream,
+                     x, t.ld, t.rows, t.vocab, t.tokens, sc, cut, gs, w.groups, w.parts, w.betters,
+                     o);
+  return hipGetLastError();
+}
+
+template <typename T, bool ENT>
+hipError_t listed_t(const TokenRows& t, const ListedOut& o, void* ws, hipStream_t stream) {
+  const Scale sc = make_scale(t.temperature);
+  const T* x = static_cast<const T*>(t.x);
+  if (whole_rows(t.rows, t.vocab, Vec<T>::n)) {
+    hipLaunchKernelGGL((listed_whole_kernel<ENT, T>), dim3(grid_of(t.rows)), dim3(kThreads), 0,
+                       stream, x, t.ld, t.rows, t.vocab, t.tokens, sc, o);
+    return hipGetLastError();
+  }
+  const Cut cut = cut_rows(t.rows, t.vocab, Vec<T>::n);
+  Part* parts = static_cast<Part*>(ws);
+  hipLaunchKernelGGL((listed_stats_kernel<ENT, T>), dim3(grid_of(int64_t{t.rows} * cut.chunks)),
+                     dim3(kThreads), 0, stream, x, t.ld, t.rows, t.vocab, t.tokens, o.n, sc, cut,
+                     parts);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((listed_rows_kernel<ENT, T>),
+                     dim3(grid_of((t.rows + int64_t{kThreads / 64} - 1) / (kThreads / 64))),
+                     dim3(kThreads), 0, stream, x, t.ld, t.rows, t.vocab, t.tokens, sc, cut, parts,
+                     o);
+  return hipGetLastError();
+}
+
+template <typename T, bool ENT>
+hipError_t listed_backward_t(const TokenRows& t, const ListedGrad& g, const GradRows& d,
+                             hipStream_t stream) {
+  const Scale sc = make_scale(t.temperature);
+  const Cut cut = cut_rows(t.rows, t.vocab, Vec<T>::n);
+  hipLaunchKernelGGL((listed_grad_kernel<T, ENT>), dim3(grid_of(int64_t{t.rows} * cut.chunks)),
+                     dim3(kThreads), 0, stream, static_cast<const T*>(t.x), t.ld, t.rows, t.vocab,
+                     t.tokens, sc, cut, g, static_cast<T*>(d.x), d.ld);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t topn_workspace_size(int64_t rows, int64_t vocab) {
+  return lay_out_topn(nullptr, rows, vocab).bytes;
+}
+
+size_t listed_workspace_size(int64_t rows, int64_t vocab) {
+  const int chunks = std::max(cut_rows(rows, vocab, Vec<float>::n).chunks,
+                              cut_rows(rows, vocab, Vec<__bf16>::n).chunks);
+  return round256(sizeof(Part) * static_cast<size_t>(rows) * chunks);
+}
+
+hipError_t launch_token_logprobs_topn(const TokenRows& t, const TopnOut& o, void* ws,
+                                      hipStream_t stream) {
+  if (t.bf16)
+    return o.entropies ? topn_t<__bf16, true>(t, o, ws, stream)
+                       : topn_t<__bf16, false>(t, o, ws, stream);
+  return o.entropies ? topn_t<float, true>(t, o, ws, stream)
+                     : topn_t<float, false>(t, o, ws, stream);
+}
+
+hipError_t launch_token_logprobs_listed(const TokenRows& t, const ListedOut& o, void* ws,
+                                        hipStream_t stream) {
+  if (t.bf16)
+    return o.entropies ? listed_t<__bf16, true>(t, o, ws, stream)
+                       : listed_t<__bf16, false>(t, o, ws, stream);
+  return o.entropies ? listed_t<float, true>(t, o, ws, stream)
+                     : listed_t<float, false>(t, o, ws, stream);
+}
+
+hipError_t launch_token_logprobs_listed_backward(const TokenRows& t, const ListedGrad& g,
+                                                 const GradRows& d, hipStream_t stream) {
+  if (t.bf16)
+    return g.grad_entropies ? listed_backward_t<__bf16, true>(t, g, d, stream)
+                            : listed_backward_t<__bf16, false>(t, g, d, stream);
+  return g.grad_entropies ? listed_backward_t<float, true>(t, g, d, stream)
+                          : listed_backward_t<float, false>(t, g, d, stream);
+}
+
+}  // namespace ts

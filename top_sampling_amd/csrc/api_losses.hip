@@ -7,6 +7,7 @@
 
 #include <initializer_list>
 
+#include "alternatives.hpp"
 #include "losses.hpp"
 
 namespace {
@@ -32,7 +33,8 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 // The logits, tokens and temperature of a call into t.  rows == 0 passes
 // without looking at the pointers.
 int token_rows(ts::TokenRows& t, const void* logits, int32_t logits_type, int64_t rows,
-               int64_t vocab, int64_t ld_logits, const int32_t* token_ids, double temperature) {
+               int64_t vocab, int64_t ld_logits, const int32_t* token_ids, double temperature,
+               bool needs_tokens = true) {
   if (rows < 0 || vocab < 0)
     return fail(TS_EINVAL, "negative size (rows=%lld vocab=%lld)", (long long)rows,
                 (long long)vocab);
@@ -51,7 +53,7 @@ int token_rows(ts::TokenRows& t, const void* logits, int32_t logits_type, int64_
   if (vocab == 0) return fail(TS_EINVAL, "vocab == 0 with rows > 0");
   if (ld_logits < vocab)
     return fail(TS_EINVAL, "ld_logits %lld < vocab %lld", (long long)ld_logits, (long long)vocab);
-  if (!logits || !token_ids) return fail(TS_EINVAL, "NULL logits/token_ids");
+  if (!logits || (needs_tokens && !token_ids)) return fail(TS_EINVAL, "NULL logits/token_ids");
   if (!aligned(logits, t.bf16 ? 2 : 4) || !aligned(token_ids, 4))
     return fail(TS_EUNSUPPORTED, "logits or token_ids misaligned");
   t.x = logits;
@@ -98,6 +100,12 @@ bool all_aligned4(std::initializer_list<const void*> ps) {
   for (const void* p : ps)
     if (!aligned(p, 4)) return false;
   return true;
+}
+
+int listed_count(int32_t n) {
+  if (n < 1) return fail(TS_EINVAL, "n_listed %d < 1", n);
+  if (n > TS_MAX_LISTED) return fail(TS_EUNSUPPORTED, "n_listed %d above %d", n, TS_MAX_LISTED);
+  return TS_OK;
 }
 
 // Finite and at least 0.
@@ -169,6 +177,93 @@ int token_logprobs_backward_ex(const void* logits, int32_t logits_type, int64_t 
   return hip_status(
       ts::launch_token_logprobs_backward(t, g, d, static_cast<hipStream_t>(stream)),
       "token_logprobs_backward launch");
+}
+
+size_t token_logprobs_topn_workspace_bytes(int64_t rows, int64_t vocab) {
+  if (rows < 0 || vocab < 0 || rows > kMaxDim || vocab > kMaxDim) return 0;
+  return ts::topn_workspace_size(rows, vocab);
+}
+
+int token_logprobs_topn(const void* logits, int32_t logits_type, int64_t rows, int64_t vocab,
+                        int64_t ld_logits, const int32_t* token_ids, double temperature,
+                        int32_t max_logprobs, float* logprobs, int32_t* ranks, float* entropies,
+                        int32_t* topn_ids, float* topn_logprobs, float* row_stats,
+                        int32_t* row_status, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  ts::TokenRows t;
+  int st = token_rows(t, logits, logits_type, rows, vocab, ld_logits, token_ids, temperature,
+                      false);
+  if (st != TS_OK) return st;
+  if (max_logprobs < 0) return fail(TS_EINVAL, "max_logprobs %d < 0", max_logprobs);
+  if (max_logprobs > TS_MAX_LOGPROBS)
+    return fail(TS_EUNSUPPORTED, "max_logprobs %d above %d", max_logprobs, TS_MAX_LOGPROBS);
+  if (rows == 0) return TS_OK;
+  if (token_ids ? !logprobs : (logprobs || ranks))
+    return fail(TS_EINVAL, "logprobs and ranks are those of token_ids: logprobs is needed with "
+                "them, and neither is written without");
+  if (max_logprobs > 0 && (!topn_ids || !topn_logprobs))
+    return fail(TS_EINVAL, "NULL topn_ids/topn_logprobs");
+  if (!all_aligned4({logprobs, ranks, entropies, topn_ids, topn_logprobs, row_stats, row_status}))
+    return fail(TS_EUNSUPPORTED, "misaligned output");
+  st = workspace_ok(workspace, workspace_bytes, token_logprobs_topn_workspace_bytes(rows, vocab));
+  if (st != TS_OK) return st;
+  const ts::TopnOut o{max_logprobs, logprobs,  ranks,     entropies,
+                      topn_ids,     topn_logprobs, row_stats, row_status};
+  return hip_status(
+      ts::launch_token_logprobs_topn(t, o, workspace, static_cast<hipStream_t>(stream)),
+      "token_logprobs_topn launch");
+}
+
+size_t token_logprobs_listed_workspace_bytes(int64_t rows, int64_t vocab) {
+  if (rows < 0 || vocab < 0 || rows > kMaxDim || vocab > kMaxDim) return 0;
+  return ts::listed_workspace_size(rows, vocab);
+}
+
+int token_logprobs_listed(const void* logits, int32_t logits_type, int64_t rows, int64_t vocab,
+                          int64_t ld_logits, const int32_t* listed_ids, int32_t n_listed,
+                          double temperature, float* logprobs, float* entropies, float* row_stats,
+                          int32_t* row_status, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  ts::TokenRows t;
+  int st = token_rows(t, logits, logits_type, rows, vocab, ld_logits, listed_ids, temperature);
+  if (st != TS_OK) return st;
+  st = listed_count(n_listed);
+  if (st != TS_OK || rows == 0) return st;
+  if (!logprobs) return fail(TS_EINVAL, "NULL logprobs");
+  if (!all_aligned4({logprobs, entropies, row_stats, row_status}))
+    return fail(TS_EUNSUPPORTED, "misaligned output");
+  st = workspace_ok(workspace, workspace_bytes, token_logprobs_listed_workspace_bytes(rows, vocab));
+  if (st != TS_OK) return st;
+  const ts::ListedOut o{n_listed, logprobs, entropies, row_stats, row_status};
+  return hip_status(
+      ts::launch_token_logprobs_listed(t, o, workspace, static_cast<hipStream_t>(stream)),
+      "token_logprobs_listed launch");
+}
+
+int token_logprobs_listed_backward(const void* logits, int32_t logits_type, int64_t rows,
+                                   int64_t vocab, int64_t ld_logits, const int32_t* listed_ids,
+                                   int32_t n_listed, double temperature, const float* row_stats,
+                                   const float* logprobs, const float* grad_logprobs,
+                                   const float* entropies, const float* grad_entropies,
+                                   void* grad_logits, int64_t ld_grad, void* stream) {
+  ts::TokenRows t;
+  int st = token_rows(t, logits, logits_type, rows, vocab, ld_logits, listed_ids, temperature);
+  if (st != TS_OK) return st;
+  st = listed_count(n_listed);
+  if (st != TS_OK || rows == 0) return st;
+  if (!row_stats || !logprobs || !grad_logprobs || !grad_logits)
+    return fail(TS_EINVAL, "NULL row_stats/logprobs/grad_logprobs/grad_logits");
+  if (grad_entropies && !entropies)
+    return fail(TS_EINVAL, "grad_entropies needs the forward pass's entropies");
+  if (!all_aligned4({row_stats, logprobs, grad_logprobs, entropies, grad_entropies}))
+    return fail(TS_EUNSUPPORTED, "misaligned input");
+  ts::GradRows d;
+  st = grad_rows(d, t, grad_logits, ld_grad);
+  if (st != TS_OK) return st;
+  const ts::ListedGrad g{n_listed, row_stats, logprobs, grad_logprobs, entropies, grad_entropies};
+  return hip_status(
+      ts::launch_token_logprobs_listed_backward(t, g, d, static_cast<hipStream_t>(stream)),
+      "token_logprobs_listed_backward launch");
 }
 
 int policy_loss(const void* logits, int32_t logits_type, int64_t rows, int64_t vocab,

@@ -221,9 +221,15 @@ struct Slab {
 // A thread's share of vectors [v0, v1) of a row joined into m, s, u; `edge`:
 // also the entries at the row's ends.  The next slab's loads are in flight
 // while a slab is added up.
-template <typename T, bool ENT, int THREADS>
+// `visit` sees every slab's entries (-inf past the row's end) and every edge entry.
+struct NoVisit {
+  static constexpr bool kOn = false;
+};
+
+template <typename T, bool ENT, int THREADS, typename Visit = NoVisit>
 __device__ __forceinline__ void row_stats(const T* row, int vocab, int v0, int v1, bool edge,
-                                          const Scale& sc, float& m, double& s, double& u) {
+                                          const Scale& sc, float& m, double& s, double& u,
+                                          Visit* visit = nullptr) {
   constexpr int VN = Vec<T>::n;
   const int tid = threadIdx.x;
   const Shape f = stats_shape(row, vocab);
@@ -244,11 +250,15 @@ __device__ __forceinline__ void row_stats(const T* row, int vocab, int v0, int v
         for (int e = 0; e < VN; ++e)
           w[j][e] = v + j * THREADS + tid < end ? w[j][e] : -INFINITY;
     }
-    float top = m;
+    float top = Visit::kOn ? -INFINITY : m;
 #pragma unroll
     for (int j = 0; j < kBatch; ++j)
 #pragma unroll
       for (int e = 0; e < VN; e += 2) top = max_nan(max_nan(top, w[j][e]), w[j][e + 1]);
+    if constexpr (Visit::kOn) {
+      visit->slab(v, end, w, top);
+      top = max_nan(m, top);
+    }
     const float ref = top == -INFINITY ? 0.0f : top;
     const float shift = fmaxf(m - ref, sc.floor);
     const double keep = exp_t(shift, sc);
@@ -272,6 +282,7 @@ __device__ __forceinline__ void row_stats(const T* row, int vocab, int v0, int v
   }
   if (edge && tid < f.edge) {
     const float x = static_cast<float>(row[f.template at<T>(tid)]);
+    if constexpr (Visit::kOn) visit->edge(f.template at<T>(tid), x);
     const float top = max_nan(m, x), ref = top == -INFINITY ? 0.0f : top;
     const float shift = fmaxf(m - ref, sc.floor), k = log2_t(x - ref, sc);
     const double keep = exp_t(shift, sc), ex = __builtin_amdgcn_exp2f(k);
