@@ -249,7 +249,7 @@ int lmhead_logits_local_e4m3(const void* hidden, const float* hidden_scales, int
  *                   (bytes), any alignment
  *   logits          fp32 [rows, vocab_local], leading dimension ld_logits
  * Requirements (else TS_EUNSUPPORTED): hidden_dim a multiple of 32, ld_hidden of
- * 8, ld_lm_head of 16, hidden and lm_head 16-byte aligned, logits 4-byte aligned,
+ * 8 and up to 2^21, ld_lm_head of 16, hidden and lm_head 16-byte aligned, logits 4-byte aligned,
  * vocab_local up to 2^31 - 1024, and no more than 2^22 - 1 tiles of 64 x 256
  * logits.  Other errors and the empty cases as for lmhead_logits_local.
  */

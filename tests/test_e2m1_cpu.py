@@ -86,7 +86,7 @@ def _project(**kw):
     (dict(h=0), ts.TS_EINVAL), (dict(x=None), ts.TS_EINVAL), (dict(w=None), ts.TS_EINVAL),
     (dict(ws=None), ts.TS_EINVAL), (dict(out=None), ts.TS_EINVAL), (dict(ldx=248), ts.TS_EINVAL),
     (dict(ldw=112), ts.TS_EINVAL), (dict(lds=7), ts.TS_EINVAL), (dict(ldo=63), ts.TS_EINVAL),
-    (dict(h=240, ldx=256), ts.TS_EUNSUPPORTED), (dict(ldx=260), ts.TS_EUNSUPPORTED),
+    (dict(ldx=(1 << 21) + 8), ts.TS_EUNSUPPORTED), (dict(h=240, ldx=256), ts.TS_EUNSUPPORTED), (dict(ldx=260), ts.TS_EUNSUPPORTED),
     (dict(ldw=136), ts.TS_EUNSUPPORTED), (dict(x=FAKE + 8), ts.TS_EUNSUPPORTED),
     (dict(w=FAKE + 4), ts.TS_EUNSUPPORTED), (dict(out=FAKE + 2), ts.TS_EUNSUPPORTED),
     (dict(vocab=(1 << 31) - 1023, ldo=1 << 31), ts.TS_EUNSUPPORTED),

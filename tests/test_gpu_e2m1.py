@@ -132,7 +132,10 @@ def test_quantize_strides(dtype):
 # ------------------------------------------------------------- projection
 SHAPES = [(1, 32, 1), (1, 4096, 531), (2, 64, 33), (5, 2560, 257), (15, 96, 300), (16, 8192, 95),
           (17, 544, 129), (31, 4128, 70), (32, 256, 1000), (33, 1024, 260), (64, 160, 511),
-          (65, 96, 257), (130, 2592, 300), (300, 64, 513), (321, 320, 258), (7, 8224, 40)]
+          (65, 96, 257), (130, 2592, 300), (300, 64, 513), (321, 320, 258), (7, 8224, 40),
+          # one to four parts of a row, whole and not, and several tiles a workgroup
+          (64, 6144, 300), (45, 4640, 133), (20, 9216, 77), (9, 10240, 50), (3, 1024, 70),
+          (30, 512, 9001), (64, 2048, 9001), (48, 4096, 4500), (16, 1536, 17000), (33, 8192, 4200)]
 
 
 def _codes(rows, cols, gen, low=120, high=135):
@@ -144,7 +147,7 @@ def _codes(rows, cols, gen, low=120, high=135):
 @pytest.mark.parametrize("rows,h,vocab", SHAPES)
 def test_projection_whole_numbers(rows, h, vocab, tile):
     """Hidden entries 0, +-1, +-2 and scales 1 and 2: twice every partial sum is
-    a whole number of at most 8224 * 2 * 12 * 2 < 2^24."""
+    a whole number of at most 10240 * 2 * 12 * 2 < 2^24."""
     gen = torch.Generator().manual_seed(rows * h + vocab)
     w, s = _codes(vocab, h, gen, 127, 129)
     x = torch.randint(-2, 3, (rows, h), generator=gen).to(torch.bfloat16).cuda()

@@ -108,6 +108,9 @@ int lmhead_logits_local_e2m1(const void* hidden, int64_t rows, int64_t hidden_di
   if (hidden_dim % ts::kE2m1Group)
     return fail(TS_EUNSUPPORTED, "hidden_dim %lld is no multiple of %d", (long long)hidden_dim,
                 ts::kE2m1Group);
+  if (ld_hidden > ts::kE2m1MaxLdHidden)
+    return fail(TS_EUNSUPPORTED, "ld_hidden %lld above %lld", (long long)ld_hidden,
+                (long long)ts::kE2m1MaxLdHidden);
   if (ld_hidden % 8 || ld_lm_head % 16)
     return fail(TS_EUNSUPPORTED, "ld_hidden must be a multiple of 8 elements, ld_lm_head of 16 "
                 "bytes");

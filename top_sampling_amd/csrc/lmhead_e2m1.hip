@@ -16,6 +16,8 @@
 // sums differ from the definition.
 #include <stdlib.h>
 
+#include <algorithm>
+
 #include "lmhead_e2m1.hpp"
 #include "tile_store.hpp"
 
@@ -27,12 +29,14 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 typedef uint16_t u16x8u __attribute__((ext_vector_type(8), aligned(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(1)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kXcds = 8;
+constexpr int kCus = 256;
 
 // The scale of a byte, as the conversions take it: they read the exponent
 // alone, so 0 is 2^-127 and 255 NaN.
@@ -164,162 +168,334 @@ __device__ __forceinline__ bf16x8 frag_of(uint32_t w, float s) {
 }
 
 // --------------------------------------------------------------- few rows
-// Up to 16 NT rows: bound by the lm_head's bytes, each read once.  A wave keeps
-// its share of every hidden row in registers (NS steps of 128 entries) and the
-// workgroup's waves take the row's shares side by side; then the workgroup goes
-// through the lm_head, 16 VT rows at a time.  A lane loads 16 bytes of codes,
-// which is one group: lane l has row l % 16, groups 4 s + l / 16.  In
-// v_mfma_f32_16x16x32_bf16 lane l holds entries 8 (l / 16) .. + 7 of a slice of
+// Up to 16 NT rows: bound by the lm_head's bytes, so nothing else may hold their
+// loads up.  A wave keeps its share of every hidden row in registers (NS steps of
+// 128 entries) and the workgroup's waves have the row's shares side by side; then
+// the workgroup goes through the lm_head, 16 VT rows (a tile) at a time, with the
+// loads of AHEAD tiles on their way.  A lane's 16 bytes of codes are one group: lane
+// l has row l % 16, groups 4 s + l / 16, and a load has 64 bytes of each of 16 rows.
+// In v_mfma_f32_16x16x32_bf16 lane l holds entries 8 (l / 16) .. + 7 of a slice of
 // 32; any order of the sum's entries will do as long as both operands share it,
 // so slice i takes the i-th eight entries of each lane's group.  The shares are
-// added up through LDS, in a fixed order.
+// added up through LDS, in a fixed order, by one wave while the others go on.
+// Where the waves' shares are not the whole row, the lm_head is gone through again
+// for each further part of it, and the sums so far come back from the logits.
+// Bound by the lm_head's loads: 1 x 4,096 x 151,936 takes 57 us (5.8 TB/s), 16 rows
+// 68, 32 rows 78.  Reading the same bytes in this pattern and nothing else takes 53;
+// the scales' loads 3 to 9 of it, the waves' meeting for a tile about 10.  Measured and
+// dropped: one tile's loads on their way only (82 us), scales byte by byte (+8), loads
+// past the caches (+10: a row's line is asked for twice), every wave at every sum
+// (+2), the hidden rows in LDS and whole rows a wave (73 us, 16 rows 76).
 constexpr int kStep = 128;  // entries of a row in one step
-constexpr int kMaxWaves = 16;
+constexpr int kFewWaves = 8;
 
-template <int NT, int NS, int VT, int MAX_WAVES>
-__global__ __launch_bounds__(64 * MAX_WAVES) void lmhead_e2m1_few_kernel(
-    const uint16_t* __restrict__ X, int64_t ldx, E2m1Rows w, float* __restrict__ C, int64_t ldc,
-    int M, int N, int K, int tiles) {
-  constexpr int BV = 16 * VT;
-  extern __shared__ float part[];  // [2][waves][16 NT][BV]
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
+// Waits for the wave's LDS writes and then for the other waves, but not for loads
+// on their way, as __syncthreads() would.
+__device__ __forceinline__ void wait_lds() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt 0; vmcnt and expcnt at their maxima
+  asm volatile("s_barrier" ::: "memory");
+}
+
+// Register i of lane row k (lanes 16 k .. 16 k + 15) and register k of lane row i
+// change places.
+__device__ __forceinline__ void turn_4x4(u32x4 (&c)[4]) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    auto swap32 = [&](int a, int b) {
+      const auto v = __builtin_amdgcn_permlane32_swap(c[a][d], c[b][d], false, false);
+      c[a][d] = v[0];
+      c[b][d] = v[1];
+    };
+    auto swap16 = [&](int a, int b) {
+      const auto v = __builtin_amdgcn_permlane16_swap(c[a][d], c[b][d], false, false);
+      c[a][d] = v[0];
+      c[b][d] = v[1];
+    };
+    swap32(0, 2);
+    swap32(1, 3);
+    swap16(0, 1);
+    swap16(2, 3);
+  }
+}
+
+// WHOLE: the waves' shares of the row's parts are all whole.  PARTS: there is more
+// than one.
+template <int NT, int NS, int VT, int AHEAD, bool WHOLE, bool PARTS>
+__global__ __launch_bounds__(64 * kFewWaves, 2) void lmhead_e2m1_few_kernel(
+    const uint16_t* __restrict__ X, int64_t ldx, E2m1Rows w, float* C, int64_t ldc, int M, int N,
+    int K, int tiles, int parts, int vec_out) {
+  constexpr int BV = 16 * VT, BV4 = BV / 4;
+  constexpr int GROUPS = 4 * NS;  // of a wave's share
+  extern __shared__ float shares[];  // [2][waves][16 NT][BV]
+  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, q = lane >> 4;
   const int groups = K / kE2m1Group;
+  typedef uint32_t Words __attribute__((ext_vector_type(NS)));
+  typedef uint32_t WordsU __attribute__((ext_vector_type(NS), aligned(1)));
 
-  // Hidden rows r16 + 16 n, the entries of this lane's groups.
-  bf16x8 x[NT][NS][4];
-  bool live[NS];
-#pragma unroll
-  for (int s = 0; s < NS; ++s) {
-    const int g = (wave * NS + s) * 4 + q;
-    live[s] = g < groups;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int r = r16 + 16 * n;
-      const uint16_t* p = X + static_cast<int64_t>(min(r, M - 1)) * ldx + min(g, groups - 1) * 32;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[n][s][i] = *reinterpret_cast<const bf16x8*>(p + 8 * i);
-        if (r >= M || g >= groups) x[n][s][i] = bf16x8{};
-      }
-    }
-  }
-
-  u32x4 code[VT][NS];
-  uint32_t scale[VT][NS];
-  auto load = [&](int tile) {
-#pragma unroll
-    for (int t = 0; t < VT; ++t) {
-      const int64_t v = min(tile * BV + t * 16 + r16, N - 1);
-      const uint8_t* pc = w.codes + v * w.ld;
-      const uint8_t* ps = w.scales + v * w.ld_scales;
-#pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        const int g = min((wave * NS + s) * 4 + q, groups - 1);
-        code[t][s] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(pc + g * 16));
-        scale[t][s] = ps[g];
-      }
-    }
+  // A tile's codes and the scales of the wave's groups: where the row has all of
+  // them (WHOLE) a row's, otherwise those of the lane's own groups, byte by byte
+  // (past the row's end another's, which meet zeros, and must not be NaN).  And the
+  // lane's sums of the parts before.
+  struct Tile {
+    u32x4 code[VT][NS];
+    Words scale[VT];
+    f32x4 before;
   };
-
-  int tile = blockIdx.x;
-  if (tile < tiles) load(tile);
-  float* mine = part + wave * (16 * NT * BV);
+  const int step = gridDim.x;
+  const int first = blockIdx.x, last = first + (tiles - 1 - first) / step * step;
+  float* mine = shares + wave * (16 * NT * BV);
   const int half = waves * 16 * NT * BV;
   int buf = 0;
-  for (; tile < tiles; tile += gridDim.x) {
-    f32x4 acc[VT][NT];
+
+  for (int part = 0; part < parts; ++part) {
+    const int g0 = (part * waves + wave) * GROUPS;  // the wave's first group
+    // Hidden rows r16 + 16 n, the entries of this lane's groups.  Loaded as a group
+    // a load, its four chunks in the four lanes of a row, and turned: with a lane's
+    // own group in four loads each of them has 64 pieces of 16 bytes.
+    bf16x8 x[NT][NS][4];
 #pragma unroll
-    for (int t = 0; t < VT; ++t)
+    for (int s = 0; s < NS; ++s) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) acc[t][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int n = 0; n < NT; ++n) {
+        const int r = r16 + 16 * n;
+        const uint16_t* p = X + static_cast<int64_t>(min(r, M - 1)) * ldx + 8 * q;
+        u32x4 c[4];
 #pragma unroll
-    for (int t = 0; t < VT; ++t)
-#pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        // A group past the row has zeros on the other side, and must not be NaN.
-        const float sc = live[s] ? scale_of(scale[t][s]) : 1.0f;
+        for (int i = 0; i < 4; ++i)
+          c[i] = *reinterpret_cast<const u32x4*>(p + min(g0 + 4 * s + i, groups - 1) * 32);
+        turn_4x4(c);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const bf16x8 a = frag_of(code[t][s][i], sc);
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            acc[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, x[n][s][i], acc[t][n], 0, 0, 0);
+          x[n][s][i] = __builtin_bit_cast(bf16x8, c[i]);
+          if (r >= M || g0 + 4 * s + q >= groups) x[n][s][i] = bf16x8{};
         }
       }
-    if (tile + static_cast<int>(gridDim.x) < tiles) load(tile + gridDim.x);
-    // Lane l holds lm_head rows 4 q .. 4 q + 3 of hidden row l % 16.
-#pragma unroll
-    for (int t = 0; t < VT; ++t)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        if (r16 + 16 * n < M)
-          *reinterpret_cast<f32x4*>(mine + buf * half + (r16 + 16 * n) * BV + t * 16 + 4 * q) =
-              acc[t][n];
-    __syncthreads();
-    for (int i = tid; i < M * BV; i += blockDim.x) {
-      const int r = i / BV, c = i % BV;
-      const float* p = part + buf * half + i;
-      float sum = p[0];
-      for (int k = 1; k < waves; ++k) sum += p[k * (16 * NT * BV)];
-      if (tile * BV + c < N) C[static_cast<int64_t>(r) * ldc + tile * BV + c] = sum;
     }
-    buf ^= 1;
+
+    // Entry i of a tile's M x BV4 quadruples of logits is added up by this lane.
+    auto place = [&](int turn) {
+      const int w_at = wave - turn;
+      return (w_at < 0 ? w_at + waves : w_at) * 64 + lane;
+    };
+    auto load = [&](int tile, int turn, Tile& to) __attribute__((always_inline)) {
+#pragma unroll
+      for (int t = 0; t < VT; ++t) {
+        const int64_t v = min(tile * BV + t * 16 + r16, N - 1);
+        const uint8_t* pc = w.codes + v * w.ld;
+        const uint8_t* ps = w.scales + v * w.ld_scales;
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          const int g = min(g0 + 4 * s + q, groups - 1);
+          to.code[t][s] = *reinterpret_cast<const u32x4*>(pc + g * 16);
+          if (!WHOLE) to.scale[t][s] = ps[g];
+        }
+        if (WHOLE) to.scale[t] = *reinterpret_cast<const WordsU*>(ps + g0);
+      }
+      if (PARTS) {
+        const int i = place(turn), r = i / BV4;
+        const int64_t col = static_cast<int64_t>(tile) * BV + i % BV4 * 4;
+        to.before = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (part > 0 && r < M) {
+          const float* from = C + static_cast<int64_t>(r) * ldc + col;
+          if (vec_out && col + 3 < N) {
+            to.before = *reinterpret_cast<const f32x4*>(from);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (col + e < N) to.before[e] = from[e];
+          }
+        }
+      }
+    };
+    auto scale_at = [&](const Tile& from, int t, int s) {
+      if (WHOLE) return scale_of(from.scale[t][s] >> (8 * q) & 255u);
+      return g0 + 4 * s + q < groups ? scale_of(from.scale[t][s]) : 1.0f;
+    };
+    auto take = [&](int tile, int turn, const Tile& from) __attribute__((always_inline)) {
+      f32x4 acc[VT][NT];
+#pragma unroll
+      for (int t = 0; t < VT; ++t)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[t][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int t = 0; t < VT; ++t)
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          const float sc = scale_at(from, t, s);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bf16x8 a = frag_of(from.code[t][s][i], sc);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              acc[t][n] =
+                  __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, x[n][s][i], acc[t][n], 0, 0, 0);
+          }
+        }
+      // Lane l holds lm_head rows 4 q .. 4 q + 3 of hidden row l % 16.
+#pragma unroll
+      for (int t = 0; t < VT; ++t)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          if (r16 + 16 * n < M)
+            *reinterpret_cast<f32x4*>(mine + buf * half + (r16 + 16 * n) * BV + t * 16 + 4 * q) =
+                acc[t][n];
+      wait_lds();
+      for (int i = place(turn); i < M * BV4; i += 64 * waves) {
+        const int r = i / BV4, c = i % BV4 * 4;
+        const float* p = shares + buf * half + r * BV + c;
+        f32x4 sum = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll
+        for (int k = 1; k < kFewWaves; ++k)
+          if (k < waves) sum += *reinterpret_cast<const f32x4*>(p + k * (16 * NT * BV));
+        if (PARTS) sum += from.before;
+        const int64_t col = static_cast<int64_t>(tile) * BV + c;
+        float* to = C + static_cast<int64_t>(r) * ldc + col;
+        if (vec_out && col + 3 < N) {
+          *reinterpret_cast<f32x4*>(to) = sum;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (col + e < N) to[e] = sum[e];
+        }
+      }
+      buf ^= 1;
+    };
+
+    // Past the last tile its loads are made again, so that the waits can count on
+    // them.
+    Tile ring[AHEAD + 1];
+    int tile = first, turn = 0;
+    auto wrap = [&](int t) { return t >= waves ? t % waves : t; };
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) load(min(tile + u * step, last), wrap(u), ring[u]);
+    for (bool more = true; more;) {
+#pragma unroll
+      for (int u = 0; u <= AHEAD; ++u) {
+        load(min(tile + AHEAD * step, last), wrap(turn + AHEAD), ring[(u + AHEAD) % (AHEAD + 1)]);
+        take(tile, turn, ring[u]);
+        tile += step;
+        turn = wrap(turn + 1);
+        more = tile < tiles;
+        if (!more) break;
+      }
+    }
+    // The next part reads these logits back, in other waves.
+    if (PARTS && part + 1 < parts) {
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+    }
+  }
+}
+
+// ------------------------------------------------------- tiles of rows
+constexpr int kBK = 64;
+
+// The hidden rows' direct loads are buffer loads: behind global ones, which the
+// compiler counts as flat, it would wait for every register load at once.  (A
+// plain function: the host pass does not emit the kernel stub when the builtin
+// sits in a lambda.)
+__device__ __forceinline__ void hidden_to_lds(__amdgpu_buffer_rsrc_t rows, uint8_t* to, int at) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rows, to, 16, at, 0, 0, 0);
+}
+
+template <int LOADS, int NW>
+__device__ __forceinline__ void issue_hidden(__amdgpu_buffer_rsrc_t rows, const int* at,
+                                             const int* back, uint8_t* stage, int wave, int k0,
+                                             bool half) {
+#pragma unroll
+  for (int q = 0; q < LOADS; ++q)
+    hidden_to_lds(rows, stage + (wave + NW * q) * 1024,
+                  (half ? at[q] - back[q] : at[q]) + 2 * k0);
+}
+
+// Waits until at most N of the wave's loads are on their way and its LDS reads
+// are done, then for the other waves; a fence would wait for the later steps'
+// loads as well.
+template <int N>
+__device__ __forceinline__ void wait_stage() {
+  static_assert(N < 64, "vmcnt has six bits");
+  asm volatile("" ::: "memory");
+  // vmcnt in bits 3:0 and 15:14, lgkmcnt 0, expcnt left at its maximum.
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);
+  asm volatile("s_barrier" ::: "memory");
+}
+
+// A wave's accumulator blocks to C; `lds` is free.
+template <int TM, int TN>
+__device__ __forceinline__ void store_output(const f32x16 (&acc)[TM][TN], uint8_t* lds, int wave,
+                                             int lane, float* __restrict__ C, int64_t ldc,
+                                             int row0, int col0, int M, int N, int vec_out) {
+  if (vec_out) {
+    store_tile_rows<false>(acc, reinterpret_cast<float*>(lds), wave, lane, C, ldc, row0, col0, M,
+                           N, nullptr, nullptr);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const int col = col0 + j * 32 + (lane & 31);
+      if (col >= N) continue;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int row = row0 + i * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
+        if (row < M) C[static_cast<int64_t>(row) * ldc + col] = acc[i][j][e];
+      }
+    }
   }
 }
 
 // -------------------------------------------------------------- many rows
-// BM x BN tiles, K in steps of 64.  The hidden rows go through double-buffered
-// LDS as in the bf16 kernel (rows of 128 bytes, 16-byte chunks swizzled by the
-// row pair); the lm_head goes straight into registers, 16 bytes a lane, which is
-// one group: lane l has row l % 32 and the step's group l / 32.  Slice i of a
-// step takes the i-th eight entries of each lane's group, so its hidden
-// fragment is chunk 4 (l / 32) + i.
-constexpr int kBK = 64;
-
-template <int LOADS, int NW>
-__device__ __forceinline__ void issue_hidden(const uint16_t* const* src, uint8_t* stage, int wave,
-                                             int k0) {
-#pragma unroll
-  for (int q = 0; q < LOADS; ++q)
-    __builtin_amdgcn_global_load_lds(src[q] + k0, stage + (wave + NW * q) * 1024, 16, 0, 0);
-}
-
-template <int BM, int BN, int WAVES_M, int WAVES_N>
-__global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void lmhead_e2m1_kernel(
+// BM x BN tiles, K in steps of 64.  The hidden rows go through a ring of AHEAD + 1
+// LDS stages (rows of 128 bytes, 16-byte chunks swizzled by the row pair); the
+// lm_head goes straight into registers, AHEAD steps ahead too, 16 bytes a lane,
+// which is one group: lane l has row l % 32 and the step's group l / 32.  Slice i
+// of a step takes the i-th eight entries of each lane's group, so its hidden
+// fragment is chunk 4 (l / 32) + i.  A wave has all of the tile's hidden rows, so the
+// conversions (four instructions a fragment, two to five products) are made once.
+// Bound by the matrix cores: 640 x 4,096 x 151,936 takes 682 us (1.17 PFLOP/s; the
+// bf16 projection 720).  Few row tiles are bound by what a step waits for: a load of
+// codes has 32 bytes of each of 32 rows, and the line's other pieces have to outlive
+// the step in the caches (64 rows past the caches: 262 us, through them 164).
+template <int BM, int BN, int NW, int AHEAD>
+__global__ __launch_bounds__(64 * NW, 2) void lmhead_e2m1_tiles_kernel(
     const uint16_t* __restrict__ X, int64_t ldx, E2m1Rows w, float* __restrict__ C, int64_t ldc,
     int M, int N, int K, int tiles_m, int tiles_total, int tiles_per_xcd, int vec_out) {
-  constexpr int NW = WAVES_M * WAVES_N;
-  constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
-  constexpr int TM = WM / 32, TN = WN / 32;
+  constexpr int WN = BN / NW;
+  constexpr int TM = BM / 32, TN = WN / 32;
+  constexpr int RING = AHEAD + 1;
   constexpr int STAGE = BM * 128;
-  constexpr int LOADS = BM / 8 / NW;
+  constexpr int A_LOADS = BM / 8 / NW;
+  constexpr int W_LOADS = 2 * TN;  // codes and scales
   constexpr int SCRATCH = NW * kTileStoreFloats * 4;
   static_assert(BM / 8 % NW == 0, "blocks must split evenly over the waves");
-  static_assert(WM % 32 == 0 && WN % 32 == 0, "wave tile of whole 32x32 blocks");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE > SCRATCH ? 2 * STAGE : SCRATCH];
+  static_assert(BM % 32 == 0 && WN % 32 == 0, "wave tile of whole 32x32 blocks");
+  __shared__ __attribute__((
+      aligned(1024))) uint8_t lds[RING * STAGE > SCRATCH ? RING * STAGE : SCRATCH];
 
   const int bid = blockIdx.x;
   const int tile = (bid % kXcds) * tiles_per_xcd + bid / kXcds;
   if (tile >= tiles_total) return;
   const int m0 = tile % tiles_m * BM, n0 = tile / tiles_m * BN;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm0 = (wave / WAVES_N) * WM, wn0 = (wave % WAVES_N) * WN;
+  const int wn0 = wave * WN;
   const int frow = lane & 31, fhalf = lane >> 5;
 
-  const int steps = (K + kBK - 1) / kBK;
-  // A last step of one group only: the other half of each LDS row repeats it
-  // and meets zeros.
-  const bool half_step = K % kBK != 0;
-  const uint16_t* src[LOADS];
-  const uint16_t* src_half[LOADS];
+  const int steps = (K + kBK - 1) / kBK, full_steps = K / kBK;
+  // A last step of one group: the other half of each LDS row repeats it and
+  // meets zeros.
+  const __amdgpu_buffer_rsrc_t hidden = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint16_t*>(X + static_cast<int64_t>(m0) * ldx), 0, -1, 0x00020000);
+  int at[A_LOADS], back[A_LOADS];  // bytes
 #pragma unroll
-  for (int q = 0; q < LOADS; ++q) {
+  for (int q = 0; q < A_LOADS; ++q) {
     const int row = 8 * (wave + NW * q) + (lane >> 3);
     const int c = (lane & 7) ^ ((row >> 1) & 7);
-    const uint16_t* p = X + static_cast<int64_t>(min(m0 + row, M - 1)) * ldx;
-    src[q] = p + c * 8;
-    src_half[q] = p + (c & 3) * 8;
+    at[q] = static_cast<int>(min(row, M - 1 - m0) * static_cast<int>(ldx)) * 2 + c * 16;
+    back[q] = c >= 4 ? 64 : 0;
   }
   const uint8_t* wp[TN];
   const uint8_t* sp[TN];
@@ -342,49 +518,41 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void lmhead_e2m1_kernel(
   int aoff[TM], aswz[TM];
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int r = wm0 + i * 32 + frow;
+    const int r = i * 32 + frow;
     aoff[i] = r * 128;
     aswz[i] = (r >> 1) & 7;
   }
 
-  u32x4 code[TN];
-  uint32_t scale[TN];
-  auto load_w = [&](int ks) {
+  u32x4 code[RING][TN];
+  uint32_t scale[RING][TN];
+  // The loads of a step, in an order that the waits count on: the hidden rows
+  // first, then codes and scales, and none across the ends.
+  auto load_step = [&](int ks, int slot) __attribute__((always_inline)) {
+    ks = min(ks, steps - 1);
+    __builtin_amdgcn_sched_barrier(0);
+    issue_hidden<A_LOADS, NW>(hidden, at, back, lds + slot * STAGE, wave, ks * kBK, ks >= full_steps);
+    __builtin_amdgcn_sched_barrier(0);
     const int g = min(2 * ks + fhalf, groups - 1);
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      code[j] = *reinterpret_cast<const u32x4*>(wp[j] + g * 16);
-      scale[j] = sp[j][g];
+      code[slot][j] = *reinterpret_cast<const u32x4*>(wp[j] + g * 16);
+      scale[slot][j] = sp[j][g];
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
-
-  issue_hidden<LOADS, NW>(steps == 1 && half_step ? src_half : src, lds, wave, 0);
-  load_w(0);
-  for (int ks = 0; ks < steps; ++ks) {
-    const int cur = ks & 1;
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
+  auto multiply = [&](int slot, bool half) __attribute__((always_inline)) {
+    const uint8_t* base = lds + slot * STAGE;
     u32x4 now[TN];
     float sc[TN];
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      now[j] = code[j];
-      sc[j] = scale_of(scale[j]);
-    }
-    const bool last_half = half_step && ks == steps - 1;
-    if (last_half && fhalf) {
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
+      now[j] = code[slot][j];
+      sc[j] = scale_of(scale[slot][j]);
+      if (half && fhalf) {
         now[j] = u32x4{0, 0, 0, 0};
         sc[j] = 1.0f;
       }
     }
-    if (ks + 1 < steps) {
-      issue_hidden<LOADS, NW>(half_step && ks + 2 == steps ? src_half : src,
-                              lds + (cur ^ 1) * STAGE, wave, (ks + 1) * kBK);
-      load_w(ks + 1);
-    }
-    const uint8_t* base = lds + cur * STAGE;
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
       const int chunk = 4 * fhalf + kk;
@@ -392,8 +560,7 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void lmhead_e2m1_kernel(
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
         af[i] = *reinterpret_cast<const bf16x8*>(base + aoff[i] + ((chunk ^ aswz[i]) << 4));
-        // 0 x inf is not 0.
-        if (last_half && fhalf) af[i] = bf16x8{};
+        if (half && fhalf) af[i] = bf16x8{};  // 0 x inf is not 0
       }
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
@@ -403,27 +570,33 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void lmhead_e2m1_kernel(
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[i], b, acc[i][j], 0, 0, 0);
       }
     }
-  }
+  };
 
-  __syncthreads();  // every wave is done reading the stages
-  if (vec_out) {
-    store_tile_rows<false>(acc, reinterpret_cast<float*>(lds), wave, lane, C, ldc, m0 + wm0,
-                           n0 + wn0, M, N, nullptr, nullptr);
-    return;
-  }
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
+  for (int u = 0; u < AHEAD; ++u) load_step(u, u);
+  int ks = 0;
+  for (; ks + RING <= full_steps; ks += RING) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const int col = n0 + wn0 + j * 32 + frow;
-      if (col >= N) continue;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int row = m0 + wm0 + i * 32 + 8 * (e >> 2) + 4 * fhalf + (e & 3);
-        if (row < M) C[static_cast<int64_t>(row) * ldc + col] = acc[i][j][e];
-      }
+    for (int u = 0; u < RING; ++u) {
+      // Behind the step's hidden rows: its codes and scales, and AHEAD - 1 steps.
+      wait_stage<W_LOADS + (AHEAD - 1) * (A_LOADS + W_LOADS)>();
+      load_step(ks + u + AHEAD, (u + AHEAD) % RING);
+      multiply(u, false);
     }
   }
+  const int rest = steps - ks;  // at most RING: their loads are on their way but for the last's
+#pragma unroll
+  for (int u = 0; u < RING; ++u) {
+    if (u < rest) {
+      wait_stage<0>();
+      if (u == 0) load_step(ks + AHEAD, AHEAD % RING);
+      multiply(u, ks + u >= full_steps);
+    }
+  }
+
+  // The loads past the last step have landed too, and every wave is done reading.
+  wait_stage<0>();
+  store_output<TM, TN>(acc, lds, wave, lane, C, ldc, m0, n0 + wn0, M, N, vec_out);
 }
 
 int unit_grid(int rows, int cols) {
@@ -440,27 +613,77 @@ struct Projection {
   int rows, vocab, hidden_dim;
 };
 
-template <int NT, int NS, int VT, int MAX_WAVES>
-hipError_t launch_few(const Projection& p, int waves, hipStream_t stream) {
+template <int NT, int NS, int VT, int AHEAD>
+hipError_t launch_few(const Projection& p, hipStream_t stream) {
+  const int shares = (p.hidden_dim - 1) / (NS * kStep) + 1;
+  const int parts = (shares - 1) / kFewWaves + 1, waves = (shares - 1) / parts + 1;
   const int tiles = (p.vocab - 1) / (16 * VT) + 1;
   const int lds = 2 * waves * 16 * NT * 16 * VT * 4;
-  const int grid = tiles < 512 ? tiles : 512;
-  hipLaunchKernelGGL((lmhead_e2m1_few_kernel<NT, NS, VT, MAX_WAVES>), dim3(grid), dim3(64 * waves), lds,
-                     stream, p.hidden, p.ld_hidden, p.w, p.logits, p.ld_logits, p.rows, p.vocab,
-                     p.hidden_dim, tiles);
-  return hipGetLastError();
+  const bool whole = p.hidden_dim == parts * waves * NS * kStep;
+  auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(std::min(tiles, kCus)), dim3(64 * waves), lds, stream, p.hidden,
+                       p.ld_hidden, p.w, p.logits, p.ld_logits, p.rows, p.vocab, p.hidden_dim,
+                       tiles, parts, rows_take_vector_stores(p.logits, p.ld_logits));
+    return hipGetLastError();
+  };
+  if (parts > 1)
+    return whole ? launch(lmhead_e2m1_few_kernel<NT, NS, VT, AHEAD, true, true>)
+                 : launch(lmhead_e2m1_few_kernel<NT, NS, VT, AHEAD, false, true>);
+  return whole ? launch(lmhead_e2m1_few_kernel<NT, NS, VT, AHEAD, true, false>)
+               : launch(lmhead_e2m1_few_kernel<NT, NS, VT, AHEAD, false, false>);
 }
 
-template <int BM, int BN, int WAVES_M, int WAVES_N>
+template <int BM, int BN, int NW, int AHEAD>
 hipError_t launch_tiles(const Projection& p, hipStream_t stream) {
   const int tiles_m = (p.rows - 1) / BM + 1, tiles_n = (p.vocab - 1) / BN + 1;
   const int total = tiles_m * tiles_n;
   const int per_xcd = (total + kXcds - 1) / kXcds;
-  hipLaunchKernelGGL((lmhead_e2m1_kernel<BM, BN, WAVES_M, WAVES_N>), dim3(per_xcd * kXcds),
-                     dim3(64 * WAVES_M * WAVES_N), 0, stream, p.hidden, p.ld_hidden, p.w, p.logits,
-                     p.ld_logits, p.rows, p.vocab, p.hidden_dim, tiles_m, total, per_xcd,
+  hipLaunchKernelGGL((lmhead_e2m1_tiles_kernel<BM, BN, NW, AHEAD>), dim3(per_xcd * kXcds),
+                     dim3(64 * NW), 0, stream, p.hidden, p.ld_hidden, p.w, p.logits, p.ld_logits,
+                     p.rows, p.vocab, p.hidden_dim, tiles_m, total, per_xcd,
                      rows_take_vector_stores(p.logits, p.ld_logits));
   return hipGetLastError();
+}
+
+constexpr int kFewRows = 64;
+
+// Shares of 512 entries a wave, of 256 where the row is short or the hidden rows
+// many, of 1,024 where a row would take two parts.  Two tiles of rows at once where
+// the row has few shares: 5 x 2,560 x 31,037 10.9 us, one 12.4; 1 x 2,560 x 248,320
+// 58 and 64; 1 x 4,096 x 151,936 61 and 57.  Four of short rows: 4 x 256 x 100,000
+// 9.5, shares of 512 14.6; 16 x 1,024 x 100,000 16.8 and 17.2; 32 x 256 x 100,000 17
+// and 22.  Rows of 8,192, 4 x 100,000: 85 us at once, 103 in two parts.
+hipError_t launch_few_rows(const Projection& p, hipStream_t stream) {
+  const int k = p.hidden_dim;
+  if (p.rows <= 16) {
+    if (k <= 1024) return launch_few<1, 2, 4, 1>(p, stream);
+    if (k <= 7 * 512) return launch_few<1, 4, 2, 1>(p, stream);
+    return k <= 8 * 512 ? launch_few<1, 4, 1, 2>(p, stream) : launch_few<1, 8, 1, 1>(p, stream);
+  }
+  if (p.rows <= 32)
+    return k <= 1024 ? launch_few<2, 2, 2, 2>(p, stream) : launch_few<2, 4, 1, 2>(p, stream);
+  return p.rows <= 48 ? launch_few<3, 2, 2, 1>(p, stream) : launch_few<4, 2, 1, 3>(p, stream);
+}
+
+// The kernel for few rows up to 32 of them, and up to 64 where its shares of 256
+// entries fill the workgroups and come to few parts: 64 rows, us, it and 64 x 256
+// tiles: 4,096 x 151,936 125 and 164; 2,048 x 100,000 45 and 54; 5,120 x 100,000 133
+// and 140; 2,560 x 100,000 78 and 64; 8,192 x 60,000 122 and 106; 1,024 x 100,000 34
+// and 29.  64 x 128 tiles where 256 columns leave CUs without one (64 x 4,096 x
+// 31,000: 32 and 49).  Beyond, 128 or 160 rows a tile, whichever takes less: a tile of
+// 160 rows takes 1.13 times one of 128 (256 x 4,096 x 151,936 307 us, 320 355, 640 682
+// and with 128 rows 707).  320 x 256 tiles of eight waves, one workgroup a CU, take
+// 702 there; two smaller ones overlap one's store with the other's products.
+int choose(const Projection& p) {
+  if (p.rows <= 32) return 1;
+  if (p.rows <= kFewRows) {
+    const int shares = (p.hidden_dim - 1) / (2 * kStep) + 1;
+    const int parts = (shares - 1) / kFewWaves + 1, waves = (shares - 1) / parts + 1;
+    if (waves >= 7 && parts <= 3) return 1;
+    return (p.vocab - 1) / 256 + 1 < kCus ? 2 : 3;
+  }
+  const int64_t by128 = (p.rows + int64_t{127}) / 128, by160 = (p.rows + int64_t{159}) / 160;
+  return by128 * 8 <= by160 * 9 ? 4 : 5;
 }
 
 }  // namespace
@@ -498,34 +721,20 @@ bool lmhead_e2m1_fits(int64_t rows, int64_t vocab) {
   return (rows + 63) / 64 <= ((int64_t{1} << 22) - 1) / tiles_n;
 }
 
-// TS_GEMM_TILE=1..5 forces a shape (the tests run every one): 1: the kernel for
-// few rows, where it can take the sizes; 2: 64 x 256; 3: 128 x 256; 4: 256 x
-// 256; 5: 320 x 256.
+// TS_GEMM_TILE=1..5 forces a shape (the tests run every one).
 hipError_t launch_lmhead_e2m1(const uint16_t* hidden, int64_t ld_hidden, const E2m1Rows& lm_head,
                               float* logits, int64_t ld_logits, int rows, int vocab,
                               int hidden_dim, hipStream_t stream) {
   const Projection p{hidden, ld_hidden, lm_head, logits, ld_logits, rows, vocab, hidden_dim};
   const char* env = getenv("TS_GEMM_TILE");
   int sel = env ? atoi(env) : 0;
-  const int steps = (hidden_dim - 1) / kStep + 1;
-  const bool few = rows <= 32 && steps <= 4 * kMaxWaves;
-  if (sel < 1 || sel > 5 || (sel == 1 && !few)) {
-    const int64_t pad256 = (rows + int64_t{255}) / 256 * 256, pad320 = (rows + int64_t{319}) / 320 * 320;
-    sel = few ? 1 : rows <= 64 ? 2 : rows <= 128 ? 3 : pad320 < pad256 ? 5 : 4;
-  }
+  if (sel < 1 || sel > 5 || (sel == 1 && rows > kFewRows)) sel = choose(p);
   switch (sel) {
-    case 1: {
-      const int waves = (steps + 3) / 4;
-      if (waves > 8)
-        return rows <= 16 ? launch_few<1, 4, 1, kMaxWaves>(p, waves, stream)
-                          : launch_few<2, 4, 1, kMaxWaves>(p, waves, stream);
-      return rows <= 16 ? launch_few<1, 4, 2, 8>(p, waves, stream)
-                        : launch_few<2, 4, 2, 8>(p, waves, stream);
-    }
-    case 2: return launch_tiles<64, 256, 1, 4>(p, stream);
-    case 3: return launch_tiles<128, 256, 2, 4>(p, stream);
-    case 4: return launch_tiles<256, 256, 2, 4>(p, stream);
-    default: return launch_tiles<320, 256, 2, 4>(p, stream);
+    case 1: return launch_few_rows(p, stream);
+    case 2: return launch_tiles<64, 128, 4, 3>(p, stream);
+    case 3: return launch_tiles<64, 256, 4, 3>(p, stream);
+    case 4: return launch_tiles<128, 256, 4, 2>(p, stream);
+    default: return launch_tiles<160, 256, 4, 2>(p, stream);
   }
 }
 

@@ -9,6 +9,9 @@ namespace ts {
 
 constexpr int kE2m1Group = 32;  // entries of a row that share a scale
 
+// A tile's hidden rows lie within 2^31 bytes of each other.
+constexpr int64_t kE2m1MaxLdHidden = int64_t{1} << 21;
+
 struct E2m1Rows {
   const uint8_t* codes;   // [rows, cols / 2], two codes a byte, the even column's in the low half
   int64_t ld;
