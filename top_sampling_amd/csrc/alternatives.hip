@@ -22,6 +22,8 @@
 // into again.
 #include "alternatives.hpp"
 
+#include <type_traits>
+
 #include "token_rows.hpp"
 
 namespace ts {
@@ -32,6 +34,8 @@ constexpr int kSlabGroups = kThreads / kGroupLanes;     // groups of a slab
 constexpr int kGroupVecs = kGroupLanes * kBatch;        // vectors of a group
 constexpr int kListedGroups = 1024;                     // groups looked into, at most
 constexpr int kCandidates = 2048;                       // entries put in order, at most
+constexpr int kHeldGroups = 5;                          // of a thread in registers
+constexpr int kQuadMost = 48;                           // see bound_of_quads
 
 // How the statistics pass leaves the largest entries of groups: group g of slab
 // s of a row's chunk c is number (c slabs + s) kSlabGroups + g.
@@ -65,16 +69,25 @@ __device__ __forceinline__ float max_of_8(float x) {
   return step(x, std::integral_constant<int, 0x141>{});  // row_half_mirror
 }
 
+// The largest fp32 number below a finite x.
+__device__ __forceinline__ float next_below(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return x == 0.0f ? __uint_as_float(0x80000001u) : __uint_as_float(x > 0.0f ? b - 1 : b + 1);
+}
+
 // What the statistics pass does beside adding up: groups, and the entries
-// before the token in the order.
+// before the token in the order.  Those are the ones above the token's logit xt and,
+// in front of it, the ones that equal it; a slab that does not reach xt is passed
+// over.
 template <typename T>
 struct TopVisit {
   static constexpr bool kOn = true;
   float* groups;   // of the row's chunk, or null
   int v0;          // the chunk's first vector
-  float xt;        // the token's logit, +inf if there is none
+  float xt, below; // the token's logit, +inf if there is none
   int token, token_vec, token_e;
-  int better;
+  int better;      // this lane's
+  int wave_better; // the wave's
 
   __device__ __forceinline__ void slab(int v, int end, const float (&w)[kBatch][Vec<T>::n],
                                        float high) {
@@ -83,20 +96,39 @@ struct TopVisit {
       if (threadIdx.x % kGroupLanes == 0)
         groups[(v - v0) / kSlab * kSlabGroups + threadIdx.x / kGroupLanes] = top;
     }
-    if (__any(high >= xt)) {
+    if (!__any(high >= xt)) return;
+    if (xt == -INFINITY) {  // nothing is below: among the masked ones the ids decide
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
         const int i = v + j * kThreads + static_cast<int>(threadIdx.x);
 #pragma unroll
-        for (int e = 0; e < Vec<T>::n; ++e) {
-          const bool before = i < token_vec || (i == token_vec && e < token_e);
-          better += (w[j][e] > xt || (w[j][e] == xt && before && i < end)) ? 1 : 0;
-        }
+        for (int e = 0; e < Vec<T>::n; ++e)
+          better += (w[j][e] > xt || (i < min(token_vec, end))) ? 1 : 0;
       }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = v + j * kThreads + static_cast<int>(threadIdx.x);
+        const float least = i < token_vec ? below : xt;
+#pragma unroll
+        for (int e = 0; e < Vec<T>::n; ++e) wave_better += __popcll(__ballot(w[j][e] > least));
+      }
+    }
+    if (v <= token_vec && token_vec < min(v + kSlab, end)) {
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (v + j * kThreads + static_cast<int>(threadIdx.x) == token_vec) {
+#pragma unroll
+          for (int e = 0; e < Vec<T>::n; ++e) better += (e < token_e && w[j][e] == xt) ? 1 : 0;
+        }
     }
   }
   __device__ __forceinline__ void edge(int at, float x) {
     better += (x > xt || (x == xt && at < token)) ? 1 : 0;
+  }
+  // A lane's share of the row's count.
+  __device__ __forceinline__ int count() const {
+    return better + ((threadIdx.x & 63) == 0 ? wave_better : 0);
   }
 };
 
@@ -107,11 +139,12 @@ __device__ __forceinline__ TopVisit<T> make_visit(const Shape& f, float* groups,
   v.groups = groups;
   v.v0 = v0;
   v.xt = xt;
+  v.below = next_below(xt);
   v.token = token;
   const bool in_body = token >= f.head;
   v.token_vec = in_body ? (token - f.head) / Vec<T>::n : -1;
   v.token_e = in_body ? (token - f.head) % Vec<T>::n : 0;
-  v.better = 0;
+  v.better = v.wave_better = 0;
   return v;
 }
 
@@ -193,6 +226,58 @@ __device__ __forceinline__ void exact_bound(const T* row, int vocab, int n, TopS
   }
 }
 
+// A bound that n of the threads' numbers reach (n <= kThreads): the n-th largest.
+// 0 if fewer of them are above 0.
+__device__ __forceinline__ uint32_t bound_of_threads(uint32_t most, int n, TopShared& sh) {
+  const int tid = threadIdx.x;
+  sh.most[tid] = most;
+  __syncthreads();
+  int place = 0;
+  const uint4* m4 = reinterpret_cast<const uint4*>(sh.most);
+#pragma unroll 4
+  for (int k = 0; k < kThreads / 4; ++k) {
+    const uint4 v = m4[k];
+    place += (v.x > most || (v.x == most && 4 * k < tid)) ? 1 : 0;
+    place += (v.y > most || (v.y == most && 4 * k + 1 < tid)) ? 1 : 0;
+    place += (v.z > most || (v.z == most && 4 * k + 2 < tid)) ? 1 : 0;
+    place += (v.w > most || (v.w == most && 4 * k + 3 < tid)) ? 1 : 0;
+  }
+  if (place == n - 1) sh.bound = most;
+  __syncthreads();
+  return sh.bound;
+}
+
+// The same from the largest of every four threads (n <= kThreads / 4), by every wave
+// for itself: a quarter of the numbers, a sixteenth of the comparisons, and a bound
+// that hardly more groups reach as long as n is small beside them (at n = 20 some 24
+// of 1,187).
+__device__ __forceinline__ uint32_t bound_of_quads(uint32_t most, int n, TopShared& sh) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  auto step = [](uint32_t v, auto ctrl) {
+    return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(
+                      0, static_cast<int>(v), decltype(ctrl)::value, 0xF, 0xF, true)));
+  };
+  most = step(most, std::integral_constant<int, 0xB1>{});  // quad_perm [1, 0, 3, 2]
+  most = step(most, std::integral_constant<int, 0x4E>{});  // quad_perm [2, 3, 0, 1]
+  if ((tid & 3) == 0) sh.most[tid >> 2] = most;
+  __syncthreads();
+  const uint32_t mine = sh.most[lane];
+  int above = 0;  // strictly
+  const uint4* m4 = reinterpret_cast<const uint4*>(sh.most);
+#pragma unroll 4
+  for (int k = 0; k < 16; ++k) {
+    const uint4 v = m4[k];
+    above += (v.x > mine ? 1 : 0) + (v.y > mine ? 1 : 0) + (v.z > mine ? 1 : 0) +
+             (v.w > mine ? 1 : 0);
+  }
+  // The n-th largest is the least of those with fewer than n above them.
+  uint32_t least = above < n ? mine : 0xffffffffu;
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1)
+    least = min(least, static_cast<uint32_t>(__shfl_xor(static_cast<int>(least), d, 64)));
+  return least;
+}
+
 // The n first entries of a row (n <= vocab) into sh.cand, with n_cand entries in
 // no order, all of which and no others reach a bound.  By the whole workgroup.
 template <typename T>
@@ -209,55 +294,69 @@ __device__ __forceinline__ void find_candidates(const T* row, int vocab, const G
            min((c + 1) * static_cast<int64_t>(gs.chunk_len), static_cast<int64_t>(f.whole));
   };
   if (by_groups) {
-    uint32_t most = 0;
-    for (int g = tid; g < gs.per_row; g += kThreads)
+    // A thread's groups, the first ones' largest entries in registers.
+    uint32_t held[kHeldGroups], most = 0;
+    const int held_end = kHeldGroups * kThreads;
+#pragma unroll
+    for (int k = 0; k < kHeldGroups; ++k) {
+      const int g = tid + k * kThreads;
+      held[k] = g < gs.per_row && live(g) ? order_of(groups[g]) : 0u;
+      most = max(most, held[k]);
+    }
+    for (int g = held_end + tid; g < gs.per_row; g += kThreads)
       if (live(g)) most = max(most, order_of(groups[g]));
-    sh.most[tid] = most;
-    __syncthreads();
-    int place = 0;
-    const uint4* m4 = reinterpret_cast<const uint4*>(sh.most);
-#pragma unroll 4
-    for (int k = 0; k < kThreads / 4; ++k) {
-      const uint4 v = m4[k];
-      place += (v.x > most || (v.x == most && 4 * k < tid)) ? 1 : 0;
-      place += (v.y > most || (v.y == most && 4 * k + 1 < tid)) ? 1 : 0;
-      place += (v.z > most || (v.z == most && 4 * k + 2 < tid)) ? 1 : 0;
-      place += (v.w > most || (v.w == most && 4 * k + 3 < tid)) ? 1 : 0;
-    }
-    if (place == n - 1) sh.bound = most;
-    __syncthreads();
-    const uint32_t bound = sh.bound;
+    const uint32_t bound = n <= kQuadMost ? bound_of_quads(most, n, sh) : bound_of_threads(most, n, sh);
     if (most >= bound) {
-      for (int g = tid; g < gs.per_row; g += kThreads)
-        if (live(g) && order_of(groups[g]) >= bound) {
-          const int at = atomicAdd(&sh.n_groups, 1);
-          if (at < kListedGroups) sh.group[at] = g;
-        }
+      auto list = [&](int g) {
+        const int at = atomicAdd(&sh.n_groups, 1);
+        if (at < kListedGroups) sh.group[at] = g;
+      };
+#pragma unroll
+      for (int k = 0; k < kHeldGroups; ++k) {
+        const int g = tid + k * kThreads;
+        if (held[k] >= bound && g < gs.per_row && live(g)) list(g);
+      }
+      for (int g = held_end + tid; g < gs.per_row; g += kThreads)
+        if (live(g) && order_of(groups[g]) >= bound) list(g);
     }
     __syncthreads();
-    by_groups = sh.n_groups <= kListedGroups;
+    const int count = sh.n_groups;
+    by_groups = count <= kListedGroups;
     if (by_groups) {
       auto add = [&](float x, int id) {
         if (order_of(x) < bound) return;
         const int at = atomicAdd(&sh.n_cand, 1);
         if (at < kCandidates) sh.cand[at] = entry_key(x, id);
       };
-      for (int k = tid / kGroupVecs; k < sh.n_groups; k += kThreads / kGroupVecs) {
-        const int g = sh.group[k], slab = g / kSlabGroups, c = slab / gs.slabs;
-        const int j = tid % kGroupVecs / kGroupLanes;
-        const int64_t v = static_cast<int64_t>(c) * gs.chunk_len + slab % gs.slabs * kSlab +
-                          j * kThreads + g % kSlabGroups * kGroupLanes + tid % kGroupLanes;
-        if (v >= min((c + 1) * static_cast<int64_t>(gs.chunk_len), static_cast<int64_t>(f.whole)))
-          continue;
-        const typename Vec<T>::Type w =
-            *reinterpret_cast<const typename Vec<T>::Type*>(row + f.head + v * VN);
-#pragma unroll
-        for (int e = 0; e < VN; ++e)
-          add(static_cast<float>(w[e]), f.head + static_cast<int>(v) * VN + e);
-      }
       if (tid < f.edge) {
         const int at = f.template at<T>(tid);
         add(static_cast<float>(row[at]), at);
+      }
+      // Vector tid % kGroupVecs of a group; several groups' loads on their way.
+      constexpr int kAtOnce = 4;
+      const int vec = (tid % kGroupVecs / kGroupLanes) * kThreads + tid % kGroupLanes;
+      for (int k0 = tid / kGroupVecs; k0 < count; k0 += kAtOnce * kThreads / kGroupVecs) {
+        typename Vec<T>::Type w[kAtOnce];
+        int at[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          const int k = k0 + u * kThreads / kGroupVecs;
+          at[u] = -1;
+          if (k >= count) continue;
+          const int g = sh.group[k], slab = g / kSlabGroups, c = slab / gs.slabs;
+          const int64_t v = static_cast<int64_t>(c) * gs.chunk_len + slab % gs.slabs * kSlab +
+                            g % kSlabGroups * kGroupLanes + vec;
+          if (v >= min((c + 1) * static_cast<int64_t>(gs.chunk_len), static_cast<int64_t>(f.whole)))
+            continue;
+          at[u] = f.head + static_cast<int>(v) * VN;
+          w[u] = *reinterpret_cast<const typename Vec<T>::Type*>(row + at[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          if (at[u] < 0) continue;
+#pragma unroll
+          for (int e = 0; e < VN; ++e) add(static_cast<float>(w[u][e]), at[u] + e);
+        }
       }
     }
     __syncthreads();
@@ -389,7 +488,7 @@ __device__ __forceinline__ void finish_topn(const T* row, int64_t r, int vocab, 
 }
 
 template <bool ENT, typename T>
-__global__ __launch_bounds__(kThreads) void topn_whole_kernel(
+__global__ __launch_bounds__(kThreads, 4) void topn_whole_kernel(
     const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,
     Scale sc, Cut cut, Groups gs, float* groups, TopnOut o) {
   __shared__ TopShared sh;
@@ -411,7 +510,7 @@ __global__ __launch_bounds__(kThreads) void topn_whole_kernel(
                                 &visit);
     join_group<ENT, kThreads>(st.m, st.s, st.u, sc, sh.wave_part);
     __syncthreads();
-    finish_topn(rx, r, vocab, token, has_token, xt, st, visit.better, gs, gr, cut, sc, o, sh);
+    finish_topn(rx, r, vocab, token, has_token, xt, st, visit.count(), gs, gr, cut, sc, o, sh);
     __syncthreads();
   }
 }
@@ -439,7 +538,7 @@ __global__ __launch_bounds__(kThreads) void topn_stats_kernel(
     row_stats<T, ENT, kThreads>(rx, vocab, chunk * cut.len, (chunk + 1) * cut.len,
                                 chunk == cut.chunks - 1, sc, m, s, u, &visit);
     join_group<ENT, kThreads>(m, s, u, sc, wave_part);
-    const int n = group_count(visit.better, wave_n);
+    const int n = group_count(visit.count(), wave_n);
     if (tid == 0) {
       parts[b] = Part{s, u, m, 0.0f};
       betters[b] = n;
@@ -633,75 +732,38 @@ __global__ __launch_bounds__(kThreads) void listed_rows_kernel(
   }
 }
 
-// The gradient's dense part of vectors [v0, v1) of a row (and with `edge` of the
-// entries at its ends), from the last slab to the first: entry j is
-// e_j (a + b log2 e_j).  `read` false: it is all `a`, which is 0.
+// A row's dense entries: entry j is e_j (a + b log2 e_j).
 struct DenseGrad {
   float m, a, b;
+
+  template <bool ENT>
+  __device__ __forceinline__ float entry(float x, const Scale& sc) const {
+    const float k = log2_t(x - m, sc);
+    const float ex = __builtin_amdgcn_exp2f(k);
+    return ENT ? ex * fmaf(b, fmaxf(k, kLeastLog2), a) : ex * a;
+  }
 };
 
+// A workgroup writes a chunk of a row's dense part, from the last slab to the first,
+// then the listed entries in it.  Their values need no logit, only the forward
+// pass's log-probabilities, so the gradient may replace the logits.  An id that is
+// listed several times is written once, by its first place, from the sum of its
+// gradients.  The first slab's loads are on their way while the row's coefficients
+// are worked out (1,021 x 100,277 bf16, 64 listed tokens and the entropy: 127 us
+// without that, 85 so).  640 x 151,936 fp32 takes 135 us (5.8 TB/s); longer chunks, a
+// row a workgroup at the end of it, are slower (167), as are five workgroups a CU
+// (146).
 template <typename T, bool ENT>
-__device__ __forceinline__ void dense_grad(const T* row, T* out, const Shape& f, int v0, int v1,
-                                           bool edge, bool read, const DenseGrad& g,
-                                           const Scale& sc) {
-  constexpr int VN = Vec<T>::n;
-  using V = typename Vec<T>::Type;
-  const int tid = threadIdx.x;
-  const int end = min(v1, f.whole);
-  auto entry = [&](float x) {
-    const float k = log2_t(x - g.m, sc);
-    const float ex = __builtin_amdgcn_exp2f(k);
-    return ENT ? ex * fmaf(g.b, fmaxf(k, kLeastLog2), g.a) : ex * g.a;
-  };
-  if (edge && tid < f.edge) {
-    const int at = f.template at<T>(tid);
-    out[at] = static_cast<T>(read ? entry(static_cast<float>(row[at])) : 0.0f);
-  }
-  if (v0 >= end) return;
-  row += f.head;
-  out += f.head;
-  int v = v0 + (end - 1 - v0) / kSlab * kSlab;
-  Slab<T, kThreads> next;
-  if (read) next.load(row, v, end);
-  for (; v >= v0; v -= kSlab) {
-    float w[kBatch][VN];
-    if (!read) {
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-#pragma unroll
-        for (int e = 0; e < VN; ++e) w[j][e] = 0.0f;
-    } else {
-      next.unpack(w);
-      if (v > v0) next.load(row, v - kSlab, end);
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-#pragma unroll
-        for (int e = 0; e < VN; ++e) w[j][e] = entry(w[j][e]);
-    }
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int i = v + j * kThreads + tid;
-      V o;
-#pragma unroll
-      for (int e = 0; e < VN; ++e) o[e] = static_cast<T>(w[j][e]);
-      if (i < end)
-        __builtin_nontemporal_store(o, reinterpret_cast<V*>(out + static_cast<int64_t>(i) * VN));
-    }
-  }
-}
-
-// A workgroup writes a chunk of a row's dense part, then the listed entries in
-// it.  Their values need no logit, only the forward pass's log-probabilities, so
-// the gradient may replace the logits.  An id that is listed several times is
-// written once, by its first place, from the sum of its gradients.
-template <typename T, bool ENT>
-__global__ __launch_bounds__(kThreads) void listed_grad_kernel(
+__global__ __launch_bounds__(kThreads, 4) void listed_grad_kernel(
     const T* x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ ids, Scale sc,
     Cut cut, ListedGrad g, T* d, int64_t ldd) {
+  constexpr int VN = Vec<T>::n;
+  using V = typename Vec<T>::Type;
   __shared__ double wave_sum[kThreads / 64];
-  __shared__ int s_ids[TS_MAX_LISTED];
+  __shared__ int4 s_ids[TS_MAX_LISTED / 4];
   __shared__ float s_g[TS_MAX_LISTED];
   const int tid = threadIdx.x;
+  const int quads = (g.n + 3) / 4;
   const int64_t total = static_cast<int64_t>(rows) * cut.chunks;
   for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
     // Last row first, as the end of the logits is what the caches still hold.
@@ -710,13 +772,25 @@ __global__ __launch_bounds__(kThreads) void listed_grad_kernel(
     const int64_t at = static_cast<int64_t>(row) * g.n;
     const T* rx = x + static_cast<int64_t>(row) * ld;
     T* rd = d + static_cast<int64_t>(row) * ldd;
-    double sum = 0.0;
+    const Shape f = row_shape(rd, vocab);
+    const int v0 = chunk * cut.len, end = min(v0 + cut.len, f.whole);
+    const bool last = chunk == cut.chunks - 1;
+    const T* body = rx + f.head;
+    T* out = rd + f.head;
+    int v = v0 + (end - 1 - v0) / kSlab * kSlab;
+    Slab<T, kThreads> next;
+    if (v0 < end) next.load(body, v, end);
+
     const double dh_row = ENT ? static_cast<double>(g.grad_entropies[row]) : 0.0;
+    const float m = g.row_stats[2 * static_cast<int64_t>(row)];
+    const double s = g.row_stats[2 * static_cast<int64_t>(row) + 1];
+    const double h_row = ENT ? static_cast<double>(g.entropies[row]) : 0.0;
+    double sum = 0.0;
     bool any = false;
-    for (int i = tid; i < g.n; i += kThreads) {
-      const int id = ids[at + i];
+    for (int i = tid; i < 4 * quads; i += kThreads) {
+      const int id = i < g.n ? ids[at + i] : -1;
       const float gi = id < 0 ? 0.0f : g.grad_logprobs[at + i];
-      s_ids[i] = id;
+      reinterpret_cast<int*>(s_ids)[i] = id;
       s_g[i] = gi;
       sum += gi;
       any |= id >= 0 && (gi != 0.0f || dh_row != 0.0);
@@ -727,40 +801,62 @@ __global__ __launch_bounds__(kThreads) void listed_grad_kernel(
     sum = 0.0;
 #pragma unroll
     for (int w = 0; w < kThreads / 64; ++w) sum += wave_sum[w];
-    const double dh = ENT && live ? dh_row : 0.0;
-    const double h = ENT && dh != 0.0 ? static_cast<double>(g.entropies[row]) : 0.0;
+    const double dh = live ? dh_row : 0.0;
+    const double h = dh != 0.0 ? h_row : 0.0;
     DenseGrad dense{0.0f, 0.0f, 0.0f};
     if (live) {
-      const double s = g.row_stats[2 * static_cast<int64_t>(row) + 1];
-      dense.m = g.row_stats[2 * static_cast<int64_t>(row)];
+      dense.m = m;
       dense.a = static_cast<float>(-(sum + (dh != 0.0 ? dh * (h - log(s)) : 0.0)) * sc.inv_t / s);
       dense.b = static_cast<float>(-dh * M_LN2 * sc.inv_t / s);
     }
-    const Shape f = row_shape(rd, vocab);
-    const int v0 = chunk * cut.len;
-    const bool last = chunk == cut.chunks - 1;
-    dense_grad<T, ENT>(rx, rd, f, v0, v0 + cut.len, last,
-                       live && !(dense.a == 0.0f && dense.b == 0.0f), dense, sc);
+    const bool zero = dense.a == 0.0f && dense.b == 0.0f;
+    if (last && tid < f.edge) {
+      const int place = f.template at<T>(tid);
+      rd[place] = static_cast<T>(
+          zero ? 0.0f : dense.template entry<ENT>(static_cast<float>(rx[place]), sc));
+    }
+    for (; v >= v0 && v0 < end; v -= kSlab) {
+      float w[kBatch][VN];
+      next.unpack(w);
+      if (v > v0) next.load(body, v - kSlab, end);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = v + j * kThreads + tid;
+        V o;
+#pragma unroll
+        for (int e = 0; e < VN; ++e)
+          o[e] = static_cast<T>(zero ? 0.0f : dense.template entry<ENT>(w[j][e], sc));
+        if (i < end)
+          __builtin_nontemporal_store(o, reinterpret_cast<V*>(out + static_cast<int64_t>(i) * VN));
+      }
+    }
     __syncthreads();  // before entries of the same places
     for (int i = tid; live && i < g.n; i += kThreads) {
-      const int id = s_ids[i];
+      const int id = reinterpret_cast<const int*>(s_ids)[i];
       if (id < 0 || id >= vocab) continue;
-      const int vec = (id - f.head) / Vec<T>::n;
+      const int vec = (id - f.head) / VN;
       const bool in_body = id >= f.head && vec < f.whole;
-      if (in_body ? vec < v0 || vec >= v0 + cut.len : !last) continue;
+      if (in_body ? vec < v0 || vec >= end : !last) continue;
       bool is_first = true;
       double mine = 0.0;
-      for (int k = 0; k < g.n; ++k) {
-        const bool same = s_ids[k] == id;
-        if (same && k < i) is_first = false;
-        if (same) mine += s_g[k];
+#pragma unroll 4
+      for (int k = 0; k < quads; ++k) {
+        const int4 q = s_ids[k];
+        if (q.x != id && q.y != id && q.z != id && q.w != id) continue;
+        const int four[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (four[e] != id) continue;
+          is_first = is_first && 4 * k + e >= i;
+          mine += s_g[4 * k + e];
+        }
       }
       if (!is_first) continue;
       // g (1 - p) of its own share, -p of the others'.
       const double lp = g.logprobs[at + i], p = exp(lp);
-      double v = mine * -expm1(lp) - (sum - mine) * p;
-      if (ENT && dh != 0.0 && !(lp < -1e30)) v -= dh * p * (lp + h);
-      rd[id] = static_cast<T>(static_cast<float>(v * sc.inv_t));
+      double value = mine * -expm1(lp) - (sum - mine) * p;
+      if (ENT && dh != 0.0 && !(lp < -1e30)) value -= dh * p * (lp + h);
+      rd[id] = static_cast<T>(static_cast<float>(value * sc.inv_t));
     }
     __syncthreads();
   }
@@ -800,7 +896,12 @@ hipError_t topn_t(const TokenRows& t, const TopnOut& o, void* ws, hipStream_t st
   const Scale sc = make_scale(t.temperature);
   const TopnSpace w = lay_out_topn(ws, t.rows, t.vocab);
   const T* x = static_cast<const T*>(t.x);
-  if (whole_rows(t.rows, t.vocab, Vec<T>::n)) {
+  // Short rows take a workgroup each in one launch (4 x 4,096 16 us, 1,000 x 32,000
+  // fp32 43 and cut up 46); longer ones are cut up whatever their number: the row's
+  // outputs need 128 registers where the statistics need 80, and hold the reads up
+  // (640 x 151,936 fp32, 20 alternatives 106 us and cut up 93; 256 x 248,320 bf16 59
+  // and 48).
+  if (t.vocab <= kShortRow) {
     const Cut cut = whole_cut(t.vocab, Vec<T>::n);
     hipLaunchKernelGGL((topn_whole_kernel<ENT, T>), dim3(grid_of(t.rows)), dim3(kThreads), 0,
                        stream, x, t.ld, t.rows, t.vocab, t.tokens, sc, cut, make_groups(cut),
