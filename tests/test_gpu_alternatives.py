@@ -496,3 +496,41 @@ def test_outputs_stand_on_their_own():
     out.logprobs.add_(1.0)
     out.topn_ids.zero_()
     assert torch.equal(out.topn_logprobs, held) and out.topn_logprobs._version == versions
+
+
+SELECT = ("plain", "15 left", "500 at the lowest", "whole numbers", "two halves", "rising")
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("vocab", (1000, 3001, 33000, 100277, 151936))
+@pytest.mark.parametrize("n", (1, 48, 49, 128, 129, 257, 700, 1024))
+def test_selection(dtype, vocab, n):
+    """The alternatives' ids are exact, ties by id: few tokens left, equal logits in
+    great number, order of ids against the order of the logits."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    say("selection", dtype, vocab, n)
+    to = {"fp32": torch.float32, "bf16": torch.bfloat16}[dtype]
+    gen = torch.Generator().manual_seed(vocab + n)
+    rows = 3
+    for kind in SELECT:
+        x = 2.0 * torch.randn(rows, vocab, generator=gen)
+        shut = torch.rand(rows, vocab, generator=gen).argsort(-1)
+        if kind == "15 left":
+            x.scatter_(1, shut[:, 15:], float("-inf"))
+        elif kind == "500 at the lowest":
+            x.scatter_(1, shut[:, 500:], torch.finfo(to).min)
+        elif kind == "whole numbers":
+            x = x.round()
+        elif kind == "two halves":
+            x = (torch.arange(vocab) >= vocab // 2).float().expand(rows, vocab)
+        elif kind == "rising":
+            x = torch.arange(vocab).float().expand(rows, vocab)
+        x = x.to(to).contiguous()
+        got = ts.token_logprobs_topn(x.cuda(), None, n).topn_ids.cpu()
+        k = min(n, vocab)
+        want = (-x.double() + 0.0).argsort(dim=-1, stable=True)[:, :k].int()
+        assert torch.equal(got[:, :k], want), kind
+        assert (got[:, k:] == -1).all(), kind

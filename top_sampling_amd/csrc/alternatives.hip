@@ -15,11 +15,10 @@
 // Bound by the logits' bytes: one read forwards, a read and a write backwards.
 //
 // The alternatives cost no second read: while the statistics pass has the
-// logits in registers it also writes the largest of every group of entries (16
-// or 32 of each of 8 neighbouring threads).  A lower bound of the n-th largest
-// logit follows from those alone (the n-th largest of the 256 threads' largest
-// groups), and only the groups that reach it, little more than n, are looked
-// into again.
+// logits in registers it also writes the largest of every group of entries, the 16
+// (fp32) or 32 of a thread or, for smaller n, of 8 neighbouring threads.  A lower
+// bound of the n-th largest logit follows from those alone, and only the groups that
+// reach it, little more than n, are looked into again.
 #include "alternatives.hpp"
 
 #include <type_traits>
@@ -29,26 +28,32 @@
 namespace ts {
 namespace {
 
-constexpr int kGroupLanes = 8;                          // threads that share a group
-constexpr int kSlabGroups = kThreads / kGroupLanes;     // groups of a slab
-constexpr int kGroupVecs = kGroupLanes * kBatch;        // vectors of a group
-constexpr int kListedGroups = 1024;                     // groups looked into, at most
-constexpr int kCandidates = 2048;                       // entries put in order, at most
-constexpr int kHeldGroups = 5;                          // of a thread in registers
-constexpr int kQuadMost = 48;                           // see bound_of_quads
+constexpr int kGroupBits = 3;         // 8 threads share a group
+constexpr int kListedGroups = 1280;   // groups looked into, at most
+constexpr int kCandidates = 2048;     // entries put in order, at most
+constexpr int kHeldGroups = 5;        // of a thread in registers
+constexpr int kQuadMost = 48;         // see bound_of_quads
+// Beyond this many alternatives every thread has its own groups (shared and own: 640 x
+// 151,936 fp32, n = 100 105 and 143 us, 150 121 and 136, 200 137 and 140; 1,021 x
+// 100,277 bf16 118 and 123, 143 and 121, 173 and 122).
+constexpr int kSharedMost = 128;
+static_assert(kSharedMost <= kThreads, "bound_of_threads takes no more");
 
-// How the statistics pass leaves the largest entries of groups: group g of slab
-// s of a row's chunk c is number (c slabs + s) kSlabGroups + g.
+// How the statistics pass leaves the largest entries of groups, each of 2^bits
+// neighbouring threads: group g of slab s of a row's chunk c is number
+// (c slabs + s) per_slab + g.
 struct Groups {
-  int chunks, chunk_len, slabs, per_row;
+  int chunk_len, slabs, bits, per_row;
+
+  __host__ __device__ __forceinline__ int per_slab() const { return kThreads >> bits; }
 };
 
-Groups make_groups(const Cut& cut) {
+Groups make_groups(const Cut& cut, int n) {
   Groups g;
-  g.chunks = cut.chunks;
   g.chunk_len = cut.len;
   g.slabs = (cut.len + kSlab - 1) / kSlab;
-  g.per_row = g.chunks * g.slabs * kSlabGroups;
+  g.bits = n > kSharedMost ? 0 : kGroupBits;
+  g.per_row = cut.chunks * g.slabs * g.per_slab();
   return g;
 }
 
@@ -83,6 +88,7 @@ template <typename T>
 struct TopVisit {
   static constexpr bool kOn = true;
   float* groups;   // of the row's chunk, or null
+  bool shared;     // by 8 threads each
   int v0;          // the chunk's first vector
   float xt, below; // the token's logit, +inf if there is none
   int token, token_vec, token_e;
@@ -92,9 +98,13 @@ struct TopVisit {
   __device__ __forceinline__ void slab(int v, int end, const float (&w)[kBatch][Vec<T>::n],
                                        float high) {
     if (groups != nullptr) {
-      const float top = max_of_8(high);
-      if (threadIdx.x % kGroupLanes == 0)
-        groups[(v - v0) / kSlab * kSlabGroups + threadIdx.x / kGroupLanes] = top;
+      const int first = (v - v0) / kSlab * kThreads + static_cast<int>(threadIdx.x);
+      if (shared) {
+        const float top = max_of_8(high);
+        if (threadIdx.x % (1 << kGroupBits) == 0) groups[first >> kGroupBits] = top;
+      } else {
+        groups[first] = high;
+      }
     }
     if (!__any(high >= xt)) return;
     if (xt == -INFINITY) {  // nothing is below: among the masked ones the ids decide
@@ -133,10 +143,11 @@ struct TopVisit {
 };
 
 template <typename T>
-__device__ __forceinline__ TopVisit<T> make_visit(const Shape& f, float* groups, int v0, float xt,
-                                                  int token) {
+__device__ __forceinline__ TopVisit<T> make_visit(const Shape& f, float* groups, int bits, int v0,
+                                                  float xt, int token) {
   TopVisit<T> v;
   v.groups = groups;
+  v.shared = bits != 0;
   v.v0 = v0;
   v.xt = xt;
   v.below = next_below(xt);
@@ -182,47 +193,48 @@ struct TopShared {
   int hist[256];
   int n_groups, n_cand, wave_n[kThreads / 64];
   uint32_t bound;
-  uint64_t bound64;
-  int need, above, first_id, done;
+  uint32_t low[kThreads / 64];
+  int need, above, step, first_id, done;
   Part wave_part[kThreads / 64];
   double s, ln_s;
 };
 
-// A bound of the n-th largest key that at most kCandidates keys reach, from the
-// whole row digit by digit.  For rows that the groups do not narrow down: many
-// equal entries, or n beyond the threads.
-template <typename T>
-__device__ __forceinline__ void exact_bound(const T* row, int vocab, int n, TopShared& sh) {
-  uint64_t prefix = 0;
+// A bound of the n-th largest of the keys from `low` to `high`, of which there are n or
+// more: in 256 steps of a power of two, and again in the step that holds it, until at
+// most `most` keys reach the bound or it is that key.  each(use) gives every thread
+// its keys; those outside are passed over.
+template <typename Key, typename Each>
+__device__ __forceinline__ Key bound_by_steps(Key low, Key high, int n, int most, TopShared& sh,
+                                              Each each) {
+  int shift = max(64 - __clzll(static_cast<long long>(high - low)) - 8, 0);
   if (threadIdx.x == 0) {
     sh.need = n;
     sh.above = 0;
-    sh.done = 0;
   }
-  for (int shift = 56; shift >= 0; shift -= 8) {
+  for (;;) {
     sh.hist[threadIdx.x] = 0;
     __syncthreads();
-    for (int64_t i = threadIdx.x; i < vocab; i += kThreads) {
-      const uint64_t key = entry_key(static_cast<float>(row[i]), static_cast<int>(i));
-      if (shift == 56 || key >> (shift + 8) == prefix >> (shift + 8))
-        atomicAdd(&sh.hist[static_cast<int>(key >> shift) & 255], 1);
-    }
+    each([&](Key key) {
+      const Key step = (key - low) >> shift;  // far out below `low`
+      if (key >= low && step < 256) atomicAdd(&sh.hist[static_cast<int>(step)], 1);
+    });
     __syncthreads();
-    // The digit that holds the key: its own keys and those above reach `need`.
+    // The step that holds the key: its own keys and those above reach `need`.
     int over = 0;
     for (int d = threadIdx.x + 1; d < 256; ++d) over += sh.hist[d];
     const int mine = sh.hist[threadIdx.x];
     const int need = sh.need, above = sh.above;
     __syncthreads();
     if (over < need && over + mine >= need) {
-      sh.bound64 = prefix | static_cast<uint64_t>(threadIdx.x) << shift;
+      sh.step = threadIdx.x;
       sh.need = need - over;
       sh.above = above + over;
-      sh.done = above + over + mine <= kCandidates;
+      sh.done = above + over + mine <= most;
     }
     __syncthreads();
-    prefix = sh.bound64;
-    if (sh.done) break;
+    low += static_cast<Key>(sh.step) << shift;
+    if (sh.done || shift == 0) return low;
+    shift = max(shift - 8, 0);
   }
 }
 
@@ -278,99 +290,209 @@ __device__ __forceinline__ uint32_t bound_of_quads(uint32_t most, int n, TopShar
   return least;
 }
 
-// The n first entries of a row (n <= vocab) into sh.cand, with n_cand entries in
-// no order, all of which and no others reach a bound.  By the whole workgroup.
+// The least of all threads' k-th largest of the numbers they hold (k <= kHeldGroups).
+__device__ __forceinline__ uint32_t low_of_held(const uint32_t (&held)[kHeldGroups], int k,
+                                                TopShared& sh) {
+  uint32_t low = 0;
+#pragma unroll
+  for (int i = 0; i < kHeldGroups; ++i) {
+    int above = 0;  // strictly
+#pragma unroll
+    for (int j = 0; j < kHeldGroups; ++j) above += held[j] > held[i] ? 1 : 0;
+    int reach = 0;
+#pragma unroll
+    for (int j = 0; j < kHeldGroups; ++j) reach += held[j] >= held[i] ? 1 : 0;
+    if (above < k && reach >= k) low = held[i];
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1)
+    low = min(low, static_cast<uint32_t>(__shfl_xor(static_cast<int>(low), d, 64)));
+  if ((threadIdx.x & 63) == 0) sh.low[threadIdx.x >> 6] = low;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) low = min(low, sh.low[w]);
+  return low;
+}
+
+// Adds the first n - n_cand entries by id that equal a number, of which there are
+// as many, to sh.cand.  Masks leave rows that end in the order of ids soon: the first
+// step finds all unless most of the first ids are allowed.
+template <typename T>
+__device__ __forceinline__ void add_equal(const T* row, int vocab, uint32_t number, int n,
+                                          TopShared& sh) {
+  constexpr int kRun = 8;
+  const int tid = threadIdx.x, lane = tid & 63;
+  int at = sh.n_cand;
+  __syncthreads();
+  for (int64_t base = 0; base < vocab && at < n; base += kThreads * kRun) {
+    const int64_t id = base + tid * kRun;
+    uint32_t hits = 0;
+#pragma unroll
+    for (int u = 0; u < kRun; ++u)
+      if (id + u < vocab && order_of(static_cast<float>(row[id + u])) == number) hits |= 1u << u;
+    const int mine = __popc(hits);
+    int before = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int up = __shfl_up(before, d, 64);
+      before += lane >= d ? up : 0;
+    }
+    if (lane == 63) sh.wave_n[tid >> 6] = before;
+    before -= mine;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 64; ++w) {
+      before += w < tid >> 6 ? sh.wave_n[w] : 0;
+      total += sh.wave_n[w];
+    }
+    for (int place = at + before; hits != 0 && place < n; ++place, hits &= hits - 1)
+      sh.cand[place] = static_cast<uint64_t>(number) << 32 |
+                       (0xffffffffu - static_cast<uint32_t>(id + __ffs(hits) - 1));
+    at += total;
+    __syncthreads();
+  }
+  if (tid == 0) sh.n_cand = n;
+  __syncthreads();
+}
+
+// Entries of a row into sh.cand, the n first ones (n <= vocab) among them and none
+// that comes before one that is missing; n_cand in no order.  By the whole workgroup.
 template <typename T>
 __device__ __forceinline__ void find_candidates(const T* row, int vocab, const Groups& gs,
-                                                const float* groups, int n, TopShared& sh) {
+                                                const float* groups, float st_m, int n, TopShared& sh) {
   constexpr int VN = Vec<T>::n;
   const int tid = threadIdx.x;
   const Shape f = stats_shape(row, vocab);
-  if (tid == 0) sh.n_groups = sh.n_cand = 0;
-  bool by_groups = n <= kThreads;
-  auto live = [&](int g) {
-    const int slab = g / kSlabGroups, c = slab / gs.slabs;
-    return c * gs.chunk_len + slab % gs.slabs * kSlab <
-           min((c + 1) * static_cast<int64_t>(gs.chunk_len), static_cast<int64_t>(f.whole));
+  // The slabs that the row reaches come first.
+  const int full = f.whole / gs.chunk_len;
+  const int slabs = full * gs.slabs + (f.whole - full * gs.chunk_len + kSlab - 1) / kSlab;
+  const int live = slabs * gs.per_slab();
+  // A thread's groups, the first ones' largest entries in registers.
+  uint32_t held[kHeldGroups];
+  const int held_end = kHeldGroups * kThreads;
+  auto each_group = [&](auto use) {
+#pragma unroll
+    for (int k = 0; k < kHeldGroups; ++k)
+      if (tid + k * kThreads < live) use(tid + k * kThreads, held[k]);
+#pragma unroll 8
+    for (int g = held_end + tid; g < live; g += kThreads) use(g, order_of(groups[g]));
   };
-  if (by_groups) {
-    // A thread's groups, the first ones' largest entries in registers.
-    uint32_t held[kHeldGroups], most = 0;
-    const int held_end = kHeldGroups * kThreads;
+  // All entries that reach a bound, unless there are too many.
+  auto collect = [&](uint32_t bound) {
+    if (tid == 0) sh.n_groups = sh.n_cand = 0;
+    __syncthreads();
+    each_group([&](int g, uint32_t top) {
+      if (top < bound) return;
+      const int at = atomicAdd(&sh.n_groups, 1);
+      if (at < kListedGroups) sh.group[at] = g;
+    });
+    __syncthreads();
+    const int count = sh.n_groups;
+    if (count > kListedGroups) return false;
+    auto add = [&](float x, int id) {
+      if (order_of(x) < bound) return;
+      const int at = atomicAdd(&sh.n_cand, 1);
+      if (at < kCandidates) sh.cand[at] = entry_key(x, id);
+    };
+    if (tid < f.edge) {
+      const int at = f.template at<T>(tid);
+      add(static_cast<float>(row[at]), at);
+    }
+    // A vector of a group; several groups' loads on their way.
+    constexpr int kAtOnce = 4;
+    const int lanes = 1 << gs.bits, vecs = lanes * kBatch, step = kThreads / vecs;
+    const int vec = ((tid & (vecs - 1)) >> gs.bits) * kThreads + (tid & (lanes - 1));
+    for (int k0 = tid / vecs; k0 < count; k0 += kAtOnce * step) {
+      typename Vec<T>::Type w[kAtOnce];
+      int at[kAtOnce];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int k = k0 + u * step;
+        at[u] = -1;
+        if (k >= count) continue;
+        const int g = sh.group[k], slab = g / gs.per_slab(), c = slab / gs.slabs;
+        const int64_t first = static_cast<int64_t>(c) * gs.chunk_len;
+        const int64_t v = first + (slab - c * gs.slabs) * kSlab +
+                          (g & (gs.per_slab() - 1)) * lanes + vec;
+        if (v >= min(first + gs.chunk_len, static_cast<int64_t>(f.whole))) continue;
+        at[u] = f.head + static_cast<int>(v) * VN;
+        w[u] = *reinterpret_cast<const typename Vec<T>::Type*>(row + at[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        if (at[u] < 0) continue;
+#pragma unroll
+        for (int e = 0; e < VN; ++e) add(static_cast<float>(w[u][e]), at[u] + e);
+      }
+    }
+    __syncthreads();
+    return sh.n_cand <= kCandidates;
+  };
+
+  // Twice the groups that a bound needs, or it lets too many entries through.
+  if (gs.bits != 0 || live >= 2 * n) {
+    uint32_t most = 0;
 #pragma unroll
     for (int k = 0; k < kHeldGroups; ++k) {
       const int g = tid + k * kThreads;
-      held[k] = g < gs.per_row && live(g) ? order_of(groups[g]) : 0u;
-      most = max(most, held[k]);
+      held[k] = g < live ? order_of(groups[g]) : 0u;
     }
-    for (int g = held_end + tid; g < gs.per_row; g += kThreads)
-      if (live(g)) most = max(most, order_of(groups[g]));
-    const uint32_t bound = n <= kQuadMost ? bound_of_quads(most, n, sh) : bound_of_threads(most, n, sh);
-    if (most >= bound) {
-      auto list = [&](int g) {
-        const int at = atomicAdd(&sh.n_groups, 1);
-        if (at < kListedGroups) sh.group[at] = g;
-      };
-#pragma unroll
-      for (int k = 0; k < kHeldGroups; ++k) {
-        const int g = tid + k * kThreads;
-        if (held[k] >= bound && g < gs.per_row && live(g)) list(g);
-      }
-      for (int g = held_end + tid; g < gs.per_row; g += kThreads)
-        if (live(g) && order_of(groups[g]) >= bound) list(g);
+    uint32_t bound;
+    if (gs.bits != 0) {
+      each_group([&](int, uint32_t top) { most = max(most, top); });
+      bound = n <= kQuadMost ? bound_of_quads(most, n, sh) : bound_of_threads(most, n, sh);
+    } else {
+      const uint32_t low = low_of_held(held, (n + kThreads - 1) / kThreads, sh);
+      bound = bound_by_steps(low, order_of(st_m), n, n + n / 8, sh, [&](auto use) {
+        each_group([&](int, uint32_t top) { use(top); });
+      });
     }
-    __syncthreads();
-    const int count = sh.n_groups;
-    by_groups = count <= kListedGroups;
-    if (by_groups) {
-      auto add = [&](float x, int id) {
-        if (order_of(x) < bound) return;
-        const int at = atomicAdd(&sh.n_cand, 1);
-        if (at < kCandidates) sh.cand[at] = entry_key(x, id);
-      };
-      if (tid < f.edge) {
-        const int at = f.template at<T>(tid);
-        add(static_cast<float>(row[at]), at);
+    // Too many: equal entries, masked ones most often.  Then those above, and of the
+    // equal ones the first.
+    for (int above = 0; above < 2; ++above) {
+      if (collect(bound + above)) {
+        if (sh.n_cand < n) add_equal(row, vocab, bound, n, sh);
+        return;
       }
-      // Vector tid % kGroupVecs of a group; several groups' loads on their way.
-      constexpr int kAtOnce = 4;
-      const int vec = (tid % kGroupVecs / kGroupLanes) * kThreads + tid % kGroupLanes;
-      for (int k0 = tid / kGroupVecs; k0 < count; k0 += kAtOnce * kThreads / kGroupVecs) {
-        typename Vec<T>::Type w[kAtOnce];
-        int at[kAtOnce];
-#pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-          const int k = k0 + u * kThreads / kGroupVecs;
-          at[u] = -1;
-          if (k >= count) continue;
-          const int g = sh.group[k], slab = g / kSlabGroups, c = slab / gs.slabs;
-          const int64_t v = static_cast<int64_t>(c) * gs.chunk_len + slab % gs.slabs * kSlab +
-                            g % kSlabGroups * kGroupLanes + vec;
-          if (v >= min((c + 1) * static_cast<int64_t>(gs.chunk_len), static_cast<int64_t>(f.whole)))
-            continue;
-          at[u] = f.head + static_cast<int>(v) * VN;
-          w[u] = *reinterpret_cast<const typename Vec<T>::Type*>(row + at[u]);
-        }
-#pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-          if (at[u] < 0) continue;
-#pragma unroll
-          for (int e = 0; e < VN; ++e) add(static_cast<float>(w[u][e]), at[u] + e);
-        }
-      }
+      __syncthreads();
     }
-    __syncthreads();
-    if (by_groups && sh.n_cand <= kCandidates) return;
-    __syncthreads();
-    if (tid == 0) sh.n_cand = 0;
   }
-  exact_bound(row, vocab, n, sh);
-  const uint64_t bound = sh.bound64;
+  // Few groups beside n: rows shorter than 32 n (fp32) or 64 n (bf16) entries, which are
+  // gone through again (1,000 x 4,000 fp32, n = 300 82 us).
+  const uint64_t bound = bound_by_steps(uint64_t{0}, ~uint64_t{0}, n, kCandidates, sh, [&](auto use) {
+    for (int64_t i = tid; i < vocab; i += kThreads)
+      use(entry_key(static_cast<float>(row[i]), static_cast<int>(i)));
+  });
+  if (tid == 0) sh.n_cand = 0;
+  __syncthreads();
   for (int64_t i = tid; i < vocab; i += kThreads) {
     const uint64_t key = entry_key(static_cast<float>(row[i]), static_cast<int>(i));
     if (key >= bound) sh.cand[atomicAdd(&sh.n_cand, 1)] = key;
   }
   __syncthreads();
+}
+
+// Puts sh.cand in falling order (bitonic sort).  More than kThreads of them: a place
+// counted for each takes as many comparisons as the square.
+__device__ __forceinline__ void sort_candidates(int count, TopShared& sh) {
+  int size = kThreads;
+  while (size < count) size *= 2;
+  for (int i = count + static_cast<int>(threadIdx.x); i < size; i += kThreads) sh.cand[i] = 0;
+  __syncthreads();
+  for (int run = 2; run <= size; run *= 2) {
+    for (int apart = run / 2; apart > 0; apart /= 2) {
+      for (int p = threadIdx.x; p < size / 2; p += kThreads) {
+        const int i = (p & ~(apart - 1)) * 2 + (p & (apart - 1)), j = i + apart;
+        const uint64_t a = sh.cand[i], b = sh.cand[j];
+        if (((i & run) == 0) == (a < b)) {
+          sh.cand[i] = b;
+          sh.cand[j] = a;
+        }
+      }
+      __syncthreads();
+    }
+  }
 }
 
 // A row that is left out, and one with a bad status.
@@ -416,22 +538,20 @@ __device__ __forceinline__ void finish_topn(const T* row, int64_t r, int vocab, 
   }
   const int n = min(o.n, vocab);
   uint64_t key = 0;
-  int place = n, rest_place = n;
+  int place = n;
+  bool sorted = false;
   if (n > 0) {
-    find_candidates(row, vocab, gs, groups, n, sh);
+    find_candidates(row, vocab, gs, groups, st.m, n, sh);
     const int count = sh.n_cand;
-    if (tid < count) {
+    sorted = count > kThreads;
+    if (sorted) {
+      sort_candidates(count, sh);
+      if (tid == 0) sh.first_id = static_cast<int>(0xffffffffu - static_cast<uint32_t>(sh.cand[0]));
+    } else if (tid < count) {
       key = sh.cand[tid];
       place = 0;
       for (int k = 0; k < count; ++k) place += sh.cand[k] > key ? 1 : 0;
       if (place == 0) sh.first_id = static_cast<int>(0xffffffffu - static_cast<uint32_t>(key));
-    }
-    for (int c = tid + kThreads; c < count; c += kThreads) {
-      const uint64_t other = sh.cand[c];
-      rest_place = 0;
-      for (int k = 0; k < count; ++k) rest_place += sh.cand[k] > other ? 1 : 0;
-      if (rest_place == 0)
-        sh.first_id = static_cast<int>(0xffffffffu - static_cast<uint32_t>(other));
     }
     __syncthreads();
   }
@@ -465,21 +585,15 @@ __device__ __forceinline__ void finish_topn(const T* row, int64_t r, int vocab, 
     if (o.row_status) o.row_status[r] = TS_ROW_OK;
   }
   auto put = [&](int at, uint64_t k) {
-    if (at >= n) return;
     const float x = number_of(static_cast<uint32_t>(k >> 32));
     o.topn_ids[r * o.n + at] = static_cast<int>(0xffffffffu - static_cast<uint32_t>(k));
     o.topn_logprobs[r * o.n + at] =
         static_cast<float>((static_cast<double>(x) - st.m) * sc.inv_t - ln_s);
   };
-  if (n > 0) {
-    const int count = sh.n_cand;
-    if (tid < count) put(place, key);
-    for (int c = tid + kThreads; c < count; c += kThreads) {
-      const uint64_t other = sh.cand[c];
-      int at = 0;
-      for (int k = 0; k < count; ++k) at += sh.cand[k] > other ? 1 : 0;
-      put(at, other);
-    }
+  if (sorted) {
+    for (int i = tid; i < n; i += kThreads) put(i, sh.cand[i]);
+  } else if (place < n) {
+    put(place, key);
   }
   for (int i = n + tid; i < o.n; i += kThreads) {
     o.topn_ids[r * o.n + i] = -1;
@@ -502,7 +616,8 @@ __global__ __launch_bounds__(kThreads, 4) void topn_whole_kernel(
     const T* rx = x + r * ld;
     const float xt = has_token ? static_cast<float>(rx[min(token, vocab - 1)]) : INFINITY;
     float* gr = groups + r * gs.per_row;
-    TopVisit<T> visit = make_visit<T>(stats_shape(rx, vocab), o.n > 0 ? gr : nullptr, 0, xt, token);
+    TopVisit<T> visit = make_visit<T>(stats_shape(rx, vocab), o.n > 0 ? gr : nullptr, gs.bits, 0,
+                                      xt, token);
     RowStats st;
     st.m = -INFINITY;
     st.s = st.u = 0.0;
@@ -530,9 +645,9 @@ __global__ __launch_bounds__(kThreads) void topn_stats_kernel(
     if (tokens && token < 0) continue;
     const T* rx = x + static_cast<int64_t>(row) * ld;
     const float xt = tokens ? static_cast<float>(rx[min(token, vocab - 1)]) : INFINITY;
-    float* gr = groups + static_cast<int64_t>(row) * gs.per_row + chunk * gs.slabs * kSlabGroups;
+    float* gr = groups + static_cast<int64_t>(row) * gs.per_row + chunk * gs.slabs * gs.per_slab();
     TopVisit<T> visit = make_visit<T>(stats_shape(rx, vocab), want_groups ? gr : nullptr,
-                                      chunk * cut.len, xt, token);
+                                      gs.bits, chunk * cut.len, xt, token);
     float m = -INFINITY;
     double s = 0.0, u = 0.0;
     row_stats<T, ENT, kThreads>(rx, vocab, chunk * cut.len, (chunk + 1) * cut.len,
@@ -875,7 +990,7 @@ TopnSpace lay_out_topn(void* base, int64_t rows, int64_t vocab) {
   for (const int vec : {Vec<float>::n, Vec<__bf16>::n}) {
     for (const Cut& cut : {cut_rows(rows, vocab, vec), whole_cut(vocab, vec)}) {
       chunks = std::max(chunks, static_cast<size_t>(cut.chunks));
-      groups = std::max(groups, static_cast<size_t>(make_groups(cut).per_row));
+      groups = std::max(groups, static_cast<size_t>(make_groups(cut, kSharedMost + 1).per_row));
     }
   }
   char* p = static_cast<char*>(base);
@@ -904,12 +1019,12 @@ hipError_t topn_t(const TokenRows& t, const TopnOut& o, void* ws, hipStream_t st
   if (t.vocab <= kShortRow) {
     const Cut cut = whole_cut(t.vocab, Vec<T>::n);
     hipLaunchKernelGGL((topn_whole_kernel<ENT, T>), dim3(grid_of(t.rows)), dim3(kThreads), 0,
-                       stream, x, t.ld, t.rows, t.vocab, t.tokens, sc, cut, make_groups(cut),
+                       stream, x, t.ld, t.rows, t.vocab, t.tokens, sc, cut, make_groups(cut, o.n),
                        w.groups, o);
     return hipGetLastError();
   }
   const Cut cut = cut_rows(t.rows, t.vocab, Vec<T>::n);
-  const Groups gs = make_groups(cut);
+  const Groups gs = make_groups(cut, o.n);
   hipLaunchKernelGGL((topn_stats_kernel<ENT, T>), dim3(grid_of(int64_t{t.rows} * cut.chunks)),
                      dim3(kThreads), 0, stream, x, t.ld, t.rows, t.vocab, t.tokens, sc, cut, gs,
                      w.groups, w.parts, w.betters, o.n > 0);

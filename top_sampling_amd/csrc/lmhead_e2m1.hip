@@ -72,8 +72,8 @@ struct Units {
 // Units whose loads a thread has on their way, a grid apart.  The grid has just these
 // for bf16 (151,936 x 4,096: 290 us to codes, 284 back, 5.5 TB/s; one unit at a time
 // in 8,192 workgroups 328 and 392) and one a thread for fp32 (60,000 x 4,096: 190 and
-// 217 us, four 202 and 277).  Stores of whole 16 bytes go past the caches (3%); fp32's
-// pairs of them must not (392 us and 217).
+// 225 us, four 202 and 277).  Stores of whole 16 bytes go past the caches (3%); fp32's
+// pairs of them must not (392 us and 225).
 constexpr int kAtOnce = 4;
 
 // A unit as it lies in memory.
