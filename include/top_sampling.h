@@ -525,8 +525,8 @@ int token_logprobs_backward_ex(const void* logits, int32_t logits_type, int64_t 
  * row takes part.  A left-out row has rank 0 and lists nothing; a bad row has rank
  * 0, ids -1 and NaN.  entropies, row_stats and row_status as in token_logprobs;
  * row_stats serve token_logprobs_backward and token_logprobs_listed_backward.
- * Rows with many equal logits beside the n-th largest, and max_logprobs above
- * 256, are read again (same results, slower).
+ * Short rows beside max_logprobs (vocab below 64 times as many) and rows with very
+ * many equal logits are read again (same results, slower).
  */
 size_t token_logprobs_topn_workspace_bytes(int64_t rows, int64_t vocab);
 int token_logprobs_topn(const void* logits, int32_t logits_type, int64_t rows, int64_t vocab,
