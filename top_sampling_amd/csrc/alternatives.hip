@@ -662,8 +662,11 @@ __global__ __launch_bounds__(kThreads) void topn_stats_kernel(
   }
 }
 
+// A row's latency from records to outputs, 9 us, is what bounds it, so the number of
+// rows on a CU counts: four with 128 registers (three with 152: 1,021 x 100,277 bf16
+// 75 us and 64, 4,000 x 40,000 118 and 108; five with 96 spill: 68 and 119).
 template <bool ENT, typename T>
-__global__ __launch_bounds__(kThreads) void topn_rows_kernel(
+__global__ __launch_bounds__(kThreads, 4) void topn_rows_kernel(
     const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,
     Scale sc, Cut cut, Groups gs, const float* __restrict__ groups,
     const Part* __restrict__ parts, const int* __restrict__ betters, TopnOut o) {
@@ -1012,10 +1015,9 @@ hipError_t topn_t(const TokenRows& t, const TopnOut& o, void* ws, hipStream_t st
   const TopnSpace w = lay_out_topn(ws, t.rows, t.vocab);
   const T* x = static_cast<const T*>(t.x);
   // Short rows take a workgroup each in one launch (4 x 4,096 16 us, 1,000 x 32,000
-  // fp32 43 and cut up 46); longer ones are cut up whatever their number: the row's
-  // outputs need 128 registers where the statistics need 80, and hold the reads up
-  // (640 x 151,936 fp32, 20 alternatives 106 us and cut up 93; 256 x 248,320 bf16 59
-  // and 48).
+  // fp32 40 and cut up 46).  Longer ones have their outputs in a second launch, whatever
+  // their number: those need 128 registers where the statistics need 80, and hold the
+  // reads up (640 x 151,936 fp32, 20 alternatives 100 us in one launch, 89 in two).
   if (t.vocab <= kShortRow) {
     const Cut cut = whole_cut(t.vocab, Vec<T>::n);
     hipLaunchKernelGGL((topn_whole_kernel<ENT, T>), dim3(grid_of(t.rows)), dim3(kThreads), 0,
@@ -1023,7 +1025,11 @@ hipError_t topn_t(const TokenRows& t, const TopnOut& o, void* ws, hipStream_t st
                        w.groups, o);
     return hipGetLastError();
   }
-  const Cut cut = cut_rows(t.rows, t.vocab, Vec<T>::n);
+  // The statistics take whole bf16 rows where there are many (512 x 151,936 62 us, cut
+  // up 68; 1,021 x 100,277 75 and 85; 400 x 100,000 40 and 38); fp32 ones never (1,000 x
+  // 60,000 71 and 67).
+  const Cut cut = Vec<T>::n > 4 && t.rows >= 512 ? whole_cut(t.vocab, Vec<T>::n)
+                                                 : cut_rows(t.rows, t.vocab, Vec<T>::n);
   const Groups gs = make_groups(cut, o.n);
   hipLaunchKernelGGL((topn_stats_kernel<ENT, T>), dim3(grid_of(int64_t{t.rows} * cut.chunks)),
                      dim3(kThreads), 0, stream, x, t.ld, t.rows, t.vocab, t.tokens, sc, cut, gs,
