@@ -534,3 +534,20 @@ def test_selection(dtype, vocab, n):
         want = (-x.double() + 0.0).argsort(dim=-1, stable=True)[:, :k].int()
         assert torch.equal(got[:, :k], want), kind
         assert (got[:, k:] == -1).all(), kind
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("n", [7, 140])
+def test_many_long_rows(dtype, n):
+    import torch
+
+    import top_sampling_amd as ts
+
+    rows, vocab = 520, 33333
+    say("many long rows", dtype, n)
+    logits, x = make_logits(rows, vocab, dtype, 3, n)
+    tok = allowed_tokens(x, 5)
+    tok[::50] = -1
+    got = ts.token_logprobs_topn(logits, to_dev(tok, torch.int32), n, 0.7, entropies=True)
+    torch.cuda.synchronize()
+    check_topn(got, ref.topn(x, tok, n, 0.7), n)
