@@ -553,8 +553,8 @@ int token_logprobs_topn(const void* logits, int32_t logits_type, int64_t rows, i
  *   dL/dlogits[r, j] = (sum_{i: id_i = j} dL/dlp_i - p_j sum_i dL/dlp_i
  *                       - dL/dH p_j (ln p_j + H)) / temperature.
  * listed_ids, temperature and the logits are the forward call's, and row_stats
- * and logprobs its outputs.  A row whose gradients are all 0 gives a row of zeros
- * without reading its logits.  No workspace.
+ * and logprobs its outputs.  A row whose gradients are all 0 gives a row of zeros,
+ * whatever its logits hold.  No workspace.
  */
 #define TS_MAX_LISTED 1024   /* largest accepted n_listed */
 size_t token_logprobs_listed_workspace_bytes(int64_t rows, int64_t vocab);

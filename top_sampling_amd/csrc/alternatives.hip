@@ -868,9 +868,9 @@ struct DenseGrad {
 // listed several times is written once, by its first place, from the sum of its
 // gradients.  The first slab's loads are on their way while the row's coefficients
 // are worked out (1,021 x 100,277 bf16, 64 listed tokens and the entropy: 127 us
-// without that, 85 so).  640 x 151,936 fp32 takes 135 us (5.8 TB/s); longer chunks, a
-// row a workgroup at the end of it, are slower (167), as are five workgroups a CU
-// (146).
+// without that, 85 so).  640 x 151,936 fp32 takes 125 us (6.2 TB/s; 135 beside other
+// inputs' calls); longer chunks, a row a workgroup at the end of it, are slower (167),
+// as are five workgroups a CU (146).
 template <typename T, bool ENT>
 __global__ __launch_bounds__(kThreads, 4) void listed_grad_kernel(
     const T* x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ ids, Scale sc,
