@@ -664,7 +664,8 @@ __global__ __launch_bounds__(kThreads) void topn_stats_kernel(
 
 // A row's latency from records to outputs, 9 us, is what bounds it, so the number of
 // rows on a CU counts: four with 128 registers (three with 152: 1,021 x 100,277 bf16
-// 75 us and 64, 4,000 x 40,000 118 and 108; five with 96 spill: 68 and 119).
+// 75 us and 64, 4,000 x 40,000 118 and 108; five with 96 spill: 68 and 119).  A wave a row, four rows
+// a workgroup, takes longer yet (640 x 151,936 fp32, 20 alternatives 117 us and 85).
 template <bool ENT, typename T>
 __global__ __launch_bounds__(kThreads, 4) void topn_rows_kernel(
     const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,
@@ -868,9 +869,8 @@ struct DenseGrad {
 // listed several times is written once, by its first place, from the sum of its
 // gradients.  The first slab's loads are on their way while the row's coefficients
 // are worked out (1,021 x 100,277 bf16, 64 listed tokens and the entropy: 127 us
-// without that, 85 so).  640 x 151,936 fp32 takes 125 us (6.2 TB/s; 135 beside other
-// inputs' calls); longer chunks, a row a workgroup at the end of it, are slower (167),
-// as are five workgroups a CU (146).
+// without that, 85 so).  640 x 151,936 fp32 takes 125 us (6.2 TB/s); with a row
+// a workgroup 167 where this took 135, with five workgroups a CU 146.
 template <typename T, bool ENT>
 __global__ __launch_bounds__(kThreads, 4) void listed_grad_kernel(
     const T* x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ ids, Scale sc,
