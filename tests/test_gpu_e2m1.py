@@ -247,3 +247,15 @@ def test_other_stream_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert np.array_equal(_np(out), ref.logits(_np(x), ref.unpack(_np(w)), _np(s)))
+
+
+@pytest.mark.parametrize("groups", range(7, 42))
+def test_projection_every_row_length(groups, tile):
+    """Whole numbers, as above; every remainder of a row's scales over what is
+    loaded of them at a time, the last rows at the buffer's end."""
+    gen = torch.Generator().manual_seed(groups)
+    for rows, vocab in ((40, 70), (70, 300)):
+        w, s = _codes(vocab, 32 * groups, gen, 127, 129)
+        x = torch.randint(-2, 3, (rows, 32 * groups), generator=gen).to(torch.bfloat16).cuda()
+        got = ts.lmhead_logits_local_e2m1(x, w, s)
+        assert np.array_equal(_np(got), ref.logits(_np(x), ref.unpack(_np(w)), _np(s))), rows

@@ -496,11 +496,39 @@ __device__ __forceinline__ void store_output(const f32x16 (&acc)[TM][TN], uint8_
 // of a step takes the i-th eight entries of each lane's group, so its hidden
 // fragment is chunk 4 (l / 32) + i.  A wave has all of the tile's hidden rows, so the
 // conversions (four instructions a fragment, two to five products) are made once.
-// Bound by the matrix cores: 640 x 4,096 x 151,936 takes 682 us (1.17 PFLOP/s; the
+// Bound by the matrix cores: 640 x 4,096 x 151,936 takes 662 us (1.20 PFLOP/s; the
 // bf16 projection 720).  Few row tiles are bound by what a step waits for: a load of
 // codes has 32 bytes of each of 32 rows, and the line's other pieces have to outlive
-// the step in the caches (64 rows past the caches: 262 us, through them 164).
-template <int BM, int BN, int NW, int AHEAD>
+// the step in the caches (64 rows past the caches: 262 us, through them 164, and 141
+// since the scales come several at a time).
+// Scales come several groups at a time, 16 for 64 rows and 8 for more, where 16 take
+// registers that are not there (rows of that many groups; us with 16, 8 and, as a
+// shorter row has them, a byte a step: 640 x 4,096 x 151,936 748, 671 and 705; 256 rows
+// 310, 309 and 337; 64 x 2,560 x 100,000 59, 65 and 70).
+template <int BM>
+constexpr int kScales = BM <= 64 ? 16 : 8;
+
+template <int WORDS>
+using Words = uint32_t __attribute__((ext_vector_type(WORDS)));
+
+// Scales from byte `bytes` (less than 4 WORDS) on, or from the one after it.
+template <int WORDS>
+__device__ __forceinline__ Words<WORDS> scales_from(Words<WORDS> w, int bytes, int one) {
+  auto word = [&](int i) { return i < WORDS ? w[i] : 0u; };
+  for (; bytes >= 4; bytes -= 4) {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) w[i] = word(i + 1);
+  }
+  const int by = 8 * (bytes + one);  // up to 32
+  Words<WORDS> to;
+#pragma unroll
+  for (int i = 0; i < WORDS; ++i)
+    to[i] = static_cast<uint32_t>((static_cast<uint64_t>(word(i + 1)) << 32 | w[i]) >> by);
+  return to;
+}
+
+// WIDE: the row has kScales<BM> groups or more.
+template <int BM, int BN, int NW, int AHEAD, bool WIDE>
 __global__ __launch_bounds__(64 * NW, 2) void lmhead_e2m1_tiles_kernel(
     const uint16_t* __restrict__ X, int64_t ldx, E2m1Rows w, float* __restrict__ C, int64_t ldc,
     int M, int N, int K, int tiles_m, int tiles_total, int tiles_per_xcd, int vec_out) {
@@ -509,7 +537,7 @@ __global__ __launch_bounds__(64 * NW, 2) void lmhead_e2m1_tiles_kernel(
   constexpr int RING = AHEAD + 1;
   constexpr int STAGE = BM * 128;
   constexpr int A_LOADS = BM / 8 / NW;
-  constexpr int W_LOADS = 2 * TN;  // codes and scales
+  constexpr int W_LOADS = WIDE ? TN : 2 * TN;  // codes, and scales if each step has its own
   constexpr int SCRATCH = NW * kTileStoreFloats * 4;
   static_assert(BM / 8 % NW == 0, "blocks must split evenly over the waves");
   static_assert(BM % 32 == 0 && WN % 32 == 0, "wave tile of whole 32x32 blocks");
@@ -564,7 +592,32 @@ __global__ __launch_bounds__(64 * NW, 2) void lmhead_e2m1_tiles_kernel(
   }
 
   u32x4 code[RING][TN];
-  uint32_t scale[RING][TN];
+  uint32_t scale[RING][TN];  // of a step; WIDE: of several steps
+  constexpr int SCALES = kScales<BM>, SWORDS = SCALES / 4;
+  typedef Words<SWORDS> ScalesU __attribute__((aligned(1)));
+  Words<SWORDS> scales[TN], next_scales[TN];
+  auto load_scales = [&](int ks) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+      next_scales[j] = *reinterpret_cast<const ScalesU*>(sp[j] + min(2 * ks, groups - SCALES));
+  };
+  // Before step ks: its scales are the first two bytes, this lane's the first.
+  auto turn_scales = [&](int ks) __attribute__((always_inline)) {
+    if (ks % (SCALES / 2) == 0) {
+      const int back = 2 * ks - min(2 * ks, groups - SCALES);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) scales[j] = scales_from<SWORDS>(next_scales[j], back, fhalf);
+      load_scales(ks + SCALES / 2);
+    } else {
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+#pragma unroll
+        for (int i = 0; i < SWORDS; ++i)
+          scales[j][i] = __builtin_amdgcn_alignbit(i + 1 < SWORDS ? scales[j][i + 1] : 0u,
+                                                   scales[j][i], 16);
+      }
+    }
+  };
   // The loads of a step, in an order that the waits count on: the hidden rows
   // first, then codes and scales, and none across the ends.
   auto load_step = [&](int ks, int slot) __attribute__((always_inline)) {
@@ -576,7 +629,7 @@ __global__ __launch_bounds__(64 * NW, 2) void lmhead_e2m1_tiles_kernel(
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
       code[slot][j] = *reinterpret_cast<const u32x4*>(wp[j] + g * 16);
-      scale[slot][j] = sp[j][g];
+      if (!WIDE) scale[slot][j] = sp[j][g];
     }
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -587,7 +640,7 @@ __global__ __launch_bounds__(64 * NW, 2) void lmhead_e2m1_tiles_kernel(
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
       now[j] = code[slot][j];
-      sc[j] = scale_of(scale[slot][j]);
+      sc[j] = scale_of(WIDE ? scales[j][0] & 255u : scale[slot][j]);
       if (half && fhalf) {
         now[j] = u32x4{0, 0, 0, 0};
         sc[j] = 1.0f;
@@ -612,14 +665,17 @@ __global__ __launch_bounds__(64 * NW, 2) void lmhead_e2m1_tiles_kernel(
     }
   };
 
+  if (WIDE) load_scales(0);
 #pragma unroll
   for (int u = 0; u < AHEAD; ++u) load_step(u, u);
   int ks = 0;
   for (; ks + RING <= full_steps; ks += RING) {
 #pragma unroll
     for (int u = 0; u < RING; ++u) {
-      // Behind the step's hidden rows: its codes and scales, and AHEAD - 1 steps.
+      // Behind the step's hidden rows: its codes and scales, and AHEAD - 1 steps (a load
+      // of several scales among them makes the wait longer than it need be).
       wait_stage<W_LOADS + (AHEAD - 1) * (A_LOADS + W_LOADS)>();
+      if (WIDE) turn_scales(ks + u);
       load_step(ks + u + AHEAD, (u + AHEAD) % RING);
       multiply(u, false);
     }
@@ -629,6 +685,7 @@ __global__ __launch_bounds__(64 * NW, 2) void lmhead_e2m1_tiles_kernel(
   for (int u = 0; u < RING; ++u) {
     if (u < rest) {
       wait_stage<0>();
+      if (WIDE) turn_scales(ks + u);
       if (u == 0) load_step(ks + AHEAD, AHEAD % RING);
       multiply(u, ks + u >= full_steps);
     }
@@ -654,7 +711,8 @@ struct Projection {
   int rows, vocab, hidden_dim;
 };
 
-template <int NT, int NS, int VT, int AHEAD>
+// ONE: the row is one part.
+template <int NT, int NS, int VT, int AHEAD, bool ONE>
 hipError_t launch_few(const Projection& p, hipStream_t stream) {
   const int shares = (p.hidden_dim - 1) / (NS * kStep) + 1;
   const int parts = (shares - 1) / kFewWaves + 1, waves = (shares - 1) / parts + 1;
@@ -667,9 +725,11 @@ hipError_t launch_few(const Projection& p, hipStream_t stream) {
                        tiles, parts, rows_take_vector_stores(p.logits, p.ld_logits));
     return hipGetLastError();
   };
-  if (parts > 1)
-    return whole ? launch(lmhead_e2m1_few_kernel<NT, NS, VT, AHEAD, true, true>)
-                 : launch(lmhead_e2m1_few_kernel<NT, NS, VT, AHEAD, false, true>);
+  if constexpr (!ONE) {
+    if (parts > 1)
+      return whole ? launch(lmhead_e2m1_few_kernel<NT, NS, VT, AHEAD, true, true>)
+                   : launch(lmhead_e2m1_few_kernel<NT, NS, VT, AHEAD, false, true>);
+  }
   return whole ? launch(lmhead_e2m1_few_kernel<NT, NS, VT, AHEAD, true, false>)
                : launch(lmhead_e2m1_few_kernel<NT, NS, VT, AHEAD, false, false>);
 }
@@ -679,14 +739,18 @@ hipError_t launch_tiles(const Projection& p, hipStream_t stream) {
   const int tiles_m = (p.rows - 1) / BM + 1, tiles_n = (p.vocab - 1) / BN + 1;
   const int total = tiles_m * tiles_n;
   const int per_xcd = (total + kXcds - 1) / kXcds;
-  hipLaunchKernelGGL((lmhead_e2m1_tiles_kernel<BM, BN, NW, AHEAD>), dim3(per_xcd * kXcds),
-                     dim3(64 * NW), 0, stream, p.hidden, p.ld_hidden, p.w, p.logits, p.ld_logits,
-                     p.rows, p.vocab, p.hidden_dim, tiles_m, total, per_xcd,
-                     rows_take_vector_stores(p.logits, p.ld_logits));
-  return hipGetLastError();
+  auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(per_xcd * kXcds), dim3(64 * NW), 0, stream, p.hidden,
+                       p.ld_hidden, p.w, p.logits, p.ld_logits, p.rows, p.vocab, p.hidden_dim,
+                       tiles_m, total, per_xcd, rows_take_vector_stores(p.logits, p.ld_logits));
+    return hipGetLastError();
+  };
+  return p.hidden_dim >= kScales<BM> * kE2m1Group
+             ? launch(lmhead_e2m1_tiles_kernel<BM, BN, NW, AHEAD, true>)
+             : launch(lmhead_e2m1_tiles_kernel<BM, BN, NW, AHEAD, false>);
 }
 
-constexpr int kFewRows = 64;
+constexpr int kFewRows = 32;
 
 // Shares of 512 entries a wave, of 256 where the row is short or the hidden rows
 // many, of 1,024 where a row would take two parts.  Two tiles of rows at once where
@@ -697,34 +761,35 @@ constexpr int kFewRows = 64;
 hipError_t launch_few_rows(const Projection& p, hipStream_t stream) {
   const int k = p.hidden_dim;
   if (p.rows <= 16) {
-    if (k <= 1024) return launch_few<1, 2, 4, 1>(p, stream);
-    if (k <= 7 * 512) return launch_few<1, 4, 2, 1>(p, stream);
-    return k <= 8 * 512 ? launch_few<1, 4, 1, 2>(p, stream) : launch_few<1, 8, 1, 1>(p, stream);
+    if (k <= 1024) return launch_few<1, 2, 4, 1, true>(p, stream);
+    if (k <= 7 * 512) return launch_few<1, 4, 2, 1, true>(p, stream);
+    return k <= 8 * 512 ? launch_few<1, 4, 1, 2, true>(p, stream)
+                        : launch_few<1, 8, 1, 1, false>(p, stream);
   }
-  if (p.rows <= 32)
-    return k <= 1024 ? launch_few<2, 2, 2, 2>(p, stream) : launch_few<2, 4, 1, 2>(p, stream);
-  return p.rows <= 48 ? launch_few<3, 2, 2, 1>(p, stream) : launch_few<4, 2, 1, 3>(p, stream);
+  return k <= 1024 ? launch_few<2, 2, 2, 2, true>(p, stream)
+                   : launch_few<2, 4, 1, 2, false>(p, stream);
 }
 
-// The kernel for few rows up to 32 of them, and up to 64 where its shares of 256
-// entries fill the workgroups and come to few parts: 64 rows, us, it and 64 x 256
-// tiles: 4,096 x 151,936 125 and 164; 2,048 x 100,000 45 and 54; 5,120 x 100,000 133
-// and 140; 2,560 x 100,000 78 and 64; 8,192 x 60,000 122 and 106; 1,024 x 100,000 34
-// and 29.  64 x 128 tiles where 256 columns leave CUs without one (64 x 4,096 x
-// 31,000: 32 and 49).  Beyond, 128 or 160 rows a tile, whichever takes less: a tile of
-// 160 rows takes 1.13 times one of 128 (256 x 4,096 x 151,936 307 us, 320 355, 640 682
-// and with 128 rows 707).  320 x 256 tiles of eight waves, one workgroup a CU, take
-// 702 there; two smaller ones overlap one's store with the other's products.
+// The kernel for few rows up to 32 of them, unless the row is short, us, it and 64-row
+// tiles: 32 x 4,096 x 151,936 91 and 132, 36 120 and 131, 48 132 and 130, 64 151 and
+// 141; 32 x 1,024 x 100,000 23 and 22, 32 x 512 20 and 14, 16 x 512 14 and 14, 16 x 256 14 and
+// 10.
+// Up to 64, 64 x 256 tiles, or 64 x 128 where those would leave a quarter of the CUs
+// without one (64 x 4,096 x 31,000: 34 and 26; 48 x 6,144 x 60,000 81 and 84).  Beyond,
+// 128 or 160 rows a tile, whichever takes less: a tile of 160 rows takes 1.2 times one of
+// 128 (4,096 x 151,936, 160 and 128 rows a tile: 160 rows 228 and 299, 256 364 and 306,
+// 320 365 and 417, 640 659 and 669; 1,024 x 100,000 730 and 711), and 64 again where
+// they are too few (128 x 4,096 x 31,000 41 and 56; 128 x 60,000 93 and 84).
 int choose(const Projection& p) {
-  if (p.rows <= 32) return 1;
-  if (p.rows <= kFewRows) {
-    const int shares = (p.hidden_dim - 1) / (2 * kStep) + 1;
-    const int parts = (shares - 1) / kFewWaves + 1, waves = (shares - 1) / parts + 1;
-    if (waves >= 7 && parts <= 3) return 1;
-    return (p.vocab - 1) / 256 + 1 < kCus ? 2 : 3;
+  if (p.rows <= kFewRows && p.hidden_dim > 32 * p.rows) return 1;
+  const int64_t wide = (p.vocab - 1) / 256 + 1;
+  auto fill = [&](int64_t rows) { return (p.rows + rows - 1) / rows * wide >= kCus * 3 / 4; };
+  if (p.rows > 64) {
+    const int64_t by128 = (p.rows + int64_t{127}) / 128, by160 = (p.rows + int64_t{159}) / 160;
+    const bool tall = by160 * 6 < by128 * 5;
+    if (fill(tall ? 160 : 128)) return tall ? 5 : 4;
   }
-  const int64_t by128 = (p.rows + int64_t{127}) / 128, by160 = (p.rows + int64_t{159}) / 160;
-  return by128 * 8 <= by160 * 9 ? 4 : 5;
+  return fill(64) ? 3 : 2;
 }
 
 }  // namespace
