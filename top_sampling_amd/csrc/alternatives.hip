@@ -664,8 +664,9 @@ __global__ __launch_bounds__(kThreads) void topn_stats_kernel(
 
 // A row's latency from records to outputs, 9 us, is what bounds it, so the number of
 // rows on a CU counts: four with 128 registers (three with 152: 1,021 x 100,277 bf16
-// 75 us and 64, 4,000 x 40,000 118 and 108; five with 96 spill: 68 and 119).  A wave a row, four rows
-// a workgroup, takes longer yet (640 x 151,936 fp32, 20 alternatives 117 us and 85).
+// 75 us and 64, 4,000 x 40,000 118 and 108; five with 96 spill: 68 and 119).  A wave
+// a row, four rows a workgroup, takes longer yet (640 x 151,936 fp32, 20 alternatives
+// 117 us and 85).
 template <bool ENT, typename T>
 __global__ __launch_bounds__(kThreads, 4) void topn_rows_kernel(
     const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,

@@ -496,11 +496,11 @@ __device__ __forceinline__ void store_output(const f32x16 (&acc)[TM][TN], uint8_
 // of a step takes the i-th eight entries of each lane's group, so its hidden
 // fragment is chunk 4 (l / 32) + i.  A wave has all of the tile's hidden rows, so the
 // conversions (four instructions a fragment, two to five products) are made once.
-// Bound by the matrix cores: 640 x 4,096 x 151,936 takes 662 us (1.20 PFLOP/s; the
-// bf16 projection 720).  Few row tiles are bound by what a step waits for: a load of
-// codes has 32 bytes of each of 32 rows, and the line's other pieces have to outlive
-// the step in the caches (64 rows past the caches: 262 us, through them 164, and 141
-// since the scales come several at a time).
+// Bound by the matrix cores: 640 x 4,096 x 151,936 takes 628 to 662 us (1.2 PFLOP/s and
+// more; the bf16 projection 720).  Few row tiles are bound by what a step waits for (64
+// rows past the caches 262 us, through them 164, 122 to 141 since the scales come
+// several at a time).  Without gain there: the codes of two steps in pieces of 64 bytes,
+// those of four at once, tiles that begin at different steps.
 // Scales come several groups at a time, 16 for 64 rows and 8 for more, where 16 take
 // registers that are not there (rows of that many groups; us with 16, 8 and, as a
 // shorter row has them, a byte a step: 640 x 4,096 x 151,936 748, 671 and 705; 256 rows
