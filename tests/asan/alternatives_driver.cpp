@@ -129,7 +129,8 @@ int main() {
   expect(listed(4, 100, I, 3, 1.0, F, A, 8), TS_EWORKSPACE, "listed small workspace");
   expect(listed(0, 100, nullptr, 3, 1.0, nullptr, nullptr, 0), TS_OK, "listed no rows");
   expect(listed_backward(0, F, nullptr, nullptr, A, 100), TS_EINVAL, "backward 0");
-  expect(listed_backward(3, nullptr, nullptr, nullptr, A, 100), TS_EINVAL, "backward null logprobs");
+  expect(listed_backward(3, nullptr, nullptr, nullptr, A, 100), TS_EINVAL,
+         "backward null logprobs");
   expect(listed_backward(3, F, nullptr, F, A, 100), TS_EINVAL, "backward no entropies");
   expect(listed_backward(3, F, nullptr, nullptr, nullptr, 100), TS_EINVAL, "backward null grad");
   expect(listed_backward(3, F, nullptr, nullptr, A, 99), TS_EINVAL, "backward ld_grad");
@@ -137,7 +138,8 @@ int main() {
   expect(listed_backward(3, odd_f, nullptr, nullptr, A, 100), TS_EUNSUPPORTED, "backward align");
 
   // a record of 24 and a count of 4 bytes a row, and an entry of its groups
-  for (int64_t rows : {int64_t{0}, int64_t{1}, int64_t{640}, int64_t{1} << 20, (int64_t{1} << 31) - 1})
+  for (int64_t rows :
+       {int64_t{0}, int64_t{1}, int64_t{640}, int64_t{1} << 20, (int64_t{1} << 31) - 1})
     for (int64_t vocab : {int64_t{1}, int64_t{4097}, int64_t{151936}, (int64_t{1} << 31) - 1}) {
       const size_t least = static_cast<size_t>(rows) * (28 + 4 * (vocab / 32));
       if (token_logprobs_topn_workspace_bytes(rows, vocab) < least ||

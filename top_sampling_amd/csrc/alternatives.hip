@@ -360,7 +360,8 @@ __device__ __forceinline__ void add_equal(const T* row, int vocab, uint32_t numb
 // that comes before one that is missing; n_cand in no order.  By the whole workgroup.
 template <typename T>
 __device__ __forceinline__ void find_candidates(const T* row, int vocab, const Groups& gs,
-                                                const float* groups, float st_m, int n, TopShared& sh) {
+                                                const float* groups, float st_m, int n,
+                                                TopShared& sh) {
   constexpr int VN = Vec<T>::n;
   const int tid = threadIdx.x;
   const Shape f = stats_shape(row, vocab);
@@ -460,16 +461,17 @@ __device__ __forceinline__ void find_candidates(const T* row, int vocab, const G
   }
   // Few groups beside n: rows shorter than 32 n (fp32) or 64 n (bf16) entries, which are
   // gone through again (1,000 x 4,000 fp32, n = 300 82 us).
-  const uint64_t bound = bound_by_steps(uint64_t{0}, ~uint64_t{0}, n, kCandidates, sh, [&](auto use) {
+  auto each_entry = [&](auto use) {
     for (int64_t i = tid; i < vocab; i += kThreads)
       use(entry_key(static_cast<float>(row[i]), static_cast<int>(i)));
-  });
+  };
+  const uint64_t bound =
+      bound_by_steps(uint64_t{0}, ~uint64_t{0}, n, kCandidates, sh, each_entry);
   if (tid == 0) sh.n_cand = 0;
   __syncthreads();
-  for (int64_t i = tid; i < vocab; i += kThreads) {
-    const uint64_t key = entry_key(static_cast<float>(row[i]), static_cast<int>(i));
+  each_entry([&](uint64_t key) {
     if (key >= bound) sh.cand[atomicAdd(&sh.n_cand, 1)] = key;
-  }
+  });
   __syncthreads();
 }
 

@@ -7,7 +7,8 @@
 // two to a byte, the even column in the low half.  4.25 bits an entry.
 //   quantize   e = least integer >= -127 with max|x| <= 7 * 2^e: what lies
 //              above 6 s then loses at most the half step of E2M1's last
-//              binade (and e <= 125, so that no finite entry becomes infinite); code = the value nearest x / s, ties to the even code
+//              binade (and e <= 125, so that no finite entry becomes infinite);
+//              code = the value nearest x / s, ties to the even code
 //   project    logits[r, v] = sum_h hidden[r, h] * 2^e[v, h / 32] * q[v, h]
 // A power of two times an E2M1 value has two significant bits, so it is a bf16
 // number and its products with bf16 are exact in fp32: the lm_head becomes
@@ -623,7 +624,8 @@ __global__ __launch_bounds__(64 * NW, 2) void lmhead_e2m1_tiles_kernel(
   auto load_step = [&](int ks, int slot) __attribute__((always_inline)) {
     ks = min(ks, steps - 1);
     __builtin_amdgcn_sched_barrier(0);
-    issue_hidden<A_LOADS, NW>(hidden, at, back, lds + slot * STAGE, wave, ks * kBK, ks >= full_steps);
+    issue_hidden<A_LOADS, NW>(hidden, at, back, lds + slot * STAGE, wave, ks * kBK,
+                              ks >= full_steps);
     __builtin_amdgcn_sched_barrier(0);
     const int g = min(2 * ks + fhalf, groups - 1);
 #pragma unroll
