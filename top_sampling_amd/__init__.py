@@ -903,6 +903,13 @@ def _group_rows(t, name, dtype, rows, width, device):
     return max(ld, width) if rows > 1 else width
 
 
+def _group_out(t, name, dtype, rows, width, device):
+    """An output (checked, or a new one) and its leading dimension."""
+    if t is None:
+        return torch.empty(rows, width, dtype=dtype, device=device), width
+    return t, _group_rows(t, name, dtype, rows, width, device)
+
+
 def _values_type(dtype):
     kind = _LOGITS_TYPES.get(dtype)
     if kind is None:
@@ -923,12 +930,9 @@ def quantize_groups_e2m1(x, codes=None, scales=None, stream=None):
         raise ValueError(f"cols {cols} is no multiple of {E2M1_GROUP}")
     ld_x = _group_rows(x, "x", x.dtype, rows, cols, dev)
     with _OnDevice(dev, stream) as s:
-        if codes is None:
-            codes = torch.empty(rows, cols // 2, dtype=torch.uint8, device=dev)
-        if scales is None:
-            scales = torch.empty(rows, cols // E2M1_GROUP, dtype=torch.uint8, device=dev)
-        ld_codes = _group_rows(codes, "codes", torch.uint8, rows, cols // 2, dev)
-        ld_scales = _group_rows(scales, "scales", torch.uint8, rows, cols // E2M1_GROUP, dev)
+        codes, ld_codes = _group_out(codes, "codes", torch.uint8, rows, cols // 2, dev)
+        scales, ld_scales = _group_out(scales, "scales", torch.uint8, rows, cols // E2M1_GROUP,
+                                       dev)
         _check(lib.quantize_groups_e2m1(x.data_ptr(), kind, rows, cols, ld_x, codes.data_ptr(),
                                         ld_codes, scales.data_ptr(), ld_scales, s))
     return codes, scales
@@ -947,9 +951,7 @@ def dequantize_groups_e2m1(codes, scales, dtype=torch.bfloat16, out=None, stream
     ld_scales = _group_rows(scales, "scales", torch.uint8, rows, cols // E2M1_GROUP, dev)
     kind = _values_type(dtype if out is None else out.dtype)
     with _OnDevice(dev, stream) as s:
-        if out is None:
-            out = torch.empty(rows, cols, dtype=dtype, device=dev)
-        ld_out = _group_rows(out, "out", out.dtype, rows, cols, dev)
+        out, ld_out = _group_out(out, "out", dtype if out is None else out.dtype, rows, cols, dev)
         _check(lib.dequantize_groups_e2m1(codes.data_ptr(), rows, cols, ld_codes,
                                           scales.data_ptr(), ld_scales, out.data_ptr(), kind,
                                           ld_out, s))
@@ -973,9 +975,7 @@ def lmhead_logits_local_e2m1(hidden, lm_head, lm_head_scales, out=None, stream=N
     ld_scales = _group_rows(lm_head_scales, "lm_head_scales", torch.uint8, vocab,
                             h // E2M1_GROUP, dev)
     with _OnDevice(dev, stream) as s:
-        if out is None:
-            out = torch.empty(rows, vocab, dtype=torch.float32, device=dev)
-        ld_out = _group_rows(out, "out", torch.float32, rows, vocab, dev)
+        out, ld_out = _group_out(out, "out", torch.float32, rows, vocab, dev)
         _check(lib.lmhead_logits_local_e2m1(
             hidden.data_ptr(), rows, h, ld_hidden, lm_head.data_ptr(), lm_head_scales.data_ptr(),
             vocab, ld_lm_head, ld_scales, out.data_ptr(), ld_out, s))
