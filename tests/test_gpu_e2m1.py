@@ -133,7 +133,7 @@ def test_quantize_strides(dtype):
 SHAPES = [(1, 32, 1), (1, 4096, 531), (2, 64, 33), (5, 2560, 257), (15, 96, 300), (16, 8192, 95),
           (17, 544, 129), (31, 4128, 70), (32, 256, 1000), (33, 1024, 260), (64, 160, 511),
           (65, 96, 257), (130, 2592, 300), (300, 64, 513), (321, 320, 258), (7, 8224, 40),
-          # one to four parts of a row, whole and not, and several tiles a workgroup
+          # one to three parts of a row, whole and not, and several tiles a workgroup
           (64, 6144, 300), (45, 4640, 133), (20, 9216, 77), (9, 10240, 50), (3, 1024, 70),
           (30, 512, 9001), (64, 2048, 9001), (48, 4096, 4500), (16, 1536, 17000), (33, 8192, 4200)]
 
@@ -259,3 +259,39 @@ def test_projection_every_row_length(groups, tile):
         x = torch.randint(-2, 3, (rows, 32 * groups), generator=gen).to(torch.bfloat16).cuda()
         got = ts.lmhead_logits_local_e2m1(x, w, s)
         assert np.array_equal(_np(got), ref.logits(_np(x), ref.unpack(_np(w)), _np(s))), rows
+
+
+# (rows, H, V): parts of a row x waves, whole or not, and the most tiles of 16 columns that
+# one of 256 workgroups takes.
+PARTS = [(9, 10240, 21001),  # 2 x 5 whole, 6 tiles
+         (5, 8224, 8300),    # 2 x 5, 3
+         (20, 9216, 13001),  # 3 x 6 whole, 4
+         (31, 4128, 25001),  # 2 x 5, 7
+         (18, 14336, 4500),  # 4 x 7 whole, 2
+         (2, 25600, 4200)]   # 4 x 7, 2
+
+
+@pytest.mark.parametrize("pad", [0, 3])
+@pytest.mark.parametrize("rows,h,vocab", PARTS)
+def test_projection_parts_of_rows(rows, h, vocab, pad, monkeypatch):
+    """Few rows whose entries the waves do not hold at once: the sums of one part come
+    back from the logits in the next, over several tiles a workgroup with a ragged last
+    one, into rows that take whole stores and rows that do not.  Whole numbers, as above:
+    twice a partial sum is at most 25600 * 2 * 12 * 2 < 2^24."""
+    monkeypatch.delenv("TS_GEMM_TILE", raising=False)
+    gen = torch.Generator().manual_seed(rows * h + vocab + pad)
+    w, s = _codes(vocab, h, gen, 127, 129)
+    x = torch.randint(-2, 3, (rows, h), generator=gen).to(torch.bfloat16).cuda()
+    wide = torch.full((rows, vocab + 2 * pad), float("nan"), device="cuda")
+    out = wide[:, pad:pad + vocab]
+    first = ts.lmhead_logits_local_e2m1(x, w, s, out=out).clone()
+    # Over the finished logits of another call, as a buffer that is used again.
+    ts.lmhead_logits_local_e2m1(x, w, s, out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(out, first)
+    if pad:
+        assert torch.isnan(wide[:, :pad]).all() and torch.isnan(wide[:, -pad:]).all()
+    for at in range(0, vocab, 2048):
+        part = slice(at, min(at + 2048, vocab))
+        want = ref.logits(_np(x), ref.unpack(_np(w[part])), _np(s[part]))
+        assert np.array_equal(_np(first[:, part]), want), at
