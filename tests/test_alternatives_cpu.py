@@ -196,3 +196,18 @@ def test_binding_refusals():
                  lambda: ts.token_logprobs_listed_backward(x, ids, fwd, torch.zeros(4, 3))):
         with pytest.raises(ValueError, match="GPU"):
             call()
+
+
+def test_alternatives_are_not_taken_for_the_tokens():
+    """With one alternative a row the given tokens' log-probabilities have the size of the
+    listed ones and would pass for them."""
+    import torch
+
+    x, one = torch.zeros(4, 64), torch.zeros(4, dtype=torch.int32)
+    top = ts.TokenLogprobsTopn(torch.zeros(4), one, None, one[:, None], torch.zeros(4, 1),
+                               torch.zeros(4, 2), one)
+    with pytest.raises(ValueError, match="topn_logprobs"):
+        ts.token_logprobs_listed_backward(x, top.topn_ids, top, torch.zeros(4, 1))
+    fwd = ts.TokenLogprobs(top.topn_logprobs, top.entropies, top.row_stats, top.row_status)
+    with pytest.raises(ValueError, match="GPU"):  # right in all but the device
+        ts.token_logprobs_listed_backward(x, top.topn_ids, fwd, torch.zeros(4, 1))

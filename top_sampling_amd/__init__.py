@@ -739,8 +739,14 @@ def token_logprobs_listed_backward(logits, listed_ids, forward: TokenLogprobs, g
                                    grad_logits=None, stream=None):
     """Gradient of the logits from ``grad_logprobs`` (fp32 ``[rows, n]``) and
     ``grad_entropies`` (fp32 ``[rows]`` or None), with the ``TokenLogprobs`` that
-    ``token_logprobs_listed`` gave for the same logits, ids and temperature.
-    ``grad_logits`` may be ``logits`` itself."""
+    ``token_logprobs_listed`` gave for the same logits, ids and temperature.  For the
+    alternatives ``top`` of ``token_logprobs_topn`` (``listed_ids`` its ``topn_ids``)
+    that is ``TokenLogprobs(top.topn_logprobs, top.entropies, top.row_stats,
+    top.row_status)``; ``top`` itself is refused, as its ``logprobs`` are the given
+    tokens'.  ``grad_logits`` may be ``logits`` itself."""
+    if isinstance(forward, TokenLogprobsTopn):
+        raise ValueError("the logprobs of a TokenLogprobsTopn are the given tokens': pass "
+                         "TokenLogprobs(topn_logprobs, entropies, row_stats, row_status)")
     n = _listed(logits, listed_ids)
     kind, ld = _token_rows(logits, listed_ids, n)
     rows, vocab = logits.shape
