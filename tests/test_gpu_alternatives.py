@@ -551,3 +551,20 @@ def test_many_long_rows(dtype, n):
     got = ts.token_logprobs_topn(logits, to_dev(tok, torch.int32), n, 0.7, entropies=True)
     torch.cuda.synchronize()
     check_topn(got, ref.topn(x, tok, n, 0.7), n)
+
+
+@pytest.mark.parametrize("rows", [0, 3])
+def test_outputs_that_are_not_asked_for(rows):
+    """None without tokens and without entropies, whatever the number of rows."""
+    import torch
+
+    import top_sampling_amd as ts
+
+    logits = torch.zeros(rows, 70, device="cuda")
+    got = ts.token_logprobs_topn(logits, None, 2)
+    assert got.logprobs is None and got.ranks is None and got.entropies is None
+    assert got.topn_ids.shape == got.topn_logprobs.shape == (rows, 2)
+    tok = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    got = ts.token_logprobs_topn(logits, tok, 2, entropies=True)
+    assert got.logprobs.shape == got.ranks.shape == got.entropies.shape == (rows,)
+    assert got.row_stats.shape == (rows, 2) and got.row_status.shape == (rows,)

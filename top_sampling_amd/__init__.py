@@ -682,14 +682,15 @@ def token_logprobs_topn(logits, token_ids, max_logprobs: int, temperature: float
     n, dev = int(max_logprobs), logits.device
     if n < 0 or n > TS_MAX_LOGPROBS:
         raise ValueError(f"max_logprobs {n} outside 0..{TS_MAX_LOGPROBS}")
-    given = rows if token_ids is not None else 0
+    asked = token_ids is not None
+    given = rows if asked else 0
     with _OnDevice(dev, stream) as s:
         workspace = _workspace(workspace, token_logprobs_topn_workspace_bytes(rows, vocab), dev)
         (stats, logprobs, ranks, status, ids, top, h), at = _outputs(
             (2 * rows, given, given, rows, rows * n, rows * n, rows if entropies else 0), dev)
         out = TokenLogprobsTopn(
-            logprobs if given == rows else None,
-            ranks.view(torch.int32).data if given == rows else None, h if entropies else None,
+            logprobs if asked else None, ranks.view(torch.int32).data if asked else None,
+            h if entropies else None,
             ids.view(torch.int32).view(rows, n).data, top.view(rows, n).data,
             stats.view(rows, 2).data, status.view(torch.int32).data)
         after = at + 4 * (2 * rows + 2 * given)
