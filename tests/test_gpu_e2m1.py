@@ -295,3 +295,25 @@ def test_projection_parts_of_rows(rows, h, vocab, pad, monkeypatch):
         part = slice(at, min(at + 2048, vocab))
         want = ref.logits(_np(x), ref.unpack(_np(w[part])), _np(s[part]))
         assert np.array_equal(_np(first[:, part]), want), at
+
+
+@pytest.mark.parametrize("rows", [2, 40, 70])
+def test_projection_ends_of_the_numbers(rows, tile):
+    """Entries past the largest number are infinite, as dequantize_groups_e2m1 gives them,
+    and the largest below are not; hidden entries below 2^-126 keep their value."""
+    h, vocab = 64, 70
+    w = torch.zeros(vocab, h // 2, dtype=torch.uint8, device="cuda")
+    s = torch.full((vocab, h // 32), 127, dtype=torch.uint8, device="cuda")
+    # 2 and 1 times 2^127, 6 and 3 times 2^126, -4 times 2^126, 1 times 2^120
+    for v, (code, byte) in enumerate([(4, 254), (2, 254), (7, 253), (5, 253), (14, 253), (2, 247)]):
+        w[v, 0], s[v, 0] = code, byte
+    x = torch.zeros(rows, h, dtype=torch.bfloat16, device="cuda")
+    x[0, 0], x[1, 0] = 2.0 ** -30, -(2.0 ** -133)
+    values = ts.dequantize_groups_e2m1(w, s)
+    assert torch.isinf(values[[0, 2, 4], 0]).all() and torch.isfinite(values[[1, 3, 5]]).all()
+    with np.errstate(invalid="ignore"):
+        want = _np(x) @ _np(values).T
+    got = _np(ts.lmhead_logits_local_e2m1(x, w, s))
+    assert np.array_equal(got, want, equal_nan=True)
+    assert got[0, 1] == 2.0 ** 97 and got[1, 5] == -(2.0 ** -13) and np.isnan(got[rows - 1, 0]) \
+        == (rows > 2)
