@@ -242,6 +242,9 @@ int lmhead_logits_local_e4m3(const void* hidden, const float* hidden_scales, int
  *   logits[r, v] = sum_h hidden[r, h] * 2^e[v, h / 32] * q[v, h],
  *   over the rank's own vocabulary slice, never gathered.  hidden stays bf16;
  *   every product is exact in fp32 and sums are fp32.
+ *   The entries 2^e q are those that dequantize_groups_e2m1 gives: past the largest
+ *   number (scale bytes 253 and 254, which quantize_groups_e2m1 does not write) they
+ *   are infinite, and 0 times them is NaN.
  *   hidden          bf16 [rows, hidden_dim], leading dimension ld_hidden
  *   lm_head         codes [vocab_local, hidden_dim / 2], leading dimension
  *                   ld_lm_head (bytes)
