@@ -528,8 +528,11 @@ int token_logprobs_backward_ex(const void* logits, int32_t logits_type, int64_t 
  * row takes part.  A left-out row has rank 0 and lists nothing; a bad row has rank
  * 0, ids -1 and NaN.  entropies, row_stats and row_status as in token_logprobs;
  * row_stats serve token_logprobs_backward and token_logprobs_listed_backward.
- * Short rows beside max_logprobs (vocab below 64 times as many) and rows with very
- * many equal logits are read again (same results, slower).
+ * Some rows may be read again, once or several times (same results, slower): those
+ * with few entries for each alternative, below about 512 in fp32 and 1,024 in bf16 for
+ * up to 48 alternatives, 128 and 256 for up to 128, 32 and 64 beyond; and those where
+ * more than 2,048 entries reach the bound that the largest of groups of neighbouring
+ * entries give, as with very many equal logits or the likely tokens side by side.
  */
 size_t token_logprobs_topn_workspace_bytes(int64_t rows, int64_t vocab);
 int token_logprobs_topn(const void* logits, int32_t logits_type, int64_t rows, int64_t vocab,

@@ -262,7 +262,7 @@ __device__ __forceinline__ uint32_t bound_of_threads(uint32_t most, int n, TopSh
 // The same from the largest of every four threads (n <= kThreads / 4), by every wave
 // for itself: a quarter of the numbers, a sixteenth of the comparisons, and a bound
 // that hardly more groups reach as long as n is small beside them (at n = 20 some 24
-// of 1,187).
+// of 1,187).  Below -inf's number if fewer than n of the quads have a group.
 __device__ __forceinline__ uint32_t bound_of_quads(uint32_t most, int n, TopShared& sh) {
   const int tid = threadIdx.x, lane = tid & 63;
   auto step = [](uint32_t v, auto ctrl) {
@@ -431,7 +431,13 @@ __device__ __forceinline__ void find_candidates(const T* row, int vocab, const G
     return sh.n_cand <= kCandidates;
   };
 
-  // Twice the groups that a bound needs, or it lets too many entries through.
+  // A thread's own groups: twice as many as a bound needs, or it lets too many entries
+  // through.  Shared ones are not counted: where fewer than n quads (8 a slab) or, above
+  // kQuadMost, groups (32 a slab) have entries, the bound is -inf's number or less, every
+  // entry reaches it, and a row of more than kCandidates is gone through twice in vain
+  // before the steps below.  640 rows, us (20 alternatives from 8,580 fp32 and 17,160 bf16
+  // entries on, and 40 from 17,284 and 34,568 on, have a bound): fp32 4,096, n = 5 17, 20
+  // 47; 8,192, 20 73; 9,000, 20 25, 40 85; 16,384, 40 140; bf16 32,000, n = 20 33, 40 222.
   if (gs.bits != 0 || live >= 2 * n) {
     uint32_t most = 0;
 #pragma unroll
@@ -450,7 +456,9 @@ __device__ __forceinline__ void find_candidates(const T* row, int vocab, const G
       });
     }
     // Too many: equal entries, masked ones most often.  Then those above, and of the
-    // equal ones the first.
+    // equal ones the first.  Still too many: the steps below, as where likely tokens lie
+    // side by side (640 x 151,936 fp32, logits that rise with the ids, n = 20: 1,140 us
+    // where 88 are usual).
     for (int above = 0; above < 2; ++above) {
       if (collect(bound + above)) {
         if (sh.n_cand < n) add_equal(row, vocab, bound, n, sh);
@@ -459,8 +467,10 @@ __device__ __forceinline__ void find_candidates(const T* row, int vocab, const G
       __syncthreads();
     }
   }
-  // Few groups beside n: rows shorter than 32 n (fp32) or 64 n (bf16) entries, which are
-  // gone through again (1,000 x 4,000 fp32, n = 300 82 us).
+  // No bound, or one that lets too many through: few groups beside n (rows shorter than
+  // 32 n fp32 or 64 n bf16 entries for a thread's own groups, 128 n and 256 n for shared
+  // ones, 512 n and 1,024 n up to kQuadMost).  The row is gone through again, at least
+  // twice (1,000 x 4,000 fp32, n = 300 78 us).
   auto each_entry = [&](auto use) {
     for (int64_t i = tid; i < vocab; i += kThreads)
       use(entry_key(static_cast<float>(row[i]), static_cast<int>(i)));
@@ -603,6 +613,11 @@ __device__ __forceinline__ void finish_topn(const T* row, int64_t r, int vocab, 
   }
 }
 
+// Statistics and outputs in one launch want 157 to 178 registers.  Four workgroups a CU,
+// 128 registers and some spilled (6 to 35), are the better half of the time.  us with four
+// and three: 20 alternatives, 640 x 32,000 fp32 29 and 27, bf16 33 and 27; 4,000 x 32,000
+// 143 and 134, 123 and 111; 100 of them, fp32 192 and 207; 5, 4,000 x 4,096 fp32 46 and
+// 54, 4,000 x 8,192 bf16 67 and 60.  Two: 27, 36, 135, 144, 208, 54 and 82.
 template <bool ENT, typename T>
 __global__ __launch_bounds__(kThreads, 4) void topn_whole_kernel(
     const T* __restrict__ x, int64_t ld, int rows, int vocab, const int32_t* __restrict__ tokens,

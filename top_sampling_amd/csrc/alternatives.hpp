@@ -1,5 +1,5 @@
 // Host-side interface of scoring with alternatives and of listed tokens
-// (alternatives.hip), used by the entry points in api_alternatives.hip.  Every
+// (alternatives.hip), used by the entry points in api_losses.hip.  Every
 // launcher assumes its arguments were validated there.
 #pragma once
 

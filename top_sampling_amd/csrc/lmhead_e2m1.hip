@@ -222,11 +222,13 @@ __device__ __forceinline__ bf16x8 frag_of(uint32_t w, float s) {
 // Where the waves' shares are not the whole row, the lm_head is gone through again
 // for each further part of it, and the sums so far come back from the logits.
 // Bound by the lm_head's loads: 1 x 4,096 x 151,936 takes 57 us (5.8 TB/s), 16 rows
-// 68, 32 rows 78.  Reading the same bytes in this pattern and nothing else takes 53;
+// 70, 32 rows 78.  Reading the same bytes in this pattern and nothing else takes 53;
 // the scales' loads 3 to 9 of it, the waves' meeting for a tile about 10.  Measured and
 // dropped: one tile's loads on their way only (82 us), scales byte by byte (+8), loads
 // past the caches (+10: a row's line is asked for twice), every wave at every sum
-// (+2), the hidden rows in LDS and whole rows a wave (73 us, 16 rows 76).
+// (+2), the hidden rows in LDS and whole rows a wave (73 us, 16 rows 76).  The widest
+// shapes spill: shares of 1,024 that are not all whole 9 registers, in several parts 21
+// (5 where whole), and 32 rows in several parts 4 where they are not whole.
 constexpr int kStep = 128;  // entries of a row in one step
 constexpr int kFewWaves = 8;
 
@@ -497,15 +499,17 @@ __device__ __forceinline__ void store_output(const f32x16 (&acc)[TM][TN], uint8_
 // of a step takes the i-th eight entries of each lane's group, so its hidden
 // fragment is chunk 4 (l / 32) + i.  A wave has all of the tile's hidden rows, so the
 // conversions (four instructions a fragment, two to five products) are made once.
-// Bound by the matrix cores: 640 x 4,096 x 151,936 takes 628 to 662 us (1.2 PFLOP/s and
-// more; the bf16 projection 720).  Few row tiles are bound by what a step waits for (64
-// rows past the caches 262 us, through them 164, 122 to 141 since the scales come
+// Bound by the matrix cores: 640 x 4,096 x 151,936 takes 628 to 662 us with the clock of
+// the run (1.2 PFLOP/s and more; the bf16 projection 720); 6 of the 160-row tile's
+// registers spill.  Few row tiles are bound by what a step waits for (64
+// rows past the caches 262 us, through them 164, 122 to 126 since the scales come
 // several at a time).  Without gain there: the codes of two steps in pieces of 64 bytes,
 // those of four at once, tiles that begin at different steps.
 // Scales come several groups at a time, 16 for 64 rows and 8 for more, where 16 take
-// registers that are not there (rows of that many groups; us with 16, 8 and, as a
-// shorter row has them, a byte a step: 640 x 4,096 x 151,936 748, 671 and 705; 256 rows
-// 310, 309 and 337; 64 x 2,560 x 100,000 59, 65 and 70).
+// registers that are not there (rows of that many groups; us in one run with 16, 8 and,
+// as a shorter row has them, a byte a step: 640 x 4,096 x 151,936 748, 671 and 705; 256
+// rows 310, 309 and 337; 64 x 2,560 x 100,000 59, 65 and 70.  Other runs are up to a tenth
+// faster throughout: 650, 283 and 53 as it is).
 template <int BM>
 constexpr int kScales = BM <= 64 ? 16 : 8;
 
@@ -759,7 +763,7 @@ constexpr int kFewRows = 32;
 // the row has few shares: 5 x 2,560 x 31,037 10.9 us, one 12.4; 1 x 2,560 x 248,320
 // 58 and 64; 1 x 4,096 x 151,936 61 and 57.  Four of short rows: 4 x 256 x 100,000
 // 9.5, shares of 512 14.6; 16 x 1,024 x 100,000 16.8 and 17.2; 32 x 256 x 100,000 17
-// and 22.  Rows of 8,192, 4 x 100,000: 85 us at once, 103 in two parts.
+// and 22.  Rows of 8,192, 4 x 100,000: 84 us at once, 103 in two parts.
 hipError_t launch_few_rows(const Projection& p, hipStream_t stream) {
   const int k = p.hidden_dim;
   if (p.rows <= 16) {
@@ -773,15 +777,15 @@ hipError_t launch_few_rows(const Projection& p, hipStream_t stream) {
 }
 
 // The kernel for few rows up to 32 of them, unless the row is short, us, it and 64-row
-// tiles: 32 x 4,096 x 151,936 91 and 132, 36 120 and 131, 48 132 and 130, 64 151 and
-// 141; 32 x 1,024 x 100,000 23 and 22, 32 x 512 20 and 14, 16 x 512 14 and 14, 16 x 256 14 and
-// 10.
+// tiles: 32 x 4,096 x 151,936 78 and 114; 32 x 1,024 x 100,000 23 and 21, 32 x 512 19 and
+// 14, 16 x 512 13.5 and 13, 16 x 256 13.5 and 10.
+// From 33 rows on the tiles take 116 us, at 64 124.
 // Up to 64, 64 x 256 tiles, or 64 x 128 where those would leave a quarter of the CUs
-// without one (64 x 4,096 x 31,000: 34 and 26; 48 x 6,144 x 60,000 81 and 84).  Beyond,
+// without one (64 x 4,096 x 31,000: 34 and 25; 48 x 6,144 x 60,000 70 and 71).  Beyond,
 // 128 or 160 rows a tile, whichever takes less: a tile of 160 rows takes 1.2 times one of
-// 128 (4,096 x 151,936, 160 and 128 rows a tile: 160 rows 228 and 299, 256 364 and 306,
-// 320 365 and 417, 640 659 and 669; 1,024 x 100,000 730 and 711), and 64 again where
-// they are too few (128 x 4,096 x 31,000 41 and 56; 128 x 60,000 93 and 84).
+// 128 (4,096 x 151,936, 160 and 128 rows a tile: 160 rows 204 and 272, 256 332 and 283,
+// 320 338 and 392, 640 650 and 658; 1,024 x 100,000 707 and 687), and 64 again where
+// they are too few (128 x 4,096 x 31,000 38 and 53; 128 x 60,000 76 and 65).
 int choose(const Projection& p) {
   if (p.rows <= kFewRows && p.hidden_dim > 32 * p.rows) return 1;
   const int64_t wide = (p.vocab - 1) / 256 + 1;
