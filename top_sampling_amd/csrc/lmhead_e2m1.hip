@@ -499,8 +499,8 @@ __device__ __forceinline__ void store_output(const f32x16 (&acc)[TM][TN], uint8_
 // of a step takes the i-th eight entries of each lane's group, so its hidden
 // fragment is chunk 4 (l / 32) + i.  A wave has all of the tile's hidden rows, so the
 // conversions (four instructions a fragment, two to five products) are made once.
-// Bound by the matrix cores: 640 x 4,096 x 151,936 takes 628 to 662 us with the clock of
-// the run (1.2 PFLOP/s and more; the bf16 projection 720); 6 of the 160-row tile's
+// Bound by the matrix cores: 640 x 4,096 x 151,936 takes 628 to 682 us with the clock of
+// the run (1.17 PFLOP/s and more; the bf16 projection 720); 6 of the 160-row tile's
 // registers spill.  Few row tiles are bound by what a step waits for (64
 // rows past the caches 262 us, through them 164, 122 to 126 since the scales come
 // several at a time).  Without gain there: the codes of two steps in pieces of 64 bytes,
